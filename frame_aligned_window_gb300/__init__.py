@@ -13,7 +13,11 @@ The names mirror the C ABI:
     wsattn_plan_info, wsattn_get_tiles, wsattn_get_block_map, wsattn_get_csr, wsattn_get_stats,
     wsattn_plan_set_debug, wsattn_plan_set_bound, wsattn_device_status,
     wsattn_selftest_timeout, wsattn_status_string, wsattn_prepare_static, wsattn_produce,
-    wsattn_build_flags
+    wsattn_build_flags,
+    wsattn_rotary_plan, wsattn_rotary_destroy, wsattn_rotary, wsattn_qknorm,
+    wsattn_qknorm_backward, wsattn_qknorm_backward_workspace, wsattn_linear,
+    wsattn_linear_workspace, wsattn_linear_backward, wsattn_linear_backward_workspace,
+    wsattn_op_status
 """
 from __future__ import annotations
 
@@ -34,6 +38,10 @@ EXPORTS = (
     "wsattn_plan_set_debug", "wsattn_plan_set_bound", "wsattn_device_status",
     "wsattn_selftest_timeout", "wsattn_status_string", "wsattn_prepare_static",
     "wsattn_produce", "wsattn_build_flags",
+    "wsattn_rotary_plan", "wsattn_rotary_destroy", "wsattn_rotary", "wsattn_qknorm",
+    "wsattn_qknorm_backward", "wsattn_qknorm_backward_workspace", "wsattn_linear",
+    "wsattn_linear_workspace", "wsattn_linear_backward", "wsattn_linear_backward_workspace",
+    "wsattn_op_status",
 )
 
 # wsattn_bound
@@ -44,6 +52,12 @@ BOUND_WINDOW = 1
 MASK_CAUSAL = 1
 MASK_REF_SUFFIX = 2
 MASK_REF_LOCAL = 4
+
+# wsattn_dtype
+BF16, FP16, FP32 = 0, 1, 2
+
+# wsattn_activation, by the name the linear products take
+ACTIVATIONS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 
 STATUS = {0: "OK", 1: "BAD_ARG", 2: "BAD_BLOCK", 3: "UNSUPPORTED", 4: "NOT_PREPARED",
           5: "BATCH_MISMATCH", 6: "CUDA", 7: "TIMEOUT", 8: "NO_MEMORY", 9: "BOUNDS"}
@@ -83,6 +97,46 @@ _lib.wsattn_status_string.argtypes = [_I]
 _lib.wsattn_prepare_static.argtypes = [_I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P, _P]
 _lib.wsattn_produce.argtypes = [_P, _I, _P, _I, _P, _P, _P, _F, _P, _P, _P, _P]
 _lib.wsattn_build_flags.argtypes = []
+
+
+class _Heads(ctypes.Structure):
+    """wsattn_heads: a [batch, heads, N, D] view."""
+    _fields_ = [("data", _P), ("heads", _I), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+
+
+class _LinearArgs(ctypes.Structure):
+    """wsattn_linear_args."""
+    _fields_ = [("dtype", _I), ("out_dtype", _I), ("m", ctypes.c_int64), ("n", _I), ("k", _I),
+                ("x", _P), ("ldx", ctypes.c_int64), ("x_heads", _I),
+                ("x_tokens", ctypes.c_int64), ("w", _P), ("ldw", ctypes.c_int64), ("bias", _P),
+                ("residual", _P), ("ldr", ctypes.c_int64), ("out", _P), ("ldo", ctypes.c_int64),
+                ("preact", _P), ("ldp", ctypes.c_int64), ("activation", _I)]
+
+
+class _LinearGradArgs(ctypes.Structure):
+    """wsattn_linear_grad_args."""
+    _fields_ = [("dtype", _I), ("m", ctypes.c_int64), ("n", _I), ("k", _I), ("dout", _P),
+                ("ldd", ctypes.c_int64), ("x", _P), ("ldx", ctypes.c_int64), ("w", _P),
+                ("ldw", ctypes.c_int64), ("preact", _P), ("ldp", ctypes.c_int64),
+                ("activation", _I), ("dx", _P), ("lddx", ctypes.c_int64), ("dw", _P),
+                ("lddw", ctypes.c_int64), ("db", _P)]
+
+
+_I64, _SZP, _HP = ctypes.c_int64, ctypes.POINTER(_SZ), ctypes.POINTER(_Heads)
+_lib.wsattn_rotary_plan.argtypes = [_I, _I, _P, _P, _I, ctypes.POINTER(_P)]
+_lib.wsattn_rotary_destroy.argtypes = [_P]
+_lib.wsattn_rotary.argtypes = [_P, _I, _I, _I64, _HP, _P, _I64, _I, _HP, _P]
+_lib.wsattn_qknorm.argtypes = [_P, _I, _I, _I64, _HP, _HP, _HP, _P, _P, _I, _F, _P, _I64, _HP,
+                               _HP, _HP, _P]
+_lib.wsattn_qknorm_backward.argtypes = [_P, _I, _I, _I64, _HP, _HP, _HP, _HP, _HP, _P, _P, _I, _F,
+                                        _P, _I64, _HP, _HP, _HP, _P, _P, _P, _SZ, _P]
+_lib.wsattn_qknorm_backward_workspace.argtypes = [_P, _SZP]
+_lib.wsattn_linear.argtypes = [ctypes.POINTER(_LinearArgs), _P, _SZ, _P]
+_lib.wsattn_linear_workspace.argtypes = [ctypes.POINTER(_LinearArgs), _SZP]
+_lib.wsattn_linear_backward.argtypes = [ctypes.POINTER(_LinearGradArgs), _P, _SZ, _P]
+_lib.wsattn_linear_backward_workspace.argtypes = [ctypes.POINTER(_LinearGradArgs), _SZP]
+_lib.wsattn_op_status.argtypes = [_P]
 _lib.wsattn_status_string.restype = ctypes.c_char_p
 for _name in EXPORTS:
     if _name != "wsattn_status_string":
@@ -345,6 +399,465 @@ def wsattn_prepare_static_outputs(batch, heads, n_tokens, head_dim, device="cuda
             "mu": torch.empty(bh, head_dim, **f), "kmax": torch.empty(bh, **f),
             "bmax": torch.empty(bh, **f),
             "elig": torch.empty(bh, dtype=torch.uint8, device=device)}
+
+
+# ------------------------------------------------ operators around the attention
+
+def _dtype_code(t, name, allowed=(BF16, FP16, FP32)):
+    import torch
+    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{name} must not be {t.dtype}")
+    return code
+
+
+def _same_device(dev, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _stream_on(dev, stream):
+    """The stream a call on tensors of `dev` goes to (default: that device's current one)."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+    return stream
+
+
+def _empty(shape, dtype, dev, stream):
+    """Memory from `stream`'s own pool, so that its reuse is ordered with the
+    work the call enqueues there (and, in a capture, belongs to the graph)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _run(dev, what, fn, *args):
+    """The C call, with the tensors' device current."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args), what)
+
+
+class RotaryPlan:
+    """Owns a wsattn_rotary_t handle (host memory only)."""
+
+    def __init__(self, handle, head_dim, axes):
+        self._h = handle
+        self.head_dim = head_dim
+        self.axes = axes
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise ValueError("rotary plan was destroyed")
+        return self._h
+
+    def destroy(self):
+        if self._h is not None:
+            _lib.wsattn_rotary_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def wsattn_rotary_plan(head_dim, sections=None, base: float = 10000.0, interleaved: bool = True,
+                       pair_axis=None, pair_freq=None) -> RotaryPlan:
+    """Turning rates of a head's pairs.  sections: pairs turned by each axis of
+    the positions (time, height, width, ...), in order; pair j of a section of
+    n turns by base**(-j / n) radians per unit of its axis, and pairs behind
+    the sections are left alone.  Or pair_axis and pair_freq [D / 2] directly.
+    interleaved: pairs are dims (2p, 2p + 1) (as wsattn_produce turns them),
+    else (p, p + D / 2)."""
+    if (pair_axis is None) != (pair_freq is None) or (sections is None) == (pair_axis is None):
+        raise ValueError("give sections, or pair_axis and pair_freq")
+    half = int(head_dim) // 2
+    if sections is not None:
+        sections = tuple(int(n) for n in sections)
+        if not sections or min(sections) < 0 or sum(sections) > half:
+            raise ValueError(f"sections {sections} do not fit {half} pairs")
+        if not base > 0:
+            raise ValueError("base must be positive")
+        pair_axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        pair_freq = [float(base) ** (-j / n) for n in sections for j in range(n)]
+        pair_axis += [0] * (half - len(pair_axis))
+        pair_freq += [0.0] * (half - len(pair_freq))
+        axes = len(sections)
+    else:
+        axes = max(pair_axis, default=-1) + 1
+    axis = np.ascontiguousarray(pair_axis, dtype=np.int32)
+    freq = np.ascontiguousarray(pair_freq, dtype=np.float64)
+    if axis.shape != (half,) or freq.shape != (half,):
+        raise ValueError(f"pair_axis and pair_freq must have {half} entries")
+    h = _P()
+    _check(_lib.wsattn_rotary_plan(int(head_dim), int(axes), axis.ctypes.data, freq.ctypes.data,
+                                   int(bool(interleaved)), ctypes.byref(h)), "wsattn_rotary_plan")
+    return RotaryPlan(h, int(head_dim), int(axes))
+
+
+def wsattn_rotary_destroy(rot: RotaryPlan):
+    rot.destroy()
+
+
+def _head_view(t, name, shape, dtype):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    sb, sh, sn, sd = t.stride()
+    if sd != 1 and t.numel():
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return _Heads(t.data_ptr(), shape[1], sb, sh, sn)
+
+
+def _positions(rot, positions, batch, tokens):
+    import torch
+    if positions.dtype != torch.float32:
+        raise TypeError(f"positions must be torch.float32, got {positions.dtype}")
+    shape = tuple(positions.shape)
+    if shape == (tokens, rot.axes):
+        stride = 0
+    elif shape == (batch, tokens, rot.axes):
+        stride = positions.stride(0) if batch > 1 else 0
+    else:
+        raise ValueError(f"positions must be [{tokens}, {rot.axes}] or [{batch}, {tokens}, "
+                         f"{rot.axes}], got {list(shape)}")
+    inner = positions if len(shape) == 2 else (positions[0] if batch else positions)
+    if positions.numel() and not inner.is_contiguous():
+        raise ValueError("positions must be contiguous")
+    return ctypes.c_void_p(positions.data_ptr()), stride
+
+
+def _heads_shape(t, name, rot):
+    if t.dim() != 4 or t.shape[3] != rot.head_dim:
+        raise ValueError(f"{name} must be [B, H, N, {rot.head_dim}], got {list(t.shape)}")
+    return tuple(t.shape)
+
+
+def wsattn_rotary(rot: RotaryPlan, x, positions, inverse: bool = False, out=None, stream=None):
+    """x [B, H, N, D] (bf16, fp16 or fp32; any strides, last dimension
+    contiguous) turned by positions fp32 [N, axes] or [B, N, axes]; inverse
+    turns back (the gradient).  out: default a contiguous tensor; may be x."""
+    shape = _heads_shape(x, "x", rot)
+    _same_device(x.device, x=x, positions=positions, out=out)
+    s = _stream_on(x.device, stream)
+    code = _dtype_code(x, "x")
+    if out is None:
+        out = _empty(shape, x.dtype, x.device, stream)
+    pos, pos_b = _positions(rot, positions, shape[0], shape[2])
+    _run(x.device, "wsattn_rotary", _lib.wsattn_rotary, rot.handle, code, shape[0], shape[2],
+         _head_view(x, "x", shape, x.dtype), pos, pos_b, int(bool(inverse)),
+         _head_view(out, "out", shape, x.dtype), s.cuda_stream)
+    return out
+
+
+def _gain(t, name, dim, dtype):
+    """(pointer, dtype code or None) of a gain vector."""
+    import torch
+    if t is None:
+        return None, None
+    if tuple(t.shape) != (dim,) or (dim > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous [{dim}], got {list(t.shape)}")
+    if t.dtype not in (dtype, torch.float32):
+        raise TypeError(f"{name} must be {dtype} or torch.float32, got {t.dtype}")
+    return ctypes.c_void_p(t.data_ptr()), _dtype_code(t, name)
+
+
+def _gains(q_weight, k_weight, dim, dtype, code):
+    wq, cq = _gain(q_weight, "q_weight", dim, dtype)
+    wk, ck = _gain(k_weight, "k_weight", dim, dtype)
+    if cq is not None and ck is not None and cq != ck:
+        raise TypeError("q_weight and k_weight must have one type")
+    return wq, wk, code if cq is None and ck is None else (ck if cq is None else cq)
+
+
+def _qkv_shapes(rot, q, k, v):
+    """Checked shapes of q, k and v (or of their gradients)."""
+    sq, sk = _heads_shape(q, "q", rot), _heads_shape(k, "k", rot)
+    sv = None if v is None else _heads_shape(v, "v", rot)
+    for name, sh in (("k", sk), ("v", sv)):
+        if sh is not None and (sh[0] != sq[0] or sh[2] != sq[2]):
+            raise ValueError(f"{name} must have q's batch and tokens, got {list(sh)}")
+    return sq, sk, sv
+
+
+def wsattn_qknorm(rot: RotaryPlan, q, k, positions, q_weight=None, k_weight=None,
+                  eps: float = 1e-6, v=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """Per-head RMS norm (with gains [D]) and rotation of q [B, Hq, N, D] and
+    k [B, Hk, N, D], and a copy of v, in one pass; q, k, v may be views of one
+    projection's rows.  Returns (q, k) or (q, k, v), by default contiguous, as
+    wsattn_prepare and wsattn_forward read them; an output may be its input."""
+    sq, sk, sv = _qkv_shapes(rot, q, k, v)
+    if v is None and v_out is not None:
+        raise ValueError("v_out without v")
+    _same_device(q.device, q=q, k=k, v=v, positions=positions, q_weight=q_weight,
+                 k_weight=k_weight, q_out=q_out, k_out=k_out, v_out=v_out)
+    s = _stream_on(q.device, stream)
+    code = _dtype_code(q, "q")
+    wq, wk, wcode = _gains(q_weight, k_weight, rot.head_dim, q.dtype, code)
+    dt, dev = q.dtype, q.device
+    q_out = _empty(sq, dt, dev, stream) if q_out is None else q_out
+    k_out = _empty(sk, dt, dev, stream) if k_out is None else k_out
+    if v is not None and v_out is None:
+        v_out = _empty(sv, dt, dev, stream)
+    pos, pos_b = _positions(rot, positions, sq[0], sq[2])
+    _run(dev, "wsattn_qknorm", _lib.wsattn_qknorm, rot.handle, code, sq[0], sq[2],
+         _head_view(q, "q", sq, dt), _head_view(k, "k", sk, dt),
+         None if v is None else _head_view(v, "v", sv, dt), wq, wk, wcode, float(eps), pos, pos_b,
+         _head_view(q_out, "q_out", sq, dt), _head_view(k_out, "k_out", sk, dt),
+         None if v is None else _head_view(v_out, "v_out", sv, dt), s.cuda_stream)
+    return (q_out, k_out) if v is None else (q_out, k_out, v_out)
+
+
+def wsattn_qknorm_backward_workspace(rot: RotaryPlan) -> int:
+    """Bytes of scratch wsattn_qknorm_backward takes for the gains' gradients."""
+    n = _SZ()
+    _check(_lib.wsattn_qknorm_backward_workspace(rot.handle, ctypes.byref(n)),
+           "wsattn_qknorm_backward_workspace")
+    return int(n.value)
+
+
+def wsattn_qknorm_backward(rot: RotaryPlan, dq_out, dk_out, q, k, positions, q_weight=None,
+                           k_weight=None, eps: float = 1e-6, dv_out=None, dq=None, dk=None,
+                           dv=None, workspace=None, stream=None):
+    """Gradients of wsattn_qknorm: (dq, dk, dv, dq_weight, dk_weight).  dq, dk
+    and dv may be views of one packed gradient (default: contiguous); dv is
+    None without dv_out, and a gain's gradient (fp32 [D]) None without the gain."""
+    import torch
+    sq, sk, sv = _qkv_shapes(rot, q, k, dv_out)
+    if dv_out is None and dv is not None:
+        raise ValueError("dv without dv_out")
+    _same_device(q.device, q=q, k=k, dq_out=dq_out, dk_out=dk_out, dv_out=dv_out,
+                 positions=positions, q_weight=q_weight, k_weight=k_weight, dq=dq, dk=dk, dv=dv,
+                 workspace=workspace)
+    s = _stream_on(q.device, stream)
+    code = _dtype_code(q, "q")
+    wq, wk, wcode = _gains(q_weight, k_weight, rot.head_dim, q.dtype, code)
+    dt, dev = q.dtype, q.device
+    dq = _empty(sq, dt, dev, stream) if dq is None else dq
+    dk = _empty(sk, dt, dev, stream) if dk is None else dk
+    if dv_out is not None and dv is None:
+        dv = _empty(sv, dt, dev, stream)
+    dwq = None if q_weight is None else _empty((rot.head_dim,), torch.float32, dev, stream)
+    dwk = None if k_weight is None else _empty((rot.head_dim,), torch.float32, dev, stream)
+    if (dwq is not None or dwk is not None) and workspace is None:
+        workspace = _empty((wsattn_qknorm_backward_workspace(rot),), torch.uint8, dev, stream)
+    pos, pos_b = _positions(rot, positions, sq[0], sq[2])
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _run(dev, "wsattn_qknorm_backward", _lib.wsattn_qknorm_backward, rot.handle, code, sq[0],
+         sq[2], _head_view(dq_out, "dq_out", sq, dt), _head_view(dk_out, "dk_out", sk, dt),
+         None if dv is None else _head_view(dv_out, "dv_out", sv, dt), _head_view(q, "q", sq, dt),
+         _head_view(k, "k", sk, dt), wq, wk, wcode, float(eps), pos, pos_b,
+         _head_view(dq, "dq", sq, dt), _head_view(dk, "dk", sk, dt),
+         None if dv is None else _head_view(dv, "dv", sv, dt), ptr(dwq), ptr(dwk), ptr(workspace),
+         0 if workspace is None else workspace.numel() * workspace.element_size(), s.cuda_stream)
+    return dq, dk, dv, dwq, dwk
+
+
+def _rows(t, name, cols, lead=None):
+    """(rows, row stride) of t seen as a matrix of `cols` columns; the leading
+    dimensions must lie one row stride apart."""
+    if t.dim() < 1 or t.shape[-1] != cols or (lead is not None and tuple(t.shape[:-1]) != lead):
+        want = "..." if lead is None else ", ".join(str(x) for x in lead)
+        raise ValueError(f"{name} must be [{want}, {cols}], got {list(t.shape)}")
+    rows, ld = 1, None
+    if t.numel() == 0:
+        return t[..., 0].numel() if cols else 0, cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] == 1:
+            continue
+        if ld is None:
+            ld = t.stride(i)
+        elif t.stride(i) != ld * rows:
+            raise ValueError(f"{name}'s rows must lie one stride apart")
+        rows *= t.shape[i]
+    if ld is not None and ld < cols:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return rows, cols if ld is None else ld
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _scratch(query, args, workspace, dev, stream):
+    """(pointer, bytes, tensor) of a call's workspace, allocated when needed."""
+    import torch
+    n = _SZ()
+    _check(query(ctypes.byref(args), ctypes.byref(n)), "workspace size")
+    if workspace is None and n.value:
+        workspace = _empty((n.value,), torch.uint8, dev, stream)
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, stream):
+    import torch
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
+    n, k = weight.shape
+    code = _dtype_code(weight, "weight", (BF16, FP16))
+    dev = weight.device
+    _same_device(dev, x=x, weight=weight, bias=bias, residual=residual, preact=preact, out=out)
+    a = _LinearArgs(dtype=code, n=n, k=k, activation=_activation(activation))
+    if x.dtype == torch.float32 and x.dim() == 4:
+        B, H, N, D = x.shape
+        if H * D != k or not x.is_contiguous():
+            raise ValueError(f"x must be contiguous [B, H, N, D] with H * D = {k}, "
+                             f"got {list(x.shape)}")
+        lead = (B, N)
+        a.m, a.x_heads, a.x_tokens = B * N, H, N
+    else:
+        if x.dtype != weight.dtype:
+            raise TypeError(f"x must be {weight.dtype} (or wsattn_forward's fp32 output), "
+                            f"got {x.dtype}")
+        lead = tuple(x.shape[:-1])
+        a.m, a.ldx = _rows(x, "x", k)
+    a.x, a.w = x.data_ptr(), weight.data_ptr()
+    _, a.ldw = _rows(weight, "weight", k)
+    if bias is not None:
+        if tuple(bias.shape) != (n,) or bias.dtype != weight.dtype or (n > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias must be contiguous {weight.dtype} [{n}]")
+        a.bias = bias.data_ptr()
+    if out is None:
+        out_dtype = weight.dtype if out_dtype is None else out_dtype
+        out = _empty(lead + (n,), out_dtype, dev, stream)
+    elif out_dtype not in (None, out.dtype):
+        raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+    a.out_dtype = _dtype_code(out, "out", (code, FP32))
+    a.out = out.data_ptr()
+    _, a.ldo = _rows(out, "out", n, lead)
+    if residual is not None:
+        if residual.dtype != out.dtype:
+            raise TypeError(f"residual must be {out.dtype}, got {residual.dtype}")
+        a.residual = residual.data_ptr()
+        _, a.ldr = _rows(residual, "residual", n, lead)
+    if preact is not None:
+        if preact.dtype != weight.dtype:
+            raise TypeError(f"preact must be {weight.dtype}, got {preact.dtype}")
+        a.preact = preact.data_ptr()
+        _, a.ldp = _rows(preact, "preact", n, lead)
+    return a, out, dev
+
+
+def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact=None, out=None,
+                  out_dtype=None, workspace=None, stream=None):
+    """residual + act(x weight^T + bias): x [..., k] in weight's type (bf16 or
+    fp16), or wsattn_forward's fp32 output [B, H, N, D], whose heads are merged
+    (the result is then [B, N, n]).  activation: a name in ACTIVATIONS.
+    preact: a tensor that receives x weight^T + bias, for
+    wsattn_linear_backward.  out (or out_dtype): weight's type or fp32, and
+    the residual's; residual may be out."""
+    a, out, dev = _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype,
+                               stream)
+    _same_device(dev, workspace=workspace)
+    s = _stream_on(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_workspace, a, workspace, dev, stream)
+    _run(dev, "wsattn_linear", _lib.wsattn_linear, a, ws, nbytes, s.cuda_stream)
+    return out
+
+
+def wsattn_linear_workspace(x, weight) -> int:
+    """Bytes of scratch wsattn_linear takes for these operands (0 when their
+    rows start on 16-byte boundaries and x is not the attention's output)."""
+    a, _, _ = _linear_args(x, weight, None, None, "none", None, None, None, None)
+    n = _SZ()
+    _check(_lib.wsattn_linear_workspace(ctypes.byref(a), ctypes.byref(n)),
+           "wsattn_linear_workspace")
+    return int(n.value)
+
+
+def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need, stream):
+    import torch
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
+    n, k = weight.shape
+    code = _dtype_code(weight, "weight", (BF16, FP16))
+    dev = weight.device
+    _same_device(dev, dout=dout, x=x, weight=weight, preact=preact, dx=dx, dw=dw, db=db)
+    a = _LinearGradArgs(dtype=code, n=n, k=k, activation=_activation(activation))
+    if a.activation and preact is None:
+        raise ValueError("an activation's gradient needs preact")
+    for t, name in ((dout, "dout"), (x, "x"), (preact, "preact"), (dx, "dx"), (dw, "dw")):
+        if t is not None and t.dtype != weight.dtype:
+            raise TypeError(f"{name} must be {weight.dtype}, got {t.dtype}")
+    lead = tuple(x.shape[:-1])
+    a.m, a.ldx = _rows(x, "x", k)
+    _, a.ldd = _rows(dout, "dout", n, lead)
+    _, a.ldw = _rows(weight, "weight", k)
+    a.dout, a.x, a.w = dout.data_ptr(), x.data_ptr(), weight.data_ptr()
+    if preact is not None:
+        a.preact = preact.data_ptr()
+        _, a.ldp = _rows(preact, "preact", n, lead)
+    need_dx, need_dw, need_db = need
+    if need_dx or dx is not None:
+        dx = _empty(lead + (k,), weight.dtype, dev, stream) if dx is None else dx
+        a.dx = dx.data_ptr()
+        _, a.lddx = _rows(dx, "dx", k, lead)
+    if need_dw or dw is not None:
+        dw = _empty((n, k), weight.dtype, dev, stream) if dw is None else dw
+        a.dw = dw.data_ptr()
+        _, a.lddw = _rows(dw, "dw", k, (n,))
+    if need_db or db is not None:
+        db = _empty((n,), torch.float32, dev, stream) if db is None else db
+        if tuple(db.shape) != (n,) or db.dtype != torch.float32 or not db.is_contiguous():
+            raise ValueError(f"db must be contiguous torch.float32 [{n}]")
+        a.db = db.data_ptr()
+    return a, dx, dw, db, dev
+
+
+def wsattn_linear_backward(dout, x, weight, preact=None, activation="none", dx=None, dw=None,
+                           db=None, need_dx=True, need_dw=True, need_db=True, workspace=None,
+                           stream=None):
+    """Gradients of wsattn_linear from dout [..., n]: (dx, dw, db), dx and dw in
+    weight's type, db fp32; None for what is not needed.  preact: what
+    wsattn_linear left there (not needed without an activation).  The
+    residual's gradient is dout itself."""
+    a, dx, dw, db, dev = _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db,
+                                           (need_dx, need_dw, need_db), stream)
+    _same_device(dev, workspace=workspace)
+    s = _stream_on(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_backward_workspace, a, workspace, dev, stream)
+    _run(dev, "wsattn_linear_backward", _lib.wsattn_linear_backward, a, ws, nbytes, s.cuda_stream)
+    return dx, dw, db
+
+
+def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="none", need_dx=True,
+                                     need_dw=True, need_db=True) -> int:
+    """Bytes of scratch wsattn_linear_backward takes for these operands."""
+    a, *_ = _linear_grad_args(dout, x, weight, preact, activation, None, None, None,
+                              (need_dx, need_dw, need_db), None)
+    n = _SZ()
+    _check(_lib.wsattn_linear_backward_workspace(ctypes.byref(a), ctypes.byref(n)),
+           "wsattn_linear_backward_workspace")
+    return int(n.value)
+
+
+def wsattn_op_status(stream=None) -> int:
+    """Status of the operators above on the current device (synchronises)."""
+    return int(_lib.wsattn_op_status(_stream_ptr(stream)))
 
 
 def raw_call(name: str):

@@ -1,8 +1,6 @@
 // C ABI of libwsattn (declared in include/wsattn.h): plan lifecycle, device
 // buffers, TMA tensor maps and kernel launches.  Nothing here computes on the
 // host beyond argument checks and the block map (plan.cpp).
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -289,6 +287,10 @@ int enqueue_prepare(wsattn_plan_s* plan, int batch, const void* q, const void* k
 }
 
 }  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 wsattn::tensor_map_encoder() {
+  return get_encode() ? g_encode : nullptr;
+}
 
 extern "C" {
 

@@ -1,0 +1,692 @@
+// C ABI of the operators around the attention (declared in
+// include/wsattn.h): argument checks, work split, tensor maps and launches.
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "ops.h"
+
+using wsattn::GemmParams;
+using wsattn::QkParams;
+using wsattn::QkPart;
+using wsattn::RotTable;
+
+struct wsattn_rotary_s {
+  RotTable table;
+};
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round8(int64_t a) { return (a + 7) / 8 * 8; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+int dtype_size(int dtype) { return dtype == WSATTN_FP32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype >= WSATTN_BF16 && dtype <= WSATTN_FP32; }
+
+int sm_count() {
+  static int sms[wsattn::kMaxDevices] = {};
+  const int dev = wsattn::current_device();
+  if (dev < 0) return 0;
+  if (!sms[dev] &&
+      cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms[dev] = 0;
+  return sms[dev];
+}
+
+// ------------------------------------------------------------- head views
+
+// The smallest strides that keep a view's elements apart, whatever the order
+// of its dimensions.
+bool apart(const wsattn_heads* v, int batch, int64_t n, int dim) {
+  int64_t size[3] = {batch, v->heads, n};
+  int64_t stride[3] = {v->stride_b, v->stride_h, v->stride_n};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (stride[j] < stride[i]) {
+        const int64_t s = stride[i], z = size[i];
+        stride[i] = stride[j];
+        size[i] = size[j];
+        stride[j] = s;
+        size[j] = z;
+      }
+  int64_t extent = dim;
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < extent) return false;
+    extent = stride[i] * (size[i] - 1) + extent;
+  }
+  return true;
+}
+
+bool view_ok(const wsattn_heads* v, int esize) {
+  if (!v || v->heads < 1 || v->stride_b < 0 || v->stride_h < 0 || v->stride_n < 0) return false;
+  return (reinterpret_cast<uintptr_t>(v->data) & static_cast<uintptr_t>(esize - 1)) == 0;
+}
+
+// Every row of the view starts on a 16-byte boundary.
+bool view_vec(const wsattn_heads* v, int batch, int64_t n, int esize) {
+  const int64_t per = 16 / esize;
+  return aligned16(v->data) && (batch <= 1 || v->stride_b % per == 0) &&
+         (v->heads <= 1 || v->stride_h % per == 0) && (n <= 1 || v->stride_n % per == 0);
+}
+
+QkPart part_of(const wsattn_heads* in, const wsattn_heads* out, int norm, int turn,
+               const void* weight) {
+  QkPart p;
+  std::memset(&p, 0, sizeof(p));
+  p.io.in = in->data;
+  p.io.out = out->data;
+  p.io.ib = in->stride_b;
+  p.io.in_ = in->stride_n;
+  p.io.ih = in->stride_h;
+  p.io.ob = out->stride_b;
+  p.io.on = out->stride_n;
+  p.io.oh = out->stride_h;
+  p.io.heads = in->heads;
+  p.norm = norm;
+  p.turn = turn;
+  p.weight = weight;
+  return p;
+}
+
+// Lanes per head row, rows per CTA and, from the wanted number of work items
+// (a warp's worth of tokens times a group of heads), the heads a warp walks.
+void split_work(QkParams* p, int64_t rows, int64_t want_items, int min_heads) {
+  const int pieces = p->rot.pairs / 8;
+  p->lanes_log2 = 0;
+  while ((1 << p->lanes_log2) < pieces) ++p->lanes_log2;
+  p->rows = rows;
+  const int per_cta = wsattn::kQkThreads / 32 * (32 >> p->lanes_log2);
+  p->row_blocks = cdiv(rows, per_cta);
+  int most = 1;
+  for (int i = 0; i < p->parts; ++i)
+    if (p->part[i].io.heads > most) most = p->part[i].io.heads;
+  int gh = most;
+  auto groups = [&](int g) {
+    int64_t n = 0;
+    for (int i = 0; i < p->parts; ++i) n += cdiv(p->part[i].io.heads, g);
+    return n;
+  };
+  while (gh > min_heads && p->row_blocks * groups(gh) < want_items) gh = (gh + 1) / 2;
+  p->group_heads = gh;
+  p->groups = 0;
+  for (int i = 0; i < p->parts; ++i) {
+    p->part[i].group0 = p->groups;
+    p->part[i].groups = static_cast<int>(cdiv(p->part[i].io.heads, gh));
+    p->groups += p->part[i].groups;
+  }
+}
+
+bool positions_ok(const float* positions, int64_t pos_stride_b) {
+  return pos_stride_b >= 0 && (reinterpret_cast<uintptr_t>(positions) & 3u) == 0;
+}
+
+// CTAs of the backward pass: fixed upper bound, so that the workspace does
+// not depend on the device.
+constexpr int kMaxBackCtas = 1024;
+
+// ------------------------------------------------------------------ linear
+
+struct Operand {
+  const void* ptr;
+  int64_t ld;  // elements
+};
+
+bool rows_vec(const void* p, int64_t ld, int64_t rows, int64_t cols, int esize) {
+  const int64_t per = 16 / esize;
+  return aligned16(p) && (rows <= 1 || ld % per == 0) && cols % per == 0;
+}
+// TMA reads rows of any length, but each must start on 16 bytes.
+bool tma_rows(const void* p, int64_t ld, int64_t rows) {
+  return aligned16(p) && (rows <= 1 || ld % 8 == 0);
+}
+
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int esize, const void* ptr, int64_t inner,
+            int64_t outer, int64_t ld, int box_inner, int box_outer) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = wsattn::tensor_map_encoder();
+  if (!fn) return false;
+  // a single row's stride is never used, but must be a valid one
+  const int64_t per = 16 / esize;
+  if (outer <= 1) ld = (inner + per - 1) / per * per;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * esize};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Product {
+  int dtype;
+  bool out_f32;
+  Operand p, q;  // rows and columns of the output
+  bool p_mn, q_mn;
+  int64_t R;
+  int C, K;
+  const void* bias;
+  const void* res;
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  void* pre;
+  int64_t ldp;
+  int act;
+};
+
+int run_product(const Product& g, int sms, cudaStream_t s) {
+  GemmParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.status = wsattn::op_status_ptr();
+  if (!prm.status) return WSATTN_ERR_CUDA;
+  const wsattn::GemmShape shape = wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, sms);
+  const CUtensorMapDataType type = g.dtype == WSATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int esize = g.out_f32 ? 4 : 2;
+  const int rows_p = shape.pair_cols ? 128 : shape.bn;
+  const int rows_q = shape.pair_cols ? shape.pair_cols / 2 : wsattn::kTileCols;
+  auto operand = [&](CUtensorMap* m, const Operand& o, bool mn, int64_t own, int box) {
+    return mn ? encode(m, type, 2, o.ptr, own, g.K, o.ld, 64, wsattn::kGemmK)
+              : encode(m, type, 2, o.ptr, g.K, own, o.ld, wsattn::kGemmK, box);
+  };
+  if (!operand(&prm.tm_p, g.p, g.p_mn, g.R, rows_p) || !operand(&prm.tm_q, g.q, g.q_mn, g.C, rows_q))
+    return WSATTN_ERR_CUDA;
+  prm.R = g.R;
+  prm.C = g.C;
+  prm.K = g.K;
+  prm.p_mn = g.p_mn;
+  prm.q_mn = g.q_mn;
+  prm.bias = g.bias;
+  prm.res = g.res;
+  prm.ldr = g.ldr;
+  prm.out = g.out;
+  prm.ldo = g.ldo;
+  prm.pre = g.pre;
+  prm.ldp = g.ldp;
+  prm.act = g.act;
+  prm.bias_vec = g.bias && aligned16(g.bias);
+  prm.res_vec = g.res && rows_vec(g.res, g.ldr, g.R, g.C, esize);
+  prm.out_vec = tma_rows(g.out, g.out_f32 ? 2 * g.ldo : g.ldo, g.R);
+  prm.pre_vec = g.pre && tma_rows(g.pre, g.ldp, g.R);
+  cudaError_t e;
+  if (shape.pair_cols) {
+    prm.tiles_r = static_cast<int>(cdiv(g.R, wsattn::kPairRows));
+    prm.tiles_c = static_cast<int>(cdiv(g.C, shape.pair_cols));
+    if (static_cast<int64_t>(prm.tiles_r) * prm.tiles_c > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+    if (prm.out_vec && !encode(&prm.tm_out, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, esize,
+                               g.out, g.C, g.R, g.ldo, 128 / esize, 32))
+      return WSATTN_ERR_CUDA;
+    if (prm.pre_vec && !g.out_f32 && !encode(&prm.tm_pre, type, 2, g.pre, g.C, g.R, g.ldp, 64, 32))
+      return WSATTN_ERR_CUDA;
+    e = wsattn::launch_gemm_pair(prm, g.dtype, g.out_f32, shape.pair_cols, sms, s);
+  } else {
+    prm.tiles_r = static_cast<int>(cdiv(g.R, shape.bn));
+    prm.tiles_c = static_cast<int>(cdiv(g.C, wsattn::kTileCols));
+    prm.bn = shape.bn;
+    prm.split = shape.split;
+    // a ring of about 96 KB: two CTAs fit an SM
+    prm.stages = 96 / (16 + shape.bn / 8);
+    e = wsattn::launch_gemm_tile(prm, g.dtype, g.out_f32, s);
+  }
+  return e == cudaSuccess ? WSATTN_OK : WSATTN_ERR_CUDA;
+}
+
+// Scratch of one operand copied to aligned rows.
+size_t packed_bytes(int64_t rows, int64_t cols) {
+  return up256(static_cast<size_t>(rows) * static_cast<size_t>(round8(cols)) * 2);
+}
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
+
+bool linear_args_ok(const wsattn_linear_args* a) {
+  if (!a || a->m < 0 || a->m > kMaxRows || a->n < 1 || a->k < 1 || a->n > (1 << 30) ||
+      a->k > (1 << 30))
+    return false;
+  if (a->activation < WSATTN_ACT_NONE || a->activation > WSATTN_ACT_SILU) return false;
+  if (a->x_heads < 0 || (a->x_heads == 0 && a->ldx < a->k) || a->ldw < a->k || a->ldo < a->n ||
+      (a->residual && a->ldr < a->n) || (a->preact && a->ldp < a->n))
+    return false;
+  if (a->x_heads > 0) {
+    if (a->k % a->x_heads || a->k / a->x_heads % 8) return false;
+    if (a->m > 0 && (a->x_tokens < 1 || a->m % a->x_tokens)) return false;
+  }
+  return true;
+}
+bool half_type(int dtype) { return dtype == WSATTN_BF16 || dtype == WSATTN_FP16; }
+bool elem_aligned(const void* p, int esize) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(esize - 1)) == 0;
+}
+
+size_t linear_ws(const wsattn_linear_args* a) {
+  size_t b = 0;
+  if (a->m == 0) return 0;
+  if (a->x_heads > 0 || !tma_rows(a->x, a->ldx, a->m)) b += packed_bytes(a->m, a->k);
+  if (!tma_rows(a->w, a->ldw, a->n)) b += packed_bytes(a->n, a->k);
+  return b;
+}
+
+bool grad_args_ok(const wsattn_linear_grad_args* a) {
+  if (!a || a->m < 0 || a->m > kMaxRows || a->n < 1 || a->k < 1 || a->n > (1 << 30) ||
+      a->k > (1 << 30))
+    return false;
+  if (a->activation < WSATTN_ACT_NONE || a->activation > WSATTN_ACT_SILU) return false;
+  if (a->ldd < a->n || a->ldx < a->k || a->ldw < a->k || (a->preact && a->ldp < a->n) ||
+      (a->dx && a->lddx < a->k) || (a->dw && a->lddw < a->k))
+    return false;
+  return true;
+}
+
+// Rows of dout per CTA of the dact pass: enough CTAs to fill the machine
+// four times over, at least 32 rows each (the partial sums stay small).
+int dact_rows(int64_t m, int n, int sms) {
+  const int64_t cols = cdiv(n, wsattn::kDactCols);
+  int64_t blocks = cdiv(static_cast<int64_t>(4) * sms, cols);
+  int64_t rows = cdiv(m, blocks < 1 ? 1 : blocks);
+  rows = (rows + 31) / 32 * 32;
+  if (cdiv(m, rows) > 65535) rows = (cdiv(m, 65535) + 31) / 32 * 32;
+  return static_cast<int>(rows);
+}
+
+struct GradPlan {
+  bool act, dz, pack_x, pack_w;
+  size_t dz_bytes, part_bytes, x_bytes, w_bytes;
+  int rows_per_block, row_blocks;
+  size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes; }
+};
+
+GradPlan plan_grad(const wsattn_linear_grad_args* a, int sms) {
+  GradPlan g;
+  std::memset(&g, 0, sizeof(g));
+  if (a->m == 0) return g;
+  const bool products = a->dx || a->dw;
+  g.act = a->activation != WSATTN_ACT_NONE;
+  g.dz = products && (g.act || !tma_rows(a->dout, a->ldd, a->m));
+  g.pack_x = a->dw && !tma_rows(a->x, a->ldx, a->m);
+  g.pack_w = a->dx && !tma_rows(a->w, a->ldw, a->n);
+  g.rows_per_block = dact_rows(a->m, a->n, sms);
+  g.row_blocks = static_cast<int>(cdiv(a->m, g.rows_per_block));
+  if (g.dz) g.dz_bytes = packed_bytes(a->m, a->n);
+  if (a->db) g.part_bytes = up256(sizeof(float) * static_cast<size_t>(g.row_blocks) * a->n);
+  if (g.pack_x) g.x_bytes = packed_bytes(a->m, a->k);
+  if (g.pack_w) g.w_bytes = packed_bytes(a->n, a->k);
+  return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+int wsattn_rotary_plan(int head_dim, int axes, const int32_t* pair_axis, const double* pair_freq,
+                       int interleaved, wsattn_rotary_t* out) {
+  if (!out) return WSATTN_ERR_BAD_ARG;
+  *out = nullptr;
+  if (!pair_axis || !pair_freq || axes < 1 || axes > wsattn::kRotMaxAxes || interleaved < 0 ||
+      interleaved > 1)
+    return WSATTN_ERR_BAD_ARG;
+  if (head_dim < 16 || head_dim % 16 || head_dim > 2 * wsattn::kRotMaxPairs)
+    return WSATTN_ERR_UNSUPPORTED;
+  const int pairs = head_dim / 2;
+  for (int i = 0; i < pairs; ++i)
+    if (pair_axis[i] < 0 || pair_axis[i] >= axes || !std::isfinite(pair_freq[i]) ||
+        std::fabs(pair_freq[i]) > 1e30)
+      return WSATTN_ERR_BAD_ARG;
+  wsattn_rotary_s* r = new (std::nothrow) wsattn_rotary_s();
+  if (!r) return WSATTN_ERR_NO_MEMORY;
+  std::memset(&r->table, 0, sizeof(r->table));
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < pairs; ++i) {
+    const double turns = pair_freq[i] / two_pi;
+    r->table.hi[i] = static_cast<float>(turns);
+    r->table.lo[i] = static_cast<float>(turns - static_cast<double>(r->table.hi[i]));
+    r->table.axis[i] = static_cast<uint8_t>(pair_axis[i]);
+  }
+  r->table.pairs = pairs;
+  r->table.axes = axes;
+  r->table.interleaved = interleaved;
+  *out = r;
+  return WSATTN_OK;
+}
+
+int wsattn_rotary_destroy(wsattn_rotary_t rot) {
+  delete rot;
+  return WSATTN_OK;
+}
+
+int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
+                  const wsattn_heads* x, const float* positions, int64_t pos_stride_b, int inverse,
+                  const wsattn_heads* y, void* stream) {
+  if (!rot || !dtype_ok(dtype) || batch < 0 || n_tokens < 0 || inverse < 0 || inverse > 1)
+    return WSATTN_ERR_BAD_ARG;
+  const int esize = dtype_size(dtype), dim = 2 * rot->table.pairs;
+  if (!view_ok(x, esize) || !view_ok(y, esize) || x->heads != y->heads ||
+      !positions_ok(positions, pos_stride_b) || !apart(y, batch, n_tokens, dim))
+    return WSATTN_ERR_BAD_ARG;
+  const int64_t rows = static_cast<int64_t>(batch) * n_tokens;
+  if (rows == 0) return WSATTN_OK;
+  if (!x->data || !y->data || !positions || n_tokens > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
+  QkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rot = rot->table;
+  p.parts = 1;
+  p.part[0] = part_of(x, y, 0, inverse ? -1 : 1, nullptr);
+  p.pos = positions;
+  p.pos_b = pos_stride_b;
+  p.tokens = n_tokens;
+  split_work(&p, rows, 6LL * sms, 1);
+  const bool vec = view_vec(x, batch, n_tokens, esize) && view_vec(y, batch, n_tokens, esize);
+  return wsattn::launch_qk_forward(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? WSATTN_OK
+             : WSATTN_ERR_CUDA;
+}
+
+int wsattn_qknorm(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
+                  const wsattn_heads* q, const wsattn_heads* k, const wsattn_heads* v,
+                  const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                  const float* positions, int64_t pos_stride_b, const wsattn_heads* q_out,
+                  const wsattn_heads* k_out, const wsattn_heads* v_out, void* stream) {
+  if (!rot || !dtype_ok(dtype) || batch < 0 || n_tokens < 0 || !(eps >= 0.f) ||
+      !std::isfinite(eps) || (weight_dtype != dtype && weight_dtype != WSATTN_FP32) || (!v) != (!v_out))
+    return WSATTN_ERR_BAD_ARG;
+  const int esize = dtype_size(dtype), dim = 2 * rot->table.pairs;
+  const wsattn_heads* in[3] = {q, k, v};
+  const wsattn_heads* out[3] = {q_out, k_out, v_out};
+  const int parts = v ? 3 : 2;
+  const int64_t rows = static_cast<int64_t>(batch) * n_tokens;
+  bool vec = true;
+  for (int i = 0; i < parts; ++i) {
+    if (!view_ok(in[i], esize) || !view_ok(out[i], esize) || in[i]->heads != out[i]->heads ||
+        !apart(out[i], batch, n_tokens, dim))
+      return WSATTN_ERR_BAD_ARG;
+    if (rows && (!in[i]->data || !out[i]->data)) return WSATTN_ERR_BAD_ARG;
+    vec = vec && view_vec(in[i], batch, n_tokens, esize) && view_vec(out[i], batch, n_tokens, esize);
+  }
+  const int wsize = dtype_size(weight_dtype);
+  if (!positions_ok(positions, pos_stride_b) || !elem_aligned(q_weight, wsize) ||
+      !elem_aligned(k_weight, wsize))
+    return WSATTN_ERR_BAD_ARG;
+  if (rows == 0) return WSATTN_OK;
+  if (!positions || n_tokens > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
+  QkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rot = rot->table;
+  p.parts = parts;
+  for (int i = 0; i < parts; ++i)
+    p.part[i] = part_of(in[i], out[i], i < 2, i < 2, i == 0 ? q_weight : i == 1 ? k_weight : nullptr);
+  p.weight_f32 = weight_dtype == WSATTN_FP32;
+  p.eps = eps;
+  p.pos = positions;
+  p.pos_b = pos_stride_b;
+  p.tokens = n_tokens;
+  split_work(&p, rows, 6LL * sms, 1);
+  return wsattn::launch_qk_forward(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? WSATTN_OK
+             : WSATTN_ERR_CUDA;
+}
+
+int wsattn_qknorm_backward_workspace(wsattn_rotary_t rot, size_t* bytes) {
+  if (!rot || !bytes) return WSATTN_ERR_BAD_ARG;
+  *bytes = sizeof(float) * 2 * kMaxBackCtas * 2 * static_cast<size_t>(rot->table.pairs);
+  return WSATTN_OK;
+}
+
+int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
+                           const wsattn_heads* dq_out, const wsattn_heads* dk_out,
+                           const wsattn_heads* dv_out, const wsattn_heads* q,
+                           const wsattn_heads* k, const void* q_weight, const void* k_weight,
+                           int weight_dtype, float eps, const float* positions,
+                           int64_t pos_stride_b, const wsattn_heads* dq, const wsattn_heads* dk,
+                           const wsattn_heads* dv, float* dq_weight, float* dk_weight,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (!rot || !dtype_ok(dtype) || batch < 0 || n_tokens < 0 || !(eps >= 0.f) ||
+      !std::isfinite(eps) || (weight_dtype != dtype && weight_dtype != WSATTN_FP32) ||
+      (!dv_out) != (!dv))
+    return WSATTN_ERR_BAD_ARG;
+  const int esize = dtype_size(dtype), dim = 2 * rot->table.pairs;
+  const wsattn_heads* in[3] = {dq_out, dk_out, dv_out};
+  const wsattn_heads* out[3] = {dq, dk, dv};
+  const wsattn_heads* x[2] = {q, k};
+  const int parts = dv ? 3 : 2;
+  const int64_t rows = static_cast<int64_t>(batch) * n_tokens;
+  bool vec = true;
+  for (int i = 0; i < parts; ++i) {
+    if (!view_ok(in[i], esize) || !view_ok(out[i], esize) || in[i]->heads != out[i]->heads ||
+        !apart(out[i], batch, n_tokens, dim))
+      return WSATTN_ERR_BAD_ARG;
+    if (rows && (!in[i]->data || !out[i]->data)) return WSATTN_ERR_BAD_ARG;
+    vec = vec && view_vec(in[i], batch, n_tokens, esize) && view_vec(out[i], batch, n_tokens, esize);
+    if (i < 2) {
+      if (!view_ok(x[i], esize) || x[i]->heads != in[i]->heads || (rows && !x[i]->data))
+        return WSATTN_ERR_BAD_ARG;
+      vec = vec && view_vec(x[i], batch, n_tokens, esize);
+    }
+  }
+  const int wsize = dtype_size(weight_dtype);
+  const bool gains = dq_weight || dk_weight;
+  size_t need = 0;
+  wsattn_qknorm_backward_workspace(rot, &need);
+  if (!positions_ok(positions, pos_stride_b) || !elem_aligned(q_weight, wsize) ||
+      !elem_aligned(k_weight, wsize) || !elem_aligned(dq_weight, 4) || !elem_aligned(dk_weight, 4) ||
+      (gains && rows && (!workspace || !aligned16(workspace) || workspace_bytes < need)))
+    return WSATTN_ERR_BAD_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if ((dq_weight && cudaMemsetAsync(dq_weight, 0, sizeof(float) * dim, s) != cudaSuccess) ||
+        (dk_weight && cudaMemsetAsync(dk_weight, 0, sizeof(float) * dim, s) != cudaSuccess))
+      return WSATTN_ERR_CUDA;
+    return WSATTN_OK;
+  }
+  if (!positions || n_tokens > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
+  QkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rot = rot->table;
+  p.parts = parts;
+  for (int i = 0; i < parts; ++i) {
+    p.part[i] = part_of(in[i], out[i], i < 2, i < 2 ? -1 : 0,
+                        i == 0 ? q_weight : i == 1 ? k_weight : nullptr);
+    if (i < 2) {
+      p.part[i].x = x[i]->data;
+      p.part[i].xb = x[i]->stride_b;
+      p.part[i].xn = x[i]->stride_n;
+      p.part[i].xh = x[i]->stride_h;
+    }
+  }
+  p.weight_f32 = weight_dtype == WSATTN_FP32;
+  p.eps = eps;
+  p.pos = positions;
+  p.pos_b = pos_stride_b;
+  p.tokens = n_tokens;
+  p.dw_part = gains ? static_cast<float*>(workspace) : nullptr;
+  int64_t blocks = static_cast<int64_t>(sms) * wsattn::kQkBackCtasPerSm;
+  if (blocks > kMaxBackCtas) blocks = kMaxBackCtas;
+  split_work(&p, rows, 32 * blocks, 4);
+  // no CTA without work of its own
+  const int64_t items =
+      p.row_blocks * static_cast<int64_t>(p.part[0].groups + p.part[1].groups);
+  if (blocks > items) blocks = items;
+  return wsattn::launch_qk_backward(p, dtype, vec, static_cast<int>(blocks), dq_weight, dk_weight,
+                                    s) == cudaSuccess
+             ? WSATTN_OK
+             : WSATTN_ERR_CUDA;
+}
+
+int wsattn_linear_workspace(const wsattn_linear_args* args, size_t* bytes) {
+  if (!bytes || !linear_args_ok(args)) return WSATTN_ERR_BAD_ARG;
+  *bytes = linear_ws(args);
+  return WSATTN_OK;
+}
+
+int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  if (!linear_args_ok(a)) return WSATTN_ERR_BAD_ARG;
+  if (!half_type(a->dtype) || (a->out_dtype != a->dtype && a->out_dtype != WSATTN_FP32))
+    return WSATTN_ERR_UNSUPPORTED;
+  if (a->m == 0) return WSATTN_OK;
+  const int osize = dtype_size(a->out_dtype);
+  if (!a->x || !a->w || !a->out || !elem_aligned(a->w, 2) || !elem_aligned(a->bias, 2) ||
+      !elem_aligned(a->preact, 2) || !elem_aligned(a->residual, osize) ||
+      !elem_aligned(a->out, osize) || (a->x_heads > 0 ? !aligned16(a->x) : !elem_aligned(a->x, 2)))
+    return WSATTN_ERR_BAD_ARG;
+  const size_t need = linear_ws(a);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  Product g;
+  std::memset(&g, 0, sizeof(g));
+  g.dtype = a->dtype;
+  g.out_f32 = a->out_dtype == WSATTN_FP32;
+  g.p = Operand{a->x, a->ldx};
+  g.q = Operand{a->w, a->ldw};
+  if (a->x_heads > 0 || !tma_rows(a->x, a->ldx, a->m)) {
+    if (wsattn::launch_pack(a->dtype, a->x, a->ldx, a->m, a->k, ws, round8(a->k), a->x_heads,
+                            a->x_tokens, s) != cudaSuccess)
+      return WSATTN_ERR_CUDA;
+    g.p = Operand{ws, round8(a->k)};
+    ws += packed_bytes(a->m, a->k);
+  }
+  if (!tma_rows(a->w, a->ldw, a->n)) {
+    if (wsattn::launch_pack(a->dtype, a->w, a->ldw, a->n, a->k, ws, round8(a->k), 0, 0, s) !=
+        cudaSuccess)
+      return WSATTN_ERR_CUDA;
+    g.q = Operand{ws, round8(a->k)};
+  }
+  g.R = a->m;
+  g.C = a->n;
+  g.K = a->k;
+  g.bias = a->bias;
+  g.res = a->residual;
+  g.ldr = a->ldr;
+  g.out = a->out;
+  g.ldo = a->ldo;
+  g.pre = a->preact;
+  g.ldp = a->ldp;
+  g.act = a->activation;
+  return run_product(g, sms, s);
+}
+
+int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes) {
+  if (!bytes || !grad_args_ok(args)) return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
+  *bytes = plan_grad(args, sms).total();
+  return WSATTN_OK;
+}
+
+int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!grad_args_ok(a)) return WSATTN_ERR_BAD_ARG;
+  if (!half_type(a->dtype)) return WSATTN_ERR_UNSUPPORTED;
+  if (!elem_aligned(a->dout, 2) || !elem_aligned(a->x, 2) || !elem_aligned(a->w, 2) ||
+      !elem_aligned(a->preact, 2) || !elem_aligned(a->dx, 2) || !elem_aligned(a->dw, 2) ||
+      !elem_aligned(a->db, 4))
+    return WSATTN_ERR_BAD_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->m == 0) {
+    if ((a->dw && cudaMemset2DAsync(a->dw, 2 * a->lddw, 0, 2 * static_cast<size_t>(a->k), a->n,
+                                    s) != cudaSuccess) ||
+        (a->db && cudaMemsetAsync(a->db, 0, sizeof(float) * a->n, s) != cudaSuccess))
+      return WSATTN_ERR_CUDA;
+    return WSATTN_OK;
+  }
+  if (!a->dout || (a->dw && !a->x) || (a->dx && !a->w) ||
+      (a->activation != WSATTN_ACT_NONE && !a->preact))
+    return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
+  const GradPlan plan = plan_grad(a, sms);
+  if (plan.total() && (!workspace || !aligned16(workspace) || workspace_bytes < plan.total()))
+    return WSATTN_ERR_BAD_ARG;
+  char* ws = static_cast<char*>(workspace);
+  char* ws_dz = ws;
+  char* ws_part = ws_dz + plan.dz_bytes;
+  char* ws_x = ws_part + plan.part_bytes;
+  char* ws_w = ws_x + plan.x_bytes;
+  Operand dz{a->dout, a->ldd}, x{a->x, a->ldx}, w{a->w, a->ldw};
+  if (plan.dz || a->db) {
+    wsattn::DactParams d;
+    std::memset(&d, 0, sizeof(d));
+    d.dout = a->dout;
+    d.ldd = a->ldd;
+    d.pre = plan.act ? a->preact : nullptr;
+    d.ldp = a->ldp;
+    d.dz = plan.dz ? ws_dz : nullptr;
+    d.ldz = round8(a->n);
+    d.part = a->db ? reinterpret_cast<float*>(ws_part) : nullptr;
+    d.ldpart = a->n;
+    d.rows = a->m;
+    d.cols = a->n;
+    d.act = a->activation;
+    d.rows_per_block = plan.rows_per_block;
+    d.row_blocks = plan.row_blocks;
+    d.vec = rows_vec(a->dout, a->ldd, a->m, a->n, 2) &&
+            (!d.pre || rows_vec(a->preact, a->ldp, a->m, a->n, 2));
+    if (wsattn::launch_dact(d, a->dtype, a->db, s) != cudaSuccess) return WSATTN_ERR_CUDA;
+    if (plan.dz) dz = Operand{ws_dz, d.ldz};
+  }
+  if (plan.pack_x) {
+    if (wsattn::launch_pack(a->dtype, a->x, a->ldx, a->m, a->k, ws_x, round8(a->k), 0, 0, s) !=
+        cudaSuccess)
+      return WSATTN_ERR_CUDA;
+    x = Operand{ws_x, round8(a->k)};
+  }
+  if (plan.pack_w) {
+    if (wsattn::launch_pack(a->dtype, a->w, a->ldw, a->n, a->k, ws_w, round8(a->k), 0, 0, s) !=
+        cudaSuccess)
+      return WSATTN_ERR_CUDA;
+    w = Operand{ws_w, round8(a->k)};
+  }
+  Product g;
+  std::memset(&g, 0, sizeof(g));
+  g.dtype = a->dtype;
+  if (a->dw) {  // dw[n, k] = sum over rows of dz[., n] x[., k]
+    g.p = dz;
+    g.p_mn = true;
+    g.q = x;
+    g.q_mn = true;
+    g.R = a->n;
+    g.C = a->k;
+    g.K = static_cast<int>(a->m);
+    g.out = a->dw;
+    g.ldo = a->lddw;
+    const int rc = run_product(g, sms, s);
+    if (rc != WSATTN_OK) return rc;
+  }
+  if (a->dx) {  // dx[m, k] = sum over features of dz[m, .] w[., k]
+    g.p = dz;
+    g.p_mn = false;
+    g.q = w;
+    g.q_mn = true;
+    g.R = a->m;
+    g.C = a->k;
+    g.K = a->n;
+    g.out = a->dx;
+    g.ldo = a->lddx;
+    const int rc = run_product(g, sms, s);
+    if (rc != WSATTN_OK) return rc;
+  }
+  return WSATTN_OK;
+}
+
+int wsattn_op_status(void* stream) {
+  int* w = wsattn::op_status_ptr();
+  if (!w) return WSATTN_ERR_CUDA;
+  int st = 0;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      cudaMemcpy(&st, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return WSATTN_ERR_CUDA;
+  if (st == 0) return WSATTN_OK;
+  if (cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return WSATTN_ERR_CUDA;
+  return (st & wsattn::kStatusBounds) ? WSATTN_ERR_BOUNDS : WSATTN_ERR_TIMEOUT;
+}
+
+}  // extern "C"

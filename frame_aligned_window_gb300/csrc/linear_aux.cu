@@ -1,0 +1,221 @@
+// Passes over memory beside the linear products, and how a product is tiled.
+//
+//   pack   rows of any stride and alignment, or the attention's fp32
+//          [B, H, N, D], to 16-bit rows that TMA can read
+//   dact   dz = dout * act'(preact) with its column sums (the bias gradient)
+#include "epilogue.cuh"
+#include "ptx.cuh"
+
+namespace wsattn {
+namespace {
+
+// 8 values a thread.  Reads element by element: the sources of this pass are
+// those whose rows start on no common boundary.
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ src, int64_t lds,
+                                                   int64_t rows, int cols, T* __restrict__ dst,
+                                                   int64_t ldd) {
+  const int64_t per = ldd / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t r = i / per;
+  const int c = static_cast<int>(i - r * per) * 8;
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(src) + r * lds + c;
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    w[e] = (c + 2 * e < cols ? q[2 * e] : 0u) | (c + 2 * e + 1 < cols ? q[2 * e + 1] : 0u) << 16;
+  *reinterpret_cast<uint4*>(dst + r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// fp32 [B, H, N, D] -> rows (b, n) of H * D, rounded once.  A thread takes 8
+// values of one head row (D is a multiple of 8): 16 bytes out, 32 in.
+template <typename T>
+__global__ void __launch_bounds__(256) pack_heads_kernel(const float* __restrict__ src, int heads,
+                                                         int64_t tokens, int dim, int64_t rows,
+                                                         T* __restrict__ dst) {
+  const int per = heads * dim / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t r = i / per, b = r / tokens, n = r - b * tokens;
+  const int c = static_cast<int>(i - r * per) * 8, h = c / dim, d = c - h * dim;
+  const float4* q = reinterpret_cast<const float4*>(src + ((b * heads + h) * tokens + n) * dim + d);
+  const float4 x = q[0], y = q[1];
+  *reinterpret_cast<uint4*>(dst + r * per * 8 + c) =
+      make_uint4(pack_pair(x.x, x.y, T()), pack_pair(x.z, x.w, T()), pack_pair(y.x, y.y, T()),
+                 pack_pair(y.z, y.w, T()));
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int cols, float (&f)[8]) {
+  if (VEC) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = unpack_pair(w[i], T());
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? to_f32(row[c + i]) : 0.f;
+  }
+}
+
+// CTA (x, y): 256 columns of rows [y * rows_per_block, ...); a warp takes
+// every eighth row, a lane 8 columns.  Bound by HBM: dout and preact in, dz
+// out.  The sums stay in fp32 registers (of the unrounded dz), then go
+// through shared memory in the order of the warps.
+template <typename T, bool VEC, int ACT>
+__global__ void __launch_bounds__(256) dact_kernel(const DactParams p) {
+  __shared__ float red[8][kDactCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int c = static_cast<int>(blockIdx.x) * kDactCols + 8 * lane;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
+  const int64_t r1 = min(p.rows, r0 + p.rows_per_block);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < p.cols) {
+#pragma unroll 4
+    for (int64_t r = r0 + warp; r < r1; r += 8) {
+      float g[8];
+      load8<VEC>(static_cast<const T*>(p.dout) + r * p.ldd, c, p.cols, g);
+      if (ACT != WSATTN_ACT_NONE) {
+        float z[8];
+        load8<VEC>(static_cast<const T*>(p.pre) + r * p.ldp, c, p.cols, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // rounded here, so that the sums are the same with and without dz
+          g[i] = __fmul_rn(g[i], act_slope<ACT>(z[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += g[i];
+      if (p.dz)
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.dz) + r * p.ldz + c) =
+            make_uint4(pack_pair(g[0], g[1], T()), pack_pair(g[2], g[3], T()),
+                       pack_pair(g[4], g[5], T()), pack_pair(g[6], g[7], T()));
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[warp][8 * lane + i] = acc[i];
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) t += red[w][threadIdx.x];
+  const int cc = static_cast<int>(blockIdx.x) * kDactCols + static_cast<int>(threadIdx.x);
+  if (cc < p.cols) p.part[static_cast<int64_t>(blockIdx.y) * p.ldpart + cc] = t;
+}
+
+// Column sums from the row blocks' parts, in a fixed order: CTA x takes 32
+// columns, thread (c, g) parts g, g + 8, ...
+__global__ void __launch_bounds__(256) sum_parts(const float* __restrict__ part, int64_t ldpart,
+                                                 int blocks, int cols, float* __restrict__ out) {
+  __shared__ float red[8][33];
+  ptx::griddep_wait();
+  const int c = 32 * static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.x);
+  float t = 0.f;
+  if (c < cols)
+    for (int i = threadIdx.y; i < blocks; i += 8) t += part[i * ldpart + c];
+  red[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < cols) {
+    float s = 0.f;
+    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+    out[c] = s;
+  }
+}
+
+template <typename T, bool VEC>
+cudaError_t dact_t(const DactParams& p, cudaStream_t s) {
+  const dim3 grid((p.cols + kDactCols - 1) / kDactCols, p.row_blocks);
+  const int act = p.pre ? p.act : WSATTN_ACT_NONE;
+  if (act == WSATTN_ACT_GELU) dact_kernel<T, VEC, WSATTN_ACT_GELU><<<grid, 256, 0, s>>>(p);
+  else if (act == WSATTN_ACT_GELU_TANH) dact_kernel<T, VEC, WSATTN_ACT_GELU_TANH><<<grid, 256, 0, s>>>(p);
+  else if (act == WSATTN_ACT_SILU) dact_kernel<T, VEC, WSATTN_ACT_SILU><<<grid, 256, 0, s>>>(p);
+  else dact_kernel<T, VEC, WSATTN_ACT_NONE><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+__device__ int g_op_status;
+
+}  // namespace
+
+int* op_status_ptr() {
+  static int* ptr[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return nullptr;
+  if (!ptr[dev]) {
+    void* a = nullptr;
+    if (cudaGetSymbolAddress(&a, g_op_status) != cudaSuccess) return nullptr;
+    ptr[dev] = static_cast<int*>(a);
+  }
+  return ptr[dev];
+}
+
+cudaError_t launch_pack(int dtype, const void* src, int64_t lds, int64_t rows, int cols, void* dst,
+                        int64_t ldd, int src_f32_heads, int64_t tokens, cudaStream_t s) {
+  const int64_t blocks = (rows * (ldd / 8) + 255) / 256;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (src_f32_heads > 0) {
+    const float* f = static_cast<const float*>(src);
+    const int dim = cols / src_f32_heads;
+    if (dtype == WSATTN_BF16)
+      pack_heads_kernel<<<grid, 256, 0, s>>>(f, src_f32_heads, tokens, dim, rows,
+                                             static_cast<__nv_bfloat16*>(dst));
+    else
+      pack_heads_kernel<<<grid, 256, 0, s>>>(f, src_f32_heads, tokens, dim, rows,
+                                             static_cast<__half*>(dst));
+  } else {
+    pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __half*>(src), lds, rows, cols,
+                                     static_cast<__half*>(dst), ldd);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dact(const DactParams& p, int dtype, float* db, cudaStream_t s) {
+  cudaError_t e;
+  if (dtype == WSATTN_BF16)
+    e = p.vec ? dact_t<__nv_bfloat16, true>(p, s) : dact_t<__nv_bfloat16, false>(p, s);
+  else
+    e = p.vec ? dact_t<__half, true>(p, s) : dact_t<__half, false>(p, s);
+  if (e != cudaSuccess || !db) return e;
+  return launch_dependent(sum_parts, dim3((p.cols + 31) / 32), dim3(32, 8), 0, s,
+                          static_cast<const float*>(p.part), p.ldpart, p.row_blocks, p.cols, db);
+}
+
+// First estimate of the time of each tiling, in SM cycles.
+GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms) {
+  const int64_t ksteps = (K + kGemmK - 1) / kGemmK;
+  GemmShape best{256, 0, 1};
+  double best_t = 1e300;
+  auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  for (int bn = 256; bn >= 128; bn -= 128) {
+    const int64_t waves = cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2);
+    const double t = 6000.0 + static_cast<double>(waves) * (ksteps * (bn == 256 ? 530.0 : 330.0) + 300.0);
+    if (t < best_t) {
+      best_t = t;
+      best = GemmShape{bn, 0, 1};
+    }
+  }
+  for (int bn = 16; bn <= 128; bn *= 2) {
+    if (p_mn && bn < 64) continue;
+    if (bn > 16 && bn / 2 >= R && !(p_mn && bn == 64)) continue;
+    for (int split = 1; split <= 8 && split <= ksteps; ++split) {
+      const int64_t ctas = cdiv(R, bn) * cdiv(C, kTileCols) * split;
+      const int64_t waves = cdiv(ctas, 2 * sms);
+      // two CTAs share an SM's bandwidth and tensor cores
+      const double share = ctas > sms ? 2.0 : 1.0;
+      const double step = bn <= 32 ? 420.0 : bn == 64 ? 420.0 : 480.0;
+      const double t = 4000.0 + (split > 1 ? 1500.0 : 0.0) +
+                       waves * (cdiv(ksteps, split) * step * share / 2 * (share > 1 ? 1.0 : 1.4) + 600.0 + bn * 12.0);
+      if (t < best_t) {
+        best_t = t;
+        best = GemmShape{0, bn, split};
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace wsattn

@@ -1,0 +1,264 @@
+// Linear products on single CTAs: out = residual + act(P Q^T + bias) for few
+// rows, and for shapes too small to fill the machine with 256 x 256 tiles.
+//
+// With a few rows the product reads Q (the weights) once and does little
+// with it: bound by HBM.  The operands trade places here: 128 columns of the
+// output (rows of Q) are the MMA's M, the BN = 16 .. 128 rows of P its N, so
+// the padding of a single row costs 15 rows of tensor-core time instead of
+// 127, and the weights stream through a TMA ring of 16 KB slices.  When the
+// tiles alone do not fill the SMs, a cluster of `split` CTAs shares the
+// contraction of one tile: each leaves its fp32 partial tile in its own
+// shared memory, and the CTAs add them through distributed shared memory,
+// each for its own rows and in the order of the ranks, so that the sums do
+// not depend on timing and no partial result goes to global memory.
+//   warp 0     TMA
+//   warp 1     MMA issue, tensor memory
+//   warps 2-5  epilogue: thread = output column (TMEM lane), so that lanes
+//              write neighbouring values of an output row
+#include "epilogue.cuh"
+#include "ptx.cuh"
+
+namespace wsattn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 192;
+constexpr uint32_t kQBytes = kTileCols * kGemmK * 2;
+constexpr int kMaxStages = 12;
+
+enum : int { FULL0 = 0, EMPTY0 = kMaxStages, ACCFULL = 2 * kMaxStages, NBARS = 2 * kMaxStages + 1 };
+
+__device__ __forceinline__ uint32_t bar(const GemmShared& s, int i) {
+  return s.bars + 8u * static_cast<uint32_t>(i);
+}
+
+__device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t parity, int code) {
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(b, parity)) return true;
+    if (*s.abort_flag) return false;
+    if (clock64() - t0 > kGemmWaitLimit) {
+      atomicOr(s.status, code);
+      *s.abort_flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t parity, int code) {
+  if (mbar_try_wait(b, parity)) return true;
+  return wait_slow(s, b, parity, code);
+}
+
+__device__ void producer(const GemmParams& p, const GemmShared& s, int row0, int col0, int k0,
+                         int k1) {
+  const uint32_t p_bytes = static_cast<uint32_t>(p.bn) * kGemmK * 2;
+  const uint32_t stage = kQBytes + p_bytes;
+  uint32_t slot = 0, phase = 0, last_phase = 0, issued = 0;
+  for (int kt = k0; kt < k1; ++kt) {
+    if (!wait(s, bar(s, EMPTY0 + slot), phase ^ 1u, kStatusTimeoutProducer)) {
+      // copies in flight land whatever the consumer does: wait (bounded)
+      for (int i = 0; i < p.stages; ++i) {
+        if (!(issued >> i & 1u)) continue;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar(s, FULL0 + i), last_phase >> i & 1u))
+          if (clock64() - t0 > kGemmWaitLimit) break;
+      }
+      return;
+    }
+    const uint32_t q = s.stages + slot * stage, pp = q + kQBytes, full = bar(s, FULL0 + slot);
+    mbar_arrive_expect_tx(full, stage);
+    const int k = kt * kGemmK;
+    if (!p.q_mn) {
+      tma_load_2d(q, &p.tm_q, full, k, col0);
+    } else {
+      tma_load_2d(q, &p.tm_q, full, col0, k);
+      tma_load_2d(q + 8192, &p.tm_q, full, col0 + 64, k);
+    }
+    if (!p.p_mn) {
+      tma_load_2d(pp, &p.tm_p, full, k, row0);
+    } else {
+      for (int j = 0; j < p.bn / 64; ++j)
+        tma_load_2d(pp + 8192u * j, &p.tm_p, full, row0 + 64 * j, k);
+    }
+    last_phase = (last_phase & ~(1u << slot)) | (phase << slot);
+    issued |= 1u << slot;
+    if (++slot == static_cast<uint32_t>(p.stages)) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
+__device__ void mma_issuer(const GemmParams& p, const GemmShared& s, int steps, uint32_t tbase,
+                           bool bf16) {
+  const uint32_t stage = kQBytes + static_cast<uint32_t>(p.bn) * kGemmK * 2;
+  const uint32_t idesc = idesc_16_f32(kTileCols, p.bn, bf16, p.q_mn != 0, p.p_mn != 0);
+  const uint32_t a_lbo = p.q_mn ? 8192u : 16u, b_lbo = p.p_mn ? 8192u : 16u;
+  const uint64_t a_step = p.q_mn ? 128 : 2, b_step = p.p_mn ? 128 : 2;
+  uint32_t slot = 0, phase = 0;
+  for (int kt = 0; kt < steps; ++kt) {
+    if (!wait(s, bar(s, FULL0 + slot), phase, kStatusTimeoutMma)) return;
+    tc_fence_after();
+    const uint32_t a = s.stages + slot * stage;
+    const uint64_t ad = sdesc_sw128(a, a_lbo, 1024), bd = sdesc_sw128(a + kQBytes, b_lbo, 1024);
+#pragma unroll
+    for (int kk = 0; kk < kGemmK / 16; ++kk)
+      mma_ss(tbase, ad + kk * a_step, bd + kk * b_step, idesc, (kt | kk) != 0 ? 1u : 0u);
+    tc_commit(bar(s, EMPTY0 + slot));
+    if (++slot == static_cast<uint32_t>(p.stages)) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  tc_commit(bar(s, ACCFULL));
+}
+
+// One output: bias, pre-activation, activation, residual, one rounding.
+template <typename T, typename O>
+__device__ __forceinline__ void emit(const GemmParams& p, int64_t row, int col, float bias, float v) {
+  float y = v + bias;
+  if (p.pre) static_cast<T*>(p.pre)[row * p.ldp + col] = from_f32<T>(y);
+  y = act_any(p.act, y);
+  if (p.res) y += to_f32(static_cast<const O*>(p.res)[row * p.ldr + col]);
+  static_cast<O*>(p.out)[row * p.ldo + col] = from_f32<O>(y);
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_constant__ GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t stage = kQBytes + static_cast<uint32_t>(p.bn) * kGemmK * 2;
+  GemmShared s;
+  s.stages = base;
+  s.bars = base + static_cast<uint32_t>(p.stages) * stage;
+  uint8_t* gb = smem_raw + (s.bars - raw);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * NBARS);
+  s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  s.status = p.status;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const uint32_t tcols = p.bn < 32 ? 32u : static_cast<uint32_t>(p.bn);
+
+  // cluster c: tile c, rows the fast index (the weights of a column tile are
+  // then in L2 for its other row tiles)
+  const int split = p.split;
+  const int rank = static_cast<int>(blockIdx.x) % split;
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int tr = tile % p.tiles_r, tc = tile / p.tiles_r;
+  const int row0 = tr * p.bn, col0 = tc * kTileCols;
+  const int ksteps = (p.K + kGemmK - 1) / kGemmK;
+  const int k0 = static_cast<int>(static_cast<int64_t>(ksteps) * rank / split);
+  const int k1 = static_cast<int>(static_cast<int64_t>(ksteps) * (rank + 1) / split);
+  const bool tile_ok = WSATTN_BOUNDS(p.status, tc < p.tiles_c && k1 > k0 && k1 <= ksteps);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(bar(s, FULL0 + i), 1);
+      mbar_init(bar(s, EMPTY0 + i), 1);
+    }
+    mbar_init(bar(s, ACCFULL), 1);
+    *s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&p.tm_p);
+    prefetch_tensormap(&p.tm_q);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tslot), tcols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  griddep_wait();
+
+  bool have = false;  // epilogue threads: the accumulator is complete
+  const int quad = warp & 3;
+  const int c = 32 * quad + lane, col = col0 + c;
+  const uint32_t tlane = tbase + (static_cast<uint32_t>(32 * quad) << 16);
+  float bias = 0.f;
+  if (warp == 0) {
+    if (lane == 0 && tile_ok) producer(p, s, row0, col0, k0, k1);
+  } else if (warp == 1) {
+    if (lane == 0 && tile_ok) mma_issuer(p, s, k1 - k0, tbase, !IsHalf<T>::value);
+  } else {
+    if (p.bias && col < p.C) bias = to_f32(static_cast<const T*>(p.bias)[col]);
+    have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax);
+    have = __all_sync(0xffffffffu, have);
+    tc_fence_after();
+    if (have) {
+      for (int j = 0; j < p.bn; j += 16) {
+        uint32_t r[16];
+        tmem_ld16(tlane + j, r);
+        tmem_wait_ld16(r);
+        if (split == 1) {
+          if (col < p.C)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (row0 + j + i < p.R)
+                emit<T, O>(p, row0 + j + i, col, bias, __uint_as_float(r[i]));
+        } else {
+          // the operand ring is idle now (every MMA of this CTA is complete):
+          // it takes the partial tile, [row][128 columns]
+          float* part = reinterpret_cast<float*>(smem_raw + (base - raw));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(j + i) * kTileCols + c] = __uint_as_float(r[i]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync();  // every CTA's partial tile is in its shared memory
+    if (warp >= 2 && col < p.C) {
+      const int j0 = p.bn * rank / split, j1 = p.bn * (rank + 1) / split;
+      for (int j = j0; j < j1 && row0 + j < p.R; ++j) {
+        const uint32_t a = base + static_cast<uint32_t>(j * kTileCols + c) * 4u;
+        float v = 0.f;
+        for (int r = 0; r < split; ++r)
+          v += ld_cluster_f32(map_to_rank(a, static_cast<uint32_t>(r)));
+        emit<T, O>(p, row0 + j, col, bias, v);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while others read its shared memory
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, tcols);
+}
+
+template <typename T, typename O>
+cudaError_t launch(const GemmParams& p, cudaStream_t s) {
+  static bool attr_set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(gemm_tile_kernel<T, O>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(tile_smem_bytes(16, kMaxStages)));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int64_t grid = static_cast<int64_t>(p.tiles_r) * p.tiles_c * p.split;
+  if (grid > INT32_MAX || p.stages > kMaxStages) return cudaErrorInvalidValue;
+  return launch_cluster(gemm_tile_kernel<T, O>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                        p.split, tile_smem_bytes(p.bn, p.stages), s, p);
+}
+
+}  // namespace
+
+size_t tile_smem_bytes(int bn, int stages) {
+  return 1024 + static_cast<size_t>(stages) * (kQBytes + static_cast<size_t>(bn) * kGemmK * 2) +
+         8 * NBARS + 16;
+}
+
+cudaError_t launch_gemm_tile(const GemmParams& p, int dtype, bool out_f32, cudaStream_t s) {
+  if (dtype == WSATTN_BF16)
+    return out_f32 ? launch<__nv_bfloat16, float>(p, s) : launch<__nv_bfloat16, __nv_bfloat16>(p, s);
+  return out_f32 ? launch<__half, float>(p, s) : launch<__half, __half>(p, s);
+}
+
+}  // namespace wsattn

@@ -226,6 +226,196 @@ int wsattn_prepare_static(int batch, int heads, int n_tokens, int head_dim, floa
                           const void* q, const void* k, float* b_rows, float* m_rows, float* mu,
                           float* kmax, float* bmax, uint8_t* elig, void* stream);
 
+/* -------------------------------------------- operators around the attention
+ *
+ * What a block needs in front of wsattn_prepare and behind wsattn_forward:
+ * rotary positions on several axes, per-head norms of queries and keys, and
+ * linear products, each with its gradients.  They need no wsattn_plan, keep
+ * no device memory of their own between calls and never synchronise or
+ * allocate: scratch is the caller's (each *_workspace call gives its size),
+ * so calls on different streams and captured graphs are independent as long
+ * as they use different workspaces.  Sizes of zero (no tokens, no rows) are
+ * accepted and enqueue only what has to be written.  Outputs must not
+ * overlap inputs or each other, except where a call says so.
+ */
+
+enum wsattn_dtype { WSATTN_BF16 = 0, WSATTN_FP16 = 1, WSATTN_FP32 = 2 };
+
+/*
+ * Turning rates of a head's dimension pairs (host memory only; immutable, so
+ * any number of calls may use one at a time).  Pair p turns by
+ *   pos[pair_axis[p]] * pair_freq[p]   radians:  (a, b) -> (a c - b s, a s + b c).
+ *   head_dim     D: a multiple of 16, 16 .. 256
+ *   axes         columns of the positions, 1 .. 4 (time, height, width, ...)
+ *   pair_axis    int32 [D / 2], each in [0, axes)
+ *   pair_freq    double [D / 2], finite; 0 leaves a pair as it is
+ *   interleaved  1: pairs are dims (2p, 2p + 1), as in wsattn_produce;
+ *                0: pairs are dims (p, p + D / 2)
+ * Errors: BAD_ARG, UNSUPPORTED (head_dim), NO_MEMORY.
+ */
+typedef struct wsattn_rotary_s* wsattn_rotary_t;
+int wsattn_rotary_plan(int head_dim, int axes, const int32_t* pair_axis, const double* pair_freq,
+                       int interleaved, wsattn_rotary_t* out);
+/* NULL is accepted and ignored.  Work already enqueued is not affected. */
+int wsattn_rotary_destroy(wsattn_rotary_t rot);
+
+/* A [batch, heads, N, D] view: element (b, h, n, d) is at
+ * data[b * stride_b + h * stride_h + n * stride_n + d].  Strides count
+ * elements and are >= 0; an output's must keep its elements apart. */
+typedef struct wsattn_heads {
+  void* data;
+  int heads;
+  int64_t stride_b, stride_h, stride_n;
+} wsattn_heads;
+
+/*
+ * y = x turned by its tokens' positions (inverse = 1: turned back, which is
+ * also the gradient: dx = turned back dy).  y may be x itself.
+ *   dtype      of x and y (wsattn_dtype); arithmetic is fp32, angles are
+ *              reduced with their full precision at any position
+ *   positions  fp32 [N, axes], or [batch, N, axes] with batch stride
+ *              pos_stride_b (0: shared by the batch); contiguous otherwise
+ * Rows need no alignment beyond the type's own (16-byte aligned rows are
+ * read in 16-byte words).
+ * Errors: BAD_ARG, CUDA.
+ */
+int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
+                  const wsattn_heads* x, const float* positions, int64_t pos_stride_b, int inverse,
+                  const wsattn_heads* y, void* stream);
+
+/*
+ * Queries and keys for the attention from a projection's output, in one
+ * pass: per head row, y = turn(g * x / sqrt(mean_d x_d^2 + eps)), and v copied
+ * (each [batch, heads, N, D]; q_out, k_out and v_out contiguous are what
+ * wsattn_prepare and wsattn_forward read).  q, k and v may have different
+ * head counts; v and v_out may be NULL.  An output may be its own input.
+ *   q_weight, k_weight  gains g [D] of weight_dtype (`dtype` or WSATTN_FP32),
+ *                       either NULL for 1
+ *   eps                 >= 0
+ * Errors: BAD_ARG, CUDA.
+ */
+int wsattn_qknorm(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
+                  const wsattn_heads* q, const wsattn_heads* k, const wsattn_heads* v,
+                  const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                  const float* positions, int64_t pos_stride_b, const wsattn_heads* q_out,
+                  const wsattn_heads* k_out, const wsattn_heads* v_out, void* stream);
+
+/*
+ * Gradients of wsattn_qknorm: dq, dk (and dv, a copy of dv_out) from dq_out,
+ * dk_out (dv_out) and the forward's q, k, gains, eps and positions.  dq, dk
+ * and dv may be views of one packed gradient; dv_out and dv may be NULL
+ * together.  dq may be dq_out itself or q itself (so for k).
+ *   dq_weight, dk_weight  fp32 [D] gain gradients (sums over batch, heads and
+ *                         tokens in a fixed order), either NULL to skip
+ *   workspace             wsattn_qknorm_backward_workspace bytes, 16-byte
+ *                         aligned; may be NULL when both gains are skipped
+ * Errors: BAD_ARG (also a workspace too small), CUDA.
+ */
+int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
+                           const wsattn_heads* dq_out, const wsattn_heads* dk_out,
+                           const wsattn_heads* dv_out, const wsattn_heads* q,
+                           const wsattn_heads* k, const void* q_weight, const void* k_weight,
+                           int weight_dtype, float eps, const float* positions,
+                           int64_t pos_stride_b, const wsattn_heads* dq, const wsattn_heads* dk,
+                           const wsattn_heads* dv, float* dq_weight, float* dk_weight,
+                           void* workspace, size_t workspace_bytes, void* stream);
+int wsattn_qknorm_backward_workspace(wsattn_rotary_t rot, size_t* bytes);
+
+enum wsattn_activation {
+  WSATTN_ACT_NONE = 0,
+  WSATTN_ACT_GELU = 1,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  WSATTN_ACT_GELU_TANH = 2, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  WSATTN_ACT_SILU = 3       /* z / (1 + exp(-z)) */
+};
+
+/*
+ * out = residual + act(x w^T + bias) in one kernel: the products run on the
+ * tensor cores from 16-bit inputs into fp32 accumulators; bias, activation
+ * and residual are applied in fp32 and the result is rounded once.
+ *   dtype      of x, w, bias and preact: WSATTN_BF16 or WSATTN_FP16
+ *   out_dtype  of residual and out: dtype or WSATTN_FP32
+ *   m, n, k    rows, output and input features (m >= 0, n, k >= 1)
+ *   x          [m, k], row stride ldx >= k; or, with x_heads > 0, the
+ *              attention's output: fp32 [m / x_tokens, x_heads, x_tokens,
+ *              k / x_heads] contiguous and 16-byte aligned, whose heads are
+ *              merged and rounded to dtype first (ldx is not used; k /
+ *              x_heads is a multiple of 8)
+ *   w          [n, k], row stride ldw >= k
+ *   bias       [n] or NULL
+ *   residual   [m, n], row stride ldr >= n, or NULL; may be out itself
+ *   out        [m, n], row stride ldo >= n
+ *   preact     [m, n], row stride ldp >= n, or NULL: receives x w^T + bias
+ *              rounded to dtype, for wsattn_linear_backward
+ * Rows of any stride and alignment are accepted; x and w with rows that are
+ * not 16-byte aligned are first copied to the workspace, and so is x with
+ * x_heads.  workspace: wsattn_linear_workspace bytes, 16-byte aligned (NULL
+ * when that is 0).
+ * Errors: BAD_ARG (also a workspace too small), UNSUPPORTED (dtypes), CUDA.
+ */
+typedef struct wsattn_linear_args {
+  int dtype, out_dtype;
+  int64_t m;
+  int n, k;
+  const void* x;
+  int64_t ldx;
+  int x_heads;
+  int64_t x_tokens;
+  const void* w;
+  int64_t ldw;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  void* preact;
+  int64_t ldp;
+  int activation;
+} wsattn_linear_args;
+int wsattn_linear(const wsattn_linear_args* args, void* workspace, size_t workspace_bytes,
+                  void* stream);
+int wsattn_linear_workspace(const wsattn_linear_args* args, size_t* bytes);
+
+/*
+ * Gradients of wsattn_linear from dout (the residual's gradient is dout
+ * itself): dz = dout * act'(preact), rounded to dtype for the products,
+ *   dx = dz w     [m, k]      dw = dz^T x   [n, k]      db = sum of dz's rows
+ * Any of dx, dw and db may be NULL to skip it.
+ *   dtype    of dout, x, w, preact, dx and dw
+ *   preact   as wsattn_linear left it; NULL only without an activation
+ *   db       fp32 [n], of the unrounded dz, in a fixed order
+ * Strides, alignment and workspace as for wsattn_linear; with m = 0, dw and
+ * db are zeroed.  dx, dw and db must not overlap any input.
+ * Errors: BAD_ARG (also a workspace too small), UNSUPPORTED (dtype), CUDA.
+ */
+typedef struct wsattn_linear_grad_args {
+  int dtype;
+  int64_t m;
+  int n, k;
+  const void* dout;
+  int64_t ldd;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* preact;
+  int64_t ldp;
+  int activation;
+  void* dx;
+  int64_t lddx;
+  void* dw;
+  int64_t lddw;
+  float* db;
+} wsattn_linear_grad_args;
+int wsattn_linear_backward(const wsattn_linear_grad_args* args, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes);
+
+/* Synchronises `stream` and reports the status word of the operators above on
+ * the current device: OK, TIMEOUT if a device-side wait expired (outputs are
+ * invalid), BOUNDS (debug build); the word is then cleared.  CUDA if the
+ * synchronisation failed. */
+int wsattn_op_status(void* stream);
+
 /* ---------------------------------------------------------- introspection */
 
 /* Plan geometry.  info[0..9] = N, block_q, block_k, q blocks, k blocks,

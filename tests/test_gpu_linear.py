@@ -1,0 +1,223 @@
+"""wsattn_linear and wsattn_linear_backward against their 64-bit definitions
+(GPU).  Tolerances: half a step of the stored type, the tensor cores' fp32
+error on the sum of magnitudes (_ops_ref.product_tol), 2^-20 relative for the
+activation (its slope is at most 1.13); the gradients' products read a dz that
+was itself rounded by half a step."""
+import pytest
+import torch
+
+from _ops_ref import act, assert_close, half_step, product_tol, tiny
+
+pytestmark = pytest.mark.gpu
+
+
+def _fw():
+    import frame_aligned_window_gb300 as fw
+    return fw
+
+
+def _case(m, n, k, dt, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((m, k), generator=g).to(dt)
+    w = (torch.randn((n, k), generator=g) / k ** 0.5).to(dt)
+    b = (0.5 * torch.randn(n, generator=g)).to(dt)
+    r = torch.randn((m, n), generator=g)
+    return x, w, b, r
+
+
+SHAPES = [
+    # m, n, k
+    (1, 1, 1), (1, 256, 320), (3, 130, 64), (1, 1000, 1500), (17, 96, 520),
+    (33, 333, 77), (100, 1024, 1024), (129, 257, 65), (240, 384, 128), (256, 256, 256),
+    (300, 511, 999), (700, 640, 200), (2080, 1024, 1024), (5000, 384, 64), (1, 8, 4096),
+    (4100, 2304, 192),
+]
+
+
+def _check_forward(fw, x, w, b, r, name, dt, odt, want_pre=True):
+    m, n = x.shape[0], w.shape[0]
+    xd, wd = x.double(), w.double()
+    z = xd @ wd.t() + (0 if b is None else b.double())
+    s = xd.abs() @ wd.abs().t() + (0 if b is None else b.double().abs())
+    ztol = product_tol(s, x.shape[1])
+    want = act(z, name) + (0 if r is None else r.to(odt).double())
+    pre = torch.full((m, n), 9.0, dtype=dt, device="cuda") if want_pre else None
+    got = fw.wsattn_linear(x.cuda(), w.cuda(), None if b is None else b.cuda(),
+                           None if r is None else r.to(odt).cuda(), name, preact=pre,
+                           out_dtype=odt)
+    torch.cuda.synchronize()
+    assert fw.wsattn_op_status() == 0
+    tol = 1.13 * ztol + 2.0 ** -20 * z.abs() + half_step(odt) * want.abs() + tiny(odt)
+    assert_close(got, want, tol, "out")
+    if want_pre:
+        assert_close(pre, z, ztol + half_step(dt) * z.abs() + tiny(dt), "preact")
+    return got
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=str)
+def test_linear_shapes(shape, dt):
+    m, n, k = shape
+    x, w, b, r = _case(m, n, k, dt, m + n + k)
+    _check_forward(_fw(), x, w, b, r, "silu", dt, dt)
+    _check_forward(_fw(), x, w, None, None, "none", dt, dt, want_pre=False)
+
+
+@pytest.mark.parametrize("name", ["none", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("odt", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("shape", [(5, 200, 136), (600, 700, 264), (1100, 2056, 72), (513, 131, 72)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_linear_activations_and_types(shape, odt, name):
+    m, n, k = shape
+    x, w, b, r = _case(m, n, k, torch.bfloat16, 5)
+    _check_forward(_fw(), x, w, b, r, name, torch.bfloat16, odt)
+    _check_forward(_fw(), x, w, b, None, name, torch.bfloat16, odt, want_pre=False)
+
+
+@pytest.mark.parametrize("shape", [(40, 264, 72), (900, 520, 200)], ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("pad", [3, 8])
+def test_linear_strided_rows_and_residual_in_place(shape, pad):
+    # rows inside wider buffers (odd and 16-byte strides): the gaps stay as they were
+    fw = _fw()
+    dt = torch.bfloat16
+    m, n, k = shape
+    x, w, b, r = _case(m, n, k, dt, 77)
+
+    def wide(t):
+        buf = torch.full((t.shape[0], t.shape[1] + pad), 5.0, dtype=dt, device="cuda")
+        buf[:, :t.shape[1]] = t.to(dt).cuda()
+        return buf
+    xb, wb, ob, pb = wide(x), wide(w), wide(r), wide(r)
+    want = fw.wsattn_linear(x.cuda(), w.cuda(), b.cuda(), r.to(dt).cuda(), "gelu")
+    out = fw.wsattn_linear(xb[:, :k], wb[:, :k], b.cuda(), ob[:, :n], "gelu", preact=pb[:, :n],
+                           out=ob[:, :n])
+    assert torch.equal(out, want)
+    for buf, c in ((ob, n), (pb, n), (xb, k), (wb, k)):
+        assert (buf[:, c:] == 5.0).all()
+    # leading dimensions fold into rows
+    if m % 4 == 0:
+        y = fw.wsattn_linear(x.cuda().view(2, m // 4, 2, k), w.cuda(), b.cuda(),
+                             r.to(dt).cuda().view(2, m // 4, 2, n), "gelu")
+        assert torch.equal(y.view(m, n), want)
+
+
+@pytest.mark.parametrize("dims", [(1, 2, 48, 64), (2, 3, 100, 128), (1, 5, 1, 8)])
+def test_linear_of_attention_output(dims):
+    # fp32 [B, H, N, D]: heads merged, rounded once
+    fw = _fw()
+    B, H, N, D = dims
+    g = torch.Generator().manual_seed(4)
+    a = torch.randn(dims, generator=g)
+    w = (torch.randn((72, H * D), generator=g) / (H * D) ** 0.5).to(torch.bfloat16)
+    got = fw.wsattn_linear(a.cuda(), w.cuda())
+    rows = a.transpose(1, 2).reshape(B, N, H * D).to(torch.bfloat16)
+    want = fw.wsattn_linear(rows.cuda(), w.cuda())
+    assert got.shape == (B, N, 72) and torch.equal(got, want)
+
+
+def _slope64(z, name):
+    z = z.clone().requires_grad_(True)
+    act(z, name).sum().backward()
+    return z.grad
+
+
+@pytest.mark.parametrize("name", ["none", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 264, 136), (37, 77, 33), (130, 200, 72), (333, 256, 512),
+                                   (1030, 515, 90), (3000, 128, 64), (640, 1288, 1160)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_linear_backward(shape, dt, name):
+    fw = _fw()
+    m, n, k = shape
+    x, w, _, r = _case(m, n, k, dt, 3 * m + n)
+    g = torch.Generator().manual_seed(1)
+    dy = (0.3 * torch.randn((m, n), generator=g)).to(dt)
+    z = None if name == "none" else (1.5 * r).to(dt)
+    dx, dw, db = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(),
+                                           None if z is None else z.cuda(), name)
+    torch.cuda.synchronize()
+    assert fw.wsattn_op_status() == 0
+    dz = dy.double() * (1 if z is None else _slope64(z.double(), name))
+    # of dz: half a step where it is rounded, 2^-19 relative to dout for the slope
+    dztol = (0 if z is None else half_step(dt) * dz.abs() + 2.0 ** -19 * dy.double().abs() + tiny(dt))
+    wa, xa = w.double().abs(), x.double().abs()
+    for got, want, mag, extra, kk in (
+            (dx, dz @ w.double(), dz.abs() @ wa, dztol @ wa if z is not None else 0, n),
+            (dw, dz.t() @ x.double(), dz.abs().t() @ xa, dztol.t() @ xa if z is not None else 0, m)):
+        tol = 1.01 * extra + product_tol(mag, kk) + half_step(dt) * want.abs() + tiny(dt)
+        assert_close(got, want, tol)
+    sums = dz.abs().sum(0)
+    assert_close(db, dz.sum(0), (2.0 ** -19 + (m / 64 + 32) * 2.0 ** -24) * (sums + dy.double().abs().sum(0)))
+    again = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name)
+    for a, b in zip(again, (dx, dw, db)):
+        assert torch.equal(a, b)
+    # each gradient by itself
+    only = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name,
+                                     need_dx=False, need_db=False)
+    assert only[0] is None and only[2] is None and torch.equal(only[1], dw)
+    only = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name,
+                                     need_dx=False, need_dw=False)
+    assert only[0] is None and only[1] is None and torch.equal(only[2], db)
+
+
+def test_linear_empty():
+    fw = _fw()
+    w = torch.ones((5, 7), dtype=torch.bfloat16, device="cuda")
+    x = torch.empty((0, 7), dtype=torch.bfloat16, device="cuda")
+    assert fw.wsattn_linear(x, w).shape == (0, 5)
+    dx, dw, db = fw.wsattn_linear_backward(torch.empty((0, 5), dtype=torch.bfloat16, device="cuda"), x, w)
+    assert dx.shape == (0, 7) and torch.equal(dw, torch.zeros_like(w)) and (db == 0).all()
+
+
+def test_linear_extreme_values():
+    # activations at the ends of bf16's range; rows of infinities reach their own rows only
+    fw = _fw()
+    dt = torch.bfloat16
+    x = torch.zeros((300, 64), dtype=dt)
+    x[:, 0] = 1
+    w = torch.zeros((8, 64), dtype=dt)
+    w[:, 0] = torch.tensor([1e30, -1e30, 100.0, -100.0, 0.0, -0.0, 3e38, -3e38])
+    for name in ("gelu", "gelu_tanh", "silu"):
+        y = fw.wsattn_linear(x.cuda(), w.cuda(), activation=name).cpu().float()
+        want = torch.relu(w[:, 0].float())
+        assert torch.equal(y, want.expand(300, 8)), name
+        z = w[:, 0].expand(300, 8).contiguous()
+        one = torch.ones((300, 8), dtype=dt)
+        _, _, db = fw.wsattn_linear_backward(one.cuda(), x.cuda(), w.cuda(), z.cuda(), name)
+        assert torch.equal(db.cpu(), 300 * torch.tensor([1, 0, 1, 0, 0.5, 0.5, 1, 0])), name
+    x[7, 3] = float("inf")
+    w[:, 3] = 1
+    y = fw.wsattn_linear(x.cuda(), w.cuda()).cpu()
+    assert y[7].isinf().all() and torch.isfinite(y[:7]).all() and torch.isfinite(y[8:]).all()
+
+
+def test_linear_capture_and_streams():
+    fw = _fw()
+    dt = torch.bfloat16
+    x, w, b, r = _case(300, 257, 77, dt, 8)   # odd widths: operands go through the workspace
+    x, w, b, r = x.cuda(), w.cuda(), b.cuda(), r.to(dt).cuda()
+    want = fw.wsattn_linear(x, w, b, r, "gelu")
+    grads = fw.wsattn_linear_backward(r, x, w, r, "silu")
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = fw.wsattn_linear(x, w, b, r, "gelu")
+            d = fw.wsattn_linear_backward(r, x, w, r, "silu")
+        graphs.append((graph, y, d))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for (graph, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, y, d in graphs:
+        assert torch.equal(y, want)
+        for a, c in zip(d, grads):
+            assert torch.equal(a, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = fw.wsattn_linear(x, w, b, r, "gelu", stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
