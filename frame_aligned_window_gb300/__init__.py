@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -99,43 +100,30 @@ _lib.wsattn_produce.argtypes = [_P, _I, _P, _I, _P, _P, _P, _F, _P, _P, _P, _P]
 _lib.wsattn_build_flags.argtypes = []
 
 
-class _Heads(ctypes.Structure):
-    """wsattn_heads: a [batch, heads, N, D] view."""
-    _fields_ = [("data", _P), ("heads", _I), ("stride_b", ctypes.c_int64),
-                ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+# The argument structs of include/wsattn.h, in the C layout ("@": native sizes
+# and alignment; "0q" pads the end).  They are packed rather than built as
+# ctypes structures: the smallest calls are bound by the host.
+_HEADS = struct.Struct("@Piqqq0q").pack  # wsattn_heads: data, heads, strides b, h, n
+# wsattn_linear_args: dtype, out_dtype, m, n, k, x, ldx, x_heads, x_tokens, w,
+# ldw, bias, residual, ldr, out, ldo, preact, ldp, activation
+_LINEAR = struct.Struct("@iiqiiPqiqPqPPqPqPqi0q").pack
+# wsattn_linear_grad_args: dtype, m, n, k, dout, ldd, x, ldx, w, ldw, preact,
+# ldp, activation, dx, lddx, dw, lddw, db
+_LINEAR_GRAD = struct.Struct("@iqiiPqPqPqPqiPqPqP0q").pack
 
-
-class _LinearArgs(ctypes.Structure):
-    """wsattn_linear_args."""
-    _fields_ = [("dtype", _I), ("out_dtype", _I), ("m", ctypes.c_int64), ("n", _I), ("k", _I),
-                ("x", _P), ("ldx", ctypes.c_int64), ("x_heads", _I),
-                ("x_tokens", ctypes.c_int64), ("w", _P), ("ldw", ctypes.c_int64), ("bias", _P),
-                ("residual", _P), ("ldr", ctypes.c_int64), ("out", _P), ("ldo", ctypes.c_int64),
-                ("preact", _P), ("ldp", ctypes.c_int64), ("activation", _I)]
-
-
-class _LinearGradArgs(ctypes.Structure):
-    """wsattn_linear_grad_args."""
-    _fields_ = [("dtype", _I), ("m", ctypes.c_int64), ("n", _I), ("k", _I), ("dout", _P),
-                ("ldd", ctypes.c_int64), ("x", _P), ("ldx", ctypes.c_int64), ("w", _P),
-                ("ldw", ctypes.c_int64), ("preact", _P), ("ldp", ctypes.c_int64),
-                ("activation", _I), ("dx", _P), ("lddx", ctypes.c_int64), ("dw", _P),
-                ("lddw", ctypes.c_int64), ("db", _P)]
-
-
-_I64, _SZP, _HP = ctypes.c_int64, ctypes.POINTER(_SZ), ctypes.POINTER(_Heads)
+_I64, _SZP = ctypes.c_int64, ctypes.POINTER(_SZ)
 _lib.wsattn_rotary_plan.argtypes = [_I, _I, _P, _P, _I, ctypes.POINTER(_P)]
 _lib.wsattn_rotary_destroy.argtypes = [_P]
-_lib.wsattn_rotary.argtypes = [_P, _I, _I, _I64, _HP, _P, _I64, _I, _HP, _P]
-_lib.wsattn_qknorm.argtypes = [_P, _I, _I, _I64, _HP, _HP, _HP, _P, _P, _I, _F, _P, _I64, _HP,
-                               _HP, _HP, _P]
-_lib.wsattn_qknorm_backward.argtypes = [_P, _I, _I, _I64, _HP, _HP, _HP, _HP, _HP, _P, _P, _I, _F,
-                                        _P, _I64, _HP, _HP, _HP, _P, _P, _P, _SZ, _P]
+_lib.wsattn_rotary.argtypes = [_P, _I, _I, _I64, _P, _P, _I64, _I, _P, _P]
+_lib.wsattn_qknorm.argtypes = [_P, _I, _I, _I64, _P, _P, _P, _P, _P, _I, _F, _P, _I64, _P,
+                               _P, _P, _P]
+_lib.wsattn_qknorm_backward.argtypes = [_P, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _F,
+                                        _P, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.wsattn_qknorm_backward_workspace.argtypes = [_P, _SZP]
-_lib.wsattn_linear.argtypes = [ctypes.POINTER(_LinearArgs), _P, _SZ, _P]
-_lib.wsattn_linear_workspace.argtypes = [ctypes.POINTER(_LinearArgs), _SZP]
-_lib.wsattn_linear_backward.argtypes = [ctypes.POINTER(_LinearGradArgs), _P, _SZ, _P]
-_lib.wsattn_linear_backward_workspace.argtypes = [ctypes.POINTER(_LinearGradArgs), _SZP]
+_lib.wsattn_linear.argtypes = [_P, _P, _SZ, _P]
+_lib.wsattn_linear_workspace.argtypes = [_P, _SZP]
+_lib.wsattn_linear_backward.argtypes = [_P, _P, _SZ, _P]
+_lib.wsattn_linear_backward_workspace.argtypes = [_P, _SZP]
 _lib.wsattn_op_status.argtypes = [_P]
 _lib.wsattn_status_string.restype = ctypes.c_char_p
 for _name in EXPORTS:
@@ -411,25 +399,34 @@ def _dtype_code(t, name, allowed=(BF16, FP16, FP32)):
     return code
 
 
-def _same_device(dev, **tensors):
+def _device_of(t, name):
+    """Index of the CUDA device a call's tensors live on, from its first one."""
     import torch
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _stream_on(dev, stream):
-    """The stream a call on tensors of `dev` goes to (default: that device's current one)."""
+def _check_tensor(t, name, dev, dtype=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _raw_stream(dev, stream):
+    """The stream a call on tensors of device `dev` goes to (default: that
+    device's current one)."""
     import torch
     if stream is None:
-        return torch.cuda.current_stream(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
-    return stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype, dev, stream):
@@ -445,11 +442,13 @@ def _empty(shape, dtype, dev, stream):
 def _run(dev, what, fn, *args):
     """The C call, with the tensors' device current."""
     import torch
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args), what)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args), what)
+            rc = fn(*args)
+    if rc:
+        raise WsattnError(rc, what)
 
 
 class RotaryPlan:
@@ -459,6 +458,10 @@ class RotaryPlan:
         self._h = handle
         self.head_dim = head_dim
         self.axes = axes
+        n = _SZ()
+        _check(_lib.wsattn_qknorm_backward_workspace(handle, ctypes.byref(n)),
+               "wsattn_qknorm_backward_workspace")
+        self.backward_workspace = int(n.value)
 
     @property
     def handle(self):
@@ -516,76 +519,75 @@ def wsattn_rotary_destroy(rot: RotaryPlan):
     rot.destroy()
 
 
-def _head_view(t, name, shape, dtype):
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+def _head_view(t, name, shape, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _check_tensor(t, name, dev, dtype)
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     sb, sh, sn, sd = t.stride()
     if sd != 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _Heads(t.data_ptr(), shape[1], sb, sh, sn)
+    return _HEADS(t.data_ptr(), shape[1], sb, sh, sn)
 
 
-def _positions(rot, positions, batch, tokens):
+def _positions(rot, t, batch, tokens, dev):
+    """(pointer, batch stride) of the positions."""
     import torch
-    if positions.dtype != torch.float32:
-        raise TypeError(f"positions must be torch.float32, got {positions.dtype}")
-    shape = tuple(positions.shape)
-    if shape == (tokens, rot.axes):
+    if t.dtype is not torch.float32 or t.get_device() != dev:
+        _check_tensor(t, "positions", dev, torch.float32)
+    axes, shape, st = rot.axes, t.shape, t.stride()
+    if shape == (tokens, axes):
         stride = 0
-    elif shape == (batch, tokens, rot.axes):
-        stride = positions.stride(0) if batch > 1 else 0
+    elif shape == (batch, tokens, axes):
+        stride = st[0] if batch > 1 else 0
     else:
-        raise ValueError(f"positions must be [{tokens}, {rot.axes}] or [{batch}, {tokens}, "
-                         f"{rot.axes}], got {list(shape)}")
-    inner = positions if len(shape) == 2 else (positions[0] if batch else positions)
-    if positions.numel() and not inner.is_contiguous():
+        raise ValueError(f"positions must be [{tokens}, {axes}] or [{batch}, {tokens}, {axes}], "
+                         f"got {list(shape)}")
+    if (axes > 1 and st[-1] != 1 or tokens > 1 and st[-2] != axes) and t.numel():
         raise ValueError("positions must be contiguous")
-    return ctypes.c_void_p(positions.data_ptr()), stride
+    return t.data_ptr(), stride
 
 
 def _heads_shape(t, name, rot):
-    if t.dim() != 4 or t.shape[3] != rot.head_dim:
-        raise ValueError(f"{name} must be [B, H, N, {rot.head_dim}], got {list(t.shape)}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != 4 or shape[3] != rot.head_dim:
+        raise ValueError(f"{name} must be [B, H, N, {rot.head_dim}], got {list(shape)}")
+    return shape
 
 
 def wsattn_rotary(rot: RotaryPlan, x, positions, inverse: bool = False, out=None, stream=None):
     """x [B, H, N, D] (bf16, fp16 or fp32; any strides, last dimension
     contiguous) turned by positions fp32 [N, axes] or [B, N, axes]; inverse
     turns back (the gradient).  out: default a contiguous tensor; may be x."""
-    shape = _heads_shape(x, "x", rot)
-    _same_device(x.device, x=x, positions=positions, out=out)
-    s = _stream_on(x.device, stream)
+    dev = _device_of(x, "x")
+    shape, dt = _heads_shape(x, "x", rot), x.dtype
     code = _dtype_code(x, "x")
+    raw = _raw_stream(dev, stream)
+    pos, pos_b = _positions(rot, positions, shape[0], shape[2], dev)
     if out is None:
-        out = _empty(shape, x.dtype, x.device, stream)
-    pos, pos_b = _positions(rot, positions, shape[0], shape[2])
-    _run(x.device, "wsattn_rotary", _lib.wsattn_rotary, rot.handle, code, shape[0], shape[2],
-         _head_view(x, "x", shape, x.dtype), pos, pos_b, int(bool(inverse)),
-         _head_view(out, "out", shape, x.dtype), s.cuda_stream)
+        out = _empty(shape, dt, dev, stream)
+    _run(dev, "wsattn_rotary", _lib.wsattn_rotary, rot.handle, code, shape[0], shape[2],
+         _head_view(x, "x", shape, dt, dev), pos, pos_b, 1 if inverse else 0,
+         _head_view(out, "out", shape, dt, dev), raw)
     return out
 
 
-def _gain(t, name, dim, dtype):
-    """(pointer, dtype code or None) of a gain vector."""
+def _gains(q_weight, k_weight, dim, dtype, code, dev):
+    """Pointers of the gain vectors and their dtype code."""
     import torch
-    if t is None:
-        return None, None
-    if tuple(t.shape) != (dim,) or (dim > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be contiguous [{dim}], got {list(t.shape)}")
-    if t.dtype not in (dtype, torch.float32):
-        raise TypeError(f"{name} must be {dtype} or torch.float32, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr()), _dtype_code(t, name)
-
-
-def _gains(q_weight, k_weight, dim, dtype, code):
-    wq, cq = _gain(q_weight, "q_weight", dim, dtype)
-    wk, ck = _gain(k_weight, "k_weight", dim, dtype)
-    if cq is not None and ck is not None and cq != ck:
-        raise TypeError("q_weight and k_weight must have one type")
-    return wq, wk, code if cq is None and ck is None else (ck if cq is None else cq)
+    ptr, kind = [None, None], None
+    for i, t in enumerate((q_weight, k_weight)):
+        if t is None:
+            continue
+        name = "qk"[i] + "_weight"
+        _check_tensor(t, name, dev)
+        if t.shape != (dim,) or t.stride(0) != 1:
+            raise ValueError(f"{name} must be contiguous [{dim}], got {list(t.shape)}")
+        if t.dtype != dtype and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be {dtype} or torch.float32, got {t.dtype}")
+        if kind is not None and kind != t.dtype:
+            raise TypeError("q_weight and k_weight must have one type")
+        kind, ptr[i] = t.dtype, t.data_ptr()
+    return ptr[0], ptr[1], FP32 if kind == torch.float32 else code
 
 
 def _qkv_shapes(rot, q, k, v):
@@ -604,34 +606,38 @@ def wsattn_qknorm(rot: RotaryPlan, q, k, positions, q_weight=None, k_weight=None
     k [B, Hk, N, D], and a copy of v, in one pass; q, k, v may be views of one
     projection's rows.  Returns (q, k) or (q, k, v), by default contiguous, as
     wsattn_prepare and wsattn_forward read them; an output may be its input."""
+    dev = _device_of(q, "q")
     sq, sk, sv = _qkv_shapes(rot, q, k, v)
     if v is None and v_out is not None:
         raise ValueError("v_out without v")
-    _same_device(q.device, q=q, k=k, v=v, positions=positions, q_weight=q_weight,
-                 k_weight=k_weight, q_out=q_out, k_out=k_out, v_out=v_out)
-    s = _stream_on(q.device, stream)
-    code = _dtype_code(q, "q")
-    wq, wk, wcode = _gains(q_weight, k_weight, rot.head_dim, q.dtype, code)
-    dt, dev = q.dtype, q.device
+    raw = _raw_stream(dev, stream)
+    code, dt = _dtype_code(q, "q"), q.dtype
+    wq, wk, wcode = _gains(q_weight, k_weight, rot.head_dim, dt, code, dev)
+    pos, pos_b = _positions(rot, positions, sq[0], sq[2], dev)
     q_out = _empty(sq, dt, dev, stream) if q_out is None else q_out
     k_out = _empty(sk, dt, dev, stream) if k_out is None else k_out
     if v is not None and v_out is None:
         v_out = _empty(sv, dt, dev, stream)
-    pos, pos_b = _positions(rot, positions, sq[0], sq[2])
     _run(dev, "wsattn_qknorm", _lib.wsattn_qknorm, rot.handle, code, sq[0], sq[2],
-         _head_view(q, "q", sq, dt), _head_view(k, "k", sk, dt),
-         None if v is None else _head_view(v, "v", sv, dt), wq, wk, wcode, float(eps), pos, pos_b,
-         _head_view(q_out, "q_out", sq, dt), _head_view(k_out, "k_out", sk, dt),
-         None if v is None else _head_view(v_out, "v_out", sv, dt), s.cuda_stream)
+         _head_view(q, "q", sq, dt, dev), _head_view(k, "k", sk, dt, dev),
+         None if v is None else _head_view(v, "v", sv, dt, dev), wq, wk, wcode, eps, pos, pos_b,
+         _head_view(q_out, "q_out", sq, dt, dev), _head_view(k_out, "k_out", sk, dt, dev),
+         None if v is None else _head_view(v_out, "v_out", sv, dt, dev), raw)
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
 def wsattn_qknorm_backward_workspace(rot: RotaryPlan) -> int:
     """Bytes of scratch wsattn_qknorm_backward takes for the gains' gradients."""
-    n = _SZ()
-    _check(_lib.wsattn_qknorm_backward_workspace(rot.handle, ctypes.byref(n)),
-           "wsattn_qknorm_backward_workspace")
-    return int(n.value)
+    return rot.backward_workspace
+
+
+def _scratch_args(workspace, dev):
+    if workspace is None:
+        return None, 0
+    _check_tensor(workspace, "workspace", dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def wsattn_qknorm_backward(rot: RotaryPlan, dq_out, dk_out, q, k, positions, q_weight=None,
@@ -641,125 +647,127 @@ def wsattn_qknorm_backward(rot: RotaryPlan, dq_out, dk_out, q, k, positions, q_w
     and dv may be views of one packed gradient (default: contiguous); dv is
     None without dv_out, and a gain's gradient (fp32 [D]) None without the gain."""
     import torch
+    dev = _device_of(q, "q")
     sq, sk, sv = _qkv_shapes(rot, q, k, dv_out)
     if dv_out is None and dv is not None:
         raise ValueError("dv without dv_out")
-    _same_device(q.device, q=q, k=k, dq_out=dq_out, dk_out=dk_out, dv_out=dv_out,
-                 positions=positions, q_weight=q_weight, k_weight=k_weight, dq=dq, dk=dk, dv=dv,
-                 workspace=workspace)
-    s = _stream_on(q.device, stream)
-    code = _dtype_code(q, "q")
-    wq, wk, wcode = _gains(q_weight, k_weight, rot.head_dim, q.dtype, code)
-    dt, dev = q.dtype, q.device
+    raw = _raw_stream(dev, stream)
+    code, dt, dim = _dtype_code(q, "q"), q.dtype, rot.head_dim
+    wq, wk, wcode = _gains(q_weight, k_weight, dim, dt, code, dev)
+    pos, pos_b = _positions(rot, positions, sq[0], sq[2], dev)
     dq = _empty(sq, dt, dev, stream) if dq is None else dq
     dk = _empty(sk, dt, dev, stream) if dk is None else dk
     if dv_out is not None and dv is None:
         dv = _empty(sv, dt, dev, stream)
-    dwq = None if q_weight is None else _empty((rot.head_dim,), torch.float32, dev, stream)
-    dwk = None if k_weight is None else _empty((rot.head_dim,), torch.float32, dev, stream)
-    if (dwq is not None or dwk is not None) and workspace is None:
-        workspace = _empty((wsattn_qknorm_backward_workspace(rot),), torch.uint8, dev, stream)
-    pos, pos_b = _positions(rot, positions, sq[0], sq[2])
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    dwq = None if wq is None else _empty((dim,), torch.float32, dev, stream)
+    dwk = None if wk is None else _empty((dim,), torch.float32, dev, stream)
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = _empty((rot.backward_workspace,), torch.uint8, dev, stream)
+    ws, ws_bytes = _scratch_args(workspace, dev)
     _run(dev, "wsattn_qknorm_backward", _lib.wsattn_qknorm_backward, rot.handle, code, sq[0],
-         sq[2], _head_view(dq_out, "dq_out", sq, dt), _head_view(dk_out, "dk_out", sk, dt),
-         None if dv is None else _head_view(dv_out, "dv_out", sv, dt), _head_view(q, "q", sq, dt),
-         _head_view(k, "k", sk, dt), wq, wk, wcode, float(eps), pos, pos_b,
-         _head_view(dq, "dq", sq, dt), _head_view(dk, "dk", sk, dt),
-         None if dv is None else _head_view(dv, "dv", sv, dt), ptr(dwq), ptr(dwk), ptr(workspace),
-         0 if workspace is None else workspace.numel() * workspace.element_size(), s.cuda_stream)
+         sq[2], _head_view(dq_out, "dq_out", sq, dt, dev),
+         _head_view(dk_out, "dk_out", sk, dt, dev),
+         None if dv is None else _head_view(dv_out, "dv_out", sv, dt, dev),
+         _head_view(q, "q", sq, dt, dev), _head_view(k, "k", sk, dt, dev), wq, wk, wcode, eps, pos,
+         pos_b, _head_view(dq, "dq", sq, dt, dev), _head_view(dk, "dk", sk, dt, dev),
+         None if dv is None else _head_view(dv, "dv", sv, dt, dev),
+         None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), ws,
+         ws_bytes, raw)
     return dq, dk, dv, dwq, dwk
 
 
-def _rows(t, name, cols, lead=None):
-    """(rows, row stride) of t seen as a matrix of `cols` columns; the leading
-    dimensions must lie one row stride apart."""
-    if t.dim() < 1 or t.shape[-1] != cols or (lead is not None and tuple(t.shape[:-1]) != lead):
+def _rows(t, name, cols, lead, dtype, dev):
+    """Row stride of t seen as a matrix of `cols` columns under the leading
+    dimensions `lead` (None: any), which must lie one row stride apart."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _check_tensor(t, name, dev, dtype)
+    shape, st = t.shape, t.stride()
+    if not shape or shape[-1] != cols or (lead is not None and shape[:-1] != lead):
         want = "..." if lead is None else ", ".join(str(x) for x in lead)
-        raise ValueError(f"{name} must be [{want}, {cols}], got {list(t.shape)}")
+        raise ValueError(f"{name} must be [{want}, {cols}], got {list(shape)}")
+    if len(shape) == 2 and st[1] == 1 and st[0] >= cols:
+        return st[0]
     rows, ld = 1, None
     if t.numel() == 0:
-        return t[..., 0].numel() if cols else 0, cols
-    if cols > 1 and t.stride(-1) != 1:
+        return cols
+    if cols > 1 and st[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] == 1:
+    for n, step in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
             continue
         if ld is None:
-            ld = t.stride(i)
-        elif t.stride(i) != ld * rows:
+            ld = step
+        elif step != ld * rows:
             raise ValueError(f"{name}'s rows must lie one stride apart")
-        rows *= t.shape[i]
+        rows *= n
     if ld is not None and ld < cols:
         raise ValueError(f"{name}'s rows must not overlap")
-    return rows, cols if ld is None else ld
+    return cols if ld is None else ld
 
 
 def _activation(name):
-    if name not in ACTIVATIONS:
+    code = ACTIVATIONS.get(name)
+    if code is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
-    return ACTIVATIONS[name]
+    return code
 
 
-def _scratch(query, args, workspace, dev, stream):
+def _scratch(query, what, args, workspace, dev, stream):
     """(pointer, bytes, tensor) of a call's workspace, allocated when needed."""
     import torch
-    n = _SZ()
-    _check(query(ctypes.byref(args), ctypes.byref(n)), "workspace size")
-    if workspace is None and n.value:
-        workspace = _empty((n.value,), torch.uint8, dev, stream)
     if workspace is None:
-        return None, 0, None
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        n = _SZ()
+        _run(dev, what, query, args, ctypes.byref(n))
+        if not n.value:
+            return None, 0, None
+        workspace = _empty((n.value,), torch.uint8, dev, stream)
+    return *_scratch_args(workspace, dev), workspace
 
 
 def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, stream):
+    """The packed wsattn_linear_args, the output and the device."""
     import torch
+    dev = _device_of(weight, "weight")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
     n, k = weight.shape
-    code = _dtype_code(weight, "weight", (BF16, FP16))
-    dev = weight.device
-    _same_device(dev, x=x, weight=weight, bias=bias, residual=residual, preact=preact, out=out)
-    a = _LinearArgs(dtype=code, n=n, k=k, activation=_activation(activation))
-    if x.dtype == torch.float32 and x.dim() == 4:
-        B, H, N, D = x.shape
-        if H * D != k or not x.is_contiguous():
+    dt, code = weight.dtype, _dtype_code(weight, "weight", (BF16, FP16))
+    act = _activation(activation)
+    if x.dtype is dt:
+        lead, heads, tokens = x.shape[:-1], 0, 0
+        ldx = _rows(x, "x", k, None, dt, dev)
+    else:
+        if x.dtype != torch.float32 or x.dim() != 4:
+            raise TypeError(f"x must be {dt} (or wsattn_forward's fp32 output), got {x.dtype}")
+        _check_tensor(x, "x", dev)
+        B, heads, tokens, D = x.shape
+        if heads * D != k or not x.is_contiguous():
             raise ValueError(f"x must be contiguous [B, H, N, D] with H * D = {k}, "
                              f"got {list(x.shape)}")
-        lead = (B, N)
-        a.m, a.x_heads, a.x_tokens = B * N, H, N
-    else:
-        if x.dtype != weight.dtype:
-            raise TypeError(f"x must be {weight.dtype} (or wsattn_forward's fp32 output), "
-                            f"got {x.dtype}")
-        lead = tuple(x.shape[:-1])
-        a.m, a.ldx = _rows(x, "x", k)
-    a.x, a.w = x.data_ptr(), weight.data_ptr()
-    _, a.ldw = _rows(weight, "weight", k)
+        lead, ldx = torch.Size((B, tokens)), 0
+    m = 1
+    for size in lead:
+        m *= size
+    ldw = _rows(weight, "weight", k, None, dt, dev)
+    bp = rp = pp = ldr = ldp = 0
     if bias is not None:
-        if tuple(bias.shape) != (n,) or bias.dtype != weight.dtype or (n > 1 and bias.stride(0) != 1):
-            raise ValueError(f"bias must be contiguous {weight.dtype} [{n}]")
-        a.bias = bias.data_ptr()
+        _check_tensor(bias, "bias", dev, dt)
+        if bias.shape != (n,) or (n > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias must be contiguous [{n}], got {list(bias.shape)}")
+        bp = bias.data_ptr()
     if out is None:
-        out_dtype = weight.dtype if out_dtype is None else out_dtype
-        out = _empty(lead + (n,), out_dtype, dev, stream)
+        out = _empty(lead + (n,), dt if out_dtype is None else out_dtype, dev, stream)
     elif out_dtype not in (None, out.dtype):
         raise TypeError(f"out is {out.dtype}, not {out_dtype}")
-    a.out_dtype = _dtype_code(out, "out", (code, FP32))
-    a.out = out.data_ptr()
-    _, a.ldo = _rows(out, "out", n, lead)
+    odt = out.dtype
+    ocode = code if odt is dt else _dtype_code(out, "out", (FP32,))
+    ldo = _rows(out, "out", n, lead, odt, dev)
     if residual is not None:
-        if residual.dtype != out.dtype:
-            raise TypeError(f"residual must be {out.dtype}, got {residual.dtype}")
-        a.residual = residual.data_ptr()
-        _, a.ldr = _rows(residual, "residual", n, lead)
+        ldr, rp = _rows(residual, "residual", n, lead, odt, dev), residual.data_ptr()
     if preact is not None:
-        if preact.dtype != weight.dtype:
-            raise TypeError(f"preact must be {weight.dtype}, got {preact.dtype}")
-        a.preact = preact.data_ptr()
-        _, a.ldp = _rows(preact, "preact", n, lead)
-    return a, out, dev
+        ldp, pp = _rows(preact, "preact", n, lead, dt, dev), preact.data_ptr()
+    return _LINEAR(code, ocode, m, n, k, x.data_ptr(), ldx, heads, tokens, weight.data_ptr(), ldw,
+                   bp, rp, ldr, out.data_ptr(), ldo, pp, ldp, act), out, dev
 
 
 def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact=None, out=None,
@@ -770,62 +778,60 @@ def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact
     preact: a tensor that receives x weight^T + bias, for
     wsattn_linear_backward.  out (or out_dtype): weight's type or fp32, and
     the residual's; residual may be out."""
-    a, out, dev = _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype,
-                               stream)
-    _same_device(dev, workspace=workspace)
-    s = _stream_on(dev, stream)
-    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_workspace, a, workspace, dev, stream)
-    _run(dev, "wsattn_linear", _lib.wsattn_linear, a, ws, nbytes, s.cuda_stream)
+    args, out, dev = _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype,
+                                  stream)
+    raw = _raw_stream(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_workspace, "wsattn_linear_workspace", args,
+                                 workspace, dev, stream)
+    _run(dev, "wsattn_linear", _lib.wsattn_linear, args, ws, nbytes, raw)
     return out
 
 
 def wsattn_linear_workspace(x, weight) -> int:
     """Bytes of scratch wsattn_linear takes for these operands (0 when their
     rows start on 16-byte boundaries and x is not the attention's output)."""
-    a, _, _ = _linear_args(x, weight, None, None, "none", None, None, None, None)
+    args, _, dev = _linear_args(x, weight, None, None, "none", None, None, None, None)
     n = _SZ()
-    _check(_lib.wsattn_linear_workspace(ctypes.byref(a), ctypes.byref(n)),
-           "wsattn_linear_workspace")
+    _run(dev, "wsattn_linear_workspace", _lib.wsattn_linear_workspace, args, ctypes.byref(n))
     return int(n.value)
 
 
-def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need, stream):
+def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need_dx, need_dw, need_db,
+                      stream):
+    """The packed wsattn_linear_grad_args, the gradients and the device."""
     import torch
+    dev = _device_of(weight, "weight")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
     n, k = weight.shape
-    code = _dtype_code(weight, "weight", (BF16, FP16))
-    dev = weight.device
-    _same_device(dev, dout=dout, x=x, weight=weight, preact=preact, dx=dx, dw=dw, db=db)
-    a = _LinearGradArgs(dtype=code, n=n, k=k, activation=_activation(activation))
-    if a.activation and preact is None:
+    dt, code = weight.dtype, _dtype_code(weight, "weight", (BF16, FP16))
+    act = _activation(activation)
+    if act and preact is None:
         raise ValueError("an activation's gradient needs preact")
-    for t, name in ((dout, "dout"), (x, "x"), (preact, "preact"), (dx, "dx"), (dw, "dw")):
-        if t is not None and t.dtype != weight.dtype:
-            raise TypeError(f"{name} must be {weight.dtype}, got {t.dtype}")
-    lead = tuple(x.shape[:-1])
-    a.m, a.ldx = _rows(x, "x", k)
-    _, a.ldd = _rows(dout, "dout", n, lead)
-    _, a.ldw = _rows(weight, "weight", k)
-    a.dout, a.x, a.w = dout.data_ptr(), x.data_ptr(), weight.data_ptr()
+    ldx = _rows(x, "x", k, None, dt, dev)
+    lead, m = x.shape[:-1], 1
+    for size in lead:
+        m *= size
+    ldd = _rows(dout, "dout", n, lead, dt, dev)
+    ldw = _rows(weight, "weight", k, None, dt, dev)
+    pp = ldp = dxp = lddx = dwp = lddw = dbp = 0
     if preact is not None:
-        a.preact = preact.data_ptr()
-        _, a.ldp = _rows(preact, "preact", n, lead)
-    need_dx, need_dw, need_db = need
+        ldp, pp = _rows(preact, "preact", n, lead, dt, dev), preact.data_ptr()
     if need_dx or dx is not None:
-        dx = _empty(lead + (k,), weight.dtype, dev, stream) if dx is None else dx
-        a.dx = dx.data_ptr()
-        _, a.lddx = _rows(dx, "dx", k, lead)
+        dx = _empty(x.shape, dt, dev, stream) if dx is None else dx
+        lddx, dxp = _rows(dx, "dx", k, lead, dt, dev), dx.data_ptr()
     if need_dw or dw is not None:
-        dw = _empty((n, k), weight.dtype, dev, stream) if dw is None else dw
-        a.dw = dw.data_ptr()
-        _, a.lddw = _rows(dw, "dw", k, (n,))
+        dw = _empty((n, k), dt, dev, stream) if dw is None else dw
+        lddw, dwp = _rows(dw, "dw", k, (n,), dt, dev), dw.data_ptr()
     if need_db or db is not None:
         db = _empty((n,), torch.float32, dev, stream) if db is None else db
-        if tuple(db.shape) != (n,) or db.dtype != torch.float32 or not db.is_contiguous():
-            raise ValueError(f"db must be contiguous torch.float32 [{n}]")
-        a.db = db.data_ptr()
-    return a, dx, dw, db, dev
+        _check_tensor(db, "db", dev, torch.float32)
+        if db.shape != (n,) or (n > 1 and db.stride(0) != 1):
+            raise ValueError(f"db must be contiguous [{n}], got {list(db.shape)}")
+        dbp = db.data_ptr()
+    args = _LINEAR_GRAD(code, m, n, k, dout.data_ptr(), ldd, x.data_ptr(), ldx, weight.data_ptr(),
+                        ldw, pp, ldp, act, dxp, lddx, dwp, lddw, dbp)
+    return args, dx, dw, db, dev
 
 
 def wsattn_linear_backward(dout, x, weight, preact=None, activation="none", dx=None, dw=None,
@@ -835,23 +841,23 @@ def wsattn_linear_backward(dout, x, weight, preact=None, activation="none", dx=N
     weight's type, db fp32; None for what is not needed.  preact: what
     wsattn_linear left there (not needed without an activation).  The
     residual's gradient is dout itself."""
-    a, dx, dw, db, dev = _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db,
-                                           (need_dx, need_dw, need_db), stream)
-    _same_device(dev, workspace=workspace)
-    s = _stream_on(dev, stream)
-    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_backward_workspace, a, workspace, dev, stream)
-    _run(dev, "wsattn_linear_backward", _lib.wsattn_linear_backward, a, ws, nbytes, s.cuda_stream)
+    args, dx, dw, db, dev = _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db,
+                                              need_dx, need_dw, need_db, stream)
+    raw = _raw_stream(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_backward_workspace,
+                                 "wsattn_linear_backward_workspace", args, workspace, dev, stream)
+    _run(dev, "wsattn_linear_backward", _lib.wsattn_linear_backward, args, ws, nbytes, raw)
     return dx, dw, db
 
 
 def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="none", need_dx=True,
                                      need_dw=True, need_db=True) -> int:
     """Bytes of scratch wsattn_linear_backward takes for these operands."""
-    a, *_ = _linear_grad_args(dout, x, weight, preact, activation, None, None, None,
-                              (need_dx, need_dw, need_db), None)
+    args, *_, dev = _linear_grad_args(dout, x, weight, preact, activation, None, None, None,
+                                      need_dx, need_dw, need_db, None)
     n = _SZ()
-    _check(_lib.wsattn_linear_backward_workspace(ctypes.byref(a), ctypes.byref(n)),
-           "wsattn_linear_backward_workspace")
+    _run(dev, "wsattn_linear_backward_workspace", _lib.wsattn_linear_backward_workspace, args,
+         ctypes.byref(n))
     return int(n.value)
 
 

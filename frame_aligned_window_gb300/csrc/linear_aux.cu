@@ -184,19 +184,28 @@ cudaError_t launch_dact(const DactParams& p, int dtype, float* db, cudaStream_t 
                           static_cast<const float*>(p.part), p.ldpart, p.row_blocks, p.cols, db);
 }
 
-// First estimate of the time of each tiling, in SM cycles.
+// Estimated time of each tiling in nanoseconds, the least one wins.  From
+// timings of every tiling over a range of shapes (back to back, operands from
+// HBM): a 64-wide step of a pair's tile takes 320 ns at 256 columns and 285
+// at 128 (both move 96 and 84 KB per microsecond and SM from L2, which is
+// what bounds them), one of a single CTA the time of its bytes at that rate,
+// shared by the CTAs of an SM.
 GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms) {
   const int64_t ksteps = (K + kGemmK - 1) / kGemmK;
   GemmShape best{256, 0, 1};
   double best_t = 1e300;
   auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  for (int bn = 256; bn >= 128; bn -= 128) {
-    const int64_t waves = cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2);
-    const double t = 6000.0 + static_cast<double>(waves) * (ksteps * (bn == 256 ? 530.0 : 330.0) + 300.0);
+  auto consider = [&](double t, const GemmShape& s) {
     if (t < best_t) {
       best_t = t;
-      best = GemmShape{bn, 0, 1};
+      best = s;
     }
+  };
+  for (int bn = 256; bn >= 128; bn -= 128) {
+    const int64_t waves = cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2);
+    consider(4500.0 + static_cast<double>(waves) *
+                          (static_cast<double>(ksteps) * (bn == 256 ? 320.0 : 285.0) + 500.0),
+             GemmShape{bn, 0, 1});
   }
   for (int bn = 16; bn <= 128; bn *= 2) {
     if (p_mn && bn < 64) continue;
@@ -204,15 +213,15 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms) {
     for (int split = 1; split <= 8 && split <= ksteps; ++split) {
       const int64_t ctas = cdiv(R, bn) * cdiv(C, kTileCols) * split;
       const int64_t waves = cdiv(ctas, 2 * sms);
-      // two CTAs share an SM's bandwidth and tensor cores
-      const double share = ctas > sms ? 2.0 : 1.0;
-      const double step = bn <= 32 ? 420.0 : bn == 64 ? 420.0 : 480.0;
-      const double t = 4000.0 + (split > 1 ? 1500.0 : 0.0) +
-                       waves * (cdiv(ksteps, split) * step * share / 2 * (share > 1 ? 1.0 : 1.4) + 600.0 + bn * 12.0);
-      if (t < best_t) {
-        best_t = t;
-        best = GemmShape{0, bn, split};
-      }
+      const int64_t per_sm = ctas > sms ? 2 : 1;
+      // bytes of a step at 100 KB a microsecond and SM, but no faster than
+      // the weights come from HBM, nor than one CTA's ring turns over
+      const double step = per_sm * (16.0 + bn / 8.0) * 10.0;
+      const double t = 2500.0 + (split > 1 ? 1200.0 : 0.0) +
+                       static_cast<double>(waves) *
+                           (static_cast<double>(cdiv(ksteps, split)) * (step > 230.0 ? step : 230.0) +
+                            600.0 + 8.0 * bn);
+      consider(t, GemmShape{0, bn, split});
     }
   }
   return best;

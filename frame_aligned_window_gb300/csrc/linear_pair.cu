@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tbase = *tslot;
   griddep_wait();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) producer<BN>(p, s, total, pair, pairs, rank);

@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tbase = *tslot;
   griddep_wait();
+  // the next kernel's set-up may overlap this one (it waits for its results)
+  griddep_launch_dependents();
 
   bool have = false;  // epilogue threads: the accumulator is complete
   const int quad = warp & 3;
