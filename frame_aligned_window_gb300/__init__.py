@@ -27,6 +27,11 @@ import struct
 
 import numpy as np
 
+try:
+    import torch
+except ImportError:  # the host-only calls (plans, block maps) need no torch
+    torch = None
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("WSATTN_LIBRARY") or os.path.join(_HERE, "libwsattn.so")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libwsattn_debug.so")
@@ -180,14 +185,12 @@ class Plan:
 
 
 def _stream_ptr(stream):
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dev_ptr(t, name, dtype=None):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -230,7 +233,6 @@ def wsattn_plan_destroy(plan: Plan):
 
 def wsattn_prepare(plan: Plan, q, k, stream=None):
     """Key mean, row bounds, row fixed max and per-head eligibility (q, k read only)."""
-    import torch
     _check_shape(plan, q, "q")
     _check_shape(plan, k, "k")
     if q.shape[0] != k.shape[0]:
@@ -245,7 +247,6 @@ def wsattn_produce(plan: Plan, x, w_qkv, rope_cos, rope_sin, eps: float = 1e-6, 
     """Pre-attention producer: x [B, N, C] bf16, w_qkv [3HD, C] bf16, rope
     tables fp32 [N, D/2] -> (q, k, v) bf16 [B, H, N, D]; the plan's
     statistics are then ready for wsattn_forward, as after wsattn_prepare."""
-    import torch
     if x.dim() != 3 or x.shape[1] != plan.n_tokens:
         raise ValueError(f"x must be [B, {plan.n_tokens}, C], got {tuple(x.shape)}")
     B, _, C = x.shape
@@ -274,7 +275,6 @@ def wsattn_produce(plan: Plan, x, w_qkv, rope_cos, rope_sin, eps: float = 1e-6, 
 
 
 def wsattn_forward(plan: Plan, q, k, v, out=None, stream=None):
-    import torch
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check_shape(plan, t, n)
     if not (q.shape[0] == k.shape[0] == v.shape[0]):
@@ -365,7 +365,6 @@ def wsattn_prepare_static(q, k, out: dict, tau: float = 40.0, stream=None):
     """No-allocation prepare: statistics into the caller's tensors in `out`
     (keys b, m, mu, kmax, bmax, elig, shaped as wsattn_prepare_static_outputs
     makes them).  For callers that must not let the library allocate."""
-    import torch
     B, H, N, D = q.shape
     if k.shape != q.shape:
         raise ValueError("q and k shapes differ")
@@ -380,7 +379,6 @@ def wsattn_prepare_static(q, k, out: dict, tau: float = 40.0, stream=None):
 
 def wsattn_prepare_static_outputs(batch, heads, n_tokens, head_dim, device="cuda"):
     """Caller-owned output tensors for wsattn_prepare_static."""
-    import torch
     bh = batch * heads
     f = dict(dtype=torch.float32, device=device)
     return {"b": torch.empty(bh, n_tokens, **f), "m": torch.empty(bh, n_tokens, **f),
@@ -391,9 +389,14 @@ def wsattn_prepare_static_outputs(batch, heads, n_tokens, head_dim, device="cuda
 
 # ------------------------------------------------ operators around the attention
 
+_DTYPES = {} if torch is None else {torch.bfloat16: BF16, torch.float16: FP16,
+                                    torch.float32: FP32}
+# the raw handle of a device's current stream without a Stream object
+_raw_current_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 def _dtype_code(t, name, allowed=(BF16, FP16, FP32)):
-    import torch
-    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code not in allowed:
         raise TypeError(f"{name} must not be {t.dtype}")
     return code
@@ -401,14 +404,12 @@ def _dtype_code(t, name, allowed=(BF16, FP16, FP32)):
 
 def _device_of(t, name):
     """Index of the CUDA device a call's tensors live on, from its first one."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     return t.get_device()
 
 
 def _check_tensor(t, name, dev, dtype=None):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
@@ -420,28 +421,26 @@ def _check_tensor(t, name, dev, dtype=None):
 def _raw_stream(dev, stream):
     """The stream a call on tensors of device `dev` goes to (default: that
     device's current one)."""
-    import torch
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+        if _raw_current_stream is not None:
+            return _raw_current_stream(dev)
+        return torch.cuda.current_stream(dev).cuda_stream
     if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, dev, stream):
-    """Memory from `stream`'s own pool, so that its reuse is ordered with the
+def _empty(shape, dtype, like, stream):
+    """Memory on the device of `like`, from `stream`'s own pool, so that its reuse is ordered with the
     work the call enqueues there (and, in a capture, belongs to the graph)."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _run(dev, what, fn, *args):
     """The C call, with the tensors' device current."""
-    import torch
     if torch.cuda.current_device() == dev:
         rc = fn(*args)
     else:
@@ -531,7 +530,6 @@ def _head_view(t, name, shape, dtype, dev):
 
 def _positions(rot, t, batch, tokens, dev):
     """(pointer, batch stride) of the positions."""
-    import torch
     if t.dtype is not torch.float32 or t.get_device() != dev:
         _check_tensor(t, "positions", dev, torch.float32)
     axes, shape, st = rot.axes, t.shape, t.stride()
@@ -564,7 +562,7 @@ def wsattn_rotary(rot: RotaryPlan, x, positions, inverse: bool = False, out=None
     raw = _raw_stream(dev, stream)
     pos, pos_b = _positions(rot, positions, shape[0], shape[2], dev)
     if out is None:
-        out = _empty(shape, dt, dev, stream)
+        out = _empty(shape, dt, x, stream)
     _run(dev, "wsattn_rotary", _lib.wsattn_rotary, rot.handle, code, shape[0], shape[2],
          _head_view(x, "x", shape, dt, dev), pos, pos_b, 1 if inverse else 0,
          _head_view(out, "out", shape, dt, dev), raw)
@@ -573,7 +571,6 @@ def wsattn_rotary(rot: RotaryPlan, x, positions, inverse: bool = False, out=None
 
 def _gains(q_weight, k_weight, dim, dtype, code, dev):
     """Pointers of the gain vectors and their dtype code."""
-    import torch
     ptr, kind = [None, None], None
     for i, t in enumerate((q_weight, k_weight)):
         if t is None:
@@ -614,10 +611,10 @@ def wsattn_qknorm(rot: RotaryPlan, q, k, positions, q_weight=None, k_weight=None
     code, dt = _dtype_code(q, "q"), q.dtype
     wq, wk, wcode = _gains(q_weight, k_weight, rot.head_dim, dt, code, dev)
     pos, pos_b = _positions(rot, positions, sq[0], sq[2], dev)
-    q_out = _empty(sq, dt, dev, stream) if q_out is None else q_out
-    k_out = _empty(sk, dt, dev, stream) if k_out is None else k_out
+    q_out = _empty(sq, dt, q, stream) if q_out is None else q_out
+    k_out = _empty(sk, dt, q, stream) if k_out is None else k_out
     if v is not None and v_out is None:
-        v_out = _empty(sv, dt, dev, stream)
+        v_out = _empty(sv, dt, q, stream)
     _run(dev, "wsattn_qknorm", _lib.wsattn_qknorm, rot.handle, code, sq[0], sq[2],
          _head_view(q, "q", sq, dt, dev), _head_view(k, "k", sk, dt, dev),
          None if v is None else _head_view(v, "v", sv, dt, dev), wq, wk, wcode, eps, pos, pos_b,
@@ -646,7 +643,6 @@ def wsattn_qknorm_backward(rot: RotaryPlan, dq_out, dk_out, q, k, positions, q_w
     """Gradients of wsattn_qknorm: (dq, dk, dv, dq_weight, dk_weight).  dq, dk
     and dv may be views of one packed gradient (default: contiguous); dv is
     None without dv_out, and a gain's gradient (fp32 [D]) None without the gain."""
-    import torch
     dev = _device_of(q, "q")
     sq, sk, sv = _qkv_shapes(rot, q, k, dv_out)
     if dv_out is None and dv is not None:
@@ -655,14 +651,14 @@ def wsattn_qknorm_backward(rot: RotaryPlan, dq_out, dk_out, q, k, positions, q_w
     code, dt, dim = _dtype_code(q, "q"), q.dtype, rot.head_dim
     wq, wk, wcode = _gains(q_weight, k_weight, dim, dt, code, dev)
     pos, pos_b = _positions(rot, positions, sq[0], sq[2], dev)
-    dq = _empty(sq, dt, dev, stream) if dq is None else dq
-    dk = _empty(sk, dt, dev, stream) if dk is None else dk
+    dq = _empty(sq, dt, q, stream) if dq is None else dq
+    dk = _empty(sk, dt, q, stream) if dk is None else dk
     if dv_out is not None and dv is None:
-        dv = _empty(sv, dt, dev, stream)
-    dwq = None if wq is None else _empty((dim,), torch.float32, dev, stream)
-    dwk = None if wk is None else _empty((dim,), torch.float32, dev, stream)
+        dv = _empty(sv, dt, q, stream)
+    dwq = None if wq is None else _empty((dim,), torch.float32, q, stream)
+    dwk = None if wk is None else _empty((dim,), torch.float32, q, stream)
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = _empty((rot.backward_workspace,), torch.uint8, dev, stream)
+        workspace = _empty((rot.backward_workspace,), torch.uint8, q, stream)
     ws, ws_bytes = _scratch_args(workspace, dev)
     _run(dev, "wsattn_qknorm_backward", _lib.wsattn_qknorm_backward, rot.handle, code, sq[0],
          sq[2], _head_view(dq_out, "dq_out", sq, dt, dev),
@@ -712,21 +708,19 @@ def _activation(name):
     return code
 
 
-def _scratch(query, what, args, workspace, dev, stream):
+def _scratch(query, what, args, workspace, dev, like, stream):
     """(pointer, bytes, tensor) of a call's workspace, allocated when needed."""
-    import torch
     if workspace is None:
         n = _SZ()
         _run(dev, what, query, args, ctypes.byref(n))
         if not n.value:
             return None, 0, None
-        workspace = _empty((n.value,), torch.uint8, dev, stream)
+        workspace = _empty((n.value,), torch.uint8, like, stream)
     return *_scratch_args(workspace, dev), workspace
 
 
 def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, stream):
     """The packed wsattn_linear_args, the output and the device."""
-    import torch
     dev = _device_of(weight, "weight")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
@@ -756,7 +750,7 @@ def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, 
             raise ValueError(f"bias must be contiguous [{n}], got {list(bias.shape)}")
         bp = bias.data_ptr()
     if out is None:
-        out = _empty(lead + (n,), dt if out_dtype is None else out_dtype, dev, stream)
+        out = _empty(lead + (n,), dt if out_dtype is None else out_dtype, weight, stream)
     elif out_dtype not in (None, out.dtype):
         raise TypeError(f"out is {out.dtype}, not {out_dtype}")
     odt = out.dtype
@@ -782,7 +776,7 @@ def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact
                                   stream)
     raw = _raw_stream(dev, stream)
     ws, nbytes, _hold = _scratch(_lib.wsattn_linear_workspace, "wsattn_linear_workspace", args,
-                                 workspace, dev, stream)
+                                 workspace, dev, weight, stream)
     _run(dev, "wsattn_linear", _lib.wsattn_linear, args, ws, nbytes, raw)
     return out
 
@@ -799,7 +793,6 @@ def wsattn_linear_workspace(x, weight) -> int:
 def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need_dx, need_dw, need_db,
                       stream):
     """The packed wsattn_linear_grad_args, the gradients and the device."""
-    import torch
     dev = _device_of(weight, "weight")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
@@ -818,13 +811,13 @@ def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need_dx, 
     if preact is not None:
         ldp, pp = _rows(preact, "preact", n, lead, dt, dev), preact.data_ptr()
     if need_dx or dx is not None:
-        dx = _empty(x.shape, dt, dev, stream) if dx is None else dx
+        dx = _empty(x.shape, dt, weight, stream) if dx is None else dx
         lddx, dxp = _rows(dx, "dx", k, lead, dt, dev), dx.data_ptr()
     if need_dw or dw is not None:
-        dw = _empty((n, k), dt, dev, stream) if dw is None else dw
+        dw = _empty((n, k), dt, weight, stream) if dw is None else dw
         lddw, dwp = _rows(dw, "dw", k, (n,), dt, dev), dw.data_ptr()
     if need_db or db is not None:
-        db = _empty((n,), torch.float32, dev, stream) if db is None else db
+        db = _empty((n,), torch.float32, weight, stream) if db is None else db
         _check_tensor(db, "db", dev, torch.float32)
         if db.shape != (n,) or (n > 1 and db.stride(0) != 1):
             raise ValueError(f"db must be contiguous [{n}], got {list(db.shape)}")
@@ -845,7 +838,8 @@ def wsattn_linear_backward(dout, x, weight, preact=None, activation="none", dx=N
                                               need_dx, need_dw, need_db, stream)
     raw = _raw_stream(dev, stream)
     ws, nbytes, _hold = _scratch(_lib.wsattn_linear_backward_workspace,
-                                 "wsattn_linear_backward_workspace", args, workspace, dev, stream)
+                                 "wsattn_linear_backward_workspace", args, workspace, dev, weight,
+                                 stream)
     _run(dev, "wsattn_linear_backward", _lib.wsattn_linear_backward, args, ws, nbytes, raw)
     return dx, dw, db
 

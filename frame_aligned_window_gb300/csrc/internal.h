@@ -243,7 +243,7 @@ cudaError_t launch_timeout_selftest(long long limit_cycles, int* status, cudaStr
 // writing anything an earlier kernel may still read.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t stream, Args... args) {
+                             cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

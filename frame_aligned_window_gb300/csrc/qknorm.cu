@@ -135,12 +135,33 @@ __device__ __forceinline__ void store8(T* p, const float* f) {
   }
 }
 
-// The lane's place in its head row and the angles of its eight pairs.
+// The lane's place in its head row.
 struct Lane {
   int c;        // piece: elements [8c, 8c + 8) of each half of the head
   bool on;      // the lane holds a piece (D / 16 need not be a power of two)
   int half;     // D / 2
 };
+
+template <int LG>
+__device__ __forceinline__ Lane make_lane(const RotTable& t) {
+  Lane ln;
+  ln.c = threadIdx.x & ((1 << LG) - 1);
+  ln.half = t.pairs;
+  ln.on = 16 * ln.c < 2 * t.pairs;
+  return ln;
+}
+
+// Row (of B * N) -> batch element and token.
+__device__ __forceinline__ void split_row(const QkParams& p, int64_t row, int64_t& b, int64_t& n) {
+  if (p.rows <= INT32_MAX) {
+    const uint32_t q = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.tokens);
+    b = q;
+    n = static_cast<uint32_t>(row) - q * static_cast<uint32_t>(p.tokens);
+  } else {
+    b = row / p.tokens;
+    n = row - b * p.tokens;
+  }
+}
 
 // Pair i (0..7) of a lane: interleaved, pairs 4c .. 4c+3 of the first half
 // and D/4 + 4c .. of the second; split, pairs 8c .. 8c+7.
@@ -151,13 +172,18 @@ __device__ __forceinline__ int pair_index(const RotTable& t, const Lane& ln, int
 
 __device__ __forceinline__ void lane_angles(const RotTable& t, const Lane& ln, const float* pos,
                                             float sign, float (&cs)[8], float (&sn)[8]) {
+  float x[kRotMaxAxes];
+#pragma unroll
+  for (int a = 0; a < kRotMaxAxes; ++a) x[a] = a < t.axes ? pos[a] : 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int p = pair_index(t, ln, i);
-    const float x = pos[t.axis[p]];
-    const float hi = x * t.hi[p];
-    const float err = fmaf(x, t.hi[p], -hi);
-    const float frac = (hi - rintf(hi)) + fmaf(x, t.lo[p], err);
+    const int a = t.axis[p];
+    const float v = a < 2 ? (a == 0 ? x[0] : x[1]) : (a == 2 ? x[2] : x[3]);
+    const float w = t.hi[p];
+    const float hi = v * w;
+    const float err = fmaf(v, w, -hi);
+    const float frac = (hi - rintf(hi)) + fmaf(v, t.lo[p], err);
     float s, c;
     sincospif(2.f * frac, &s, &c);
     cs[i] = c;
@@ -185,9 +211,11 @@ __device__ __forceinline__ void turn16(float (&x)[16], const float (&cs)[8], con
   }
 }
 
-// Sum over the 2^lg lanes of a head row (every lane gets it).
-__device__ __forceinline__ float row_sum(float v, int lg) {
-  for (int o = 1 << lg >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sum over the 2^LG lanes of a head row (every lane gets it).
+template <int LG>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = 1 << LG >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -197,79 +225,136 @@ __device__ __forceinline__ void load_gain(const QkParams& p, const QkPart& part,
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = 1.f;
   if (!part.weight || !ln.on) return;
-  for (int i = 0; i < 16; ++i) {
-    const int e = (i < 8 ? 0 : ln.half) + 8 * ln.c + (i & 7);
-    w[i] = p.weight_f32 ? static_cast<const float*>(part.weight)[e]
-                        : static_cast<float>(static_cast<const T*>(part.weight)[e]);
+  if (p.weight_f32) {
+    const float* g = static_cast<const float*>(part.weight) + 8 * ln.c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = g[(i < 8 ? 0 : ln.half) + (i & 7)];
+  } else {
+    const T* g = static_cast<const T*>(part.weight) + 8 * ln.c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = static_cast<float>(g[(i < 8 ? 0 : ln.half) + (i & 7)]);
   }
 }
 
-// Heads whose loads are in flight together.
-template <typename T>
-constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
+template <bool VEC>
+__device__ __forceinline__ void store_raw8(float* p, const Half8<float>& r) {
+  float f[8];
+  unpack8(r, f);
+  store8<VEC>(p, f);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_raw8(T* p, const Half8<T>& r) {
+  if (VEC) {
+    *reinterpret_cast<uint4*>(p) = r.a;
+  } else {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    uint16_t* u = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[2 * i] = static_cast<uint16_t>(w[i]);
+      u[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+    }
+  }
+}
 
+// Copies a lane's share of `heads` head rows (v: neither norm nor turn).
 template <typename T, bool VEC>
+__device__ __forceinline__ void copy_heads(const T* src, int64_t sstep, T* dst, int64_t dstep,
+                                           int heads, int half) {
+  constexpr int U = sizeof(T) == 4 ? 2 : 4;
+  for (int h = 0; h < heads; h += U) {
+    Half8<T> r0[U], r1[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u < heads) {
+        r0[u] = load8<VEC>(src + u * sstep);
+        r1[u] = load8<VEC>(src + u * sstep + half);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u < heads) {
+        store_raw8<VEC>(dst + u * dstep, r0[u]);
+        store_raw8<VEC>(dst + u * dstep + half, r1[u]);
+      }
+    src += U * sstep;
+    dst += U * dstep;
+  }
+}
+
+// One warp: the heads of one group, each lane group for one token.
+template <typename T, bool VEC, int LG, bool NORM>
 __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_constant__ QkParams p) {
-  constexpr int U = kUnroll<T>;
-  const int lane = threadIdx.x & 31;
-  const int lg = p.lanes_log2;
-  Lane ln;
-  ln.c = lane & ((1 << lg) - 1);
-  ln.half = p.rot.pairs;
-  ln.on = 16 * ln.c < 2 * p.rot.pairs;
+  constexpr int U = sizeof(T) == 4 ? 2 : 4;  // heads whose loads are in flight together
+  const Lane ln = make_lane<LG>(p.rot);
   const int g = static_cast<int>(blockIdx.x % p.groups);
   const int64_t rb = blockIdx.x / p.groups;
-  const int per_warp = 32 >> lg;
-  const int64_t row = (rb * (kQkThreads / 32) + threadIdx.x / 32) * per_warp + (lane >> lg);
+  constexpr int kPerWarp = 32 >> LG;
+  const int64_t row =
+      (rb * (kQkThreads / 32) + threadIdx.x / 32) * kPerWarp + ((threadIdx.x & 31) >> LG);
   const bool active = row < p.rows && ln.on;
   int pi = 0;
   while (pi + 1 < p.parts && g >= p.part[pi + 1].group0) ++pi;
   const QkPart& part = p.part[pi];
   const int h0 = (g - part.group0) * p.group_heads;
-  const int h1 = min(part.io.heads, h0 + p.group_heads);
-  const int64_t b = active ? row / p.tokens : 0, n = active ? row - b * p.tokens : 0;
-  const T* src = static_cast<const T*>(part.io.in) + b * part.io.ib + n * part.io.in_ + 8 * ln.c;
-  T* dst = static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on + 8 * ln.c;
-
-  float cs[8], sn[8], w[16];
-  if (part.turn && active)
-    lane_angles(p.rot, ln, p.pos + b * p.pos_b + n * p.rot.axes, static_cast<float>(part.turn), cs,
-                sn);
-  load_gain<T>(p, part, ln, w);
-  const float inv_d = 0.5f / static_cast<float>(p.rot.pairs);
-
-  for (int h = h0; h < h1; h += U) {
-    Half8<T> r0[U], r1[U];
+  const int heads = min(part.io.heads - h0, p.group_heads);
+  int64_t b = 0, n = 0;
+  if (active) split_row(p, row, b, n);
+  const int64_t sstep = part.io.ih, dstep = part.io.oh;
+  const T* src = static_cast<const T*>(part.io.in) + b * part.io.ib + n * part.io.in_ + h0 * sstep +
+                 8 * ln.c;
+  T* dst =
+      static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on + h0 * dstep + 8 * ln.c;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!part.turn) {
+    if (active) copy_heads<T, VEC>(src, sstep, dst, dstep, heads, ln.half);
+    return;
+  }
+  // the first loads go out before the angles are formed
+  Half8<T> r0[U], r1[U];
+  auto load = [&](int left) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (active && h + u < h1) {
-        const T* q = src + (h + u) * part.io.ih;
-        r0[u] = load8<VEC>(q);
-        r1[u] = load8<VEC>(q + ln.half);
+      if (active && u < left) {
+        r0[u] = load8<VEC>(src + u * sstep);
+        r1[u] = load8<VEC>(src + u * sstep + ln.half);
       } else {
         r0[u] = Half8<T>{};
         r1[u] = Half8<T>{};
       }
+  };
+  load(heads);
+  float cs[8], sn[8], w[16];
+  if (active)
+    lane_angles(p.rot, ln, p.pos + b * p.pos_b + n * p.rot.axes, static_cast<float>(part.turn), cs,
+                sn);
+  if (NORM) load_gain<T>(p, part, ln, w);
+  const float inv_d = 0.5f / static_cast<float>(p.rot.pairs);
+  const bool inter = p.rot.interleaved != 0;
+
+  for (int h = 0; h < heads; h += U) {
+    if (h > 0) load(heads - h);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float x[16];
       unpack8(r0[u], x);
       unpack8(r1[u], x + 8);
-      if (part.norm) {
+      if (NORM) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-        const float r = 1.f / sqrtf(fmaf(row_sum(ss, lg), inv_d, p.eps));
+        const float r = rsqrtf(fmaf(row_sum<LG>(ss), inv_d, p.eps));
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] *= r * w[i];
       }
-      if (part.turn) turn16(x, cs, sn, p.rot.interleaved != 0);
-      if (active && h + u < h1) {
-        T* q = dst + (h + u) * part.io.oh;
-        store8<VEC>(q, x);
-        store8<VEC>(q + ln.half, x + 8);
+      turn16(x, cs, sn, inter);
+      if (active && u < heads - h) {
+        store8<VEC>(dst + u * dstep, x);
+        store8<VEC>(dst + u * dstep + ln.half, x + 8);
       }
     }
+    src += U * sstep;
+    dst += U * dstep;
   }
 }
 
@@ -278,31 +363,84 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
 // contiguous share; then the same for v's copies.  A CTA's share of the gain
 // gradients stays in registers until its part changes, and one partial row
 // per CTA and part goes to global memory: the sums have a fixed order.
-template <typename T, bool VEC>
+//
+// A head row takes about 300 instructions here and 128 registers a thread
+// hold little beside its sums, gains and angles, so loads in registers would
+// leave too few bytes in flight: the rows come through a ring of cp.async
+// stages in shared memory, one head row a stage and lane group, that runs
+// ahead across the items (each lane reads what it loaded: no barrier).
+template <typename T>
+constexpr int kBackStages = sizeof(T) == 4 ? 3 : 5;
+template <typename T>
+constexpr int kBackStageBytes = 32 * 32 * static_cast<int>(sizeof(T));  // a warp's x and dy rows
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where a warp is in its list of items: the item, and the head within it.
+struct BackCursor {
+  int64_t rb;     // row block
+  int64_t left;   // items from here on, this one included
+  int g, pi;      // head group, part
+  int h, heads;   // head within the group, heads of the group
+  int64_t b, n;   // this lane group's token
+  bool active;
+};
+
+template <int LG>
+__device__ __forceinline__ void open_item(const QkParams& p, const Lane& ln, BackCursor& c) {
+  while (c.pi == 0 && c.g >= p.part[1].group0) c.pi = 1;
+  const QkPart& part = p.part[c.pi];
+  c.h = 0;
+  c.heads = min(part.io.heads - (c.g - part.group0) * p.group_heads, p.group_heads);
+  const int64_t row = (c.rb * (kQkThreads / 32) + threadIdx.x / 32) * (32 >> LG) +
+                      ((threadIdx.x & 31) >> LG);
+  c.active = row < p.rows && ln.on;
+  c.b = c.n = 0;
+  if (c.active) split_row(p, row, c.b, c.n);
+}
+__device__ __forceinline__ void next_item(const QkParams& p, BackCursor& c) {
+  --c.left;
+  if (++c.rb == p.row_blocks) {
+    c.rb = 0;
+    ++c.g;
+  }
+}
+
+template <typename T, bool VEC, int LG>
 __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
     qk_backward_kernel(const __grid_constant__ QkParams p) {
-  constexpr int U = sizeof(T) == 4 ? 1 : 2;
-  __shared__ float red[kQkThreads / 32][2 * kRotMaxPairs];
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  constexpr int kStages = kBackStages<T>, kBytes = kBackStageBytes<T>;
+  constexpr int kPieces = sizeof(T) / 2;  // 16-byte pieces of 8 elements
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int lg = p.lanes_log2;
-  Lane ln;
-  ln.c = lane & ((1 << lg) - 1);
-  ln.half = p.rot.pairs;
-  ln.on = 16 * ln.c < 2 * p.rot.pairs;
-  const int per_warp = 32 >> lg;
+  const Lane ln = make_lane<LG>(p.rot);
   const float inv_d = 0.5f / static_cast<float>(p.rot.pairs);
+  const bool inter = p.rot.interleaved != 0;
   const int D = 2 * p.rot.pairs;
+  // stage: 16-byte pieces [dy 0, dy 1, x 0, x 1][lane] (twice as many in fp32)
+  const uint32_t ring = smem_u32(ring_raw) + static_cast<uint32_t>(warp * kStages * kBytes + 16 * lane);
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 
   // adds the CTA's gain gradient of part pi and writes its partial row
+  __shared__ float red[kQkThreads / 32][2 * kRotMaxPairs];
   auto flush = [&](int pi) {
-    if (!p.dw_part || pi > 1) return;
+    if (!p.dw_part) return;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      for (int o = 1 << lg; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (lane < (1 << lg) && ln.on) red[warp][(i < 8 ? 0 : ln.half) + 8 * ln.c + (i & 7)] = acc[i];
+#pragma unroll
+      for (int o = 1 << LG; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      if (lane < (1 << LG) && ln.on) red[warp][(i < 8 ? 0 : ln.half) + 8 * ln.c + (i & 7)] = acc[i];
       acc[i] = 0.f;
     }
     __syncthreads();
@@ -314,94 +452,168 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
     }
     __syncthreads();
   };
-
-  // the groups of parts [a, z) share the work of one pass over the list
-  auto pass = [&](int a, int z) {
+  // first and last item of this CTA in the list of parts [a, z)
+  auto share = [&](int a, int z, int64_t& i0, int64_t& i1) {
     const int g0 = p.part[a].group0;
-    const int64_t items = static_cast<int64_t>(p.part[z - 1].group0 + p.part[z - 1].groups - g0) *
-                          p.row_blocks;
-    const int64_t i1 = items * (blockIdx.x + 1) / gridDim.x;
-    int64_t i = items * blockIdx.x / gridDim.x;
-    int pi = a;
-    float w[16];
-    bool have_w = false;
-    for (; i < i1; ++i) {
-      const int g = g0 + static_cast<int>(i / p.row_blocks);
-      const int64_t rb = i % p.row_blocks;
-      while (pi + 1 < z && g >= p.part[pi + 1].group0) {
-        flush(pi++);
-        have_w = false;
+    const int64_t items =
+        static_cast<int64_t>(p.part[z - 1].group0 + p.part[z - 1].groups - g0) * p.row_blocks;
+    i0 = items * blockIdx.x / gridDim.x;
+    i1 = items * (blockIdx.x + 1) / gridDim.x;
+  };
+
+  griddep_wait();
+  griddep_launch_dependents();
+  int64_t i, i1;
+  share(0, 2, i, i1);
+  int g = static_cast<int>(i / p.row_blocks);
+  int64_t rb = i - g * p.row_blocks;
+  int done_part = 0;
+  if (i < i1) {
+    BackCursor cur;
+    cur.g = g;
+    cur.rb = rb;
+    cur.left = i1 - i;
+    cur.pi = 0;
+    BackCursor ahead = cur;
+    const T* gy = nullptr;  // the next head row to load (the ring) or to use (plain loads)
+    const T* xs = nullptr;
+    auto open_ahead = [&] {
+      open_item<LG>(p, ln, ahead);
+      const QkPart& part = p.part[ahead.pi];
+      const int64_t h0 = static_cast<int64_t>(ahead.g - part.group0) * p.group_heads;
+      gy = static_cast<const T*>(part.io.in) + ahead.b * part.io.ib + ahead.n * part.io.in_ +
+           h0 * part.io.ih + 8 * ln.c;
+      xs = static_cast<const T*>(part.x) + ahead.b * part.xb + ahead.n * part.xn + h0 * part.xh +
+           8 * ln.c;
+    };
+    auto step_ahead = [&] {
+      const QkPart& part = p.part[ahead.pi];
+      gy += part.io.ih;
+      xs += part.xh;
+      if (++ahead.h == ahead.heads) {
+        next_item(p, ahead);
+        if (ahead.left > 0) open_ahead();
       }
-      const QkPart& part = p.part[pi];
-      if (!have_w) load_gain<T>(p, part, ln, w);
-      have_w = true;
-      const int h0 = (g - part.group0) * p.group_heads;
-      const int h1 = min(part.io.heads, h0 + p.group_heads);
-      const int64_t row = (rb * (kQkThreads / 32) + warp) * per_warp + (lane >> lg);
-      const bool active = row < p.rows && ln.on;
-      const int64_t b = active ? row / p.tokens : 0, n = active ? row - b * p.tokens : 0;
-      const T* gy = static_cast<const T*>(part.io.in) + b * part.io.ib + n * part.io.in_ + 8 * ln.c;
-      const T* xs = static_cast<const T*>(part.x) + b * part.xb + n * part.xn + 8 * ln.c;
-      T* dx = static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on + 8 * ln.c;
+    };
+    uint32_t load_slot = 0;
+    auto issue = [&] {
+      if (ahead.left > 0) {
+        if (ahead.active) {
+          const uint32_t d = ring + load_slot * kBytes;
+#pragma unroll
+          for (int q = 0; q < kPieces; ++q) {
+            const int e = q * 4;  // fp32: the second 16 bytes of 8 elements
+            cp_async16(d + (0 + q) * 512, gy + e);
+            cp_async16(d + (kPieces + q) * 512, gy + ln.half + e);
+            cp_async16(d + (2 * kPieces + q) * 512, xs + e);
+            cp_async16(d + (3 * kPieces + q) * 512, xs + ln.half + e);
+          }
+        }
+        step_ahead();
+      }
+      cp_async_commit();
+      if (++load_slot == kStages) load_slot = 0;
+    };
+    open_ahead();
+    if (VEC)
+      for (int k = 0; k < kStages - 1; ++k) issue();
+    uint32_t slot = 0;
+    float w[16];
+    int w_part = -1;
+    for (; cur.left > 0; next_item(p, cur)) {
+      open_item<LG>(p, ln, cur);
+      const QkPart& part = p.part[cur.pi];
+      if (w_part != cur.pi) {
+        for (; done_part < cur.pi; ++done_part) flush(done_part);
+        load_gain<T>(p, part, ln, w);
+        w_part = cur.pi;
+      }
+      const int64_t dstep = part.io.oh;
+      T* dx = static_cast<T*>(part.io.out) + cur.b * part.io.ob + cur.n * part.io.on +
+              static_cast<int64_t>(cur.g - part.group0) * p.group_heads * dstep + 8 * ln.c;
       // idle lanes hold zeros and join the row sums: no turn there
       float cs[8] = {}, sn[8] = {};
-      if (part.turn && active)
-        lane_angles(p.rot, ln, p.pos + b * p.pos_b + n * p.rot.axes,
-                    static_cast<float>(part.turn), cs, sn);
-      for (int h = h0; h < h1; h += U) {
-        Half8<T> g0r[U], g1r[U], x0r[U], x1r[U];
+      if (cur.active)
+        lane_angles(p.rot, ln, p.pos + cur.b * p.pos_b + cur.n * p.rot.axes, -1.f, cs, sn);
+      for (; cur.h < cur.heads; ++cur.h) {
+        float gr[16], x[16];
+        if (VEC) {
+          issue();
+          cp_async_wait<kStages - 1>();
+          const uint32_t d = ring + slot * kBytes;
+          if (++slot == kStages) slot = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool on = active && h + u < h1;
-          g0r[u] = on ? load8<VEC>(gy + (h + u) * part.io.ih) : Half8<T>{};
-          g1r[u] = on ? load8<VEC>(gy + (h + u) * part.io.ih + ln.half) : Half8<T>{};
-          if (part.norm) {
-            x0r[u] = on ? load8<VEC>(xs + (h + u) * part.xh) : Half8<T>{};
-            x1r[u] = on ? load8<VEC>(xs + (h + u) * part.xh + ln.half) : Half8<T>{};
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool on = active && h + u < h1;
-          float gr[16];
-          unpack8(g0r[u], gr);
-          unpack8(g1r[u], gr + 8);
-          if (part.turn) turn16(gr, cs, sn, p.rot.interleaved != 0);
-          if (part.norm) {
-            float x[16];
-            unpack8(x0r[u], x);
-            unpack8(x1r[u], x + 8);
-            float ss = 0.f, dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              ss = fmaf(x[i], x[i], ss);
-              dot = fmaf(gr[i] * w[i], x[i], dot);
+          for (int q = 0; q < 2; ++q) {
+            Half8<T> a, c;
+            a.a = ld_shared_v4(d + q * kPieces * 512);
+            c.a = ld_shared_v4(d + (2 + q) * kPieces * 512);
+            if constexpr (sizeof(T) == 4) {
+              a.b = ld_shared_v4(d + (q * kPieces + 1) * 512);
+              c.b = ld_shared_v4(d + ((2 + q) * kPieces + 1) * 512);
             }
-            // idle lanes and rows hold zeros; an all-zero row keeps r finite
-            // through eps, and with eps = 0 its own NaN stays its own
-            const float r = 1.f / sqrtf(fmaf(row_sum(ss, lg), inv_d, p.eps));
-            const float m = row_sum(dot, lg) * inv_d * r * r;
-            if (on) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                acc[i] = fmaf(gr[i], x[i] * r, acc[i]);
-                gr[i] = r * fmaf(-x[i], m, gr[i] * w[i]);
-              }
-            }
+            unpack8(a, gr + 8 * q);
+            unpack8(c, x + 8 * q);
           }
-          if (on) {
-            store8<VEC>(dx + (h + u) * part.io.oh, gr);
-            store8<VEC>(dx + (h + u) * part.io.oh + ln.half, gr + 8);
-          }
+        } else if (cur.active) {
+          unpack8(load8<false>(gy), gr);
+          unpack8(load8<false>(gy + ln.half), gr + 8);
+          unpack8(load8<false>(xs), x);
+          unpack8(load8<false>(xs + ln.half), x + 8);
         }
+        if (!VEC) step_ahead();
+        if (!cur.active) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) gr[e] = x[e] = 0.f;
+        }
+        turn16(gr, cs, sn, inter);
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          ss = fmaf(x[e], x[e], ss);
+          dot = fmaf(gr[e] * w[e], x[e], dot);
+        }
+        const float r = rsqrtf(fmaf(row_sum<LG>(ss), inv_d, p.eps));
+        const float m = row_sum<LG>(dot) * inv_d * r * r;
+        if (cur.active) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            acc[e] = fmaf(gr[e], x[e] * r, acc[e]);
+            gr[e] = r * fmaf(-x[e], m, gr[e] * w[e]);
+          }
+          store8<VEC>(dx, gr);
+          store8<VEC>(dx + ln.half, gr + 8);
+        }
+        dx += dstep;
       }
     }
-    // partial rows of the parts this CTA did not reach are zero
-    for (; pi < z; ++pi) flush(pi);
-  };
-  griddep_launch_dependents();
-  pass(0, 2);
-  if (p.parts > 2) pass(2, 3);
+  }
+  // partial rows of the parts this CTA did not reach are zero
+  for (; done_part < 2; ++done_part) flush(done_part);
+  if (p.parts < 3) return;
+
+  const QkPart& part = p.part[2];
+  share(2, 3, i, i1);
+  g = static_cast<int>(i / p.row_blocks);
+  rb = i - g * p.row_blocks;
+  for (; i < i1; ++i) {
+    const int h0 = g * p.group_heads;
+    const int heads = min(part.io.heads - h0, p.group_heads);
+    const int64_t row = (rb * (kQkThreads / 32) + warp) * (32 >> LG) + (lane >> LG);
+    if (row < p.rows && ln.on) {
+      int64_t b, n;
+      split_row(p, row, b, n);
+      copy_heads<T, VEC>(static_cast<const T*>(part.io.in) + b * part.io.ib + n * part.io.in_ +
+                             h0 * part.io.ih + 8 * ln.c,
+                         part.io.ih,
+                         static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on +
+                             h0 * part.io.oh + 8 * ln.c,
+                         part.io.oh, heads, ln.half);
+    }
+    if (++rb == p.row_blocks) {
+      rb = 0;
+      ++g;
+    }
+  }
 }
 
 // Gain gradients from the partial rows: CTA (x, y) takes 32 columns of part
@@ -425,24 +637,52 @@ __global__ void __launch_bounds__(1024) qk_reduce_gain(const float* __restrict__
   }
 }
 
+template <typename T, bool VEC, int LG>
+cudaError_t forward_lg(const QkParams& p, unsigned grid, cudaStream_t s) {
+  return p.part[0].norm
+             ? launch_dependent(qk_forward_kernel<T, VEC, LG, true>, dim3(grid), dim3(kQkThreads),
+                                0, s, p)
+             : launch_dependent(qk_forward_kernel<T, VEC, LG, false>, dim3(grid), dim3(kQkThreads),
+                                0, s, p);
+}
+template <typename T, bool VEC, int LG>
+cudaError_t backward_lg(const QkParams& p, unsigned grid, cudaStream_t s) {
+  static bool attr_set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  constexpr int kSmem = VEC ? kQkThreads / 32 * kBackStages<T> * kBackStageBytes<T> : 0;
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(qk_backward_kernel<T, VEC, LG>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  return launch_dependent(qk_backward_kernel<T, VEC, LG>, dim3(grid), dim3(kQkThreads), kSmem, s, p);
+}
+
+// Calls F<T, VEC, LG> for the lanes of a head row.
+#define WSATTN_BY_LANES(F, T, VEC)                  \
+  switch (p.lanes_log2) {                           \
+    case 0: return F<T, VEC, 0>(p, grid, s);        \
+    case 1: return F<T, VEC, 1>(p, grid, s);        \
+    case 2: return F<T, VEC, 2>(p, grid, s);        \
+    case 3: return F<T, VEC, 3>(p, grid, s);        \
+    default: return F<T, VEC, 4>(p, grid, s);       \
+  }
+
 template <typename T>
 cudaError_t forward_t(const QkParams& p, bool vec, cudaStream_t s) {
-  const int64_t grid = p.row_blocks * p.groups;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  if (vec)
-    qk_forward_kernel<T, true><<<static_cast<unsigned>(grid), kQkThreads, 0, s>>>(p);
-  else
-    qk_forward_kernel<T, false><<<static_cast<unsigned>(grid), kQkThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const int64_t blocks = p.row_blocks * p.groups;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (vec) WSATTN_BY_LANES(forward_lg, T, true)
+  WSATTN_BY_LANES(forward_lg, T, false)
 }
 
 template <typename T>
-cudaError_t backward_t(const QkParams& p, bool vec, int blocks, cudaStream_t s) {
-  if (vec)
-    qk_backward_kernel<T, true><<<blocks, kQkThreads, 0, s>>>(p);
-  else
-    qk_backward_kernel<T, false><<<blocks, kQkThreads, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t backward_t(const QkParams& p, bool vec, unsigned grid, cudaStream_t s) {
+  if (vec) WSATTN_BY_LANES(backward_lg, T, true)
+  WSATTN_BY_LANES(backward_lg, T, false)
 }
 
 }  // namespace
@@ -457,11 +697,11 @@ cudaError_t launch_qk_backward(const QkParams& p, int dtype, bool vec, int block
                                float* dwk, cudaStream_t s) {
   cudaError_t e;
   if (dtype == WSATTN_BF16)
-    e = backward_t<__nv_bfloat16>(p, vec, blocks, s);
+    e = backward_t<__nv_bfloat16>(p, vec, static_cast<unsigned>(blocks), s);
   else if (dtype == WSATTN_FP16)
-    e = backward_t<__half>(p, vec, blocks, s);
+    e = backward_t<__half>(p, vec, static_cast<unsigned>(blocks), s);
   else
-    e = backward_t<float>(p, vec, blocks, s);
+    e = backward_t<float>(p, vec, static_cast<unsigned>(blocks), s);
   if (e != cudaSuccess || !p.dw_part) return e;
   const int D = 2 * p.rot.pairs;
   return launch_dependent(qk_reduce_gain, dim3((D + 31) / 32, 2), dim3(32, 32), 0, s,
