@@ -176,12 +176,10 @@ struct Product {
   int act;
 };
 
-int run_product(const Product& g, int sms, cudaStream_t s) {
-  GemmParams prm;
-  std::memset(&prm, 0, sizeof(prm));
-  prm.status = wsattn::op_status_ptr();
-  if (!prm.status) return WSATTN_ERR_CUDA;
-  const wsattn::GemmShape shape = wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, sms);
+// The kernel's parameters for one product under a tiling; false: a tensor
+// map could not be made, or the sizes exceed an int's range of tiles.
+bool fill(const Product& g, const wsattn::GemmShape& shape, GemmParams* out) {
+  GemmParams& prm = *out;
   const CUtensorMapDataType type = g.dtype == WSATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int esize = g.out_f32 ? 4 : 2;
@@ -192,7 +190,9 @@ int run_product(const Product& g, int sms, cudaStream_t s) {
               : encode(m, type, 2, o.ptr, g.K, own, o.ld, wsattn::kGemmK, box);
   };
   if (!operand(&prm.tm_p, g.p, g.p_mn, g.R, rows_p) || !operand(&prm.tm_q, g.q, g.q_mn, g.C, rows_q))
-    return WSATTN_ERR_CUDA;
+    return false;
+  prm.status = wsattn::op_status_ptr();
+  if (!prm.status) return false;
   prm.R = g.R;
   prm.C = g.C;
   prm.K = g.K;
@@ -210,27 +210,73 @@ int run_product(const Product& g, int sms, cudaStream_t s) {
   prm.res_vec = g.res && rows_vec(g.res, g.ldr, g.R, g.C, esize);
   prm.out_vec = tma_rows(g.out, g.out_f32 ? 2 * g.ldo : g.ldo, g.R);
   prm.pre_vec = g.pre && tma_rows(g.pre, g.ldp, g.R);
-  cudaError_t e;
+  int64_t tr, tc;
   if (shape.pair_cols) {
-    prm.tiles_r = static_cast<int>(cdiv(g.R, wsattn::kPairRows));
-    prm.tiles_c = static_cast<int>(cdiv(g.C, shape.pair_cols));
-    if (static_cast<int64_t>(prm.tiles_r) * prm.tiles_c > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+    tr = cdiv(g.R, wsattn::kPairRows);
+    tc = cdiv(g.C, shape.pair_cols);
     if (prm.out_vec && !encode(&prm.tm_out, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, esize,
                                g.out, g.C, g.R, g.ldo, 128 / esize, 32))
-      return WSATTN_ERR_CUDA;
+      return false;
     if (prm.pre_vec && !g.out_f32 && !encode(&prm.tm_pre, type, 2, g.pre, g.C, g.R, g.ldp, 64, 32))
-      return WSATTN_ERR_CUDA;
-    e = wsattn::launch_gemm_pair(prm, g.dtype, g.out_f32, shape.pair_cols, sms, s);
+      return false;
   } else {
-    prm.tiles_r = static_cast<int>(cdiv(g.R, shape.bn));
-    prm.tiles_c = static_cast<int>(cdiv(g.C, wsattn::kTileCols));
+    tr = cdiv(g.R, shape.bn);
+    tc = cdiv(g.C, wsattn::kTileCols);
     prm.bn = shape.bn;
     prm.split = shape.split;
     // a ring of about 96 KB: two CTAs fit an SM
     prm.stages = 96 / (16 + shape.bn / 8);
-    e = wsattn::launch_gemm_tile(prm, g.dtype, g.out_f32, s);
   }
+  prm.tiles_r = static_cast<int>(tr);
+  prm.tiles_c = static_cast<int>(tc);
+  return tr * tc <= INT32_MAX;
+}
+
+int run_product(const Product& g, int sms, cudaStream_t s) {
+  double ns = 0.0;
+  const wsattn::GemmShape shape = wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, sms, &ns);
+  wsattn::PairParams pp;
+  std::memset(&pp, 0, sizeof(pp));
+  if (!fill(g, shape, &pp.g[0])) return WSATTN_ERR_CUDA;
+  const cudaError_t e =
+      shape.pair_cols ? wsattn::launch_gemm_pair(&pp, g.dtype, g.out_f32, shape.pair_cols, sms, s)
+                      : wsattn::launch_gemm_tile(pp.g[0], g.dtype, g.out_f32, s);
   return e == cudaSuccess ? WSATTN_OK : WSATTN_ERR_CUDA;
+}
+
+// Two products of the same types, in one launch where that is expected to be
+// the faster way.
+int run_two_products(const Product& g, const Product& h, int sms, cudaStream_t s) {
+  double ng = 0.0, nh = 0.0;
+  wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, sms, &ng);
+  wsattn::choose_gemm(h.R, h.C, h.K, h.p_mn, sms, &nh);
+  const double both = wsattn::pair_time_of_two(g.R, g.C, g.K, h.R, h.C, h.K, sms);
+  if (both > ng + nh) {
+    const int rc = run_product(g, sms, s);
+    return rc == WSATTN_OK ? run_product(h, sms, s) : rc;
+  }
+  const wsattn::GemmShape shape{256, 0, 1};
+  const bool g_first = g.K >= h.K;
+  wsattn::PairParams pp;
+  std::memset(&pp, 0, sizeof(pp));
+  if (!fill(g_first ? g : h, shape, &pp.g[0]) || !fill(g_first ? h : g, shape, &pp.g[1]))
+    return WSATTN_ERR_CUDA;
+  return wsattn::launch_gemm_pair(&pp, g.dtype, g.out_f32, 256, sms, s) == cudaSuccess
+             ? WSATTN_OK
+             : WSATTN_ERR_CUDA;
+}
+
+// A job of the pack pass (rows = 0: none).
+wsattn::PackJob pack_job(const void* src, int64_t lds, int64_t rows, int cols, void* dst) {
+  wsattn::PackJob j;
+  std::memset(&j, 0, sizeof(j));
+  j.src = src;
+  j.lds = lds;
+  j.rows = rows;
+  j.cols = cols;
+  j.dst = dst;
+  j.ldd = round8(cols);
+  return j;
 }
 
 // Scratch of one operand copied to aligned rows.
@@ -547,19 +593,19 @@ int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace
   g.out_f32 = a->out_dtype == WSATTN_FP32;
   g.p = Operand{a->x, a->ldx};
   g.q = Operand{a->w, a->ldw};
+  wsattn::PackJob jx = pack_job(nullptr, 0, 0, 8, nullptr), jw = jx;
   if (a->x_heads > 0 || !tma_rows(a->x, a->ldx, a->m)) {
-    if (wsattn::launch_pack(a->dtype, a->x, a->ldx, a->m, a->k, ws, round8(a->k), a->x_heads,
-                            a->x_tokens, s) != cudaSuccess)
-      return WSATTN_ERR_CUDA;
-    g.p = Operand{ws, round8(a->k)};
+    jx = pack_job(a->x, a->ldx, a->m, a->k, ws);
+    jx.f32_heads = a->x_heads;
+    jx.tokens = a->x_tokens;
+    g.p = Operand{ws, jx.ldd};
     ws += packed_bytes(a->m, a->k);
   }
   if (!tma_rows(a->w, a->ldw, a->n)) {
-    if (wsattn::launch_pack(a->dtype, a->w, a->ldw, a->n, a->k, ws, round8(a->k), 0, 0, s) !=
-        cudaSuccess)
-      return WSATTN_ERR_CUDA;
-    g.q = Operand{ws, round8(a->k)};
+    jw = pack_job(a->w, a->ldw, a->n, a->k, ws);
+    g.q = Operand{ws, jw.ldd};
   }
+  if (wsattn::launch_pack(a->dtype, jx, jw, s) != cudaSuccess) return WSATTN_ERR_CUDA;
   g.R = a->m;
   g.C = a->n;
   g.K = a->k;
@@ -633,47 +679,42 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
     if (wsattn::launch_dact(d, a->dtype, a->db, s) != cudaSuccess) return WSATTN_ERR_CUDA;
     if (plan.dz) dz = Operand{ws_dz, d.ldz};
   }
+  wsattn::PackJob jx = pack_job(nullptr, 0, 0, 8, nullptr), jw = jx;
   if (plan.pack_x) {
-    if (wsattn::launch_pack(a->dtype, a->x, a->ldx, a->m, a->k, ws_x, round8(a->k), 0, 0, s) !=
-        cudaSuccess)
-      return WSATTN_ERR_CUDA;
-    x = Operand{ws_x, round8(a->k)};
+    jx = pack_job(a->x, a->ldx, a->m, a->k, ws_x);
+    x = Operand{ws_x, jx.ldd};
   }
   if (plan.pack_w) {
-    if (wsattn::launch_pack(a->dtype, a->w, a->ldw, a->n, a->k, ws_w, round8(a->k), 0, 0, s) !=
-        cudaSuccess)
-      return WSATTN_ERR_CUDA;
-    w = Operand{ws_w, round8(a->k)};
+    jw = pack_job(a->w, a->ldw, a->n, a->k, ws_w);
+    w = Operand{ws_w, jw.ldd};
   }
-  Product g;
-  std::memset(&g, 0, sizeof(g));
-  g.dtype = a->dtype;
-  if (a->dw) {  // dw[n, k] = sum over rows of dz[., n] x[., k]
-    g.p = dz;
-    g.p_mn = true;
-    g.q = x;
-    g.q_mn = true;
-    g.R = a->n;
-    g.C = a->k;
-    g.K = static_cast<int>(a->m);
-    g.out = a->dw;
-    g.ldo = a->lddw;
-    const int rc = run_product(g, sms, s);
-    if (rc != WSATTN_OK) return rc;
-  }
-  if (a->dx) {  // dx[m, k] = sum over features of dz[m, .] w[., k]
-    g.p = dz;
-    g.p_mn = false;
-    g.q = w;
-    g.q_mn = true;
-    g.R = a->m;
-    g.C = a->k;
-    g.K = a->n;
-    g.out = a->dx;
-    g.ldo = a->lddx;
-    const int rc = run_product(g, sms, s);
-    if (rc != WSATTN_OK) return rc;
-  }
+  if (wsattn::launch_pack(a->dtype, jx, jw, s) != cudaSuccess) return WSATTN_ERR_CUDA;
+  Product gw, gx;
+  std::memset(&gw, 0, sizeof(gw));
+  gw.dtype = a->dtype;
+  gx = gw;
+  // dw[n, k] = sum over rows of dz[., n] x[., k]
+  gw.p = dz;
+  gw.p_mn = true;
+  gw.q = x;
+  gw.q_mn = true;
+  gw.R = a->n;
+  gw.C = a->k;
+  gw.K = static_cast<int>(a->m);
+  gw.out = a->dw;
+  gw.ldo = a->lddw;
+  // dx[m, k] = sum over features of dz[m, .] w[., k]
+  gx.p = dz;
+  gx.q = w;
+  gx.q_mn = true;
+  gx.R = a->m;
+  gx.C = a->k;
+  gx.K = a->n;
+  gx.out = a->dx;
+  gx.ldo = a->lddx;
+  if (a->dw && a->dx) return run_two_products(gw, gx, sms, s);
+  if (a->dw) return run_product(gw, sms, s);
+  if (a->dx) return run_product(gx, sms, s);
   return WSATTN_OK;
 }
 

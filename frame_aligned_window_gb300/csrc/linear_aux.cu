@@ -9,41 +9,50 @@
 namespace wsattn {
 namespace {
 
-// 8 values a thread.  Reads element by element: the sources of this pass are
+using namespace ptx;
+
+// 8 values a thread, read element by element: the sources of this pass are
 // those whose rows start on no common boundary.
-template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ src, int64_t lds,
-                                                   int64_t rows, int cols, T* __restrict__ dst,
-                                                   int64_t ldd) {
-  const int64_t per = ldd / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= rows * per) return;
-  const int64_t r = i / per;
+__device__ __forceinline__ void pack_rows(const PackJob& j, int64_t i) {
+  const int64_t per = j.ldd / 8, r = i / per;
+  if (r >= j.rows) return;
   const int c = static_cast<int>(i - r * per) * 8;
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(src) + r * lds + c;
+  const uint16_t* q = static_cast<const uint16_t*>(j.src) + r * j.lds + c;
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    w[e] = (c + 2 * e < cols ? q[2 * e] : 0u) | (c + 2 * e + 1 < cols ? q[2 * e + 1] : 0u) << 16;
-  *reinterpret_cast<uint4*>(dst + r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    w[e] = (c + 2 * e < j.cols ? q[2 * e] : 0u) | (c + 2 * e + 1 < j.cols ? q[2 * e + 1] : 0u) << 16;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.dst) + r * j.ldd + c) =
+      make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // fp32 [B, H, N, D] -> rows (b, n) of H * D, rounded once.  A thread takes 8
 // values of one head row (D is a multiple of 8): 16 bytes out, 32 in.
 template <typename T>
-__global__ void __launch_bounds__(256) pack_heads_kernel(const float* __restrict__ src, int heads,
-                                                         int64_t tokens, int dim, int64_t rows,
-                                                         T* __restrict__ dst) {
-  const int per = heads * dim / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= rows * per) return;
-  const int64_t r = i / per, b = r / tokens, n = r - b * tokens;
+__device__ __forceinline__ void pack_heads(const PackJob& j, int64_t i) {
+  const int per = j.cols / 8, dim = j.cols / j.f32_heads;
+  const int64_t r = i / per;
+  if (r >= j.rows) return;
+  const int64_t b = r / j.tokens, n = r - b * j.tokens;
   const int c = static_cast<int>(i - r * per) * 8, h = c / dim, d = c - h * dim;
-  const float4* q = reinterpret_cast<const float4*>(src + ((b * heads + h) * tokens + n) * dim + d);
+  const float4* q = reinterpret_cast<const float4*>(
+      static_cast<const float*>(j.src) + ((b * j.f32_heads + h) * j.tokens + n) * dim + d);
   const float4 x = q[0], y = q[1];
-  *reinterpret_cast<uint4*>(dst + r * per * 8 + c) =
+  *reinterpret_cast<uint4*>(static_cast<T*>(j.dst) + r * j.ldd + c) =
       make_uint4(pack_pair(x.x, x.y, T()), pack_pair(x.z, x.w, T()), pack_pair(y.x, y.y, T()),
                  pack_pair(y.z, y.w, T()));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const PackJob a, const PackJob b,
+                                                   int64_t blocks_a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool first = blockIdx.x < blocks_a;
+  const int64_t i = (blockIdx.x - (first ? 0 : blocks_a)) * 256 + threadIdx.x;
+  if (!first) pack_rows(b, i);
+  else if (a.f32_heads > 0) pack_heads<T>(a, i);
+  else pack_rows(a, i);
 }
 
 template <bool VEC, typename T>
@@ -68,8 +77,10 @@ __device__ __forceinline__ void load8(const T* row, int c, int cols, float (&f)[
 // out.  The sums stay in fp32 registers (of the unrounded dz), then go
 // through shared memory in the order of the warps.
 template <typename T, bool VEC, int ACT>
-__global__ void __launch_bounds__(256) dact_kernel(const DactParams p) {
+__global__ void __launch_bounds__(256) dact_kernel(DactParams p) {
   __shared__ float red[8][kDactCols];
+  griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int c = static_cast<int>(blockIdx.x) * kDactCols + 8 * lane;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
@@ -111,7 +122,8 @@ __global__ void __launch_bounds__(256) dact_kernel(const DactParams p) {
 __global__ void __launch_bounds__(256) sum_parts(const float* __restrict__ part, int64_t ldpart,
                                                  int blocks, int cols, float* __restrict__ out) {
   __shared__ float red[8][33];
-  ptx::griddep_wait();
+  griddep_wait();
+  griddep_launch_dependents();
   const int c = 32 * static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.x);
   float t = 0.f;
   if (c < cols)
@@ -129,11 +141,13 @@ template <typename T, bool VEC>
 cudaError_t dact_t(const DactParams& p, cudaStream_t s) {
   const dim3 grid((p.cols + kDactCols - 1) / kDactCols, p.row_blocks);
   const int act = p.pre ? p.act : WSATTN_ACT_NONE;
-  if (act == WSATTN_ACT_GELU) dact_kernel<T, VEC, WSATTN_ACT_GELU><<<grid, 256, 0, s>>>(p);
-  else if (act == WSATTN_ACT_GELU_TANH) dact_kernel<T, VEC, WSATTN_ACT_GELU_TANH><<<grid, 256, 0, s>>>(p);
-  else if (act == WSATTN_ACT_SILU) dact_kernel<T, VEC, WSATTN_ACT_SILU><<<grid, 256, 0, s>>>(p);
-  else dact_kernel<T, VEC, WSATTN_ACT_NONE><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  auto run = [&](void (*kernel)(DactParams)) {
+    return launch_dependent(kernel, grid, dim3(256), 0, s, p);
+  };
+  if (act == WSATTN_ACT_GELU) return run(dact_kernel<T, VEC, WSATTN_ACT_GELU>);
+  if (act == WSATTN_ACT_GELU_TANH) return run(dact_kernel<T, VEC, WSATTN_ACT_GELU_TANH>);
+  if (act == WSATTN_ACT_SILU) return run(dact_kernel<T, VEC, WSATTN_ACT_SILU>);
+  return run(dact_kernel<T, VEC, WSATTN_ACT_NONE>);
 }
 
 __device__ int g_op_status;
@@ -152,25 +166,15 @@ int* op_status_ptr() {
   return ptr[dev];
 }
 
-cudaError_t launch_pack(int dtype, const void* src, int64_t lds, int64_t rows, int cols, void* dst,
-                        int64_t ldd, int src_f32_heads, int64_t tokens, cudaStream_t s) {
-  const int64_t blocks = (rows * (ldd / 8) + 255) / 256;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
-  if (src_f32_heads > 0) {
-    const float* f = static_cast<const float*>(src);
-    const int dim = cols / src_f32_heads;
-    if (dtype == WSATTN_BF16)
-      pack_heads_kernel<<<grid, 256, 0, s>>>(f, src_f32_heads, tokens, dim, rows,
-                                             static_cast<__nv_bfloat16*>(dst));
-    else
-      pack_heads_kernel<<<grid, 256, 0, s>>>(f, src_f32_heads, tokens, dim, rows,
-                                             static_cast<__half*>(dst));
-  } else {
-    pack_kernel<<<grid, 256, 0, s>>>(static_cast<const __half*>(src), lds, rows, cols,
-                                     static_cast<__half*>(dst), ldd);
-  }
-  return cudaGetLastError();
+cudaError_t launch_pack(int dtype, const PackJob& a, const PackJob& b, cudaStream_t s) {
+  auto blocks = [](const PackJob& j) { return (j.rows * (j.ldd / 8) + 255) / 256; };
+  const int64_t na = blocks(a), nb = blocks(b);
+  if (na + nb == 0) return cudaSuccess;
+  if (na + nb > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(na + nb));
+  return dtype == WSATTN_BF16
+             ? launch_dependent(pack_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, b, na)
+             : launch_dependent(pack_kernel<__half>, grid, dim3(256), 0, s, a, b, na);
 }
 
 cudaError_t launch_dact(const DactParams& p, int dtype, float* db, cudaStream_t s) {
@@ -190,7 +194,10 @@ cudaError_t launch_dact(const DactParams& p, int dtype, float* db, cudaStream_t 
 // at 128 (both move 96 and 84 KB per microsecond and SM from L2, which is
 // what bounds them), one of a single CTA the time of its bytes at that rate,
 // shared by the CTAs of an SM.
-GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms) {
+constexpr double kPairStart = 4500.0, kPairTile = 500.0, kPairStep256 = 320.0,
+                 kPairStep128 = 285.0;
+
+GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns) {
   const int64_t ksteps = (K + kGemmK - 1) / kGemmK;
   GemmShape best{256, 0, 1};
   double best_t = 1e300;
@@ -203,8 +210,9 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms) {
   };
   for (int bn = 256; bn >= 128; bn -= 128) {
     const int64_t waves = cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2);
-    consider(4500.0 + static_cast<double>(waves) *
-                          (static_cast<double>(ksteps) * (bn == 256 ? 320.0 : 285.0) + 500.0),
+    consider(kPairStart + static_cast<double>(waves) *
+                              (static_cast<double>(ksteps) *
+                                   (bn == 256 ? kPairStep256 : kPairStep128) + kPairTile),
              GemmShape{bn, 0, 1});
   }
   for (int bn = 16; bn <= 128; bn *= 2) {
@@ -224,7 +232,25 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms) {
       consider(t, GemmShape{0, bn, split});
     }
   }
+  *ns = best_t;
   return best;
+}
+
+double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb, int sms) {
+  auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  auto tiles = [&](int64_t R, int C) {
+    return static_cast<double>(cdiv(R, kPairRows) * cdiv(C, 256));
+  };
+  auto tile_ns = [&](int K) {
+    return static_cast<double>(cdiv(K, kGemmK)) * kPairStep256 + kPairTile;
+  };
+  const double na = tiles(Ra, Ca), nb = tiles(Rb, Cb), la = tile_ns(Ka), lb = tile_ns(Kb);
+  const double longest = la > lb ? la : lb, shorter = la > lb ? lb : la;
+  // all pairs busy to within one of the shorter tiles, or one round of the
+  // longer ones
+  const double even = (na * la + nb * lb) / (sms / 2) + 0.5 * shorter;
+  const double rounds = static_cast<double>(cdiv(static_cast<int64_t>(la > lb ? na : nb), sms / 2));
+  return kPairStart + (even > rounds * longest ? even : rounds * longest);
 }
 
 }  // namespace wsattn

@@ -21,6 +21,11 @@
 // pairs at work together then read about 8 slices of P and 10 of Q, which
 // L2 serves to the others.
 //
+// One launch may hold two products (both gradients of a linear layer): the
+// tiles of the one with the longer contraction go round the pairs first and
+// the other's fill in behind them in the order in which pairs fall free, so
+// that neither product ends in a wave of its own that is mostly empty.
+//
 // Epilogue: residual rows are read and outputs are written in whole lines
 // through a 128-byte-swizzled staging buffer (TMA store, or per-row stores
 // when out's rows are not 16-byte aligned); sums and activation in fp32, one
@@ -66,7 +71,11 @@ __device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t p
   return wait_slow(s, b, parity, code);
 }
 
-// Row and column tile of tile t.
+// A pair's it-th tile: which product, and its row and column tile.
+struct TileRef {
+  int which, tr, tc;
+};
+
 __device__ __forceinline__ void tile_at(const GemmParams& p, int t, int& tr, int& tc) {
   const int per = kRowGroup * p.tiles_c;
   const int g = t / per, rest = t - g * per;
@@ -75,17 +84,53 @@ __device__ __forceinline__ void tile_at(const GemmParams& p, int t, int& tr, int
   tr = g * kRowGroup + rest - tc * rows;
 }
 
-template <int BN>
-__device__ void producer(const GemmParams& p, const GemmShared& s, int total, int pair, int pairs,
+template <bool TWO>
+__device__ __forceinline__ bool nth_tile(const PairParams& pp, int pair, int pairs, int it,
+                                         TileRef& r) {
+  if (!TWO) {
+    const int t = pair + it * pairs;
+    if (t >= pp.tiles_a) return false;
+    r.which = 0;
+    tile_at(pp.g[0], t, r.tr, r.tc);
+    return true;
+  }
+  const int full = pp.tiles_a / pairs, rest = pp.tiles_a - full * pairs;
+  const int own = full + (pair < rest ? 1 : 0);
+  if (it < own) {
+    r.which = 0;
+    tile_at(pp.g[0], pair + it * pairs, r.tr, r.tc);
+    return true;
+  }
+  int t = it - own;
+  if (rest == 0) {
+    t = t * pairs + pair;
+  } else {
+    const int others = pairs - rest, head = pp.head_rounds;
+    if (pair < rest) t = head * others + t * pairs + pair;
+    else if (t < head) t = t * others + pair - rest;
+    else t = head * others + (t - head) * pairs + pair;
+  }
+  if (t >= pp.tiles_b) return false;
+  r.which = 1;
+  tile_at(pp.g[1], t, r.tr, r.tc);
+  return true;
+}
+
+template <int BN, bool TWO>
+__device__ void producer(const PairParams& pp, const GemmShared& s, int pair, int pairs,
                          uint32_t rank) {
   constexpr int kStages = n_stages(BN);
   constexpr uint32_t kStage = stage_bytes(BN);
-  const int ksteps = (p.K + kGemmK - 1) / kGemmK;
   uint32_t slot = 0, phase = 0, last_phase = 0, issued = 0;
   bool ok = true;
-  for (int t = pair; ok && t < total; t += pairs) {
-    int tr, tc;
-    tile_at(p, t, tr, tc);
+  TileRef ref;
+  for (int it = 0; ok && nth_tile<TWO>(pp, pair, pairs, it, ref); ++it) {
+    const GemmParams& p = pp.g[TWO ? ref.which : 0];
+    const int tr = ref.tr, tc = ref.tc;
+    const int ksteps = (p.K + kGemmK - 1) / kGemmK;
+    const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
+    const CUtensorMap* const tm_p = &p.tm_p;
+    const CUtensorMap* const tm_q = &p.tm_q;
     const int row0 = tr * kPairRows + 128 * static_cast<int>(rank);
     const int col0 = tc * BN + BN / 2 * static_cast<int>(rank);
     if (!WSATTN_BOUNDS(p.status, tr >= 0 && tr < p.tiles_r && tc >= 0 && tc < p.tiles_c)) break;
@@ -99,18 +144,18 @@ __device__ void producer(const GemmParams& p, const GemmShared& s, int total, in
       const uint32_t full = map_to_rank(bar(s, FULL0 + slot), 0);
       if (rank == 0) mbar_arrive_expect_tx(bar(s, FULL0 + slot), 2 * kStage);
       const int k0 = kt * kGemmK;
-      if (!p.p_mn) {
-        tma_load_2d_pair(a, &p.tm_p, full, k0, row0);
+      if (!p_mn) {
+        tma_load_2d_pair(a, tm_p, full, k0, row0);
       } else {
-        tma_load_2d_pair(a, &p.tm_p, full, row0, k0);
-        tma_load_2d_pair(a + kABytes / 2, &p.tm_p, full, row0 + 64, k0);
+        tma_load_2d_pair(a, tm_p, full, row0, k0);
+        tma_load_2d_pair(a + kABytes / 2, tm_p, full, row0 + 64, k0);
       }
-      if (!p.q_mn) {
-        tma_load_2d_pair(b, &p.tm_q, full, k0, col0);
+      if (!q_mn) {
+        tma_load_2d_pair(b, tm_q, full, k0, col0);
       } else {
 #pragma unroll
         for (int j = 0; j < BN / 128; ++j)
-          tma_load_2d_pair(b + 8192u * j, &p.tm_q, full, col0 + 64 * j, k0);
+          tma_load_2d_pair(b + 8192u * j, tm_q, full, col0 + 64 * j, k0);
       }
       last_phase = (last_phase & ~(1u << slot)) | (phase << slot);
       issued |= 1u << slot;
@@ -133,19 +178,21 @@ __device__ void producer(const GemmParams& p, const GemmShared& s, int total, in
     }
 }
 
-template <int BN>
-__device__ void mma_issuer(const GemmParams& p, const GemmShared& s, int total, int pair,
-                           int pairs, uint32_t tbase, bool bf16) {
+template <int BN, bool TWO>
+__device__ void mma_issuer(const PairParams& pp, const GemmShared& s, int pair, int pairs,
+                           uint32_t tbase, bool bf16) {
   constexpr int kStages = n_stages(BN);
   constexpr uint32_t kStage = stage_bytes(BN);
-  const uint32_t idesc = idesc_16_f32(kPairRows, BN, bf16, p.p_mn != 0, p.q_mn != 0);
-  // contraction contiguous: 16 values are 32 bytes further on in a row;
-  // own dimension contiguous: 16 rows of 128 bytes, 8 KB per 64 columns
-  const uint32_t a_lbo = p.p_mn ? 8192u : 16u, b_lbo = p.q_mn ? 8192u : 16u;
-  const uint64_t a_step = p.p_mn ? 128 : 2, b_step = p.q_mn ? 128 : 2;
-  const int ksteps = (p.K + kGemmK - 1) / kGemmK;
-  uint32_t slot = 0, phase = 0, it = 0;
-  for (int t = pair; t < total; t += pairs, ++it) {
+  uint32_t slot = 0, phase = 0;
+  TileRef ref;
+  for (uint32_t it = 0; nth_tile<TWO>(pp, pair, pairs, static_cast<int>(it), ref); ++it) {
+    const GemmParams& p = pp.g[TWO ? ref.which : 0];
+    const uint32_t idesc = idesc_16_f32(kPairRows, BN, bf16, p.p_mn != 0, p.q_mn != 0);
+    // contraction contiguous: 16 values are 32 bytes further on in a row;
+    // own dimension contiguous: 16 rows of 128 bytes, 8 KB per 64 columns
+    const uint32_t a_lbo = p.p_mn ? 8192u : 16u, b_lbo = p.q_mn ? 8192u : 16u;
+    const uint64_t a_step = p.p_mn ? 128 : 2, b_step = p.q_mn ? 128 : 2;
+    const int ksteps = (p.K + kGemmK - 1) / kGemmK;
     const uint32_t ab = it & 1u, use = it >> 1;
     if (!wait(s, bar(s, ACCEMPTY0 + ab), (use & 1u) ^ 1u, kStatusTimeoutMma)) return;
     tc_fence_after();
@@ -255,9 +302,9 @@ __device__ __forceinline__ void act16(float (&y)[16]) {
   for (int i = 0; i < 16; ++i) y[i] = act_value<ACT>(y[i]);
 }
 
-template <typename T, typename O, int BN>
-__device__ void epilogue(const GemmParams& p, const GemmShared& s, uint32_t staging, int total,
-                         int pair, int pairs, uint32_t rank, uint32_t tbase) {
+template <typename T, typename O, int BN, bool TWO>
+__device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t staging, int pair,
+                         int pairs, uint32_t rank, uint32_t tbase) {
   constexpr int kCols = 128 / sizeof(O);  // columns of a staging chunk
   const int warp = threadIdx.x / 32 - kEpiWarp0, lane = threadIdx.x & 31;
   const int wq = warp & 3, half = warp >> 2;
@@ -265,13 +312,14 @@ __device__ void epilogue(const GemmParams& p, const GemmShared& s, uint32_t stag
   const uint32_t buf0 = staging + 2 * kBuf * static_cast<uint32_t>(warp);
   const uint32_t acc_free[2] = {map_to_rank(bar(s, ACCEMPTY0), 0),
                                 map_to_rank(bar(s, ACCEMPTY0 + 1), 0)};
-  // pre-activations of 16 bits beside outputs of 16 bits go through staging
-  const bool stage_pre = p.pre != nullptr && sizeof(O) == 2;
-  uint32_t it = 0, ob = 0;
+  uint32_t ob = 0;
   bool aborted = false;
-  for (int t = pair; !aborted && t < total; t += pairs, ++it) {
-    int tr, tc;
-    tile_at(p, t, tr, tc);
+  TileRef ref;
+  for (uint32_t it = 0; !aborted && nth_tile<TWO>(pp, pair, pairs, static_cast<int>(it), ref); ++it) {
+    const GemmParams& p = pp.g[TWO ? ref.which : 0];
+    const int tr = ref.tr, tc = ref.tc;
+    // pre-activations of 16 bits beside outputs of 16 bits go through staging
+    const bool stage_pre = p.pre != nullptr && sizeof(O) == 2;
     const uint32_t ab = it & 1u, use = it >> 1;
     const int64_t row0 = static_cast<int64_t>(tr) * kPairRows + 128 * rank + 32 * wq;
     const bool tile_ok =
@@ -418,8 +466,8 @@ __device__ void epilogue(const GemmParams& p, const GemmShared& s, uint32_t stag
   if (lane == 0) bulk_wait_all();  // the stores have left shared memory before the CTA does
 }
 
-template <typename T, typename O, int BN>
-__global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+template <typename T, typename O, int BN, bool TWO>
+__global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t smem_raw[];
   constexpr int kStages = n_stages(BN);
   const uint32_t raw = smem_u32(smem_raw);
@@ -431,11 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
   uint8_t* gb = smem_raw + (s.bars - raw);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * NBARS);
   s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  s.status = p.status;
+  s.status = p.g[0].status;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
-  const int total = p.tiles_r * p.tiles_c;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -450,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&p.tm_p);
-    prefetch_tensormap(&p.tm_q);
-    if (p.out_vec) prefetch_tensormap(&p.tm_out);
+    prefetch_tensormap(&p.g[0].tm_p);
+    prefetch_tensormap(&p.g[0].tm_q);
+    if (p.g[0].out_vec) prefetch_tensormap(&p.g[0].tm_out);
   }
   if (warp == 2) {
     tmem_alloc_pair(smem_u32(tslot), 2 * BN);
@@ -467,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
   griddep_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) producer<BN>(p, s, total, pair, pairs, rank);
+    if (lane == 0) producer<BN, TWO>(p, s, pair, pairs, rank);
   } else if (warp == 1) {
     if (lane == 0 && rank == 0)
-      mma_issuer<BN>(p, s, total, pair, pairs, tbase, !IsHalf<T>::value);
+      mma_issuer<BN, TWO>(p, s, pair, pairs, tbase, !IsHalf<T>::value);
   } else if (warp >= kEpiWarp0) {
-    epilogue<T, O, BN>(p, s, staging, total, pair, pairs, rank, tbase);
+    epilogue<T, O, BN, TWO>(p, s, staging, pair, pairs, rank, tbase);
   }
 
   __syncwarp();
@@ -483,27 +530,39 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
   if (warp == 2) tmem_dealloc_pair(tbase, 2 * BN);
 }
 
-template <typename T, typename O, int BN>
-cudaError_t launch(const GemmParams& p, int sms, cudaStream_t s) {
+template <typename T, typename O, int BN, bool TWO>
+cudaError_t launch(PairParams* p, int sms, cudaStream_t s) {
   static bool attr_set[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   const size_t smem = pair_smem_bytes(BN);
   if (!attr_set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(gemm_pair_kernel<T, O, BN>,
+        cudaFuncSetAttribute(gemm_pair_kernel<T, O, BN, TWO>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const int64_t tiles = static_cast<int64_t>(p.tiles_r) * p.tiles_c;
-  const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_cluster(gemm_pair_kernel<T, O, BN>, dim3(2 * pairs), dim3(kThreads), 2, smem, s, p);
+  const int64_t ta = static_cast<int64_t>(p->g[0].tiles_r) * p->g[0].tiles_c;
+  const int64_t tb = static_cast<int64_t>(p->g[1].tiles_r) * p->g[1].tiles_c;
+  // the index of the last tile, plus one round, has to fit an int
+  if (ta + tb > INT32_MAX - 4 * sms) return cudaErrorInvalidValue;
+  p->tiles_a = static_cast<int>(ta);
+  p->tiles_b = static_cast<int>(tb);
+  const int ka = (p->g[0].K + kGemmK - 1) / kGemmK, kb = (p->g[1].K + kGemmK - 1) / kGemmK;
+  p->head_rounds = tb > 0 ? (ka + kb - 1) / kb : 0;
+  const int pairs = static_cast<int>(ta + tb < sms / 2 ? ta + tb : sms / 2);
+  return launch_cluster(gemm_pair_kernel<T, O, BN, TWO>, dim3(2 * pairs), dim3(kThreads), 2, smem, s,
+                        *p);
 }
 
 template <typename T, typename O>
-cudaError_t launch_bn(const GemmParams& p, int pair_cols, int sms, cudaStream_t s) {
-  return pair_cols == 256 ? launch<T, O, 256>(p, sms, s) : launch<T, O, 128>(p, sms, s);
+cudaError_t launch_bn(PairParams* p, int pair_cols, int sms, cudaStream_t s) {
+  if constexpr (sizeof(O) == 2) {  // two products: the gradients, 256 columns
+    if (p->g[1].tiles_r > 0) return launch<T, O, 256, true>(p, sms, s);
+  }
+  return pair_cols == 256 ? launch<T, O, 256, false>(p, sms, s)
+                          : launch<T, O, 128, false>(p, sms, s);
 }
 
 }  // namespace
@@ -512,7 +571,7 @@ size_t pair_smem_bytes(int bn) {
   return 1024 + n_stages(bn) * stage_bytes(bn) + 2 * kEpiWarps * kBuf + 8 * NBARS + 16;
 }
 
-cudaError_t launch_gemm_pair(const GemmParams& p, int dtype, bool out_f32, int pair_cols, int sms,
+cudaError_t launch_gemm_pair(PairParams* p, int dtype, bool out_f32, int pair_cols, int sms,
                              cudaStream_t s) {
   if (dtype == WSATTN_BF16)
     return out_f32 ? launch_bn<__nv_bfloat16, float>(p, pair_cols, sms, s)

@@ -105,18 +105,31 @@ struct GemmParams {
   int* status;         // device status word (bit set on an expired wait)
 };
 
+// One launch of the CTA-pair kernel: one product, or two with the same types
+// (a and b) whose tiles it deals out together (tiles_b = 0: only a).
+struct PairParams {
+  GemmParams g[2];
+  int tiles_a, tiles_b;
+  // a's tiles go round the pairs first; the pairs that get one less take
+  // `head_rounds` rounds of b's tiles meanwhile, then all of them the rest
+  int head_rounds;
+};
+
 // How a product is tiled.
 struct GemmShape {
   int pair_cols;  // columns of a CTA pair's tile (256 or 128), 0: single-CTA tiles
   int bn;         // single-CTA tiles: rows per tile
   int split;      // single-CTA tiles: CTAs per tile
 };
-GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms);
+GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns);
+// Estimated nanoseconds of two products in one launch of the pair kernel.
+double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb, int sms);
 
 size_t pair_smem_bytes(int pair_cols);
 size_t tile_smem_bytes(int bn, int stages);
 // 16-bit operands of type `dtype`; out and residual of that type or fp32.
-cudaError_t launch_gemm_pair(const GemmParams& p, int dtype, bool out_f32, int pair_cols, int sms,
+// tiles_a, tiles_b and head_rounds are set here.
+cudaError_t launch_gemm_pair(PairParams* p, int dtype, bool out_f32, int pair_cols, int sms,
                              cudaStream_t s);
 cudaError_t launch_gemm_tile(const GemmParams& p, int dtype, bool out_f32, cudaStream_t s);
 
@@ -124,11 +137,21 @@ cudaError_t launch_gemm_tile(const GemmParams& p, int dtype, bool out_f32, cudaS
 // the library's image; its address is looked up once per device).
 int* op_status_ptr();
 
-// Copies a [rows, cols] matrix with any row stride and alignment to rows of
-// `ldd` elements (a multiple of 8); src_f32_heads > 0: src is fp32
-// [rows / tokens, heads, tokens, cols / heads] and is rounded to dtype.
-cudaError_t launch_pack(int dtype, const void* src, int64_t lds, int64_t rows, int cols, void* dst,
-                        int64_t ldd, int src_f32_heads, int64_t tokens, cudaStream_t s);
+// Copies [rows, cols] matrices with any row stride and alignment to rows of
+// `ldd` elements (a multiple of 8), up to two in one launch; f32_heads > 0
+// (the first one only): src is fp32 [rows / tokens, heads, tokens,
+// cols / heads] and is rounded to dtype.
+struct PackJob {
+  const void* src;
+  int64_t lds;
+  int64_t rows;  // 0: nothing to copy
+  int cols;
+  void* dst;
+  int64_t ldd;
+  int f32_heads;
+  int64_t tokens;
+};
+cudaError_t launch_pack(int dtype, const PackJob& a, const PackJob& b, cudaStream_t s);
 
 // dz = dout * act'(preact) (dz null: not stored) and, in parts, its column
 // sums: part [row_blocks, ldpart].

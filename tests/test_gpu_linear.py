@@ -133,31 +133,32 @@ def test_linear_backward(shape, dt, name):
     g = torch.Generator().manual_seed(1)
     dy = (0.3 * torch.randn((m, n), generator=g)).to(dt)
     z = None if name == "none" else (1.5 * r).to(dt)
-    dx, dw, db = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(),
-                                           None if z is None else z.cuda(), name)
+    args = (dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name)
+    dx, dw, db = fw.wsattn_linear_backward(*args)
     torch.cuda.synchronize()
     assert fw.wsattn_op_status() == 0
     dz = dy.double() * (1 if z is None else _slope64(z.double(), name))
     # of dz: half a step where it is rounded, 2^-19 relative to dout for the slope
     dztol = (0 if z is None else half_step(dt) * dz.abs() + 2.0 ** -19 * dy.double().abs() + tiny(dt))
     wa, xa = w.double().abs(), x.double().abs()
+    # each gradient by itself too (its product may be tiled, and so summed, another way)
+    only_dx = fw.wsattn_linear_backward(*args, need_dw=False, need_db=False)
+    only_dw = fw.wsattn_linear_backward(*args, need_dx=False, need_db=False)
+    only_db = fw.wsattn_linear_backward(*args, need_dx=False, need_dw=False)
+    assert only_dx[1:] == (None, None) and only_dw[::2] == (None, None)
+    assert only_db[:2] == (None, None) and torch.equal(only_db[2], db)
     for got, want, mag, extra, kk in (
-            (dx, dz @ w.double(), dz.abs() @ wa, dztol @ wa if z is not None else 0, n),
-            (dw, dz.t() @ x.double(), dz.abs().t() @ xa, dztol.t() @ xa if z is not None else 0, m)):
+            ((dx, only_dx[0]), dz @ w.double(), dz.abs() @ wa, dztol @ wa if z is not None else 0, n),
+            ((dw, only_dw[1]), dz.t() @ x.double(), dz.abs().t() @ xa,
+             dztol.t() @ xa if z is not None else 0, m)):
         tol = 1.01 * extra + product_tol(mag, kk) + half_step(dt) * want.abs() + tiny(dt)
-        assert_close(got, want, tol)
+        for t in got:
+            assert_close(t, want, tol)
     sums = dz.abs().sum(0)
     assert_close(db, dz.sum(0), (2.0 ** -19 + (m / 64 + 32) * 2.0 ** -24) * (sums + dy.double().abs().sum(0)))
-    again = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name)
+    again = fw.wsattn_linear_backward(*args)
     for a, b in zip(again, (dx, dw, db)):
         assert torch.equal(a, b)
-    # each gradient by itself
-    only = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name,
-                                     need_dx=False, need_db=False)
-    assert only[0] is None and only[2] is None and torch.equal(only[1], dw)
-    only = fw.wsattn_linear_backward(dy.cuda(), x.cuda(), w.cuda(), None if z is None else z.cuda(), name,
-                                     need_dx=False, need_dw=False)
-    assert only[0] is None and only[1] is None and torch.equal(only[2], db)
 
 
 def test_linear_empty():
