@@ -5,39 +5,70 @@
 #include <cuda_fp16.h>
 
 #include "ops.h"
+#include "ptx.cuh"
 
 namespace wsattn {
 
-// Activations and their slopes in fp32.  The logistic function is formed
-// with the fast exponential and division: their error (a few 2^-22 relative)
-// is far below the rounding of the stored 16-bit value.
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// Activations and their slopes in fp32, on the approximate exponential and
+// reciprocal of the special-function unit (each within 2^-22 relative, and
+// the exponential's argument within 2^-23 of itself): far below the rounding
+// of the stored 16-bit value, and a third of the instructions of the exact
+// ones, which the epilogue of a short contraction would wait for.
+//
+// logistic(x) = 1 / (1 + exp(-x)), from t = -x log2(e)
+__device__ __forceinline__ float logistic_log2(float t) {
+  return ptx::rcp_approx(1.f + ptx::ex2_approx(t));
+}
 
-// tanh form of gelu: 0.5 z (1 + tanh u) = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
-__device__ __forceinline__ float gelu_2u(float z) {
-  return z * fmaf(0.0713548162726f, z * z, 1.5957691216057f);
+// tanh form of gelu: 0.5 z (1 + tanh u) = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3);
+// -2 u log2(e):
+__device__ __forceinline__ float gelu_log2(float z, float zz) {
+  return z * fmaf(-0.10294323967f, zz, -2.30220819814f);
+}
+
+// The normal distribution function, and e = exp(-z^2 / 2), which its density
+// shares: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), for
+// x >= 0 (Abramowitz and Stegun 7.1.26, absolute error below 1.5e-7).  A
+// third of the instructions of erff and expf, and no cancellation on the
+// negative side, where the value itself is small.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = fabsf(z) * 0.70710678118655f;
+  const float t = ptx::rcp_approx(fmaf(0.3275911f, x, 1.f));
+  e = ptx::ex2_approx(z * z * -0.72134752044448f);
+  float h = fmaf(t, 1.061405429f, -1.453152027f);
+  h = fmaf(t, h, 1.421413741f);
+  h = fmaf(t, h, -0.284496736f);
+  h = fmaf(t, h, 0.254829592f);
+  h *= 0.5f * t * e;
+  return z < 0.f ? h : 1.f - h;
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-  if (ACT == WSATTN_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118655f));
-  if (ACT == WSATTN_ACT_GELU_TANH) return z * logistic(gelu_2u(z));
-  if (ACT == WSATTN_ACT_SILU) return z * logistic(z);
+  if (ACT == WSATTN_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
+  if (ACT == WSATTN_ACT_GELU_TANH) return z * logistic_log2(gelu_log2(z, z * z));
+  if (ACT == WSATTN_ACT_SILU) return z * logistic_log2(z * -1.44269504088896f);
   return z;
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-  if (ACT == WSATTN_ACT_GELU)
-    return fmaf(z * 0.39894228040143f, __expf(-0.5f * z * z),
-                0.5f * (1.f + erff(z * 0.70710678118655f)));
+  if (ACT == WSATTN_ACT_GELU) {
+    float e;
+    const float c = normal_cdf(z, e);
+    return fmaf(z * 0.39894228040143f, e, c);
+  }
   if (ACT == WSATTN_ACT_GELU_TANH) {
     // past |z| = 1000, s (1 - s) is zero: the square is kept finite for it
-    const float s = logistic(gelu_2u(z));
-    return fmaf(s * (1.f - s) * z, fmaf(0.2140644488178f, fminf(z * z, 1e6f), 1.5957691216057f), s);
+    const float zz = fminf(z * z, 1e6f);
+    const float s = logistic_log2(gelu_log2(z, zz));
+    return fmaf(s * (1.f - s) * z, fmaf(0.2140644488178f, zz, 1.5957691216057f), s);
   }
   if (ACT == WSATTN_ACT_SILU) {
-    const float s = logistic(z);
+    const float s = logistic_log2(z * -1.44269504088896f);
     return s * fmaf(z, 1.f - s, 1.f);
   }
   return 1.f;

@@ -55,55 +55,65 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackJob a, const PackJo
   else pack_rows(a, i);
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int cols, float (&f)[8]) {
-  if (VEC) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+template <bool VEC>
+__device__ __forceinline__ uint4 load_raw8(const void* base, int64_t ld, int64_t r, int c, int cols) {
+  const uint16_t* q = static_cast<const uint16_t*>(base) + r * ld + c;
+  if (VEC) return *reinterpret_cast<const uint4*>(q);
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = unpack_pair(w[i], T());
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? to_f32(row[c + i]) : 0.f;
-  }
+  for (int e = 0; e < 4; ++e)
+    w[e] = (c + 2 * e < cols ? q[2 * e] : 0u) | (c + 2 * e + 1 < cols ? q[2 * e + 1] : 0u) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // CTA (x, y): 256 columns of rows [y * rows_per_block, ...); a warp takes
-// every eighth row, a lane 8 columns.  Bound by HBM: dout and preact in, dz
-// out.  The sums stay in fp32 registers (of the unrounded dz), then go
-// through shared memory in the order of the warps.
+// every eighth row, a lane 8 columns of it, four rows' loads in flight.
+// Bound by HBM (dout and preact in, dz out).  The sums stay in fp32
+// registers (of the unrounded dz), then go through shared memory in the
+// order of the warps.
 template <typename T, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) dact_kernel(DactParams p) {
+  constexpr int U = 4;
   __shared__ float red[8][kDactCols];
-  griddep_wait();
-  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int c = static_cast<int>(blockIdx.x) * kDactCols + 8 * lane;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
   const int64_t r1 = min(p.rows, r0 + p.rows_per_block);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  griddep_wait();
+  griddep_launch_dependents();
   if (c < p.cols) {
-#pragma unroll 4
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      float g[8];
-      load8<VEC>(static_cast<const T*>(p.dout) + r * p.ldd, c, p.cols, g);
-      if (ACT != WSATTN_ACT_NONE) {
-        float z[8];
-        load8<VEC>(static_cast<const T*>(p.pre) + r * p.ldp, c, p.cols, z);
+    for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
+      uint4 gw[U], zw[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // rounded here, so that the sums are the same with and without dz
-          g[i] = __fmul_rn(g[i], act_slope<ACT>(z[i]));
+      for (int u = 0; u < U; ++u) {
+        const bool on = r + 8 * u < r1;
+        gw[u] = on ? load_raw8<VEC>(p.dout, p.ldd, r + 8 * u, c, p.cols) : make_uint4(0, 0, 0, 0);
+        if (ACT != WSATTN_ACT_NONE)
+          zw[u] = on ? load_raw8<VEC>(p.pre, p.ldp, r + 8 * u, c, p.cols) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += g[i];
-      if (p.dz)
-        *reinterpret_cast<uint4*>(static_cast<T*>(p.dz) + r * p.ldz + c) =
-            make_uint4(pack_pair(g[0], g[1], T()), pack_pair(g[2], g[3], T()),
-                       pack_pair(g[4], g[5], T()), pack_pair(g[6], g[7], T()));
+      for (int u = 0; u < U; ++u) {
+        const uint32_t g[4] = {gw[u].x, gw[u].y, gw[u].z, gw[u].w};
+        const uint32_t z[4] = {zw[u].x, zw[u].y, zw[u].z, zw[u].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 d = unpack_pair(g[i], T());
+          if (ACT != WSATTN_ACT_NONE) {
+            // rounded here, so that the sums are the same with and without dz
+            const float2 y = unpack_pair(z[i], T());
+            d.x = __fmul_rn(d.x, act_slope<ACT>(y.x));
+            d.y = __fmul_rn(d.y, act_slope<ACT>(y.y));
+          }
+          acc[2 * i] += d.x;
+          acc[2 * i + 1] += d.y;
+          o[i] = pack_pair(d.x, d.y, T());
+        }
+        if (p.dz && r + 8 * u < r1)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dz) + (r + 8 * u) * p.ldz + c) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
   if (!p.part) return;

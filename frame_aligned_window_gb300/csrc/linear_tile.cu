@@ -114,14 +114,31 @@ __device__ void mma_issuer(const GemmParams& p, const GemmShared& s, int steps, 
   tc_commit(bar(s, ACCFULL));
 }
 
-// One output: bias, pre-activation, activation, residual, one rounding.
-template <typename T, typename O>
-__device__ __forceinline__ void emit(const GemmParams& p, int64_t row, int col, float bias, float v) {
-  float y = v + bias;
-  if (p.pre) static_cast<T*>(p.pre)[row * p.ldp + col] = from_f32<T>(y);
-  y = act_any(p.act, y);
-  if (p.res) y += to_f32(static_cast<const O*>(p.res)[row * p.ldr + col]);
-  static_cast<O*>(p.out)[row * p.ldo + col] = from_f32<O>(y);
+// N outputs of one column in consecutive rows: bias, pre-activation,
+// activation, residual, one rounding.  The residuals are read first, all in
+// flight together (load_res), the accumulators come next.
+template <typename O, int N>
+__device__ __forceinline__ void load_res(const GemmParams& p, int64_t row, int rows, int col,
+                                         O (&r)[N]) {
+  const O* src = static_cast<const O*>(p.res) + row * p.ldr + col;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < rows) r[i] = src[i * p.ldr];
+}
+template <typename T, typename O, int N>
+__device__ __forceinline__ void emit(const GemmParams& p, int64_t row, int rows, int col, float bias,
+                                     const float (&v)[N], const O (&r)[N]) {
+  T* pre = p.pre ? static_cast<T*>(p.pre) + row * p.ldp + col : nullptr;
+  O* out = static_cast<O*>(p.out) + row * p.ldo + col;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i >= rows) break;
+    float y = v[i] + bias;
+    if (pre) pre[i * p.ldp] = from_f32<T>(y);
+    y = act_any(p.act, y);
+    if (p.res) y += to_f32(r[i]);
+    out[i * p.ldo] = from_f32<O>(y);
+  }
 }
 
 template <typename T, typename O>
@@ -179,33 +196,38 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
   const int quad = warp & 3;
   const int c = 32 * quad + lane, col = col0 + c;
   const uint32_t tlane = tbase + (static_cast<uint32_t>(32 * quad) << 16);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.bn), p.R - row0));
   float bias = 0.f;
+  O res[16];
   if (warp == 0) {
     if (lane == 0 && tile_ok) producer(p, s, row0, col0, k0, k1);
   } else if (warp == 1) {
     if (lane == 0 && tile_ok) mma_issuer(p, s, k1 - k0, tbase, !IsHalf<T>::value);
   } else {
     if (p.bias && col < p.C) bias = to_f32(static_cast<const T*>(p.bias)[col]);
+    if (split == 1 && p.res && col < p.C) load_res(p, row0, rows, col, res);
     have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax);
     have = __all_sync(0xffffffffu, have);
     tc_fence_after();
     if (have) {
       for (int j = 0; j < p.bn; j += 16) {
-        uint32_t r[16];
-        tmem_ld16(tlane + j, r);
-        tmem_wait_ld16(r);
+        uint32_t a[16];
+        tmem_ld16(tlane + j, a);
         if (split == 1) {
-          if (col < p.C)
+          if (j > 0 && p.res && col < p.C) load_res(p, row0 + j, rows - j, col, res);
+          tmem_wait_ld16(a);
+          float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (row0 + j + i < p.R)
-                emit<T, O>(p, row0 + j + i, col, bias, __uint_as_float(r[i]));
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
+          if (col < p.C) emit<T, O>(p, row0 + j, rows - j, col, bias, v, res);
         } else {
           // the operand ring is idle now (every MMA of this CTA is complete):
           // it takes the partial tile, [row][128 columns]
+          tmem_wait_ld16(a);
           float* part = reinterpret_cast<float*>(smem_raw + (base - raw));
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(j + i) * kTileCols + c] = __uint_as_float(r[i]);
+          for (int i = 0; i < 16; ++i)
+            if (j + i < rows) part[(j + i) * kTileCols + c] = __uint_as_float(a[i]);
         }
       }
     }
@@ -214,13 +236,29 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
   if (split > 1) {
     cluster_sync();  // every CTA's partial tile is in its shared memory
     if (warp >= 2 && col < p.C) {
-      const int j0 = p.bn * rank / split, j1 = p.bn * (rank + 1) / split;
-      for (int j = j0; j < j1 && row0 + j < p.R; ++j) {
+      const int j0 = rows * rank / split, j1 = rows * (rank + 1) / split;
+      for (int j = j0; j < j1; j += 8) {
+        const int n = min(8, j1 - j);
+        O r8[8];
+        if (p.res) load_res(p, row0 + j, n, col, r8);
         const uint32_t a = base + static_cast<uint32_t>(j * kTileCols + c) * 4u;
-        float v = 0.f;
-        for (int r = 0; r < split; ++r)
-          v += ld_cluster_f32(map_to_rank(a, static_cast<uint32_t>(r)));
-        emit<T, O>(p, row0 + j, col, bias, v);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < split; q += 4) {  // up to 32 remote loads in flight
+          float t[4][8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              t[k][i] = q + k < split && i < n
+                            ? ld_cluster_f32(map_to_rank(a + 4u * kTileCols * i,
+                                                         static_cast<uint32_t>(q + k)))
+                            : 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += t[k][i];
+        }
+        emit<T, O>(p, row0 + j, n, col, bias, v, r8);
       }
     }
     __syncwarp();
