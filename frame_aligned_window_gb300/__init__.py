@@ -393,6 +393,8 @@ _DTYPES = {} if torch is None else {torch.bfloat16: BF16, torch.float16: FP16,
                                     torch.float32: FP32}
 # the raw handle of a device's current stream without a Stream object
 _raw_current_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+_current_device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None) or (
+    lambda: torch.cuda.current_device())
 
 
 def _dtype_code(t, name, allowed=(BF16, FP16, FP32)):
@@ -441,7 +443,7 @@ def _empty(shape, dtype, like, stream):
 
 def _run(dev, what, fn, *args):
     """The C call, with the tensors' device current."""
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -677,12 +679,13 @@ def _rows(t, name, cols, lead, dtype, dev):
     dimensions `lead` (None: any), which must lie one row stride apart."""
     if t.dtype is not dtype or t.get_device() != dev:
         _check_tensor(t, name, dev, dtype)
-    shape, st = t.shape, t.stride()
+    shape = t.shape
     if not shape or shape[-1] != cols or (lead is not None and shape[:-1] != lead):
         want = "..." if lead is None else ", ".join(str(x) for x in lead)
         raise ValueError(f"{name} must be [{want}, {cols}], got {list(shape)}")
-    if len(shape) == 2 and st[1] == 1 and st[0] >= cols:
-        return st[0]
+    if t.is_contiguous():
+        return cols
+    st = t.stride()
     rows, ld = 1, None
     if t.numel() == 0:
         return cols
@@ -739,10 +742,9 @@ def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, 
             raise ValueError(f"x must be contiguous [B, H, N, D] with H * D = {k}, "
                              f"got {list(x.shape)}")
         lead, ldx = torch.Size((B, tokens)), 0
-    m = 1
-    for size in lead:
-        m *= size
+    m = lead.numel()
     ldw = _rows(weight, "weight", k, None, dt, dev)
+    xp, wp = x.data_ptr(), weight.data_ptr()
     bp = rp = pp = ldr = ldp = 0
     if bias is not None:
         _check_tensor(bias, "bias", dev, dt)
@@ -760,8 +762,10 @@ def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, 
         ldr, rp = _rows(residual, "residual", n, lead, odt, dev), residual.data_ptr()
     if preact is not None:
         ldp, pp = _rows(preact, "preact", n, lead, dt, dev), preact.data_ptr()
-    return _LINEAR(code, ocode, m, n, k, x.data_ptr(), ldx, heads, tokens, weight.data_ptr(), ldw,
-                   bp, rp, ldr, out.data_ptr(), ldo, pp, ldp, act), out, dev
+    # operands whose rows start on 16-byte boundaries need no workspace
+    plain = not (heads or (xp | wp) & 15 or (ldx | ldw) & 7)
+    return _LINEAR(code, ocode, m, n, k, xp, ldx, heads, tokens, wp, ldw, bp, rp, ldr,
+                   out.data_ptr(), ldo, pp, ldp, act), out, dev, plain
 
 
 def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact=None, out=None,
@@ -772,19 +776,21 @@ def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact
     preact: a tensor that receives x weight^T + bias, for
     wsattn_linear_backward.  out (or out_dtype): weight's type or fp32, and
     the residual's; residual may be out."""
-    args, out, dev = _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype,
-                                  stream)
+    args, out, dev, plain = _linear_args(x, weight, bias, residual, activation, preact, out,
+                                         out_dtype, stream)
     raw = _raw_stream(dev, stream)
-    ws, nbytes, _hold = _scratch(_lib.wsattn_linear_workspace, "wsattn_linear_workspace", args,
-                                 workspace, dev, weight, stream)
-    _run(dev, "wsattn_linear", _lib.wsattn_linear, args, ws, nbytes, raw)
+    ws = nbytes = _hold = None
+    if workspace is not None or not plain:
+        ws, nbytes, _hold = _scratch(_lib.wsattn_linear_workspace, "wsattn_linear_workspace", args,
+                                     workspace, dev, weight, stream)
+    _run(dev, "wsattn_linear", _lib.wsattn_linear, args, ws, nbytes or 0, raw)
     return out
 
 
 def wsattn_linear_workspace(x, weight) -> int:
     """Bytes of scratch wsattn_linear takes for these operands (0 when their
     rows start on 16-byte boundaries and x is not the attention's output)."""
-    args, _, dev = _linear_args(x, weight, None, None, "none", None, None, None, None)
+    args, _, dev, _ = _linear_args(x, weight, None, None, "none", None, None, None, None)
     n = _SZ()
     _run(dev, "wsattn_linear_workspace", _lib.wsattn_linear_workspace, args, ctypes.byref(n))
     return int(n.value)
@@ -802,9 +808,8 @@ def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need_dx, 
     if act and preact is None:
         raise ValueError("an activation's gradient needs preact")
     ldx = _rows(x, "x", k, None, dt, dev)
-    lead, m = x.shape[:-1], 1
-    for size in lead:
-        m *= size
+    lead = x.shape[:-1]
+    m = lead.numel()
     ldd = _rows(dout, "dout", n, lead, dt, dev)
     ldw = _rows(weight, "weight", k, None, dt, dev)
     pp = ldp = dxp = lddx = dwp = lddw = dbp = 0

@@ -174,6 +174,11 @@ struct Product {
   void* pre;
   int64_t ldp;
   int act;
+  // column sums to add on the side (db null: none)
+  const float* part;
+  int parts;
+  float* db;
+  int db_cols;
 };
 
 // The kernel's parameters for one product under a tiling; false: a tensor
@@ -206,6 +211,11 @@ bool fill(const Product& g, const wsattn::GemmShape& shape, GemmParams* out) {
   prm.pre = g.pre;
   prm.ldp = g.ldp;
   prm.act = g.act;
+  prm.part = g.part;
+  prm.ldpart = g.db_cols;
+  prm.parts = g.parts;
+  prm.db = g.db;
+  prm.db_cols = g.db_cols;
   prm.bias_vec = g.bias && aligned16(g.bias);
   prm.res_vec = g.res && rows_vec(g.res, g.ldr, g.R, g.C, esize);
   prm.out_vec = tma_rows(g.out, g.out_f32 ? 2 * g.ldo : g.ldo, g.R);
@@ -259,7 +269,12 @@ int run_two_products(const Product& g, const Product& h, int sms, cudaStream_t s
   const bool g_first = g.K >= h.K;
   wsattn::PairParams pp;
   std::memset(&pp, 0, sizeof(pp));
-  if (!fill(g_first ? g : h, shape, &pp.g[0]) || !fill(g_first ? h : g, shape, &pp.g[1]))
+  Product first = g_first ? g : h;
+  first.part = g.part;  // g carries the column sums
+  first.parts = g.parts;
+  first.db = g.db;
+  first.db_cols = g.db_cols;
+  if (!fill(first, shape, &pp.g[0]) || !fill(g_first ? h : g, shape, &pp.g[1]))
     return WSATTN_ERR_CUDA;
   return wsattn::launch_gemm_pair(&pp, g.dtype, g.out_f32, 256, sms, s) == cudaSuccess
              ? WSATTN_OK
@@ -658,9 +673,9 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
   char* ws_x = ws_part + plan.part_bytes;
   char* ws_w = ws_x + plan.x_bytes;
   Operand dz{a->dout, a->ldd}, x{a->x, a->ldx}, w{a->w, a->ldw};
+  wsattn::DactParams d;
+  std::memset(&d, 0, sizeof(d));
   if (plan.dz || a->db) {
-    wsattn::DactParams d;
-    std::memset(&d, 0, sizeof(d));
     d.dout = a->dout;
     d.ldd = a->ldd;
     d.pre = plan.act ? a->preact : nullptr;
@@ -676,7 +691,9 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
     d.row_blocks = plan.row_blocks;
     d.vec = rows_vec(a->dout, a->ldd, a->m, a->n, 2) &&
             (!d.pre || rows_vec(a->preact, a->ldp, a->m, a->n, 2));
-    if (wsattn::launch_dact(d, a->dtype, a->db, s) != cudaSuccess) return WSATTN_ERR_CUDA;
+    if (wsattn::launch_dact(d, a->dtype, s) != cudaSuccess) return WSATTN_ERR_CUDA;
+    if (a->db && !a->dx && !a->dw)
+      return wsattn::launch_sum_parts(d, a->db, s) == cudaSuccess ? WSATTN_OK : WSATTN_ERR_CUDA;
     if (plan.dz) dz = Operand{ws_dz, d.ldz};
   }
   wsattn::PackJob jx = pack_job(nullptr, 0, 0, 8, nullptr), jw = jx;
@@ -712,6 +729,11 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
   gx.K = a->n;
   gx.out = a->dx;
   gx.ldo = a->lddx;
+  Product& side = a->dw ? gw : gx;  // the first product launched
+  side.part = d.part;
+  side.parts = d.row_blocks;
+  side.db = a->db;
+  side.db_cols = a->n;
   if (a->dw && a->dx) return run_two_products(gw, gx, sms, s);
   if (a->dw) return run_product(gw, sms, s);
   if (a->dx) return run_product(gx, sms, s);

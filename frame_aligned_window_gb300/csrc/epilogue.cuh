@@ -132,4 +132,26 @@ struct GemmShared {
   int* status;
 };
 
+// Column c of the partial rows, summed in a fixed order (eight interleaved
+// sums, loads in flight together, then those in order).
+__device__ __forceinline__ float sum_column(const float* part, int64_t ld, int parts, int c) {
+  float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < parts; i += 8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < parts ? part[(i + j) * ld + c] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] += v[j];
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s += a[j];
+  return s;
+}
+// Thread `first` of `n` in all takes columns first, first + n, ...
+__device__ __forceinline__ void side_sums(const GemmParams& p, int first, int n) {
+  if (!p.db) return;
+  for (int c = first; c < p.db_cols; c += n) p.db[c] = sum_column(p.part, p.ldpart, p.parts, c);
+}
+
 }  // namespace wsattn

@@ -127,24 +127,12 @@ __global__ void __launch_bounds__(256) dact_kernel(DactParams p) {
   if (cc < p.cols) p.part[static_cast<int64_t>(blockIdx.y) * p.ldpart + cc] = t;
 }
 
-// Column sums from the row blocks' parts, in a fixed order: CTA x takes 32
-// columns, thread (c, g) parts g, g + 8, ...
-__global__ void __launch_bounds__(256) sum_parts(const float* __restrict__ part, int64_t ldpart,
-                                                 int blocks, int cols, float* __restrict__ out) {
-  __shared__ float red[8][33];
+__global__ void __launch_bounds__(128) sum_parts(const float* __restrict__ part, int64_t ldpart,
+                                                 int parts, int cols, float* __restrict__ out) {
   griddep_wait();
   griddep_launch_dependents();
-  const int c = 32 * static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.x);
-  float t = 0.f;
-  if (c < cols)
-    for (int i = threadIdx.y; i < blocks; i += 8) t += part[i * ldpart + c];
-  red[threadIdx.y][threadIdx.x] = t;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < cols) {
-    float s = 0.f;
-    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-    out[c] = s;
-  }
+  const int c = 128 * static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.x);
+  if (c < cols) out[c] = sum_column(part, ldpart, parts, c);
 }
 
 template <typename T, bool VEC>
@@ -187,25 +175,30 @@ cudaError_t launch_pack(int dtype, const PackJob& a, const PackJob& b, cudaStrea
              : launch_dependent(pack_kernel<__half>, grid, dim3(256), 0, s, a, b, na);
 }
 
-cudaError_t launch_dact(const DactParams& p, int dtype, float* db, cudaStream_t s) {
-  cudaError_t e;
+cudaError_t launch_dact(const DactParams& p, int dtype, cudaStream_t s) {
   if (dtype == WSATTN_BF16)
-    e = p.vec ? dact_t<__nv_bfloat16, true>(p, s) : dact_t<__nv_bfloat16, false>(p, s);
-  else
-    e = p.vec ? dact_t<__half, true>(p, s) : dact_t<__half, false>(p, s);
-  if (e != cudaSuccess || !db) return e;
-  return launch_dependent(sum_parts, dim3((p.cols + 31) / 32), dim3(32, 8), 0, s,
+    return p.vec ? dact_t<__nv_bfloat16, true>(p, s) : dact_t<__nv_bfloat16, false>(p, s);
+  return p.vec ? dact_t<__half, true>(p, s) : dact_t<__half, false>(p, s);
+}
+
+cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s) {
+  return launch_dependent(sum_parts, dim3((p.cols + 127) / 128), dim3(128), 0, s,
                           static_cast<const float*>(p.part), p.ldpart, p.row_blocks, p.cols, db);
 }
 
-// Estimated time of each tiling in nanoseconds, the least one wins.  From
-// timings of every tiling over a range of shapes (back to back, operands from
-// HBM): a 64-wide step of a pair's tile takes 320 ns at 256 columns and 285
-// at 128 (both move 96 and 84 KB per microsecond and SM from L2, which is
-// what bounds them), one of a single CTA the time of its bytes at that rate,
-// shared by the CTAs of an SM.
-constexpr double kPairStart = 4500.0, kPairTile = 500.0, kPairStep256 = 320.0,
-                 kPairStep128 = 285.0;
+// Estimated time of each tiling in nanoseconds; the least one wins.  The
+// constants are fitted to the timings of every tiling at 60 shapes (1 to
+// 20000 rows, 128 to 5120 columns and values, all three orders of the
+// operands, back to back with operands from HBM): the tiling taken is then
+// within 2 % of the best one on average, 1.47 at worst.
+//   pair   a 64-wide step of a 256-column tile takes 290 ns (the MMAs alone
+//          270 at full clocks), of a 128-column tile 269 (bound by the 24 KB a
+//          CTA reads of L2 for it); 1.4 to 2.5 us a tile for its epilogue
+//   tile   a step of a CTA takes the time of its bytes at 134 KB a
+//          microsecond and SM, shared by two CTAs, or 200 ns; a row of the
+//          tile 45 ns of epilogue, and the cluster's exchange 800 ns
+constexpr double kPairStart = 2670.0, kPairTile256 = 2520.0, kPairStep256 = 290.0,
+                 kPairTile128 = 1420.0, kPairStep128 = 269.0;
 
 GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns) {
   const int64_t ksteps = (K + kGemmK - 1) / kGemmK;
@@ -218,28 +211,33 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns) {
       best = s;
     }
   };
+  const double steps = static_cast<double>(ksteps);
   for (int bn = 256; bn >= 128; bn -= 128) {
-    const int64_t waves = cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2);
-    consider(kPairStart + static_cast<double>(waves) *
-                              (static_cast<double>(ksteps) *
-                                   (bn == 256 ? kPairStep256 : kPairStep128) + kPairTile),
+    const double waves = static_cast<double>(cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2));
+    consider(kPairStart + waves * (bn == 256 ? steps * kPairStep256 + kPairTile256
+                                             : steps * kPairStep128 + kPairTile128),
              GemmShape{bn, 0, 1});
   }
+  // SMs that clusters of `split` CTAs reach (the occupancy query's answer for
+  // one CTA an SM): they stay within a GPC, whose SMs need not divide evenly
+  static const struct { int split, of_152; } kSplits[] = {
+      {1, 152}, {2, 152}, {3, 138}, {4, 144}, {8, 120}};
   for (int bn = 16; bn <= 128; bn *= 2) {
     if (p_mn && bn < 64) continue;
     if (bn > 16 && bn / 2 >= R && !(p_mn && bn == 64)) continue;
-    for (int split = 1; split <= 8 && split <= ksteps; ++split) {
-      const int64_t ctas = cdiv(R, bn) * cdiv(C, kTileCols) * split;
-      const int64_t waves = cdiv(ctas, 2 * sms);
-      const int64_t per_sm = ctas > sms ? 2 : 1;
-      // bytes of a step at 100 KB a microsecond and SM, but no faster than
-      // the weights come from HBM, nor than one CTA's ring turns over
-      const double step = per_sm * (16.0 + bn / 8.0) * 10.0;
-      const double t = 2500.0 + (split > 1 ? 1200.0 : 0.0) +
-                       static_cast<double>(waves) *
-                           (static_cast<double>(cdiv(ksteps, split)) * (step > 230.0 ? step : 230.0) +
-                            600.0 + 8.0 * bn);
-      consider(t, GemmShape{0, bn, split});
+    const double rows = static_cast<double>(R < bn ? R : bn);
+    for (const auto& sp : kSplits) {
+      if (sp.split > ksteps) break;
+      const int64_t ctas = cdiv(R, bn) * cdiv(C, kTileCols) * sp.split;
+      const int64_t reach = static_cast<int64_t>(sms) * sp.of_152 / 152;
+      const double waves = static_cast<double>(cdiv(ctas, 2 * reach));
+      const double per_sm = ctas > reach ? 2.0 : 1.0;
+      const double bytes = per_sm * (16.0 + bn / 8.0) * 7.45, least = 203.0 + 1.6 * bn;
+      const double t = (sp.split > 1 ? 800.0 : 0.0) +
+                       waves * (static_cast<double>(cdiv(ksteps, sp.split)) *
+                                    (bytes > least ? bytes : least) +
+                                3170.0 + 13.7 * rows * per_sm / sp.split + 44.7 * rows);
+      consider(t, GemmShape{0, bn, sp.split});
     }
   }
   *ns = best_t;
@@ -252,7 +250,7 @@ double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb, 
     return static_cast<double>(cdiv(R, kPairRows) * cdiv(C, 256));
   };
   auto tile_ns = [&](int K) {
-    return static_cast<double>(cdiv(K, kGemmK)) * kPairStep256 + kPairTile;
+    return static_cast<double>(cdiv(K, kGemmK)) * kPairStep256 + kPairTile256;
   };
   const double na = tiles(Ra, Ca), nb = tiles(Rb, Cb), la = tile_ns(Ka), lb = tile_ns(Kb);
   const double longest = la > lb ? la : lb, shorter = la > lb ? lb : la;

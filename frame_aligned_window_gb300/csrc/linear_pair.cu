@@ -11,6 +11,7 @@
 //   warp 0      TMA: 64-wide contraction slices, ring of 5 (6 at 128 columns)
 //   warp 1      MMA issue (CTA 0 of the pair)
 //   warp 2      tensor memory
+//   warp 3      the bias gradient's partial sums, where there is one
 //   warps 4-11  epilogue: thread = row (TMEM lane), two warps per lane
 //               quarter, each on half of the tile's columns
 // P and Q may lie either way round (the contraction contiguous, or the
@@ -518,6 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
   } else if (warp == 1) {
     if (lane == 0 && rank == 0)
       mma_issuer<BN, TWO>(p, s, pair, pairs, tbase, !IsHalf<T>::value);
+  } else if (warp == 3) {
+    side_sums(p.g[0], static_cast<int>(blockIdx.x) * 32 + lane, static_cast<int>(gridDim.x) * 32);
   } else if (warp >= kEpiWarp0) {
     epilogue<T, O, BN, TWO>(p, s, staging, pair, pairs, rank, tbase);
   }

@@ -206,6 +206,9 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
   } else {
     if (p.bias && col < p.C) bias = to_f32(static_cast<const T*>(p.bias)[col]);
     if (split == 1 && p.res && col < p.C) load_res(p, row0, rows, col, res);
+    side_sums(p, static_cast<int>(blockIdx.x) * 128 + static_cast<int>(threadIdx.x) - 64,
+              static_cast<int>(gridDim.x) * 128);
+    __syncwarp();
     have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax);
     have = __all_sync(0xffffffffu, have);
     tc_fence_after();

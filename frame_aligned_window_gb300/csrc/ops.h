@@ -103,6 +103,12 @@ struct GemmParams {
   int split;           // CTAs (one cluster) that share the contraction
   int stages;
   int* status;         // device status word (bit set on an expired wait)
+  // the bias gradient: column sums of the slope pass's partial rows, added by
+  // warps that have nothing else to do meanwhile (db null: none)
+  const float* part;   // [parts, ldpart]
+  int64_t ldpart;
+  int parts, db_cols;
+  float* db;
 };
 
 // One launch of the CTA-pair kernel: one product, or two with the same types
@@ -171,7 +177,9 @@ struct DactParams {
   int row_blocks;
   int vec;          // dout and preact rows start on 16-byte boundaries
 };
-cudaError_t launch_dact(const DactParams& p, int dtype, float* db, cudaStream_t s);
+cudaError_t launch_dact(const DactParams& p, int dtype, cudaStream_t s);
+// db = sums of part's rows (where no product does it on the side).
+cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s);
 constexpr int kDactCols = 256;
 
 }  // namespace wsattn
