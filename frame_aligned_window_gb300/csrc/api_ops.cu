@@ -92,7 +92,8 @@ QkPart part_of(const wsattn_heads* in, const wsattn_heads* out, int norm, int tu
 
 // Lanes per head row, rows per CTA and, from the wanted number of work items
 // (a warp's worth of tokens times a group of heads), the heads a warp walks.
-void split_work(QkParams* p, int64_t rows, int64_t want_items, int min_heads) {
+// False: more CTAs than a launch may have.
+bool split_work(QkParams* p, int64_t rows, int64_t want_items, int min_heads) {
   const int pieces = p->rot.pairs / 8;
   p->lanes_log2 = 0;
   while ((1 << p->lanes_log2) < pieces) ++p->lanes_log2;
@@ -116,6 +117,7 @@ void split_work(QkParams* p, int64_t rows, int64_t want_items, int min_heads) {
     p->part[i].groups = static_cast<int>(cdiv(p->part[i].io.heads, gh));
     p->groups += p->part[i].groups;
   }
+  return p->row_blocks <= INT32_MAX / p->groups;
 }
 
 bool positions_ok(const float* positions, int64_t pos_stride_b) {
@@ -339,11 +341,12 @@ bool grad_args_ok(const wsattn_linear_grad_args* a) {
   return true;
 }
 
-// Rows of dout per CTA of the dact pass: enough CTAs to fill the machine
-// four times over, at least 32 rows each (the partial sums stay small).
-int dact_rows(int64_t m, int n, int sms) {
+// Rows of dout per CTA of the dact pass: about 608 CTAs (four an SM, a
+// constant, so that the workspace does not depend on the device), at least 32
+// rows each (the partial sums stay small).
+int dact_rows(int64_t m, int n) {
   const int64_t cols = cdiv(n, wsattn::kDactCols);
-  int64_t blocks = cdiv(static_cast<int64_t>(4) * sms, cols);
+  int64_t blocks = cdiv(608, cols);
   int64_t rows = cdiv(m, blocks < 1 ? 1 : blocks);
   rows = (rows + 31) / 32 * 32;
   if (cdiv(m, rows) > 65535) rows = (cdiv(m, 65535) + 31) / 32 * 32;
@@ -357,7 +360,7 @@ struct GradPlan {
   size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes; }
 };
 
-GradPlan plan_grad(const wsattn_linear_grad_args* a, int sms) {
+GradPlan plan_grad(const wsattn_linear_grad_args* a) {
   GradPlan g;
   std::memset(&g, 0, sizeof(g));
   if (a->m == 0) return g;
@@ -366,7 +369,7 @@ GradPlan plan_grad(const wsattn_linear_grad_args* a, int sms) {
   g.dz = products && (g.act || !tma_rows(a->dout, a->ldd, a->m));
   g.pack_x = a->dw && !tma_rows(a->x, a->ldx, a->m);
   g.pack_w = a->dx && !tma_rows(a->w, a->ldw, a->n);
-  g.rows_per_block = dact_rows(a->m, a->n, sms);
+  g.rows_per_block = dact_rows(a->m, a->n);
   g.row_blocks = static_cast<int>(cdiv(a->m, g.rows_per_block));
   if (g.dz) g.dz_bytes = packed_bytes(a->m, a->n);
   if (a->db) g.part_bytes = up256(sizeof(float) * static_cast<size_t>(g.row_blocks) * a->n);
@@ -437,7 +440,9 @@ int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
   p.pos = positions;
   p.pos_b = pos_stride_b;
   p.tokens = n_tokens;
-  split_work(&p, rows, 6LL * sms, 1);
+  p.status = wsattn::op_status_ptr();
+  if (!p.status) return WSATTN_ERR_CUDA;
+  if (!split_work(&p, rows, 6LL * sms, 1)) return WSATTN_ERR_BAD_ARG;
   const bool vec = view_vec(x, batch, n_tokens, esize) && view_vec(y, batch, n_tokens, esize);
   return wsattn::launch_qk_forward(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? WSATTN_OK
@@ -484,7 +489,9 @@ int wsattn_qknorm(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
   p.pos = positions;
   p.pos_b = pos_stride_b;
   p.tokens = n_tokens;
-  split_work(&p, rows, 6LL * sms, 1);
+  p.status = wsattn::op_status_ptr();
+  if (!p.status) return WSATTN_ERR_CUDA;
+  if (!split_work(&p, rows, 6LL * sms, 1)) return WSATTN_ERR_BAD_ARG;
   return wsattn::launch_qk_forward(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? WSATTN_OK
              : WSATTN_ERR_CUDA;
@@ -564,10 +571,12 @@ int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_
   p.pos = positions;
   p.pos_b = pos_stride_b;
   p.tokens = n_tokens;
+  p.status = wsattn::op_status_ptr();
+  if (!p.status) return WSATTN_ERR_CUDA;
   p.dw_part = gains ? static_cast<float*>(workspace) : nullptr;
   int64_t blocks = static_cast<int64_t>(sms) * wsattn::kQkBackCtasPerSm;
   if (blocks > kMaxBackCtas) blocks = kMaxBackCtas;
-  split_work(&p, rows, 32 * blocks, 4);
+  if (!split_work(&p, rows, 32 * blocks, 4)) return WSATTN_ERR_BAD_ARG;
   // no CTA without work of its own
   const int64_t items =
       p.row_blocks * static_cast<int64_t>(p.part[0].groups + p.part[1].groups);
@@ -637,9 +646,7 @@ int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace
 
 int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes) {
   if (!bytes || !grad_args_ok(args)) return WSATTN_ERR_BAD_ARG;
-  const int sms = sm_count();
-  if (!sms) return WSATTN_ERR_CUDA;
-  *bytes = plan_grad(args, sms).total();
+  *bytes = plan_grad(args).total();
   return WSATTN_OK;
 }
 
@@ -662,11 +669,11 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
   if (!a->dout || (a->dw && !a->x) || (a->dx && !a->w) ||
       (a->activation != WSATTN_ACT_NONE && !a->preact))
     return WSATTN_ERR_BAD_ARG;
-  const int sms = sm_count();
-  if (!sms) return WSATTN_ERR_CUDA;
-  const GradPlan plan = plan_grad(a, sms);
+  const GradPlan plan = plan_grad(a);
   if (plan.total() && (!workspace || !aligned16(workspace) || workspace_bytes < plan.total()))
     return WSATTN_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return WSATTN_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
   char* ws_dz = ws;
   char* ws_part = ws_dz + plan.dz_bytes;

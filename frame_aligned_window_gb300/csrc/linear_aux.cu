@@ -58,12 +58,15 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackJob a, const PackJo
 template <bool VEC>
 __device__ __forceinline__ uint4 load_raw8(const void* base, int64_t ld, int64_t r, int c, int cols) {
   const uint16_t* q = static_cast<const uint16_t*>(base) + r * ld + c;
-  if (VEC) return *reinterpret_cast<const uint4*>(q);
-  uint32_t w[4];
+  if constexpr (VEC) {
+    return *reinterpret_cast<const uint4*>(q);
+  } else {
+    uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    w[e] = (c + 2 * e < cols ? q[2 * e] : 0u) | (c + 2 * e + 1 < cols ? q[2 * e + 1] : 0u) << 16;
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int e = 0; e < 4; ++e)
+      w[e] = (c + 2 * e < cols ? q[2 * e] : 0u) | (c + 2 * e + 1 < cols ? q[2 * e + 1] : 0u) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // CTA (x, y): 256 columns of rows [y * rows_per_block, ...); a warp takes

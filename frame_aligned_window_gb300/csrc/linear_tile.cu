@@ -167,7 +167,11 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
   const int ksteps = (p.K + kGemmK - 1) / kGemmK;
   const int k0 = static_cast<int>(static_cast<int64_t>(ksteps) * rank / split);
   const int k1 = static_cast<int>(static_cast<int64_t>(ksteps) * (rank + 1) / split);
-  const bool tile_ok = WSATTN_BOUNDS(p.status, tc < p.tiles_c && k1 > k0 && k1 <= ksteps);
+  const bool tile_ok =
+      WSATTN_BOUNDS(p.status, tc < p.tiles_c && row0 < p.R && col0 < p.C && k1 > k0 &&
+                                  k1 <= ksteps && p.stages >= 1 && p.stages <= kMaxStages &&
+                                  (split == 1 || static_cast<uint32_t>(p.bn) * kTileCols * 4u <=
+                                                     static_cast<uint32_t>(p.stages) * stage));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {

@@ -62,6 +62,7 @@ struct QkParams {
   int group_heads;       // heads a warp walks for one token
   int groups;            // head groups of all parts together
   float* dw_part;        // backward: [2][blocks][D] partial gain gradients, or null
+  int* status;           // device status word (debug build: bounds checks)
 };
 
 // dtype: WSATTN_BF16, WSATTN_FP16 or WSATTN_FP32.  vec: every row starts on a

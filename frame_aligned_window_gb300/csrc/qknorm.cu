@@ -291,12 +291,15 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
   constexpr int kPerWarp = 32 >> LG;
   const int64_t row =
       (rb * (kQkThreads / 32) + threadIdx.x / 32) * kPerWarp + ((threadIdx.x & 31) >> LG);
-  const bool active = row < p.rows && ln.on;
   int pi = 0;
   while (pi + 1 < p.parts && g >= p.part[pi + 1].group0) ++pi;
   const QkPart& part = p.part[pi];
   const int h0 = (g - part.group0) * p.group_heads;
   const int heads = min(part.io.heads - h0, p.group_heads);
+  const bool active = row < p.rows && ln.on &&
+                      WSATTN_BOUNDS(p.status, g < p.groups && h0 >= 0 && heads >= 1 &&
+                                                  h0 + heads <= part.io.heads &&
+                                                  8 * ln.c + 8 <= ln.half);
   int64_t b = 0, n = 0;
   if (active) split_row(p, row, b, n);
   const int64_t sstep = part.io.ih, dstep = part.io.oh;
@@ -403,7 +406,11 @@ __device__ __forceinline__ void open_item(const QkParams& p, const Lane& ln, Bac
   c.heads = min(part.io.heads - (c.g - part.group0) * p.group_heads, p.group_heads);
   const int64_t row = (c.rb * (kQkThreads / 32) + threadIdx.x / 32) * (32 >> LG) +
                       ((threadIdx.x & 31) >> LG);
-  c.active = row < p.rows && ln.on;
+  c.active = row < p.rows && ln.on &&
+             WSATTN_BOUNDS(p.status, c.rb < p.row_blocks && c.heads >= 1 &&
+                                         (c.g - part.group0) * p.group_heads + c.heads <=
+                                             part.io.heads &&
+                                         8 * ln.c + 8 <= ln.half);
   c.b = c.n = 0;
   if (c.active) split_row(p, row, c.b, c.n);
 }
