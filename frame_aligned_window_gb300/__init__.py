@@ -762,8 +762,9 @@ def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, 
         ldr, rp = _rows(residual, "residual", n, lead, odt, dev), residual.data_ptr()
     if preact is not None:
         ldp, pp = _rows(preact, "preact", n, lead, dt, dev), preact.data_ptr()
-    # operands whose rows start on 16-byte boundaries need no workspace
-    plain = not (heads or (xp | wp) & 15 or (ldx | ldw) & 7)
+    # no workspace: operands whose rows start on 16-byte boundaries, and too
+    # little work for a contraction to be split
+    plain = not (heads or (xp | wp) & 15 or (ldx | ldw) & 7 or m * n * k >= 1 << 33)
     return _LINEAR(code, ocode, m, n, k, xp, ldx, heads, tokens, wp, ldw, bp, rp, ldr,
                    out.data_ptr(), ldo, pp, ldp, act), out, dev, plain
 
@@ -788,8 +789,9 @@ def wsattn_linear(x, weight, bias=None, residual=None, activation="none", preact
 
 
 def wsattn_linear_workspace(x, weight) -> int:
-    """Bytes of scratch wsattn_linear takes for these operands (0 when their
-    rows start on 16-byte boundaries and x is not the attention's output)."""
+    """Bytes of scratch wsattn_linear takes for these operands (0 for products
+    below 2^33 multiply-adds whose rows start on 16-byte boundaries, unless x
+    is the attention's output)."""
     args, _, dev, _ = _linear_args(x, weight, None, None, "none", None, None, None, None)
     n = _SZ()
     _run(dev, "wsattn_linear_workspace", _lib.wsattn_linear_workspace, args, ctypes.byref(n))

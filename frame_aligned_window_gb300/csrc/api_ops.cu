@@ -185,7 +185,7 @@ struct Product {
 
 // The kernel's parameters for one product under a tiling; false: a tensor
 // map could not be made, or the sizes exceed an int's range of tiles.
-bool fill(const Product& g, const wsattn::GemmShape& shape, GemmParams* out) {
+bool fill(const Product& g, const wsattn::GemmShape& shape, void* partial, GemmParams* out) {
   GemmParams& prm = *out;
   const CUtensorMapDataType type = g.dtype == WSATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -235,48 +235,58 @@ bool fill(const Product& g, const wsattn::GemmShape& shape, GemmParams* out) {
     tr = cdiv(g.R, shape.bn);
     tc = cdiv(g.C, wsattn::kTileCols);
     prm.bn = shape.bn;
-    prm.split = shape.split;
     // a ring of about 96 KB: two CTAs fit an SM
     prm.stages = 96 / (16 + shape.bn / 8);
   }
   prm.tiles_r = static_cast<int>(tr);
   prm.tiles_c = static_cast<int>(tc);
+  prm.split = shape.split;
+  prm.whole_tiles = shape.split > 1 ? shape.whole : static_cast<int>(tr * tc);
+  prm.partial = static_cast<float*>(partial);
   return tr * tc <= INT32_MAX;
 }
 
-int run_product(const Product& g, int sms, cudaStream_t s) {
+// partial: scratch of product_bytes(g).
+int run_product(const Product& g, int sms, void* partial, cudaStream_t s) {
   double ns = 0.0;
-  const wsattn::GemmShape shape = wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, sms, &ns);
+  const wsattn::GemmShape shape = wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, &ns);
   wsattn::PairParams pp;
   std::memset(&pp, 0, sizeof(pp));
-  if (!fill(g, shape, &pp.g[0])) return WSATTN_ERR_CUDA;
+  if (!fill(g, shape, partial, &pp.g[0])) return WSATTN_ERR_CUDA;
   const cudaError_t e =
       shape.pair_cols ? wsattn::launch_gemm_pair(&pp, g.dtype, g.out_f32, shape.pair_cols, sms, s)
                       : wsattn::launch_gemm_tile(pp.g[0], g.dtype, g.out_f32, s);
   return e == cudaSuccess ? WSATTN_OK : WSATTN_ERR_CUDA;
 }
 
-// Two products of the same types, in one launch where that is expected to be
-// the faster way.
-int run_two_products(const Product& g, const Product& h, int sms, cudaStream_t s) {
-  double ng = 0.0, nh = 0.0;
-  wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, sms, &ng);
-  wsattn::choose_gemm(h.R, h.C, h.K, h.p_mn, sms, &nh);
-  const double both = wsattn::pair_time_of_two(g.R, g.C, g.K, h.R, h.C, h.K, sms);
-  if (both > ng + nh) {
-    const int rc = run_product(g, sms, s);
-    return rc == WSATTN_OK ? run_product(h, sms, s) : rc;
-  }
-  const wsattn::GemmShape shape{256, 0, 1};
+// Scratch of one product's partial tiles.
+size_t product_bytes(int64_t R, int C, int K, bool p_mn) {
+  double ns = 0.0;
+  return wsattn::choose_gemm(R, C, K, p_mn, &ns).bytes(R, C);
+}
+
+// Whether both gradients of m rows, n and k features go out in one launch:
+// where that is expected to be the faster way.
+bool grads_together(int64_t m, int n, int k) {
+  double nw = 0.0, nx = 0.0;
+  wsattn::choose_gemm(n, k, static_cast<int>(m), true, &nw);
+  wsattn::choose_gemm(m, k, n, false, &nx);
+  return wsattn::pair_time_of_two(n, k, static_cast<int>(m), m, k, n) < nw + nx;
+}
+
+// Both in one launch; g carries the column sums.
+int run_together(const Product& g, const Product& h, int sms, cudaStream_t s) {
+  const wsattn::GemmShape shape{256, 0, 1, 0};
   const bool g_first = g.K >= h.K;
   wsattn::PairParams pp;
   std::memset(&pp, 0, sizeof(pp));
   Product first = g_first ? g : h;
-  first.part = g.part;  // g carries the column sums
+  first.part = g.part;
   first.parts = g.parts;
   first.db = g.db;
   first.db_cols = g.db_cols;
-  if (!fill(first, shape, &pp.g[0]) || !fill(g_first ? h : g, shape, &pp.g[1]))
+  if (!fill(first, shape, nullptr, &pp.g[0]) ||
+      !fill(g_first ? h : g, shape, nullptr, &pp.g[1]))
     return WSATTN_ERR_CUDA;
   return wsattn::launch_gemm_pair(&pp, g.dtype, g.out_f32, 256, sms, s) == cudaSuccess
              ? WSATTN_OK
@@ -327,7 +337,7 @@ size_t linear_ws(const wsattn_linear_args* a) {
   if (a->m == 0) return 0;
   if (a->x_heads > 0 || !tma_rows(a->x, a->ldx, a->m)) b += packed_bytes(a->m, a->k);
   if (!tma_rows(a->w, a->ldw, a->n)) b += packed_bytes(a->n, a->k);
-  return b;
+  return b + product_bytes(a->m, a->n, a->k, false);
 }
 
 bool grad_args_ok(const wsattn_linear_grad_args* a) {
@@ -354,10 +364,10 @@ int dact_rows(int64_t m, int n) {
 }
 
 struct GradPlan {
-  bool act, dz, pack_x, pack_w;
-  size_t dz_bytes, part_bytes, x_bytes, w_bytes;
+  bool act, dz, pack_x, pack_w, together;
+  size_t dz_bytes, part_bytes, x_bytes, w_bytes, tile_bytes;
   int rows_per_block, row_blocks;
-  size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes; }
+  size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes + tile_bytes; }
 };
 
 GradPlan plan_grad(const wsattn_linear_grad_args* a) {
@@ -375,6 +385,12 @@ GradPlan plan_grad(const wsattn_linear_grad_args* a) {
   if (a->db) g.part_bytes = up256(sizeof(float) * static_cast<size_t>(g.row_blocks) * a->n);
   if (g.pack_x) g.x_bytes = packed_bytes(a->m, a->k);
   if (g.pack_w) g.w_bytes = packed_bytes(a->n, a->k);
+  g.together = a->dw && a->dx && grads_together(a->m, a->n, a->k);
+  if (!g.together) {  // one after the other, through the same partial tiles
+    const size_t bw = a->dw ? product_bytes(a->n, a->k, static_cast<int>(a->m), true) : 0;
+    const size_t bx = a->dx ? product_bytes(a->m, a->k, a->n, false) : 0;
+    g.tile_bytes = bw > bx ? bw : bx;
+  }
   return g;
 }
 
@@ -628,6 +644,7 @@ int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace
   if (!tma_rows(a->w, a->ldw, a->n)) {
     jw = pack_job(a->w, a->ldw, a->n, a->k, ws);
     g.q = Operand{ws, jw.ldd};
+    ws += packed_bytes(a->n, a->k);
   }
   if (wsattn::launch_pack(a->dtype, jx, jw, s) != cudaSuccess) return WSATTN_ERR_CUDA;
   g.R = a->m;
@@ -641,7 +658,7 @@ int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace
   g.pre = a->preact;
   g.ldp = a->ldp;
   g.act = a->activation;
-  return run_product(g, sms, s);
+  return run_product(g, sms, ws, s);
 }
 
 int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes) {
@@ -679,6 +696,7 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
   char* ws_part = ws_dz + plan.dz_bytes;
   char* ws_x = ws_part + plan.part_bytes;
   char* ws_w = ws_x + plan.x_bytes;
+  char* ws_tiles = ws_w + plan.w_bytes;
   Operand dz{a->dout, a->ldd}, x{a->x, a->ldx}, w{a->w, a->ldw};
   wsattn::DactParams d;
   std::memset(&d, 0, sizeof(d));
@@ -741,10 +759,11 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
   side.parts = d.row_blocks;
   side.db = a->db;
   side.db_cols = a->n;
-  if (a->dw && a->dx) return run_two_products(gw, gx, sms, s);
-  if (a->dw) return run_product(gw, sms, s);
-  if (a->dx) return run_product(gx, sms, s);
-  return WSATTN_OK;
+  if (plan.together) return run_together(gw, gx, sms, s);
+  int rc = WSATTN_OK;
+  if (a->dw) rc = run_product(gw, sms, ws_tiles, s);
+  if (a->dx && rc == WSATTN_OK) rc = run_product(gx, sms, ws_tiles, s);
+  return rc;
 }
 
 int wsattn_op_status(void* stream) {

@@ -203,9 +203,10 @@ cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s) {
 constexpr double kPairStart = 2670.0, kPairTile256 = 2520.0, kPairStep256 = 290.0,
                  kPairTile128 = 1420.0, kPairStep128 = 269.0;
 
-GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns) {
+GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, double* ns) {
+  constexpr int sms = kTilingSms;
   const int64_t ksteps = (K + kGemmK - 1) / kGemmK;
-  GemmShape best{256, 0, 1};
+  GemmShape best{256, 0, 1, 0};
   double best_t = 1e300;
   auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   auto consider = [&](double t, const GemmShape& s) {
@@ -219,7 +220,24 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns) {
     const double waves = static_cast<double>(cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2));
     consider(kPairStart + waves * (bn == 256 ? steps * kPairStep256 + kPairTile256
                                              : steps * kPairStep128 + kPairTile128),
-             GemmShape{bn, 0, 1});
+             GemmShape{bn, 0, 1, 0});
+  }
+  // pairs whose last round is split: parts of at least 8 steps, one a pair.
+  // The partial tiles and the second kernel cost 4 us and 100 ns a part
+  // (dw of 5120 x 5120 over 21952 rows, 400 tiles: 690 us whole, 634 with the
+  // last 20 in 3 parts each; 1024 x 5120: 223 and 140), so not below 2^33
+  // multiply-adds, where that is what it could save
+  const int64_t tiles = cdiv(R, kPairRows) * cdiv(C, 256), pairs = sms / 2;
+  const int64_t rest = tiles % pairs;
+  if (rest > 0 && static_cast<double>(R) * C * K >= 8589934592.0) {
+    int64_t parts = pairs / rest;
+    if (parts > ksteps / 8) parts = ksteps / 8;
+    if (parts > 16) parts = 16;
+    if (parts >= 2 && tiles <= INT32_MAX)
+      consider(kPairStart + static_cast<double>(tiles / pairs) * (steps * kPairStep256 + kPairTile256) +
+                   static_cast<double>(cdiv(ksteps, parts)) * kPairStep256 + 4000.0 +
+                   100.0 * static_cast<double>(rest * parts),
+               GemmShape{256, 0, static_cast<int>(parts), static_cast<int>(tiles - rest)});
   }
   // SMs that clusters of `split` CTAs reach (the occupancy query's answer for
   // one CTA an SM): they stay within a GPC, whose SMs need not divide evenly
@@ -240,28 +258,41 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns) {
                        waves * (static_cast<double>(cdiv(ksteps, sp.split)) *
                                     (bytes > least ? bytes : least) +
                                 3170.0 + 13.7 * rows * per_sm / sp.split + 44.7 * rows);
-      consider(t, GemmShape{0, bn, sp.split});
+      consider(t, GemmShape{0, bn, sp.split, 0});
     }
   }
   *ns = best_t;
   return best;
 }
 
-double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb, int sms) {
+double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb) {
+  constexpr int64_t pairs = kTilingSms / 2;
   auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  auto tiles = [&](int64_t R, int C) {
-    return static_cast<double>(cdiv(R, kPairRows) * cdiv(C, 256));
-  };
+  if (Ka < Kb) return pair_time_of_two(Rb, Cb, Kb, Ra, Ca, Ka);
+  // the steps of a mixed launch take 8 % longer than one product's own (its
+  // pairs walk through L2 at different places)
   auto tile_ns = [&](int K) {
-    return static_cast<double>(cdiv(K, kGemmK)) * kPairStep256 + kPairTile256;
+    return static_cast<double>(cdiv(K, kGemmK)) * 1.08 * kPairStep256 + kPairTile256;
   };
-  const double na = tiles(Ra, Ca), nb = tiles(Rb, Cb), la = tile_ns(Ka), lb = tile_ns(Kb);
-  const double longest = la > lb ? la : lb, shorter = la > lb ? lb : la;
-  // all pairs busy to within one of the shorter tiles, or one round of the
-  // longer ones
-  const double even = (na * la + nb * lb) / (sms / 2) + 0.5 * shorter;
-  const double rounds = static_cast<double>(cdiv(static_cast<int64_t>(la > lb ? na : nb), sms / 2));
-  return kPairStart + (even > rounds * longest ? even : rounds * longest);
+  const int64_t na = cdiv(Ra, kPairRows) * cdiv(Ca, 256), nb = cdiv(Rb, kPairRows) * cdiv(Cb, 256);
+  const double la = tile_ns(Ka), lb = tile_ns(Kb);
+  // the pairs' loads as the kernel deals the tiles out
+  const int64_t full = na / pairs, rest = na % pairs;
+  double t;
+  if (rest == 0) {
+    t = static_cast<double>(full) * la + static_cast<double>(cdiv(nb, pairs)) * lb;
+  } else {
+    const int64_t others = pairs - rest, head = cdiv(cdiv(Ka, kGemmK), cdiv(Kb, kGemmK));
+    const int64_t left = nb > head * others ? nb - head * others : 0;
+    const int64_t rounds = left / pairs, extra = left % pairs;
+    const int64_t first = left > 0 ? head : cdiv(nb, others);
+    const double t1 = static_cast<double>(full + 1) * la +
+                      static_cast<double>(rounds + (extra > 0)) * lb;
+    const double t2 = static_cast<double>(full) * la +
+                      static_cast<double>(first + rounds + (extra > rest)) * lb;
+    t = t1 > t2 ? t1 : t2;
+  }
+  return kPairStart + t;
 }
 
 }  // namespace wsattn

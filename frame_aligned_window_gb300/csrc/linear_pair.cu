@@ -22,6 +22,11 @@
 // pairs at work together then read about 8 slices of P and 10 of Q, which
 // L2 serves to the others.
 //
+// When the last round of tiles would leave most pairs idle, its tiles are
+// split along the contraction instead (`split` parts each, one a pair): the
+// partial tiles go to the workspace in fp32, and a small kernel adds them in
+// order and applies the epilogue.
+//
 // One launch may hold two products (both gradients of a linear layer): the
 // tiles of the one with the longer contraction go round the pairs first and
 // the other's fill in behind them in the order in which pairs fall free, so
@@ -72,9 +77,10 @@ __device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t p
   return wait_slow(s, b, parity, code);
 }
 
-// A pair's it-th tile: which product, and its row and column tile.
+// A pair's it-th tile: which product, its row and column tile, the steps of
+// the contraction, and (part >= 0) which partial tile they make.
 struct TileRef {
-  int which, tr, tc;
+  int which, tr, tc, k0, k1, part;
 };
 
 __device__ __forceinline__ void tile_at(const GemmParams& p, int t, int& tr, int& tc) {
@@ -88,17 +94,31 @@ __device__ __forceinline__ void tile_at(const GemmParams& p, int t, int& tr, int
 template <bool TWO>
 __device__ __forceinline__ bool nth_tile(const PairParams& pp, int pair, int pairs, int it,
                                          TileRef& r) {
+  r.part = -1;
+  r.k0 = 0;
   if (!TWO) {
-    const int t = pair + it * pairs;
-    if (t >= pp.tiles_a) return false;
+    const GemmParams& p = pp.g[0];
+    int t = pair + it * pairs;
     r.which = 0;
-    tile_at(pp.g[0], t, r.tr, r.tc);
+    r.k1 = (p.K + kGemmK - 1) / kGemmK;
+    if (t >= p.whole_tiles) {
+      if (p.split < 2) return false;
+      const int u = t - p.whole_tiles, rest = pp.tiles_a - p.whole_tiles;
+      if (u >= rest * p.split) return false;
+      const int part = u / rest;
+      t = p.whole_tiles + u - part * rest;
+      r.part = (t - p.whole_tiles) * p.split + part;
+      r.k0 = static_cast<int>(static_cast<int64_t>(r.k1) * part / p.split);
+      r.k1 = static_cast<int>(static_cast<int64_t>(r.k1) * (part + 1) / p.split);
+    }
+    tile_at(p, t, r.tr, r.tc);
     return true;
   }
   const int full = pp.tiles_a / pairs, rest = pp.tiles_a - full * pairs;
   const int own = full + (pair < rest ? 1 : 0);
   if (it < own) {
     r.which = 0;
+    r.k1 = (pp.g[0].K + kGemmK - 1) / kGemmK;
     tile_at(pp.g[0], pair + it * pairs, r.tr, r.tc);
     return true;
   }
@@ -113,6 +133,7 @@ __device__ __forceinline__ bool nth_tile(const PairParams& pp, int pair, int pai
   }
   if (t >= pp.tiles_b) return false;
   r.which = 1;
+  r.k1 = (pp.g[1].K + kGemmK - 1) / kGemmK;
   tile_at(pp.g[1], t, r.tr, r.tc);
   return true;
 }
@@ -128,14 +149,15 @@ __device__ void producer(const PairParams& pp, const GemmShared& s, int pair, in
   for (int it = 0; ok && nth_tile<TWO>(pp, pair, pairs, it, ref); ++it) {
     const GemmParams& p = pp.g[TWO ? ref.which : 0];
     const int tr = ref.tr, tc = ref.tc;
-    const int ksteps = (p.K + kGemmK - 1) / kGemmK;
+    const int kt1 = ref.k1;
     const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
     const CUtensorMap* const tm_p = &p.tm_p;
     const CUtensorMap* const tm_q = &p.tm_q;
     const int row0 = tr * kPairRows + 128 * static_cast<int>(rank);
     const int col0 = tc * BN + BN / 2 * static_cast<int>(rank);
-    if (!WSATTN_BOUNDS(p.status, tr >= 0 && tr < p.tiles_r && tc >= 0 && tc < p.tiles_c)) break;
-    for (int kt = 0; kt < ksteps; ++kt) {
+    if (!WSATTN_BOUNDS(p.status, tr >= 0 && tr < p.tiles_r && tc >= 0 && tc < p.tiles_c))
+      break;
+    for (int kt = ref.k0; kt < kt1; ++kt) {
       if (!wait(s, bar(s, EMPTY0 + slot), phase ^ 1u, kStatusTimeoutProducer)) {
         ok = false;
         break;
@@ -193,19 +215,19 @@ __device__ void mma_issuer(const PairParams& pp, const GemmShared& s, int pair, 
     // own dimension contiguous: 16 rows of 128 bytes, 8 KB per 64 columns
     const uint32_t a_lbo = p.p_mn ? 8192u : 16u, b_lbo = p.q_mn ? 8192u : 16u;
     const uint64_t a_step = p.p_mn ? 128 : 2, b_step = p.q_mn ? 128 : 2;
-    const int ksteps = (p.K + kGemmK - 1) / kGemmK;
+    const int kt0 = ref.k0, kt1 = ref.k1;
     const uint32_t ab = it & 1u, use = it >> 1;
     if (!wait(s, bar(s, ACCEMPTY0 + ab), (use & 1u) ^ 1u, kStatusTimeoutMma)) return;
     tc_fence_after();
     const uint32_t d = tbase + ab * BN;
-    for (int kt = 0; kt < ksteps; ++kt) {
+    for (int kt = kt0; kt < kt1; ++kt) {
       if (!wait(s, bar(s, FULL0 + slot), phase, kStatusTimeoutMma)) return;
       tc_fence_after();
       const uint32_t a = s.stages + slot * kStage;
       const uint64_t ad = sdesc_sw128(a, a_lbo, 1024), bd = sdesc_sw128(a + kABytes, b_lbo, 1024);
 #pragma unroll
       for (int kk = 0; kk < kGemmK / 16; ++kk)
-        mma_ss_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kt | kk) != 0 ? 1u : 0u);
+        mma_ss_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, kt > kt0 || kk > 0 ? 1u : 0u);
       tc_commit_pair(bar(s, EMPTY0 + slot));
       if (++slot == kStages) {
         slot = 0;
@@ -325,6 +347,30 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
     const int64_t row0 = static_cast<int64_t>(tr) * kPairRows + 128 * rank + 32 * wq;
     const bool tile_ok =
         WSATTN_BOUNDS(p.status, tr >= 0 && tr < p.tiles_r && tc >= 0 && tc < p.tiles_c);
+    if (!TWO && ref.part >= 0) {  // fp32 partial tile [256][256] to global memory
+      const bool ok = wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax);
+      if (!__all_sync(0xffffffffu, ok)) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      float* dst = p.partial + static_cast<int64_t>(ref.part) * kPairRows * BN +
+                   static_cast<int64_t>(128 * rank + 32 * wq + lane) * BN + half * (BN / 2);
+#pragma unroll 1
+      for (int g = 0; tile_ok && g < BN / 32; ++g) {
+        uint32_t r[16];
+        tmem_ld16(tlane + ab * BN + half * (BN / 2) + 16 * g, r);
+        tmem_wait_ld16(r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(dst + 16 * g + 4 * i) =
+              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_free[ab]);
+      continue;
+    }
     bool waited = false;
 #pragma unroll 1
     for (int j = 0; j < BN / 2 / kCols; ++j) {
@@ -554,9 +600,51 @@ cudaError_t launch(PairParams* p, int sms, cudaStream_t s) {
   p->tiles_b = static_cast<int>(tb);
   const int ka = (p->g[0].K + kGemmK - 1) / kGemmK, kb = (p->g[1].K + kGemmK - 1) / kGemmK;
   p->head_rounds = tb > 0 ? (ka + kb - 1) / kb : 0;
-  const int pairs = static_cast<int>(ta + tb < sms / 2 ? ta + tb : sms / 2);
-  return launch_cluster(gemm_pair_kernel<T, O, BN, TWO>, dim3(2 * pairs), dim3(kThreads), 2, smem, s,
-                        *p);
+  const GemmParams& g = p->g[0];
+  // tiles and parts of tiles to deal out
+  const int64_t units = tb > 0 || g.split < 2 ? ta + tb
+                                              : g.whole_tiles + (ta - g.whole_tiles) * g.split;
+  const int pairs = static_cast<int>(units < sms / 2 ? units : sms / 2);
+  return launch_cluster(gemm_pair_kernel<T, O, BN, TWO>, dim3(2 * pairs), dim3(kThreads), 2, smem,
+                        s, *p);
+}
+
+// Sums of a split tile's partial tiles, with the epilogue.  A thread takes
+// four columns of a row; the parts are added in their order.
+template <typename T, typename O>
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ GemmParams p) {
+  constexpr int kTile = kPairRows * 256;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tile = static_cast<int>(blockIdx.x / (kTile / 1024));
+  const int e = static_cast<int>(blockIdx.x % (kTile / 1024)) * 1024 + 4 * static_cast<int>(threadIdx.x);
+  int tr, tc;
+  tile_at(p, p.whole_tiles + tile, tr, tc);
+  const int64_t row = static_cast<int64_t>(tr) * kPairRows + e / 256;
+  const int col = tc * 256 + e % 256;
+  if (row >= p.R || col >= p.C) return;
+  const float* src = p.partial + static_cast<int64_t>(tile) * p.split * kTile + e;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < p.split; ++i) {
+    const float4 q = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * kTile);
+    v.x += q.x;
+    v.y += q.y;
+    v.z += q.z;
+    v.w += q.w;
+  }
+  const float y4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = col + i;
+    if (c >= p.C) break;
+    float y = y4[i];
+    if (p.bias) y += to_f32(static_cast<const T*>(p.bias)[c]);
+    if (p.pre) static_cast<T*>(p.pre)[row * p.ldp + c] = from_f32<T>(y);
+    y = act_any(p.act, y);
+    if (p.res) y += to_f32(static_cast<const O*>(p.res)[row * p.ldr + c]);
+    static_cast<O*>(p.out)[row * p.ldo + c] = from_f32<O>(y);
+  }
 }
 
 template <typename T, typename O>
@@ -564,8 +652,13 @@ cudaError_t launch_bn(PairParams* p, int pair_cols, int sms, cudaStream_t s) {
   if constexpr (sizeof(O) == 2) {  // two products: the gradients, 256 columns
     if (p->g[1].tiles_r > 0) return launch<T, O, 256, true>(p, sms, s);
   }
-  return pair_cols == 256 ? launch<T, O, 256, false>(p, sms, s)
-                          : launch<T, O, 128, false>(p, sms, s);
+  if (pair_cols == 128) return launch<T, O, 128, false>(p, sms, s);
+  const cudaError_t e = launch<T, O, 256, false>(p, sms, s);
+  const GemmParams& g = p->g[0];
+  if (e != cudaSuccess || g.split < 2) return e;
+  const int rest = p->tiles_a - g.whole_tiles;
+  return launch_dependent(finish_kernel<T, O>, dim3(rest * (kPairRows * 256 / 1024)), dim3(256), 0,
+                          s, g);
 }
 
 }  // namespace

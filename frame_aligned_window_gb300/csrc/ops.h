@@ -99,9 +99,13 @@ struct GemmParams {
   int act;
   int bias_vec, res_vec, out_vec, pre_vec;  // 16-byte accesses hold
   int tiles_r, tiles_c;
-  // single-CTA tiles only
+  int split;           // parts of the contraction: the CTAs of a cluster (single-CTA
+                       // tiles), or of the pair kernel's last tiles
+  // CTA pairs
+  int whole_tiles;     // tiles before those that are split
+  float* partial;      // [(tiles - whole_tiles) * split][256][256]
+  // single-CTA tiles
   int bn;              // rows of a tile (the MMA's N)
-  int split;           // CTAs (one cluster) that share the contraction
   int stages;
   int* status;         // device status word (bit set on an expired wait)
   // the bias gradient: column sums of the slope pass's partial rows, added by
@@ -126,11 +130,21 @@ struct PairParams {
 struct GemmShape {
   int pair_cols;  // columns of a CTA pair's tile (256 or 128), 0: single-CTA tiles
   int bn;         // single-CTA tiles: rows per tile
-  int split;      // single-CTA tiles: CTAs per tile
+  int split;      // CTAs per tile; pairs: parts of each tile behind `whole`
+  int whole;      // pairs: tiles that are not split
+  // Scratch for the partial tiles.
+  size_t bytes(int64_t R, int C) const {
+    if (!pair_cols || split < 2) return 0;
+    const int64_t tiles = ((R + kPairRows - 1) / kPairRows) * ((C + pair_cols - 1) / pair_cols);
+    return static_cast<size_t>(tiles - whole) * split * kPairRows * pair_cols * sizeof(float);
+  }
 };
-GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, int sms, double* ns);
+// Tilings are chosen for 152 SMs whatever the device has (they stay right on
+// any), so that a workspace's size needs no device.
+constexpr int kTilingSms = 152;
+GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, double* ns);
 // Estimated nanoseconds of two products in one launch of the pair kernel.
-double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb, int sms);
+double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb);
 
 size_t pair_smem_bytes(int pair_cols);
 size_t tile_smem_bytes(int bn, int stages);

@@ -348,8 +348,9 @@ enum wsattn_activation {
  *              rounded to dtype, for wsattn_linear_backward
  * Rows of any stride and alignment are accepted; x and w with rows that are
  * not 16-byte aligned are first copied to the workspace, and so is x with
- * x_heads.  workspace: wsattn_linear_workspace bytes, 16-byte aligned (NULL
- * when that is 0).
+ * x_heads; products of 2^33 multiply-adds and more may also keep partial
+ * sums there.  workspace: wsattn_linear_workspace bytes, 16-byte aligned
+ * (NULL when that is 0).
  * Errors: BAD_ARG (also a workspace too small), UNSUPPORTED (dtypes), CUDA.
  */
 typedef struct wsattn_linear_args {

@@ -174,6 +174,8 @@ def test_early_start_waits_for_the_results_before():
 
 
 RERUN = ["tests/test_gpu_linear.py::test_linear_shapes", "tests/test_gpu_linear.py::test_linear_backward",
+         "tests/test_gpu_linear.py::test_linear_split_contraction",
+         "tests/test_gpu_linear.py::test_linear_backward_split_contraction",
          "tests/test_gpu_linear.py::test_linear_strided_rows_and_residual_in_place",
          "tests/test_gpu_linear.py::test_linear_of_attention_output",
          "tests/test_gpu_qknorm.py::test_rotary", "tests/test_gpu_qknorm.py::test_qknorm",

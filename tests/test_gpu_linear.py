@@ -63,6 +63,51 @@ def test_linear_shapes(shape, dt):
     _check_forward(_fw(), x, w, None, None, "none", dt, dt, want_pre=False)
 
 
+@pytest.mark.parametrize("odt", [torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("shape", [(300, 512, 57600), (261, 501, 66001)], ids=lambda c: "x".join(map(str, c)))
+def test_linear_split_contraction(shape, odt):
+    # four tiles of 256 x 256 and a long contraction: 16 parts each, added by
+    # a second kernel with the epilogue
+    fw = _fw()
+    m, n, k = shape
+    x, w, b, r = _case(m, n, k, torch.float16, 12)
+    x, w = x.cuda(), w.cuda()
+    assert fw.wsattn_linear_workspace(x, w) >= 4 * 16 * 256 * 256 * 4
+    z = (x.double() @ w.double().t()).cpu() + b.double()
+    ztol = product_tol((x.double().abs() @ w.double().abs().t()).cpu() + b.double().abs(), k)
+    pre = torch.empty((m, n), dtype=torch.float16, device="cuda")
+    got = fw.wsattn_linear(x, w, b.cuda(), r.to(odt).cuda(), "gelu_tanh", preact=pre, out_dtype=odt)
+    torch.cuda.synchronize()
+    assert fw.wsattn_op_status() == 0
+    want = act(z, "gelu_tanh") + r.to(odt).double()
+    assert_close(got, want, 1.13 * ztol + 2.0 ** -20 * z.abs() + half_step(odt) * want.abs() + tiny(odt))
+    assert_close(pre, z, ztol + half_step(torch.float16) * z.abs() + tiny(torch.float16))
+    buf = r.to(odt).cuda()     # the residual in place: the same values
+    fw.wsattn_linear(x, w, b.cuda(), buf, "gelu_tanh", out=buf)
+    assert torch.equal(buf, got)
+
+
+def test_linear_backward_split_contraction():
+    # dw [300, 500] over 57601 rows is split, dx is not; one after the other
+    fw = _fw()
+    m, n, k = 57601, 300, 500
+    dt = torch.bfloat16
+    x, w, _, _ = _case(m, n, k, dt, 21)
+    dy = (0.3 * torch.randn((m, n), generator=torch.Generator().manual_seed(1))).to(dt)
+    args = (dy.cuda(), x.cuda(), w.cuda())
+    assert fw.wsattn_linear_backward_workspace(*args, need_db=False) >= 4 * 16 * 256 * 256 * 4
+    dx, dw, _ = fw.wsattn_linear_backward(*args, need_db=False)
+    torch.cuda.synchronize()
+    assert fw.wsattn_op_status() == 0
+    d, xd, wd = (t.double() for t in args)
+    for got, want, mag, kk in ((dx, d @ wd, d.abs() @ wd.abs(), n),
+                               (dw, d.t() @ xd, d.abs().t() @ xd.abs(), m)):
+        want, mag = want.cpu(), mag.cpu()
+        assert_close(got, want, product_tol(mag, kk) + half_step(dt) * want.abs() + tiny(dt))
+    again = fw.wsattn_linear_backward(*args, need_db=False)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
 @pytest.mark.parametrize("name", ["none", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("odt", [torch.bfloat16, torch.float32], ids=str)
 @pytest.mark.parametrize("shape", [(5, 200, 136), (600, 700, 264), (1100, 2056, 72), (513, 131, 72)],
