@@ -70,13 +70,13 @@ __device__ __forceinline__ uint4 load_raw8(const void* base, int64_t ld, int64_t
 }
 
 // CTA (x, y): 256 columns of rows [y * rows_per_block, ...); a warp takes
-// every eighth row, a lane 8 columns of it, four rows' loads in flight.
+// every eighth row, a lane 8 columns of it, two rows' loads in flight.
 // Bound by HBM (dout and preact in, dz out).  The sums stay in fp32
 // registers (of the unrounded dz), then go through shared memory in the
 // order of the warps.
 template <typename T, bool VEC, int ACT>
-__global__ void __launch_bounds__(256) dact_kernel(DactParams p) {
-  constexpr int U = 4;
+__global__ void __launch_bounds__(256, 4) dact_kernel(DactParams p) {
+  constexpr int U = 2;
   __shared__ float red[8][kDactCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int c = static_cast<int>(blockIdx.x) * kDactCols + 8 * lane;
