@@ -193,7 +193,7 @@ cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s) {
 // constants are fitted to the timings of every tiling at 60 shapes (1 to
 // 20000 rows, 128 to 5120 columns and values, all three orders of the
 // operands, back to back with operands from HBM): the tiling taken is then
-// within 2 % of the best one on average, 1.47 at worst.
+// within 5 % of the best one on average, 1.33 at worst.
 //   pair   a 64-wide step of a 256-column tile takes 290 ns (the MMAs alone
 //          270 at full clocks), of a 128-column tile 269 (bound by the 24 KB a
 //          CTA reads of L2 for it); 1.4 to 2.5 us a tile for its epilogue

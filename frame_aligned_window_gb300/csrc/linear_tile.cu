@@ -13,8 +13,8 @@
 // not depend on timing and no partial result goes to global memory.
 //   warp 0     TMA
 //   warp 1     MMA issue, tensor memory
-//   warps 2-5  epilogue: thread = output column (TMEM lane), so that lanes
-//              write neighbouring values of an output row
+//   warps 2-5  epilogue: the accumulator goes to shared memory (over the idle
+//              ring), from where a warp takes whole rows of 128 columns
 #include "epilogue.cuh"
 #include "ptx.cuh"
 
@@ -114,30 +114,102 @@ __device__ void mma_issuer(const GemmParams& p, const GemmShared& s, int steps, 
   tc_commit(bar(s, ACCFULL));
 }
 
-// N outputs of one column in consecutive rows: bias, pre-activation,
-// activation, residual, one rounding.  The residuals are read first, all in
-// flight together (load_res), the accumulators come next.
-template <typename O, int N>
-__device__ __forceinline__ void load_res(const GemmParams& p, int64_t row, int rows, int col,
-                                         O (&r)[N]) {
-  const O* src = static_cast<const O*>(p.res) + row * p.ldr + col;
+// Four consecutive columns of a row, from or to global memory: one access
+// where the row allows it and all four are inside, else one by one.
+template <typename E>
+__device__ __forceinline__ void load4(const void* base, int64_t ld, int64_t row, int col, int C,
+                                      bool vec, float (&v)[4]) {
+  const E* p = static_cast<const E*>(base) + row * ld + col;
+  if (vec && col + 4 <= C) {
+    if constexpr (sizeof(E) == 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      const float2 lo = unpack_pair(q.x, E()), hi = unpack_pair(q.y, E());
+      v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i < rows) r[i] = src[i * p.ldr];
+    for (int i = 0; i < 4; ++i) v[i] = col + i < C ? to_f32(p[i]) : 0.f;
+  }
 }
-template <typename T, typename O, int N>
-__device__ __forceinline__ void emit(const GemmParams& p, int64_t row, int rows, int col, float bias,
-                                     const float (&v)[N], const O (&r)[N]) {
-  T* pre = p.pre ? static_cast<T*>(p.pre) + row * p.ldp + col : nullptr;
-  O* out = static_cast<O*>(p.out) + row * p.ldo + col;
+template <typename E>
+__device__ __forceinline__ void store4(void* base, int64_t ld, int64_t row, int col, int C, bool vec,
+                                       const float (&v)[4]) {
+  E* p = static_cast<E*>(base) + row * ld + col;
+  if (vec && col + 4 <= C) {
+    if constexpr (sizeof(E) == 4)
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(p) =
+          make_uint2(pack_pair(v[0], v[1], E()), pack_pair(v[2], v[3], E()));
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i >= rows) break;
-    float y = v[i] + bias;
-    if (pre) pre[i * p.ldp] = from_f32<T>(y);
-    y = act_any(p.act, y);
-    if (p.res) y += to_f32(r[i]);
-    out[i * p.ldo] = from_f32<O>(y);
+    for (int i = 0; i < 4; ++i)
+      if (col + i < C) p[i] = from_f32<E>(v[i]);
+  }
+}
+
+// Rows [j0, j1) of the tile from the partial tiles of `split` CTAs, summed in
+// the order of their ranks.  A warp takes U of its rows at a time (every
+// fourth row of the tile is its own), a lane four columns: the residuals, and
+// the loads from Q CTAs, are in flight together.
+template <typename T, typename O, int U, int Q>
+__device__ void finish_rows(const GemmParams& p, uint32_t part, int split, int64_t row0, int j0,
+                            int j1, int col, int warp) {
+  const int lane = threadIdx.x & 31;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.bias) load4<T>(p.bias, 0, 0, col, p.C, false, bias);
+  const uint32_t mine = part + 16u * static_cast<uint32_t>(lane);
+  for (int j = j0 + warp; j < j1; j += 4 * U) {
+    float res[U][4], v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (p.res && j + 4 * u < j1)
+        load4<O>(p.res, p.ldr, row0 + j + 4 * u, col, p.C, p.res_vec != 0, res[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
+    for (int q = 0; q < split; q += Q) {
+      float4 t[Q][U];
+#pragma unroll
+      for (int k = 0; k < Q; ++k) {
+        const uint32_t from =
+            map_to_rank(mine, static_cast<uint32_t>(q + k < split ? q + k : split - 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t a = static_cast<uint32_t>(min(j + 4 * u, j1 - 1)) * kTileCols * 4u;
+          t[k][u] = ld_cluster_v4(from + a);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < Q; ++k)
+        if (q + k < split)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            v[u][0] += t[k][u].x;
+            v[u][1] += t[k][u].y;
+            v[u][2] += t[k][u].z;
+            v[u][3] += t[k][u].w;
+          }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j + 4 * u >= j1) break;
+      const int64_t row = row0 + j + 4 * u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] += bias[i];
+      if (p.pre) store4<T>(p.pre, p.ldp, row, col, p.C, p.pre_vec != 0, v[u]);
+      if (p.act != WSATTN_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = act_any(p.act, v[u][i]);
+      }
+      if (p.res) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] += res[u][i];
+      }
+      store4<O>(p.out, p.ldo, row, col, p.C, p.out_vec != 0, v[u]);
+    }
   }
 }
 
@@ -196,78 +268,46 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
   // the next kernel's set-up may overlap this one (it waits for its results)
   griddep_launch_dependents();
 
-  bool have = false;  // epilogue threads: the accumulator is complete
-  const int quad = warp & 3;
-  const int c = 32 * quad + lane, col = col0 + c;
-  const uint32_t tlane = tbase + (static_cast<uint32_t>(32 * quad) << 16);
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.bn), p.R - row0));
-  float bias = 0.f;
-  O res[16];
   if (warp == 0) {
     if (lane == 0 && tile_ok) producer(p, s, row0, col0, k0, k1);
   } else if (warp == 1) {
     if (lane == 0 && tile_ok) mma_issuer(p, s, k1 - k0, tbase, !IsHalf<T>::value);
   } else {
-    if (p.bias && col < p.C) bias = to_f32(static_cast<const T*>(p.bias)[col]);
-    if (split == 1 && p.res && col < p.C) load_res(p, row0, rows, col, res);
     side_sums(p, static_cast<int>(blockIdx.x) * 128 + static_cast<int>(threadIdx.x) - 64,
               static_cast<int>(gridDim.x) * 128);
     __syncwarp();
-    have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax);
+    bool have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax);
     have = __all_sync(0xffffffffu, have);
     tc_fence_after();
     if (have) {
-      for (int j = 0; j < p.bn; j += 16) {
+      // the operand ring is idle now (every MMA of this CTA is complete): it
+      // takes the tile, [row][128 columns] in fp32
+      const int quad = warp & 3;
+      const uint32_t tlane = tbase + (static_cast<uint32_t>(32 * quad) << 16);
+      float* part = reinterpret_cast<float*>(smem_raw + (base - raw)) + 32 * quad + lane;
+#pragma unroll 1
+      for (int j = 0; j < rows; j += 16) {
         uint32_t a[16];
         tmem_ld16(tlane + j, a);
-        if (split == 1) {
-          if (j > 0 && p.res && col < p.C) load_res(p, row0 + j, rows - j, col, res);
-          tmem_wait_ld16(a);
-          float v[16];
+        tmem_wait_ld16(a);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
-          if (col < p.C) emit<T, O>(p, row0 + j, rows - j, col, bias, v, res);
-        } else {
-          // the operand ring is idle now (every MMA of this CTA is complete):
-          // it takes the partial tile, [row][128 columns]
-          tmem_wait_ld16(a);
-          float* part = reinterpret_cast<float*>(smem_raw + (base - raw));
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (j + i < rows) part[(j + i) * kTileCols + c] = __uint_as_float(a[i]);
-        }
+        for (int i = 0; i < 16; ++i)
+          if (j + i < rows) part[(j + i) * kTileCols] = __uint_as_float(a[i]);
       }
     }
   }
   __syncwarp();
+  if (split > 1) cluster_sync();  // every CTA's partial tile is in its shared memory
+  else __syncthreads();
+  if (warp >= 2 && tile_ok && *s.abort_flag == 0) {
+    const int j0 = rows * rank / split, j1 = rows * (rank + 1) / split, col = col0 + 4 * lane;
+    if (j1 - j0 <= 4)  // a row a warp: everything it needs at once
+      finish_rows<T, O, 1, 8>(p, base, split, row0, j0, j1, col, warp - 2);
+    else
+      finish_rows<T, O, 4, 2>(p, base, split, row0, j0, j1, col, warp - 2);
+  }
   if (split > 1) {
-    cluster_sync();  // every CTA's partial tile is in its shared memory
-    if (warp >= 2 && col < p.C) {
-      const int j0 = rows * rank / split, j1 = rows * (rank + 1) / split;
-      for (int j = j0; j < j1; j += 8) {
-        const int n = min(8, j1 - j);
-        O r8[8];
-        if (p.res) load_res(p, row0 + j, n, col, r8);
-        const uint32_t a = base + static_cast<uint32_t>(j * kTileCols + c) * 4u;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int q = 0; q < split; q += 4) {  // up to 32 remote loads in flight
-          float t[4][8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              t[k][i] = q + k < split && i < n
-                            ? ld_cluster_f32(map_to_rank(a + 4u * kTileCols * i,
-                                                         static_cast<uint32_t>(q + k)))
-                            : 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += t[k][i];
-        }
-        emit<T, O>(p, row0 + j, n, col, bias, v, r8);
-      }
-    }
     __syncwarp();
     cluster_sync();  // no CTA leaves while others read its shared memory
   }
