@@ -18,7 +18,7 @@ constexpr int kRotMaxAxes = 4;
 // Per-pair turning rates, passed to the kernels by value.  A pair turns by
 // pos[axis] * (hi + lo) revolutions: freq / 2 pi split into two floats, so
 // that the product keeps 48 bits and far positions lose nothing.
-struct RotTable {
+struct alignas(16) RotTable {
   float hi[kRotMaxPairs];
   float lo[kRotMaxPairs];
   uint8_t axis[kRotMaxPairs];

@@ -163,11 +163,27 @@ __device__ __forceinline__ void split_row(const QkParams& p, int64_t row, int64_
   }
 }
 
-// Pair i (0..7) of a lane: interleaved, pairs 4c .. 4c+3 of the first half
-// and D/4 + 4c .. of the second; split, pairs 8c .. 8c+7.
-__device__ __forceinline__ int pair_index(const RotTable& t, const Lane& ln, int i) {
-  if (!t.interleaved) return 8 * ln.c + i;
-  return (i < 4 ? 0 : ln.half / 2) + 4 * ln.c + (i & 3);
+// The rates of a lane's eight pairs: interleaved, pairs 4c .. 4c+3 of the
+// first half and D/4 + 4c .. of the second; split, pairs 8c .. 8c+7.  They
+// are read from the kernel's parameters through generic addresses: indexed
+// reads of constant memory would go lane by lane.
+struct Rates {
+  float4 hi[2], lo[2];
+  uint32_t axis[2];  // four bytes each
+};
+__device__ __forceinline__ Rates lane_rates(const RotTable& t, const Lane& ln) {
+  const int i0 = t.interleaved ? 4 * ln.c : 8 * ln.c;
+  const int i1 = t.interleaved ? ln.half / 2 + 4 * ln.c : 8 * ln.c + 4;
+  const RotTable* g = &t;
+  asm volatile("" : "+l"(g));  // an address like any other from here on
+  Rates r;
+  r.hi[0] = *reinterpret_cast<const float4*>(g->hi + i0);
+  r.hi[1] = *reinterpret_cast<const float4*>(g->hi + i1);
+  r.lo[0] = *reinterpret_cast<const float4*>(g->lo + i0);
+  r.lo[1] = *reinterpret_cast<const float4*>(g->lo + i1);
+  r.axis[0] = *reinterpret_cast<const uint32_t*>(g->axis + i0);
+  r.axis[1] = *reinterpret_cast<const uint32_t*>(g->axis + i1);
+  return r;
 }
 
 __device__ __forceinline__ void lane_angles(const RotTable& t, const Lane& ln, const float* pos,
@@ -175,15 +191,17 @@ __device__ __forceinline__ void lane_angles(const RotTable& t, const Lane& ln, c
   float x[kRotMaxAxes];
 #pragma unroll
   for (int a = 0; a < kRotMaxAxes; ++a) x[a] = a < t.axes ? pos[a] : 0.f;
+  const Rates r = lane_rates(t, ln);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int p = pair_index(t, ln, i);
-    const int a = t.axis[p];
+    const float4 h4 = r.hi[i >> 2], l4 = r.lo[i >> 2];
+    const float w = (i & 3) == 0 ? h4.x : (i & 3) == 1 ? h4.y : (i & 3) == 2 ? h4.z : h4.w;
+    const float wl = (i & 3) == 0 ? l4.x : (i & 3) == 1 ? l4.y : (i & 3) == 2 ? l4.z : l4.w;
+    const uint32_t a = r.axis[i >> 2] >> (8 * (i & 3)) & 255u;
     const float v = a < 2 ? (a == 0 ? x[0] : x[1]) : (a == 2 ? x[2] : x[3]);
-    const float w = t.hi[p];
     const float hi = v * w;
     const float err = fmaf(v, w, -hi);
-    const float frac = (hi - rintf(hi)) + fmaf(v, t.lo[p], err);
+    const float frac = (hi - rintf(hi)) + fmaf(v, wl, err);
     float s, c;
     sincospif(2.f * frac, &s, &c);
     cs[i] = c;
@@ -219,21 +237,25 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+template <typename E>
+__device__ __forceinline__ void gain16(const void* weight, const Lane& ln, float (&w)[16]) {
+  const E* g = static_cast<const E*>(weight) + 8 * ln.c;
+  if ((reinterpret_cast<uintptr_t>(weight) & 15u) == 0) {
+    unpack8(load8<true>(g), w);
+    unpack8(load8<true>(g + ln.half), w + 8);
+  } else {
+    unpack8(load8<false>(g), w);
+    unpack8(load8<false>(g + ln.half), w + 8);
+  }
+}
 template <typename T>
 __device__ __forceinline__ void load_gain(const QkParams& p, const QkPart& part, const Lane& ln,
                                           float (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = 1.f;
   if (!part.weight || !ln.on) return;
-  if (p.weight_f32) {
-    const float* g = static_cast<const float*>(part.weight) + 8 * ln.c;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = g[(i < 8 ? 0 : ln.half) + (i & 7)];
-  } else {
-    const T* g = static_cast<const T*>(part.weight) + 8 * ln.c;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = static_cast<float>(g[(i < 8 ? 0 : ln.half) + (i & 7)]);
-  }
+  if (p.weight_f32) gain16<float>(part.weight, ln, w);
+  else gain16<T>(part.weight, ln, w);
 }
 
 template <bool VEC>
@@ -284,7 +306,9 @@ __device__ __forceinline__ void copy_heads(const T* src, int64_t sstep, T* dst, 
 // One warp: the heads of one group, each lane group for one token.
 template <typename T, bool VEC, int LG, bool NORM>
 __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_constant__ QkParams p) {
-  constexpr int U = sizeof(T) == 4 ? 2 : 4;  // heads whose loads are in flight together
+  // heads whose loads are in flight together (with the norm's registers, four of
+  // 16 bits are 2 % faster at 40 heads, two 5 to 30 % at 12 and fewer)
+  constexpr int U = sizeof(T) == 4 || NORM ? 2 : 4;
   const Lane ln = make_lane<LG>(p.rot);
   const int g = static_cast<int>(blockIdx.x % p.groups);
   const int64_t rb = blockIdx.x / p.groups;
@@ -335,26 +359,33 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
   const float inv_d = 0.5f / static_cast<float>(p.rot.pairs);
   const bool inter = p.rot.interleaved != 0;
 
+  auto head = [&](int u) {
+    float x[16];
+    unpack8(r0[u], x);
+    unpack8(r1[u], x + 8);
+    if (NORM) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+      const float r = rsqrtf(fmaf(row_sum<LG>(ss), inv_d, p.eps));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= r * w[i];
+    }
+    turn16(x, cs, sn, inter);
+    if (active) {
+      store8<VEC>(dst + u * dstep, x);
+      store8<VEC>(dst + u * dstep + ln.half, x + 8);
+    }
+  };
   for (int h = 0; h < heads; h += U) {
     if (h > 0) load(heads - h);
+    if (heads - h >= U) {  // all of them, interleaved by the compiler
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[16];
-      unpack8(r0[u], x);
-      unpack8(r1[u], x + 8);
-      if (NORM) {
-        float ss = 0.f;
+      for (int u = 0; u < U; ++u) head(u);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-        const float r = rsqrtf(fmaf(row_sum<LG>(ss), inv_d, p.eps));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= r * w[i];
-      }
-      turn16(x, cs, sn, inter);
-      if (active && u < heads - h) {
-        store8<VEC>(dst + u * dstep, x);
-        store8<VEC>(dst + u * dstep + ln.half, x + 8);
-      }
+      for (int u = 0; u < U; ++u)
+        if (u < heads - h) head(u);
     }
     src += U * sstep;
     dst += U * dstep;

@@ -319,3 +319,30 @@ def test_capture_and_other_stream():
     c = fw.wsattn_qknorm_backward(rot, up, up, q, q, pos, w, w, stream=side)
     side.synchronize()
     assert torch.equal(c[0], bwd[0]) and torch.equal(c[3], bwd[3])
+
+
+@pytest.mark.parametrize("heads,kv", [(2, 1), (24, 24)])
+def test_qknorm_many_tokens(heads, kv):
+    # enough tokens for several rounds of CTAs, with few heads (one warp walks
+    # q, k and v of its tokens) and with many (head groups of their own)
+    fw = _fw()
+    B, N, D, eps = 2, 10007, 32, 1e-6
+    g = _gen(31)
+    rows = torch.randn((B, N, heads + 2 * kv, D), generator=g).to(torch.bfloat16)
+    t = rows.transpose(1, 2)
+    parts = t[:, :heads], t[:, heads:heads + kv], t[:, heads + kv:]
+    w = [(1 + 0.3 * torch.randn(D + 1, generator=g))[1:] for _ in range(2)]
+    pos = _positions(N, 2, g, batch=B)
+    sec = sections_for(D, 2)
+    rot = fw.wsattn_rotary_plan(D, sec)
+    dev = rows.cuda().transpose(1, 2)
+    wd = [torch.empty(D + 1, device="cuda")[1:].copy_(x) for x in w]   # gains off 16 bytes
+    got = fw.wsattn_qknorm(rot, dev[:, :heads], dev[:, heads:heads + kv], pos.cuda(), wd[0], wd[1],
+                           eps, v=dev[:, heads + kv:])
+    ang = angles(pos, sec, D)
+    for i in range(2):
+        _, y, _ = normed(parts[i].double(), w[i].double(), eps)
+        want = turn(y, ang, True)
+        tol = half_step(torch.bfloat16) * want.abs() + (TURN + 2 * NORM) * _pairmax(y, True)
+        assert_close(got[i], want, tol + tiny(torch.bfloat16), f"part {i}")
+    assert torch.equal(got[2].cpu(), parts[2])
