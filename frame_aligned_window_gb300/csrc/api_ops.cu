@@ -246,10 +246,9 @@ bool fill(const Product& g, const wsattn::GemmShape& shape, void* partial, GemmP
   return tr * tc <= INT32_MAX;
 }
 
-// partial: scratch of product_bytes(g).
-int run_product(const Product& g, int sms, void* partial, cudaStream_t s) {
-  double ns = 0.0;
-  const wsattn::GemmShape shape = wsattn::choose_gemm(g.R, g.C, g.K, g.p_mn, &ns);
+// partial: scratch of shape.bytes(g.R, g.C).
+int run_product(const Product& g, const wsattn::GemmShape& shape, int sms, void* partial,
+                cudaStream_t s) {
   wsattn::PairParams pp;
   std::memset(&pp, 0, sizeof(pp));
   if (!fill(g, shape, partial, &pp.g[0])) return WSATTN_ERR_CUDA;
@@ -257,21 +256,6 @@ int run_product(const Product& g, int sms, void* partial, cudaStream_t s) {
       shape.pair_cols ? wsattn::launch_gemm_pair(&pp, g.dtype, g.out_f32, shape.pair_cols, sms, s)
                       : wsattn::launch_gemm_tile(pp.g[0], g.dtype, g.out_f32, s);
   return e == cudaSuccess ? WSATTN_OK : WSATTN_ERR_CUDA;
-}
-
-// Scratch of one product's partial tiles.
-size_t product_bytes(int64_t R, int C, int K, bool p_mn) {
-  double ns = 0.0;
-  return wsattn::choose_gemm(R, C, K, p_mn, &ns).bytes(R, C);
-}
-
-// Whether both gradients of m rows, n and k features go out in one launch:
-// where that is expected to be the faster way.
-bool grads_together(int64_t m, int n, int k) {
-  double nw = 0.0, nx = 0.0;
-  wsattn::choose_gemm(n, k, static_cast<int>(m), true, &nw);
-  wsattn::choose_gemm(m, k, n, false, &nx);
-  return wsattn::pair_time_of_two(n, k, static_cast<int>(m), m, k, n) < nw + nx;
 }
 
 // Both in one launch; g carries the column sums.
@@ -332,12 +316,17 @@ bool elem_aligned(const void* p, int esize) {
   return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(esize - 1)) == 0;
 }
 
-size_t linear_ws(const wsattn_linear_args* a) {
+wsattn::GemmShape linear_shape(const wsattn_linear_args* a) {
+  double ns = 0.0;
+  return wsattn::choose_gemm(a->m, a->n, a->k, false, &ns);
+}
+
+size_t linear_ws(const wsattn_linear_args* a, const wsattn::GemmShape& shape) {
   size_t b = 0;
   if (a->m == 0) return 0;
   if (a->x_heads > 0 || !tma_rows(a->x, a->ldx, a->m)) b += packed_bytes(a->m, a->k);
   if (!tma_rows(a->w, a->ldw, a->n)) b += packed_bytes(a->n, a->k);
-  return b + product_bytes(a->m, a->n, a->k, false);
+  return b + shape.bytes(a->m, a->n);
 }
 
 bool grad_args_ok(const wsattn_linear_grad_args* a) {
@@ -364,7 +353,9 @@ int dact_rows(int64_t m, int n) {
 }
 
 struct GradPlan {
-  bool act, dz, pack_x, pack_w, together;
+  bool act, dz, pack_x, pack_w;
+  bool together;  // both products in one launch
+  wsattn::GemmShape shape_w, shape_x;
   size_t dz_bytes, part_bytes, x_bytes, w_bytes, tile_bytes;
   int rows_per_block, row_blocks;
   size_t total() const { return dz_bytes + part_bytes + x_bytes + w_bytes + tile_bytes; }
@@ -385,10 +376,15 @@ GradPlan plan_grad(const wsattn_linear_grad_args* a) {
   if (a->db) g.part_bytes = up256(sizeof(float) * static_cast<size_t>(g.row_blocks) * a->n);
   if (g.pack_x) g.x_bytes = packed_bytes(a->m, a->k);
   if (g.pack_w) g.w_bytes = packed_bytes(a->n, a->k);
-  g.together = a->dw && a->dx && grads_together(a->m, a->n, a->k);
+  double nw = 0.0, nx = 0.0;
+  if (a->dw) g.shape_w = wsattn::choose_gemm(a->n, a->k, static_cast<int>(a->m), true, &nw);
+  if (a->dx) g.shape_x = wsattn::choose_gemm(a->m, a->k, a->n, false, &nx);
+  g.together = a->dw && a->dx &&
+               wsattn::pair_time_of_two(a->n, a->k, static_cast<int>(a->m), a->m, a->k, a->n) <
+                   nw + nx;
   if (!g.together) {  // one after the other, through the same partial tiles
-    const size_t bw = a->dw ? product_bytes(a->n, a->k, static_cast<int>(a->m), true) : 0;
-    const size_t bx = a->dx ? product_bytes(a->m, a->k, a->n, false) : 0;
+    const size_t bw = a->dw ? g.shape_w.bytes(a->n, a->k) : 0;
+    const size_t bx = a->dx ? g.shape_x.bytes(a->m, a->k) : 0;
     g.tile_bytes = bw > bx ? bw : bx;
   }
   return g;
@@ -605,7 +601,7 @@ int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_
 
 int wsattn_linear_workspace(const wsattn_linear_args* args, size_t* bytes) {
   if (!bytes || !linear_args_ok(args)) return WSATTN_ERR_BAD_ARG;
-  *bytes = linear_ws(args);
+  *bytes = args->m ? linear_ws(args, linear_shape(args)) : 0;
   return WSATTN_OK;
 }
 
@@ -620,7 +616,8 @@ int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace
       !elem_aligned(a->preact, 2) || !elem_aligned(a->residual, osize) ||
       !elem_aligned(a->out, osize) || (a->x_heads > 0 ? !aligned16(a->x) : !elem_aligned(a->x, 2)))
     return WSATTN_ERR_BAD_ARG;
-  const size_t need = linear_ws(a);
+  const wsattn::GemmShape shape = linear_shape(a);
+  const size_t need = linear_ws(a, shape);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return WSATTN_ERR_BAD_ARG;
   const int sms = sm_count();
@@ -658,7 +655,7 @@ int wsattn_linear(const wsattn_linear_args* a, void* workspace, size_t workspace
   g.pre = a->preact;
   g.ldp = a->ldp;
   g.act = a->activation;
-  return run_product(g, sms, ws, s);
+  return run_product(g, shape, sms, ws, s);
 }
 
 int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes) {
@@ -761,8 +758,8 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
   side.db_cols = a->n;
   if (plan.together) return run_together(gw, gx, sms, s);
   int rc = WSATTN_OK;
-  if (a->dw) rc = run_product(gw, sms, ws_tiles, s);
-  if (a->dx && rc == WSATTN_OK) rc = run_product(gx, sms, ws_tiles, s);
+  if (a->dw) rc = run_product(gw, plan.shape_w, sms, ws_tiles, s);
+  if (a->dx && rc == WSATTN_OK) rc = run_product(gx, plan.shape_x, sms, ws_tiles, s);
   return rc;
 }
 

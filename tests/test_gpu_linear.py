@@ -30,7 +30,7 @@ SHAPES = [
     (1, 1, 1), (1, 256, 320), (3, 130, 64), (1, 1000, 1500), (17, 96, 520),
     (33, 333, 77), (100, 1024, 1024), (129, 257, 65), (240, 384, 128), (256, 256, 256),
     (300, 511, 999), (700, 640, 200), (2080, 1024, 1024), (5000, 384, 64), (1, 8, 4096),
-    (4100, 2304, 192),
+    (4100, 2304, 192), (20000, 20, 40), (70000, 9, 24),
 ]
 
 
@@ -169,7 +169,7 @@ def _slope64(z, name):
 @pytest.mark.parametrize("name", ["none", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=str)
 @pytest.mark.parametrize("shape", [(1, 1, 1), (1, 264, 136), (37, 77, 33), (130, 200, 72), (333, 256, 512),
-                                   (1030, 515, 90), (3000, 128, 64), (640, 1288, 1160)],
+                                   (1030, 515, 90), (3000, 128, 64), (640, 1288, 1160), (9000, 20, 36)],
                          ids=lambda c: "x".join(map(str, c)))
 def test_linear_backward(shape, dt, name):
     fw = _fw()
@@ -267,3 +267,70 @@ def test_linear_capture_and_streams():
     y = fw.wsattn_linear(x, w, b, r, "gelu", stream=side)
     side.synchronize()
     assert torch.equal(y, want)
+
+
+def test_first_call_may_be_captured():
+    # a fresh process whose first call of each operator is inside a capture
+    import subprocess
+    import sys
+    code = """
+import torch, frame_aligned_window_gb300 as fw
+x = torch.randn(300, 77, device="cuda").bfloat16(); w = torch.randn(40, 77, device="cuda").bfloat16()
+q = torch.randn(1, 2, 9, 64, device="cuda"); pos = torch.zeros(9, 1, device="cuda")
+rot = fw.wsattn_rotary_plan(64, (32,))
+def run():
+    y = fw.wsattn_linear(x, w, activation="silu")
+    d = fw.wsattn_linear_backward(y, x, w, preact=y, activation="silu")
+    a = fw.wsattn_qknorm(rot, q, q, pos)
+    b = fw.wsattn_qknorm_backward(rot, q, q, q, q, pos, q[0, 0, 0], q[0, 0, 1])
+    return [y, *d, *a, b[0], b[3], fw.wsattn_rotary(rot, q, pos)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = run()
+g.replay()
+torch.cuda.synchronize()
+want = run()
+assert all(torch.equal(a, b) for a, b in zip(out, want)) and fw.wsattn_op_status() == 0
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_binding_refusals():
+    fw = _fw()
+    x = torch.zeros((6, 24), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((16, 24), dtype=torch.bfloat16, device="cuda")
+    y = fw.wsattn_linear(x, w)
+    for bad, err in (
+            (lambda: fw.wsattn_linear(x[:, :23], w), ValueError),
+            (lambda: fw.wsattn_linear(x.half(), w), TypeError),
+            (lambda: fw.wsattn_linear(x.float(), w.float()), TypeError),
+            (lambda: fw.wsattn_linear(x, w.t()), ValueError),
+            (lambda: fw.wsattn_linear(x.t().contiguous().t(), w), ValueError),
+            (lambda: fw.wsattn_linear(x[:1].expand(6, 24), w), ValueError),
+            (lambda: fw.wsattn_linear(x, w, activation="relu"), ValueError),
+            (lambda: fw.wsattn_linear(x, w, bias=torch.zeros(15, dtype=x.dtype, device="cuda")), ValueError),
+            (lambda: fw.wsattn_linear(x, w, bias=torch.zeros(16, device="cuda")), TypeError),
+            (lambda: fw.wsattn_linear(x, w, residual=y.float()), TypeError),
+            (lambda: fw.wsattn_linear(x, w, residual=y[:5]), ValueError),
+            (lambda: fw.wsattn_linear(x, w, residual=y[:1].expand(6, 16)), ValueError),
+            (lambda: fw.wsattn_linear(x, w, out=y, out_dtype=torch.float32), TypeError),
+            (lambda: fw.wsattn_linear(x, w, out_dtype=torch.float16), TypeError),
+            (lambda: fw.wsattn_linear(x, w, preact=y.float()), TypeError),
+            (lambda: fw.wsattn_linear(x.cpu(), w), TypeError),
+            (lambda: fw.wsattn_linear(torch.zeros((1, 3, 2, 7), device="cuda"), w), ValueError),
+            (lambda: fw.wsattn_linear(torch.zeros((1, 6, 2, 4), device="cuda"), w), fw.WsattnError),
+            (lambda: fw.wsattn_linear(x[:, :23].contiguous(), w[:, :23].contiguous(),
+                                      workspace=torch.empty(16, device="cuda")), fw.WsattnError),
+            (lambda: fw.wsattn_linear_backward(y, x, w, activation="gelu"), ValueError),
+            (lambda: fw.wsattn_linear_backward(y[:5], x, w), ValueError),
+            (lambda: fw.wsattn_linear_backward(y, x, w, dw=w.float()), TypeError),
+            (lambda: fw.wsattn_linear_backward(y, x, w, db=torch.zeros(16, dtype=x.dtype, device="cuda")),
+             TypeError)):
+        with pytest.raises(err):
+            bad()
+    assert fw.wsattn_op_status() == 0

@@ -346,3 +346,60 @@ def test_qknorm_many_tokens(heads, kv):
         tol = half_step(torch.bfloat16) * want.abs() + (TURN + 2 * NORM) * _pairmax(y, True)
         assert_close(got[i], want, tol + tiny(torch.bfloat16), f"part {i}")
     assert torch.equal(got[2].cpu(), parts[2])
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("pad", [0, 3])
+def test_qknorm_backward_in_place(dt, pad):
+    # gradients over the incoming ones, and over the forward's inputs; rows on
+    # 16 bytes (the asynchronous ring) and off them
+    fw = _fw()
+    B, H, N, D, eps = 2, 5, 700, 64, 1e-5
+    g = _gen(41)
+
+    def heads():
+        buf = torch.randn((B, H, N, D + pad), generator=g).to(dt).cuda()
+        return buf[..., :D]
+    q, k, gq, gk = heads(), heads(), heads(), heads()
+    w = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    pos = _positions(N, 1, g).cuda()
+    rot = fw.wsattn_rotary_plan(D, (32,))
+    dq, dk, _, dwq, dwk = fw.wsattn_qknorm_backward(rot, gq, gk, q, k, pos, w, w, eps)
+    over = [t.clone() for t in (gq, gk, q, k)]  # clone of a view: contiguous rows of D
+    a = fw.wsattn_qknorm_backward(rot, over[0], over[1], q, k, pos, w, w, eps, dq=over[0], dk=over[1])
+    assert a[0] is over[0] and torch.equal(over[0], dq) and torch.equal(over[1], dk)
+    a = fw.wsattn_qknorm_backward(rot, gq, gk, over[2], over[3], pos, w, w, eps, dq=over[2], dk=over[3])
+    assert torch.equal(over[2], dq) and torch.equal(over[3], dk)
+    assert torch.equal(a[3], dwq) and torch.equal(a[4], dwk)
+
+
+def test_binding_refusals():
+    fw = _fw()
+    rot = fw.wsattn_rotary_plan(64, (16, 16))
+    x = torch.zeros((2, 3, 5, 64), dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros((5, 2), device="cuda")
+    ok = fw.wsattn_rotary(rot, x, pos)
+    for bad, err in (
+            (lambda: fw.wsattn_rotary(rot, x[..., :32], pos), ValueError),
+            (lambda: fw.wsattn_rotary(rot, x.transpose(2, 3), pos), ValueError),
+            (lambda: fw.wsattn_rotary(rot, x[:, :, ::2, ::1].transpose(0, 1)[..., ::1], pos), ValueError),
+            (lambda: fw.wsattn_rotary(rot, x, pos.double()), TypeError),
+            (lambda: fw.wsattn_rotary(rot, x, pos[:, :1]), ValueError),
+            (lambda: fw.wsattn_rotary(rot, x, torch.zeros((2, 5), device="cuda").t()), ValueError),
+            (lambda: fw.wsattn_rotary(rot, x, pos.cpu()), TypeError),
+            (lambda: fw.wsattn_rotary(rot, x.to(torch.int16), pos), TypeError),
+            (lambda: fw.wsattn_rotary(rot, x, pos, out=ok.float()), TypeError),
+            (lambda: fw.wsattn_rotary(rot, x, pos, out=ok[:1]), ValueError),
+            (lambda: fw.wsattn_rotary(rot, x, pos, out=ok[:, :1].expand(2, 3, 5, 64)), fw.WsattnError),
+            (lambda: fw.wsattn_qknorm(rot, x, x.half(), pos), TypeError),
+            (lambda: fw.wsattn_qknorm(rot, x, x[:1], pos), ValueError),
+            (lambda: fw.wsattn_qknorm(rot, x, x, pos, q_weight=pos[:, 0]), ValueError),
+            (lambda: fw.wsattn_qknorm(rot, x, x, pos, eps=-1.0), fw.WsattnError),
+            (lambda: fw.wsattn_qknorm(rot, x, x, pos, v_out=ok), ValueError),
+            (lambda: fw.wsattn_qknorm(rot, x, x, pos, torch.ones(64, device="cuda"),
+                                      torch.ones(64, device="cuda").bfloat16()), TypeError),
+            (lambda: fw.wsattn_qknorm_backward(rot, x, x, x, x, pos, dv=ok), ValueError),
+            (lambda: fw.wsattn_qknorm_backward(rot, x, x, x, x, pos, torch.ones(64, device="cuda"),
+                                               workspace=torch.empty(8, device="cuda")), fw.WsattnError)):
+        with pytest.raises(err):
+            bad()
