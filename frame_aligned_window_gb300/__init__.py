@@ -459,10 +459,17 @@ class RotaryPlan:
         self._h = handle
         self.head_dim = head_dim
         self.axes = axes
-        n = _SZ()
-        _check(_lib.wsattn_qknorm_backward_workspace(handle, ctypes.byref(n)),
-               "wsattn_qknorm_backward_workspace")
-        self.backward_workspace = int(n.value)
+        self._workspace = None
+
+    @property
+    def backward_workspace(self):
+        """Bytes of scratch of wsattn_qknorm_backward."""
+        if self._workspace is None:
+            n = _SZ()
+            _check(_lib.wsattn_qknorm_backward_workspace(self.handle, ctypes.byref(n)),
+                   "wsattn_qknorm_backward_workspace")
+            self._workspace = int(n.value)
+        return self._workspace
 
     @property
     def handle(self):
@@ -492,24 +499,25 @@ def wsattn_rotary_plan(head_dim, sections=None, base: float = 10000.0, interleav
     else (p, p + D / 2)."""
     if (pair_axis is None) != (pair_freq is None) or (sections is None) == (pair_axis is None):
         raise ValueError("give sections, or pair_axis and pair_freq")
-    half = int(head_dim) // 2
+    half = max(int(head_dim), 0) // 2
     if sections is not None:
         sections = tuple(int(n) for n in sections)
         if not sections or min(sections) < 0 or sum(sections) > half:
             raise ValueError(f"sections {sections} do not fit {half} pairs")
         if not base > 0:
             raise ValueError("base must be positive")
-        pair_axis = [a for a, n in enumerate(sections) for _ in range(n)]
-        pair_freq = [float(base) ** (-j / n) for n in sections for j in range(n)]
-        pair_axis += [0] * (half - len(pair_axis))
-        pair_freq += [0.0] * (half - len(pair_freq))
-        axes = len(sections)
+        axes, first = len(sections), 0
+        axis, freq = np.zeros(half, dtype=np.int32), np.zeros(half)
+        for a, n in enumerate(sections):
+            axis[first:first + n] = a
+            freq[first:first + n] = float(base) ** (np.arange(n) / -max(n, 1))
+            first += n
     else:
-        axes = max(pair_axis, default=-1) + 1
-    axis = np.ascontiguousarray(pair_axis, dtype=np.int32)
-    freq = np.ascontiguousarray(pair_freq, dtype=np.float64)
-    if axis.shape != (half,) or freq.shape != (half,):
-        raise ValueError(f"pair_axis and pair_freq must have {half} entries")
+        axis = np.ascontiguousarray(pair_axis, dtype=np.int32)
+        freq = np.ascontiguousarray(pair_freq, dtype=np.float64)
+        if axis.shape != (half,) or freq.shape != (half,):
+            raise ValueError(f"pair_axis and pair_freq must have {half} entries")
+        axes = int(axis.max()) + 1 if half else 0
     h = _P()
     _check(_lib.wsattn_rotary_plan(int(head_dim), int(axes), axis.ctypes.data, freq.ctypes.data,
                                    int(bool(interleaved)), ctypes.byref(h)), "wsattn_rotary_plan")
