@@ -12,8 +12,8 @@
 // axis, not from a table of D values per token).
 //
 // Work split: 2^l lanes (the least power of two that covers D / 16) hold one
-// head row, 16 elements a lane in two 16-byte pieces, one from each half of
-// the head: element e of the first half and e + D/2 then sit in one thread,
+// head row, 16 elements a lane in 16-byte pieces, the same ones of each half
+// of the head: element e of the first half and e + D/2 then sit in one thread,
 // which serves both pair layouts without an exchange.  A lane group keeps one
 // token and walks its heads: sine and cosine are formed once for all heads
 // of q (or k), the loads of several heads are in flight together, and the
@@ -73,19 +73,20 @@ __device__ __forceinline__ uint32_t elem_bits(__half v) { return __half_as_ushor
 // Raw 8-element load; VEC: 16-byte loads, else element by element (rows that
 // start on any element).
 template <bool VEC>
-__device__ __forceinline__ Half8<float> load8(const float* p) {
+__device__ __forceinline__ Half8<float> load8(const float* p, int step) {
+  const float* q = p + step;
   Half8<float> r;
   if (VEC) {
     r.a = *reinterpret_cast<const uint4*>(p);
-    r.b = *reinterpret_cast<const uint4*>(p + 4);
+    r.b = *reinterpret_cast<const uint4*>(q);
   } else {
     r.a = make_uint4(elem_bits(p[0]), elem_bits(p[1]), elem_bits(p[2]), elem_bits(p[3]));
-    r.b = make_uint4(elem_bits(p[4]), elem_bits(p[5]), elem_bits(p[6]), elem_bits(p[7]));
+    r.b = make_uint4(elem_bits(q[0]), elem_bits(q[1]), elem_bits(q[2]), elem_bits(q[3]));
   }
   return r;
 }
 template <bool VEC, typename T>
-__device__ __forceinline__ Half8<T> load8(const T* p) {
+__device__ __forceinline__ Half8<T> load8(const T* p, int) {
   Half8<T> r;
   if (VEC) {
     r.a = *reinterpret_cast<const uint4*>(p);
@@ -109,17 +110,20 @@ __device__ __forceinline__ void unpack8(const Half8<T>& r, float* f) {
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(float* p, const float* f) {
+__device__ __forceinline__ void store8(float* p, int step, const float* f) {
+  float* q = p + step;
   if (VEC) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    *reinterpret_cast<float4*>(q) = make_float4(f[4], f[5], f[6], f[7]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = f[i];
+    for (int i = 0; i < 4; ++i) p[i] = f[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = f[4 + i];
   }
 }
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* p, const float* f) {
+__device__ __forceinline__ void store8(T* p, int, const float* f) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1], T());
@@ -135,20 +139,33 @@ __device__ __forceinline__ void store8(T* p, const float* f) {
   }
 }
 
-// The lane's place in its head row.
+// The lane's place in its head row: eight elements of each half of the head,
+// in 16 bits elements [8c, 8c + 8), in fp32 [4c, 4c + 4) of the half's first
+// half and of its second (either way neighbouring lanes touch neighbouring
+// 16 bytes).
 struct Lane {
-  int c;        // piece: elements [8c, 8c + 8) of each half of the head
-  bool on;      // the lane holds a piece (D / 16 need not be a power of two)
-  int half;     // D / 2
+  int c;
+  bool on;   // the lane holds a piece (D / 16 need not be a power of two)
+  int half;  // D / 2
+  int off;   // its first element
+  int step;  // fp32: from its first four elements to its second
 };
 
-template <int LG>
+template <typename T, int LG>
 __device__ __forceinline__ Lane make_lane(const RotTable& t) {
   Lane ln;
   ln.c = threadIdx.x & ((1 << LG) - 1);
   ln.half = t.pairs;
   ln.on = 16 * ln.c < 2 * t.pairs;
+  ln.off = (sizeof(T) == 4 ? 4 : 8) * ln.c;
+  ln.step = t.pairs / 2;
   return ln;
+}
+// Element (of the head) that the lane's i-th value is.
+template <typename T>
+__device__ __forceinline__ int lane_element(const Lane& ln, int i) {
+  const int in_half = sizeof(T) == 4 ? (i & 4 ? ln.step : 0) + (i & 3) : i & 7;
+  return (i < 8 ? 0 : ln.half) + ln.off + in_half;
 }
 
 // Row (of B * N) -> batch element and token.
@@ -163,41 +180,65 @@ __device__ __forceinline__ void split_row(const QkParams& p, int64_t row, int64_
   }
 }
 
-// The rates of a lane's eight pairs: interleaved, pairs 4c .. 4c+3 of the
-// first half and D/4 + 4c .. of the second; split, pairs 8c .. 8c+7.  They
-// are read from the kernel's parameters through generic addresses: indexed
-// reads of constant memory would go lane by lane.
+// The rates of a lane's eight pairs, in the order in which turn16 takes them.
+// They are read from the kernel's parameters through generic addresses:
+// indexed reads of constant memory would go lane by lane.
 struct Rates {
-  float4 hi[2], lo[2];
-  uint32_t axis[2];  // four bytes each
+  float hi[8], lo[8];
+  uint32_t axis[8];
 };
+// N consecutive pairs from p0 on
+template <int N>
+__device__ __forceinline__ void read_rates(const RotTable* g, int p0, float* hi, float* lo,
+                                           uint32_t* axis) {
+  if constexpr (N == 4) {
+    const float4 h = *reinterpret_cast<const float4*>(g->hi + p0);
+    const float4 l = *reinterpret_cast<const float4*>(g->lo + p0);
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(g->axis + p0);
+    hi[0] = h.x, hi[1] = h.y, hi[2] = h.z, hi[3] = h.w;
+    lo[0] = l.x, lo[1] = l.y, lo[2] = l.z, lo[3] = l.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) axis[i] = a >> (8 * i) & 255u;
+  } else {
+    const float2 h = *reinterpret_cast<const float2*>(g->hi + p0);
+    const float2 l = *reinterpret_cast<const float2*>(g->lo + p0);
+    const uint32_t a = *reinterpret_cast<const uint16_t*>(g->axis + p0);
+    hi[0] = h.x, hi[1] = h.y;
+    lo[0] = l.x, lo[1] = l.y;
+    axis[0] = a & 255u, axis[1] = a >> 8;
+  }
+}
+template <typename T>
 __device__ __forceinline__ Rates lane_rates(const RotTable& t, const Lane& ln) {
-  const int i0 = t.interleaved ? 4 * ln.c : 8 * ln.c;
-  const int i1 = t.interleaved ? ln.half / 2 + 4 * ln.c : 8 * ln.c + 4;
   const RotTable* g = &t;
   asm volatile("" : "+l"(g));  // an address like any other from here on
   Rates r;
-  r.hi[0] = *reinterpret_cast<const float4*>(g->hi + i0);
-  r.hi[1] = *reinterpret_cast<const float4*>(g->hi + i1);
-  r.lo[0] = *reinterpret_cast<const float4*>(g->lo + i0);
-  r.lo[1] = *reinterpret_cast<const float4*>(g->lo + i1);
-  r.axis[0] = *reinterpret_cast<const uint32_t*>(g->axis + i0);
-  r.axis[1] = *reinterpret_cast<const uint32_t*>(g->axis + i1);
+  if (!t.interleaved) {  // pair e: elements e and e + D / 2
+    const int second = sizeof(T) == 4 ? ln.off + ln.step : ln.off + 4;
+    read_rates<4>(g, ln.off, r.hi, r.lo, r.axis);
+    read_rates<4>(g, second, r.hi + 4, r.lo + 4, r.axis + 4);
+  } else if constexpr (sizeof(T) == 4) {  // pair e / 2: elements e and e + 1
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      read_rates<2>(g, (ln.off + k * ln.step) / 2, r.hi + 2 * k, r.lo + 2 * k, r.axis + 2 * k);
+  } else {
+    read_rates<4>(g, ln.off / 2, r.hi, r.lo, r.axis);
+    read_rates<4>(g, (ln.half + ln.off) / 2, r.hi + 4, r.lo + 4, r.axis + 4);
+  }
   return r;
 }
 
+template <typename T>
 __device__ __forceinline__ void lane_angles(const RotTable& t, const Lane& ln, const float* pos,
                                             float sign, float (&cs)[8], float (&sn)[8]) {
   float x[kRotMaxAxes];
 #pragma unroll
   for (int a = 0; a < kRotMaxAxes; ++a) x[a] = a < t.axes ? pos[a] : 0.f;
-  const Rates r = lane_rates(t, ln);
+  const Rates r = lane_rates<T>(t, ln);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 h4 = r.hi[i >> 2], l4 = r.lo[i >> 2];
-    const float w = (i & 3) == 0 ? h4.x : (i & 3) == 1 ? h4.y : (i & 3) == 2 ? h4.z : h4.w;
-    const float wl = (i & 3) == 0 ? l4.x : (i & 3) == 1 ? l4.y : (i & 3) == 2 ? l4.z : l4.w;
-    const uint32_t a = r.axis[i >> 2] >> (8 * (i & 3)) & 255u;
+    const float w = r.hi[i], wl = r.lo[i];
+    const uint32_t a = r.axis[i];
     const float v = a < 2 ? (a == 0 ? x[0] : x[1]) : (a == 2 ? x[2] : x[3]);
     const float hi = v * w;
     const float err = fmaf(v, w, -hi);
@@ -237,15 +278,18 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-template <typename E>
+// The lane's gains, from E values laid out as its T elements are.
+template <typename E, typename T>
 __device__ __forceinline__ void gain16(const void* weight, const Lane& ln, float (&w)[16]) {
-  const E* g = static_cast<const E*>(weight) + 8 * ln.c;
+  const E* g = static_cast<const E*>(weight) + ln.off;
+  // fp32 gains of 16-bit heads: eight in a row
+  const int step = sizeof(T) == 4 ? ln.step : 4;
   if ((reinterpret_cast<uintptr_t>(weight) & 15u) == 0) {
-    unpack8(load8<true>(g), w);
-    unpack8(load8<true>(g + ln.half), w + 8);
+    unpack8(load8<true>(g, step), w);
+    unpack8(load8<true>(g + ln.half, step), w + 8);
   } else {
-    unpack8(load8<false>(g), w);
-    unpack8(load8<false>(g + ln.half), w + 8);
+    unpack8(load8<false>(g, step), w);
+    unpack8(load8<false>(g + ln.half, step), w + 8);
   }
 }
 template <typename T>
@@ -254,18 +298,18 @@ __device__ __forceinline__ void load_gain(const QkParams& p, const QkPart& part,
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = 1.f;
   if (!part.weight || !ln.on) return;
-  if (p.weight_f32) gain16<float>(part.weight, ln, w);
-  else gain16<T>(part.weight, ln, w);
+  if (p.weight_f32) gain16<float, T>(part.weight, ln, w);
+  else gain16<T, T>(part.weight, ln, w);
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_raw8(float* p, const Half8<float>& r) {
+__device__ __forceinline__ void store_raw8(float* p, int step, const Half8<float>& r) {
   float f[8];
   unpack8(r, f);
-  store8<VEC>(p, f);
+  store8<VEC>(p, step, f);
 }
 template <bool VEC, typename T>
-__device__ __forceinline__ void store_raw8(T* p, const Half8<T>& r) {
+__device__ __forceinline__ void store_raw8(T* p, int, const Half8<T>& r) {
   if (VEC) {
     *reinterpret_cast<uint4*>(p) = r.a;
   } else {
@@ -282,21 +326,21 @@ __device__ __forceinline__ void store_raw8(T* p, const Half8<T>& r) {
 // Copies a lane's share of `heads` head rows (v: neither norm nor turn).
 template <typename T, bool VEC>
 __device__ __forceinline__ void copy_heads(const T* src, int64_t sstep, T* dst, int64_t dstep,
-                                           int heads, int half) {
+                                           int heads, const Lane& ln) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;
   for (int h = 0; h < heads; h += U) {
     Half8<T> r0[U], r1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (h + u < heads) {
-        r0[u] = load8<VEC>(src + u * sstep);
-        r1[u] = load8<VEC>(src + u * sstep + half);
+        r0[u] = load8<VEC>(src + u * sstep, ln.step);
+        r1[u] = load8<VEC>(src + u * sstep + ln.half, ln.step);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (h + u < heads) {
-        store_raw8<VEC>(dst + u * dstep, r0[u]);
-        store_raw8<VEC>(dst + u * dstep + half, r1[u]);
+        store_raw8<VEC>(dst + u * dstep, ln.step, r0[u]);
+        store_raw8<VEC>(dst + u * dstep + ln.half, ln.step, r1[u]);
       }
     src += U * sstep;
     dst += U * dstep;
@@ -309,7 +353,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
   // heads whose loads are in flight together (with the norm's registers, four of
   // 16 bits are 2 % faster at 40 heads, two 5 to 30 % at 12 and fewer)
   constexpr int U = sizeof(T) == 4 || NORM ? 2 : 4;
-  const Lane ln = make_lane<LG>(p.rot);
+  const Lane ln = make_lane<T, LG>(p.rot);
   const int g = static_cast<int>(blockIdx.x % p.groups);
   const int64_t rb = blockIdx.x / p.groups;
   constexpr int kPerWarp = 32 >> LG;
@@ -323,18 +367,18 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
   const bool active = row < p.rows && ln.on &&
                       WSATTN_BOUNDS(p.status, g < p.groups && h0 >= 0 && heads >= 1 &&
                                                   h0 + heads <= part.io.heads &&
-                                                  8 * ln.c + 8 <= ln.half);
+                                                  16 * ln.c + 16 <= 2 * ln.half);
   int64_t b = 0, n = 0;
   if (active) split_row(p, row, b, n);
   const int64_t sstep = part.io.ih, dstep = part.io.oh;
   const T* src = static_cast<const T*>(part.io.in) + b * part.io.ib + n * part.io.in_ + h0 * sstep +
-                 8 * ln.c;
+                 ln.off;
   T* dst =
-      static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on + h0 * dstep + 8 * ln.c;
+      static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on + h0 * dstep + ln.off;
   griddep_wait();
   griddep_launch_dependents();
   if (!part.turn) {
-    if (active) copy_heads<T, VEC>(src, sstep, dst, dstep, heads, ln.half);
+    if (active) copy_heads<T, VEC>(src, sstep, dst, dstep, heads, ln);
     return;
   }
   // the first loads go out before the angles are formed
@@ -343,8 +387,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (active && u < left) {
-        r0[u] = load8<VEC>(src + u * sstep);
-        r1[u] = load8<VEC>(src + u * sstep + ln.half);
+        r0[u] = load8<VEC>(src + u * sstep, ln.step);
+        r1[u] = load8<VEC>(src + u * sstep + ln.half, ln.step);
       } else {
         r0[u] = Half8<T>{};
         r1[u] = Half8<T>{};
@@ -353,7 +397,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
   load(heads);
   float cs[8], sn[8], w[16];
   if (active)
-    lane_angles(p.rot, ln, p.pos + b * p.pos_b + n * p.rot.axes, static_cast<float>(part.turn), cs,
+    lane_angles<T>(p.rot, ln, p.pos + b * p.pos_b + n * p.rot.axes, static_cast<float>(part.turn), cs,
                 sn);
   if (NORM) load_gain<T>(p, part, ln, w);
   const float inv_d = 0.5f / static_cast<float>(p.rot.pairs);
@@ -373,8 +417,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
     }
     turn16(x, cs, sn, inter);
     if (active) {
-      store8<VEC>(dst + u * dstep, x);
-      store8<VEC>(dst + u * dstep + ln.half, x + 8);
+      store8<VEC>(dst + u * dstep, ln.step, x);
+      store8<VEC>(dst + u * dstep + ln.half, ln.step, x + 8);
     }
   };
   for (int h = 0; h < heads; h += U) {
@@ -441,7 +485,7 @@ __device__ __forceinline__ void open_item(const QkParams& p, const Lane& ln, Bac
              WSATTN_BOUNDS(p.status, c.rb < p.row_blocks && c.heads >= 1 &&
                                          (c.g - part.group0) * p.group_heads + c.heads <=
                                              part.io.heads &&
-                                         8 * ln.c + 8 <= ln.half);
+                                         16 * ln.c + 16 <= 2 * ln.half);
   c.b = c.n = 0;
   if (c.active) split_row(p, row, c.b, c.n);
 }
@@ -460,7 +504,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
   constexpr int kStages = kBackStages<T>, kBytes = kBackStageBytes<T>;
   constexpr int kPieces = sizeof(T) / 2;  // 16-byte pieces of 8 elements
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const Lane ln = make_lane<LG>(p.rot);
+  const Lane ln = make_lane<T, LG>(p.rot);
   const float inv_d = 0.5f / static_cast<float>(p.rot.pairs);
   const bool inter = p.rot.interleaved != 0;
   const int D = 2 * p.rot.pairs;
@@ -478,7 +522,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
     for (int i = 0; i < 16; ++i) {
 #pragma unroll
       for (int o = 1 << LG; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (lane < (1 << LG) && ln.on) red[warp][(i < 8 ? 0 : ln.half) + 8 * ln.c + (i & 7)] = acc[i];
+      if (lane < (1 << LG) && ln.on) red[warp][lane_element<T>(ln, i)] = acc[i];
       acc[i] = 0.f;
     }
     __syncthreads();
@@ -520,9 +564,9 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
       const QkPart& part = p.part[ahead.pi];
       const int64_t h0 = static_cast<int64_t>(ahead.g - part.group0) * p.group_heads;
       gy = static_cast<const T*>(part.io.in) + ahead.b * part.io.ib + ahead.n * part.io.in_ +
-           h0 * part.io.ih + 8 * ln.c;
+           h0 * part.io.ih + ln.off;
       xs = static_cast<const T*>(part.x) + ahead.b * part.xb + ahead.n * part.xn + h0 * part.xh +
-           8 * ln.c;
+           ln.off;
     };
     auto step_ahead = [&] {
       const QkPart& part = p.part[ahead.pi];
@@ -540,7 +584,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
           const uint32_t d = ring + load_slot * kBytes;
 #pragma unroll
           for (int q = 0; q < kPieces; ++q) {
-            const int e = q * 4;  // fp32: the second 16 bytes of 8 elements
+            const int e = q * ln.step;  // fp32: the lane's second four elements
             cp_async16(d + (0 + q) * 512, gy + e);
             cp_async16(d + (kPieces + q) * 512, gy + ln.half + e);
             cp_async16(d + (2 * kPieces + q) * 512, xs + e);
@@ -568,11 +612,11 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
       }
       const int64_t dstep = part.io.oh;
       T* dx = static_cast<T*>(part.io.out) + cur.b * part.io.ob + cur.n * part.io.on +
-              static_cast<int64_t>(cur.g - part.group0) * p.group_heads * dstep + 8 * ln.c;
+              static_cast<int64_t>(cur.g - part.group0) * p.group_heads * dstep + ln.off;
       // idle lanes hold zeros and join the row sums: no turn there
       float cs[8] = {}, sn[8] = {};
       if (cur.active)
-        lane_angles(p.rot, ln, p.pos + cur.b * p.pos_b + cur.n * p.rot.axes, -1.f, cs, sn);
+        lane_angles<T>(p.rot, ln, p.pos + cur.b * p.pos_b + cur.n * p.rot.axes, -1.f, cs, sn);
       for (; cur.h < cur.heads; ++cur.h) {
         float gr[16], x[16];
         if (VEC) {
@@ -593,10 +637,10 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
             unpack8(c, x + 8 * q);
           }
         } else if (cur.active) {
-          unpack8(load8<false>(gy), gr);
-          unpack8(load8<false>(gy + ln.half), gr + 8);
-          unpack8(load8<false>(xs), x);
-          unpack8(load8<false>(xs + ln.half), x + 8);
+          unpack8(load8<false>(gy, ln.step), gr);
+          unpack8(load8<false>(gy + ln.half, ln.step), gr + 8);
+          unpack8(load8<false>(xs, ln.step), x);
+          unpack8(load8<false>(xs + ln.half, ln.step), x + 8);
         }
         if (!VEC) step_ahead();
         if (!cur.active) {
@@ -618,8 +662,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
             acc[e] = fmaf(gr[e], x[e] * r, acc[e]);
             gr[e] = r * fmaf(-x[e], m, gr[e] * w[e]);
           }
-          store8<VEC>(dx, gr);
-          store8<VEC>(dx + ln.half, gr + 8);
+          store8<VEC>(dx, ln.step, gr);
+          store8<VEC>(dx + ln.half, ln.step, gr + 8);
         }
         dx += dstep;
       }
@@ -641,11 +685,11 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
       int64_t b, n;
       split_row(p, row, b, n);
       copy_heads<T, VEC>(static_cast<const T*>(part.io.in) + b * part.io.ib + n * part.io.in_ +
-                             h0 * part.io.ih + 8 * ln.c,
+                             h0 * part.io.ih + ln.off,
                          part.io.ih,
                          static_cast<T*>(part.io.out) + b * part.io.ob + n * part.io.on +
-                             h0 * part.io.oh + 8 * ln.c,
-                         part.io.oh, heads, ln.half);
+                             h0 * part.io.oh + ln.off,
+                         part.io.oh, heads, ln);
     }
     if (++rb == p.row_blocks) {
       rb = 0;
