@@ -90,31 +90,48 @@ QkPart part_of(const wsattn_heads* in, const wsattn_heads* out, int norm, int tu
   return p;
 }
 
-// Lanes per head row, rows per CTA and, from the wanted number of work items
-// (a warp's worth of tokens times a group of heads), the heads a warp walks.
-// False: more CTAs than a launch may have.
-bool split_work(QkParams* p, int64_t rows, int64_t want_items, int min_heads) {
+// Lanes per head row, rows per CTA, and the heads that a warp walks for one
+// token: all of a part's, or a half, a quarter ... until there are enough work
+// items (a CTA's tokens times a group of heads).  Forward: one group size for
+// all parts (a CTA is an item), want_items of them.  Backward: each part its
+// own, 32 items a CTA as long as a warp keeps more than 12 heads (an item costs
+// its angles, one and a half heads' time), and 8 items with fewer.
+// False: more items than an int counts.
+bool split_work(QkParams* p, int64_t rows, int64_t ctas, bool back) {
+  const bool equal = !back;
   const int pieces = p->rot.pairs / 8;
   p->lanes_log2 = 0;
   while ((1 << p->lanes_log2) < pieces) ++p->lanes_log2;
   p->rows = rows;
   const int per_cta = wsattn::kQkThreads / 32 * (32 >> p->lanes_log2);
   p->row_blocks = cdiv(rows, per_cta);
-  int most = 1;
-  for (int i = 0; i < p->parts; ++i)
-    if (p->part[i].io.heads > most) most = p->part[i].io.heads;
-  int gh = most;
-  auto groups = [&](int g) {
+  int gh[3] = {1, 1, 1}, most = 1;
+  for (int i = 0; i < p->parts; ++i) {
+    gh[i] = p->part[i].io.heads;
+    if (gh[i] > most) most = gh[i];
+  }
+  if (equal) gh[0] = gh[1] = gh[2] = most;
+  const int counted = equal || p->parts < 2 ? p->parts : 2;  // the backward's copies go apart
+  auto groups = [&] {
     int64_t n = 0;
-    for (int i = 0; i < p->parts; ++i) n += cdiv(p->part[i].io.heads, g);
+    for (int i = 0; i < counted; ++i) n += cdiv(p->part[i].io.heads, gh[i]);
     return n;
   };
-  while (gh > min_heads && p->row_blocks * groups(gh) < want_items) gh = (gh + 1) / 2;
-  p->group_heads = gh;
+  while (true) {
+    int k = 0;
+    for (int i = 1; i < counted; ++i)
+      if (gh[i] > gh[k]) k = i;
+    const int64_t want = !back ? ctas : gh[k] > 12 ? 32 * ctas : 8 * ctas;
+    if (p->row_blocks * groups() >= want || gh[k] <= (back ? 4 : 1)) break;
+    const int less = (gh[k] + 1) / 2;
+    if (equal) gh[0] = gh[1] = gh[2] = less;
+    else gh[k] = less;
+  }
   p->groups = 0;
   for (int i = 0; i < p->parts; ++i) {
     p->part[i].group0 = p->groups;
-    p->part[i].groups = static_cast<int>(cdiv(p->part[i].io.heads, gh));
+    p->part[i].group_heads = gh[i];
+    p->part[i].groups = static_cast<int>(cdiv(p->part[i].io.heads, gh[i]));
     p->groups += p->part[i].groups;
   }
   return p->row_blocks <= INT32_MAX / p->groups;
@@ -454,7 +471,7 @@ int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
   p.tokens = n_tokens;
   p.status = wsattn::op_status_ptr();
   if (!p.status) return WSATTN_ERR_CUDA;
-  if (!split_work(&p, rows, 6LL * sms, 1)) return WSATTN_ERR_BAD_ARG;
+  if (!split_work(&p, rows, 6LL * sms, false)) return WSATTN_ERR_BAD_ARG;
   const bool vec = view_vec(x, batch, n_tokens, esize) && view_vec(y, batch, n_tokens, esize);
   return wsattn::launch_qk_forward(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? WSATTN_OK
@@ -503,7 +520,7 @@ int wsattn_qknorm(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
   p.tokens = n_tokens;
   p.status = wsattn::op_status_ptr();
   if (!p.status) return WSATTN_ERR_CUDA;
-  if (!split_work(&p, rows, 6LL * sms, 1)) return WSATTN_ERR_BAD_ARG;
+  if (!split_work(&p, rows, 6LL * sms, false)) return WSATTN_ERR_BAD_ARG;
   return wsattn::launch_qk_forward(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? WSATTN_OK
              : WSATTN_ERR_CUDA;
@@ -588,7 +605,7 @@ int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_
   p.dw_part = gains ? static_cast<float*>(workspace) : nullptr;
   int64_t blocks = static_cast<int64_t>(sms) * wsattn::kQkBackCtasPerSm;
   if (blocks > kMaxBackCtas) blocks = kMaxBackCtas;
-  if (!split_work(&p, rows, 32 * blocks, 4)) return WSATTN_ERR_BAD_ARG;
+  if (!split_work(&p, rows, blocks, true)) return WSATTN_ERR_BAD_ARG;
   // no CTA without work of its own
   const int64_t items =
       p.row_blocks * static_cast<int64_t>(p.part[0].groups + p.part[1].groups);

@@ -45,6 +45,7 @@ struct QkPart {
   int turn;              // 1 turns, -1 turns back, 0 leaves the angles alone
   int group0;            // first head group of this part
   int groups;
+  int group_heads;       // heads a warp walks for one token
 };
 
 struct QkParams {
@@ -59,7 +60,6 @@ struct QkParams {
   int64_t rows;          // B * N
   int64_t row_blocks;    // ceil(rows / rows per CTA)
   int lanes_log2;        // lanes of one head row: 2^lanes_log2 >= D / 16
-  int group_heads;       // heads a warp walks for one token
   int groups;            // head groups of all parts together
   float* dw_part;        // backward: [2][blocks][D] partial gain gradients, or null
   int* status;           // device status word (debug build: bounds checks)

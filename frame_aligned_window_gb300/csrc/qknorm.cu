@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
   int pi = 0;
   while (pi + 1 < p.parts && g >= p.part[pi + 1].group0) ++pi;
   const QkPart& part = p.part[pi];
-  const int h0 = (g - part.group0) * p.group_heads;
-  const int heads = min(part.io.heads - h0, p.group_heads);
+  const int h0 = (g - part.group0) * part.group_heads;
+  const int heads = min(part.io.heads - h0, part.group_heads);
   const bool active = row < p.rows && ln.on &&
                       WSATTN_BOUNDS(p.status, g < p.groups && h0 >= 0 && heads >= 1 &&
                                                   h0 + heads <= part.io.heads &&
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_con
 
 // Backward.  Persistent: the work items (rows of one CTA, one head group) of
 // q and k form one list, the group the slow index, of which each CTA takes a
-// contiguous share; then the same for v's copies.  A CTA's share of the gain
+// contiguous share of equal weight; then the same for v's copies.  A CTA's share of the gain
 // gradients stays in registers until its part changes, and one partial row
 // per CTA and part goes to global memory: the sums have a fixed order.
 //
@@ -478,12 +478,12 @@ __device__ __forceinline__ void open_item(const QkParams& p, const Lane& ln, Bac
   while (c.pi == 0 && c.g >= p.part[1].group0) c.pi = 1;
   const QkPart& part = p.part[c.pi];
   c.h = 0;
-  c.heads = min(part.io.heads - (c.g - part.group0) * p.group_heads, p.group_heads);
+  c.heads = min(part.io.heads - (c.g - part.group0) * part.group_heads, part.group_heads);
   const int64_t row = (c.rb * (kQkThreads / 32) + threadIdx.x / 32) * (32 >> LG) +
                       ((threadIdx.x & 31) >> LG);
   c.active = row < p.rows && ln.on &&
              WSATTN_BOUNDS(p.status, c.rb < p.row_blocks && c.heads >= 1 &&
-                                         (c.g - part.group0) * p.group_heads + c.heads <=
+                                         (c.g - part.group0) * part.group_heads + c.heads <=
                                              part.io.heads &&
                                          16 * ln.c + 16 <= 2 * ln.half);
   c.b = c.n = 0;
@@ -534,19 +534,19 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
     }
     __syncthreads();
   };
-  // first and last item of this CTA in the list of parts [a, z)
-  auto share = [&](int a, int z, int64_t& i0, int64_t& i1) {
-    const int g0 = p.part[a].group0;
-    const int64_t items =
-        static_cast<int64_t>(p.part[z - 1].group0 + p.part[z - 1].groups - g0) * p.row_blocks;
-    i0 = items * blockIdx.x / gridDim.x;
-    i1 = items * (blockIdx.x + 1) / gridDim.x;
+  // This CTA's share of q's and k's items.  An item weighs its heads and about
+  // one and a half more for its angles; the shares are equal in weight.
+  const int64_t nq = p.part[0].groups * p.row_blocks;
+  const int64_t wq = 2 * p.part[0].group_heads + 3, wk = 2 * p.part[1].group_heads + 3;
+  const int64_t weight = nq * wq + p.part[1].groups * p.row_blocks * wk;
+  auto item_at = [&](int64_t x) {
+    return x <= nq * wq ? (x + wq - 1) / wq : nq + (x - nq * wq + wk - 1) / wk;
   };
 
   griddep_wait();
   griddep_launch_dependents();
-  int64_t i, i1;
-  share(0, 2, i, i1);
+  int64_t i = item_at(weight * blockIdx.x / gridDim.x);
+  int64_t i1 = item_at(weight * (blockIdx.x + 1) / gridDim.x);
   int g = static_cast<int>(i / p.row_blocks);
   int64_t rb = i - g * p.row_blocks;
   int done_part = 0;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
     auto open_ahead = [&] {
       open_item<LG>(p, ln, ahead);
       const QkPart& part = p.part[ahead.pi];
-      const int64_t h0 = static_cast<int64_t>(ahead.g - part.group0) * p.group_heads;
+      const int64_t h0 = static_cast<int64_t>(ahead.g - part.group0) * part.group_heads;
       gy = static_cast<const T*>(part.io.in) + ahead.b * part.io.ib + ahead.n * part.io.in_ +
            h0 * part.io.ih + ln.off;
       xs = static_cast<const T*>(part.x) + ahead.b * part.xb + ahead.n * part.xn + h0 * part.xh +
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
       }
       const int64_t dstep = part.io.oh;
       T* dx = static_cast<T*>(part.io.out) + cur.b * part.io.ob + cur.n * part.io.on +
-              static_cast<int64_t>(cur.g - part.group0) * p.group_heads * dstep + ln.off;
+              static_cast<int64_t>(cur.g - part.group0) * part.group_heads * dstep + ln.off;
       // idle lanes hold zeros and join the row sums: no turn there
       float cs[8] = {}, sn[8] = {};
       if (cur.active)
@@ -674,12 +674,14 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackCtasPerSm)
   if (p.parts < 3) return;
 
   const QkPart& part = p.part[2];
-  share(2, 3, i, i1);
+  const int64_t copies = part.groups * p.row_blocks;
+  i = copies * blockIdx.x / gridDim.x;
+  i1 = copies * (blockIdx.x + 1) / gridDim.x;
   g = static_cast<int>(i / p.row_blocks);
   rb = i - g * p.row_blocks;
   for (; i < i1; ++i) {
-    const int h0 = g * p.group_heads;
-    const int heads = min(part.io.heads - h0, p.group_heads);
+    const int h0 = g * part.group_heads;
+    const int heads = min(part.io.heads - h0, part.group_heads);
     const int64_t row = (rb * (kQkThreads / 32) + warp) * (32 >> LG) + (lane >> LG);
     if (row < p.rows && ln.on) {
       int64_t b, n;
