@@ -1,4 +1,5 @@
-// What the epilogues of the linear products and their gradients share.
+// Activations, 16-bit pairs and what the epilogues of the linear products and
+// their gradients share.
 #pragma once
 
 #include <cuda_bf16.h>
