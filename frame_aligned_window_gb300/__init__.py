@@ -490,15 +490,18 @@ class RotaryPlan:
 
 
 def wsattn_rotary_plan(head_dim, sections=None, base: float = 10000.0, interleaved: bool = True,
-                       pair_axis=None, pair_freq=None) -> RotaryPlan:
+                       pair_axis=None, pair_freq=None, axes=None) -> RotaryPlan:
     """Turning rates of a head's pairs.  sections: pairs turned by each axis of
     the positions (time, height, width, ...), in order; pair j of a section of
     n turns by base**(-j / n) radians per unit of its axis, and pairs behind
-    the sections are left alone.  Or pair_axis and pair_freq [D / 2] directly.
+    the sections are left alone.  Or pair_axis and pair_freq [D / 2] directly,
+    with `axes` columns of positions (default: as many as pair_axis names).
     interleaved: pairs are dims (2p, 2p + 1) (as wsattn_produce turns them),
     else (p, p + D / 2)."""
     if (pair_axis is None) != (pair_freq is None) or (sections is None) == (pair_axis is None):
         raise ValueError("give sections, or pair_axis and pair_freq")
+    if sections is not None and axes not in (None, len(sections)):
+        raise ValueError(f"{len(sections)} sections for {axes} axes")
     half = max(int(head_dim), 0) // 2
     if sections is not None:
         sections = tuple(int(n) for n in sections)
@@ -517,7 +520,7 @@ def wsattn_rotary_plan(head_dim, sections=None, base: float = 10000.0, interleav
         freq = np.ascontiguousarray(pair_freq, dtype=np.float64)
         if axis.shape != (half,) or freq.shape != (half,):
             raise ValueError(f"pair_axis and pair_freq must have {half} entries")
-        axes = int(axis.max()) + 1 if half else 0
+        axes = axes if axes is not None else int(axis.max()) + 1 if half else 0
     h = _P()
     _check(_lib.wsattn_rotary_plan(int(head_dim), int(axes), axis.ctypes.data, freq.ctypes.data,
                                    int(bool(interleaved)), ctypes.byref(h)), "wsattn_rotary_plan")

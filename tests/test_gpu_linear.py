@@ -269,6 +269,36 @@ def test_linear_capture_and_streams():
     assert torch.equal(y, want)
 
 
+def test_linear_more_than_2_to_31_elements():
+    # outputs, pre-activations and residuals whose offsets pass 32 bits
+    fw = _fw()
+    m, n, k = 540000, 4104, 64
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    dt = torch.bfloat16
+    x = torch.empty((m, k), dtype=dt, device="cuda").normal_()
+    w = (torch.empty((n, k), device="cuda").normal_() / 8).to(dt)
+    r = torch.empty((m, n), dtype=dt, device="cuda").normal_()
+    assert r.numel() > 1 << 31
+    z = torch.empty_like(r)
+    y = fw.wsattn_linear(x, w, residual=r, activation="silu", preact=z)
+    dx, dw, db = fw.wsattn_linear_backward(r, x, w, preact=z, activation="silu")
+    torch.cuda.synchronize()
+    assert fw.wsattn_op_status() == 0
+    for rows in (slice(0, 300), slice(m // 2, m // 2 + 300), slice(m - 300, m)):
+        zz = x[rows].double() @ w.double().t()
+        ztol = product_tol(x[rows].double().abs() @ w.double().abs().t(), k)
+        assert_close(z[rows], zz.cpu(), (ztol + half_step(dt) * zz.abs() + tiny(dt)).cpu())
+        want = act(zz, "silu") + r[rows].double()
+        assert_close(y[rows], want.cpu(),
+                     (1.13 * ztol + 2.0 ** -20 * zz.abs() + half_step(dt) * want.abs()).cpu())
+        dz = r[rows].double() * _slope64(z[rows].double(), "silu")
+        want = dz @ w.double()
+        tol = (1.01 * half_step(dt) + 2.0 ** -19) * (dz.abs() + r[rows].double().abs() * 2.0 ** -10) @ w.double().abs()
+        tol = tol + product_tol(dz.abs() @ w.double().abs(), n) + half_step(dt) * want.abs()
+        assert_close(dx[rows], want.cpu(), tol.cpu())
+
+
 def test_first_call_may_be_captured():
     # a fresh process whose first call of each operator is inside a capture
     import subprocess

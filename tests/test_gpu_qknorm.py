@@ -403,3 +403,43 @@ def test_binding_refusals():
                                                workspace=torch.empty(8, device="cuda")), fw.WsattnError)):
         with pytest.raises(err):
             bad()
+
+
+def test_rates_given_pair_by_pair():
+    # any axis for any pair, any rate, one column of the positions not used
+    fw = _fw()
+    g = _gen(51)
+    D, N = 32, 50
+    axis = torch.randint(0, 2, (16,), generator=g)
+    freq = torch.randn(16, generator=g, dtype=torch.float64)
+    freq[3] = 0
+    rot = fw.wsattn_rotary_plan(D, pair_axis=axis.tolist(), pair_freq=freq.tolist(), axes=3,
+                                interleaved=False)
+    pos = 40 * torch.randn((N, 3), generator=g)
+    x = torch.randn((1, 2, N, D), generator=g)
+    want = turn(x.double(), pos.double()[:, axis] * freq, False)
+    got = fw.wsattn_rotary(rot, x.cuda(), pos.cuda())
+    assert_close(got, want, _turn_tol(x.double(), want, False, torch.float32))
+
+
+def test_more_than_2_to_31_elements():
+    # the last heads and tokens of a tensor whose offsets pass 32 bits
+    fw = _fw()
+    H, N, D = 34, 500000, 128
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    x = torch.empty((1, H, N, D), dtype=torch.bfloat16, device="cuda").normal_()
+    assert x.numel() > 1 << 31
+    pos = torch.arange(N, device="cuda", dtype=torch.float32)[:, None].contiguous()
+    rot = fw.wsattn_rotary_plan(D, (64,))
+    w = torch.full((D,), 1.5, device="cuda")
+    for y, gain in ((fw.wsattn_rotary(rot, x, pos), None),
+                    (fw.wsattn_qknorm(rot, x, x[:, :1], pos, w, w, 1e-6)[0], 1.5)):
+        for h, n0 in ((0, 0), (H - 1, N - 300), (H - 2, N // 2)):
+            part = x[:, h:h + 1, n0:n0 + 300].cpu().double()
+            if gain:
+                part = gain * normed(part, None, 1e-6)[0]
+            want = turn(part, angles(pos[n0:n0 + 300], (64,), D), True)
+            tol = _turn_tol(part, want, True, torch.bfloat16) + 2 * NORM * _pairmax(part, True)
+            assert_close(y[:, h:h + 1, n0:n0 + 300], want, tol)
+        del y
