@@ -53,7 +53,7 @@ bool apart(const wsattn_heads* v, int batch, int64_t n, int dim) {
   int64_t extent = dim;
   for (int i = 0; i < 3; ++i) {
     if (size[i] <= 1) continue;
-    if (stride[i] < extent) return false;
+    if (stride[i] < extent || stride[i] > (INT64_MAX - extent) / size[i]) return false;
     extent = stride[i] * (size[i] - 1) + extent;
   }
   return true;
@@ -137,6 +137,8 @@ bool split_work(QkParams* p, int64_t rows, int64_t ctas, bool back) {
   return p->row_blocks <= INT32_MAX / p->groups;
 }
 
+// Rows (batch times tokens) then fit 64 bits.
+bool tokens_ok(int64_t n_tokens) { return n_tokens >= 0 && n_tokens <= INT32_MAX; }
 bool positions_ok(const float* positions, int64_t pos_stride_b) {
   return pos_stride_b >= 0 && (reinterpret_cast<uintptr_t>(positions) & 3u) == 0;
 }
@@ -450,7 +452,7 @@ int wsattn_rotary_destroy(wsattn_rotary_t rot) {
 int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
                   const wsattn_heads* x, const float* positions, int64_t pos_stride_b, int inverse,
                   const wsattn_heads* y, void* stream) {
-  if (!rot || !dtype_ok(dtype) || batch < 0 || n_tokens < 0 || inverse < 0 || inverse > 1)
+  if (!rot || !dtype_ok(dtype) || batch < 0 || !tokens_ok(n_tokens) || inverse < 0 || inverse > 1)
     return WSATTN_ERR_BAD_ARG;
   const int esize = dtype_size(dtype), dim = 2 * rot->table.pairs;
   if (!view_ok(x, esize) || !view_ok(y, esize) || x->heads != y->heads ||
@@ -458,7 +460,7 @@ int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
     return WSATTN_ERR_BAD_ARG;
   const int64_t rows = static_cast<int64_t>(batch) * n_tokens;
   if (rows == 0) return WSATTN_OK;
-  if (!x->data || !y->data || !positions || n_tokens > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  if (!x->data || !y->data || !positions) return WSATTN_ERR_BAD_ARG;
   const int sms = sm_count();
   if (!sms) return WSATTN_ERR_CUDA;
   QkParams p;
@@ -483,7 +485,7 @@ int wsattn_qknorm(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
                   const void* q_weight, const void* k_weight, int weight_dtype, float eps,
                   const float* positions, int64_t pos_stride_b, const wsattn_heads* q_out,
                   const wsattn_heads* k_out, const wsattn_heads* v_out, void* stream) {
-  if (!rot || !dtype_ok(dtype) || batch < 0 || n_tokens < 0 || !(eps >= 0.f) ||
+  if (!rot || !dtype_ok(dtype) || batch < 0 || !tokens_ok(n_tokens) || !(eps >= 0.f) ||
       !std::isfinite(eps) || (weight_dtype != dtype && weight_dtype != WSATTN_FP32) || (!v) != (!v_out))
     return WSATTN_ERR_BAD_ARG;
   const int esize = dtype_size(dtype), dim = 2 * rot->table.pairs;
@@ -504,7 +506,7 @@ int wsattn_qknorm(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
       !elem_aligned(k_weight, wsize))
     return WSATTN_ERR_BAD_ARG;
   if (rows == 0) return WSATTN_OK;
-  if (!positions || n_tokens > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  if (!positions) return WSATTN_ERR_BAD_ARG;
   const int sms = sm_count();
   if (!sms) return WSATTN_ERR_CUDA;
   QkParams p;
@@ -540,7 +542,7 @@ int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_
                            int64_t pos_stride_b, const wsattn_heads* dq, const wsattn_heads* dk,
                            const wsattn_heads* dv, float* dq_weight, float* dk_weight,
                            void* workspace, size_t workspace_bytes, void* stream) {
-  if (!rot || !dtype_ok(dtype) || batch < 0 || n_tokens < 0 || !(eps >= 0.f) ||
+  if (!rot || !dtype_ok(dtype) || batch < 0 || !tokens_ok(n_tokens) || !(eps >= 0.f) ||
       !std::isfinite(eps) || (weight_dtype != dtype && weight_dtype != WSATTN_FP32) ||
       (!dv_out) != (!dv))
     return WSATTN_ERR_BAD_ARG;
@@ -578,7 +580,7 @@ int wsattn_qknorm_backward(wsattn_rotary_t rot, int dtype, int batch, int64_t n_
       return WSATTN_ERR_CUDA;
     return WSATTN_OK;
   }
-  if (!positions || n_tokens > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  if (!positions) return WSATTN_ERR_BAD_ARG;
   const int sms = sm_count();
   if (!sms) return WSATTN_ERR_CUDA;
   QkParams p;

@@ -235,7 +235,8 @@ int wsattn_prepare_static(int batch, int heads, int n_tokens, int head_dim, floa
  * allocate: scratch is the caller's (each *_workspace call gives its size),
  * so calls on different streams and captured graphs are independent as long
  * as they use different workspaces.  Sizes of zero (no tokens, no rows) are
- * accepted and enqueue only what has to be written.  Outputs must not
+ * accepted and enqueue only what has to be written; tokens of a batch element
+ * and rows stay below 2^31 - 511.  Outputs must not
  * overlap inputs or each other, except where a call says so.
  */
 

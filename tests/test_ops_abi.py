@@ -129,6 +129,23 @@ def test_rotary_errors_without_device_work():
         assert call() == CUDA
 
 
+def test_sizes_past_64_bits_are_refused():
+    # 4 x 2^62 tokens are 0 in 64 bits, and a stride times a size may wrap round
+    fw = _fw()
+    fn, rot = fw.raw_call("wsattn_rotary"), _rot()
+    for b, n in ((4, 1 << 62), (1, 1 << 31), (0, 1 << 31)):
+        v = Heads(A, 1, 1 << 40, 0, 64)
+        assert fn(rot.handle, BF16, b, n, _ref(v), A, 0, 0, _ref(v), None) == BAD
+        assert fw.raw_call("wsattn_qknorm")(
+            rot.handle, BF16, b, n, _ref(v), _ref(v), None, A, A, BF16, ctypes.c_float(1e-6), A, 0,
+            _ref(v), _ref(v), None, None) == BAD
+        assert fw.raw_call("wsattn_qknorm_backward")(
+            rot.handle, BF16, b, n, _ref(v), _ref(v), None, _ref(v), _ref(v), A, A, BF16,
+            ctypes.c_float(1e-6), A, 0, _ref(v), _ref(v), None, A, A, A, 1 << 40, None) == BAD
+    x, y = Heads(A, 4, 0, 64, 256), Heads(A, 4, 0, 1 << 62, 256)
+    assert fn(rot.handle, BF16, 1, 3, _ref(x), A, 0, 0, _ref(y), None) == BAD
+
+
 def test_qknorm_errors_without_device_work():
     fw = _fw()
     fwd, bwd, rot = fw.raw_call("wsattn_qknorm"), fw.raw_call("wsattn_qknorm_backward"), _rot()
