@@ -237,6 +237,50 @@ def test_linear_extreme_values():
     assert y[7].isinf().all() and torch.isfinite(y[:7]).all() and torch.isfinite(y[8:]).all()
 
 
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh", "silu"])
+def test_activations_keep_their_relative_precision(name):
+    """Every bf16 value up to 12, the far negative side too: value and slope.
+    The exponential's argument T has up to six roundings of 2^-24 on its way
+    (2^-21 T relative in the result); the reciprocal, the exponential, the fit
+    of the normal distribution and the products are below 2^-18 together, and
+    a logistic or exponential below 2^-126 may be flushed to zero, which the
+    value multiplies by |z| and the slope by |z| u'(z), up to 12 * 33."""
+    fw = _fw()
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16)
+    z = bits.view(torch.bfloat16)
+    z = z[z.float().abs() <= 12]
+    z = z[: z.numel() // 8 * 8]
+    zd = z.double()
+    phi = torch.exp(-zd * zd / 2) / (2 * torch.pi) ** 0.5
+    if name == "gelu":
+        s = 0.5 * torch.special.erfc(-zd / 2 ** 0.5)
+        arg, slope, mag, du = zd * zd / 2, s + zd * phi, s + zd.abs() * phi, 1
+    else:
+        u = zd if name == "silu" else (8 / torch.pi) ** 0.5 * (zd + 0.044715 * zd ** 3)
+        du = torch.ones_like(zd) if name == "silu" else (8 / torch.pi) ** 0.5 * (1 + 0.134145 * zd ** 2)
+        s, other = 1 / (1 + torch.exp(-u)), 1 / (1 + torch.exp(u))
+        # the slope's 1 - s is rounded at the size of s
+        arg, slope, mag = u.abs(), s + zd * s * other * du, s * (1 + zd.abs() * du)
+    rel = 2.0 ** -18 + 2.0 ** -21 * arg
+    # value: one product with 1, so that the activation's argument is z itself
+    x = torch.zeros((z.numel(), 8), dtype=torch.bfloat16)
+    x[:, 0] = z
+    w = torch.zeros((8, 8), dtype=torch.bfloat16)
+    w[:, 0] = 1
+    got = fw.wsattn_linear(x.cuda(), w.cuda(), activation=name, out_dtype=torch.float32)
+    want = (zd * s)[:, None].expand(-1, 8)
+    flush = 2.0 ** -125 * (1 + zd.abs())
+    assert_close(got, want, (rel * want[:, 0].abs() + flush)[:, None].expand(-1, 8), "value")
+    # slope: the bias gradient of one row is dz itself
+    one = torch.ones((1, z.numel()), dtype=torch.bfloat16)
+    wide = torch.zeros((z.numel(), 8), dtype=torch.bfloat16)
+    _, _, db = fw.wsattn_linear_backward(one.cuda(), one[:, :8].contiguous().cuda(), wide.cuda(),
+                                         z[None].contiguous().cuda(), name, need_dx=False, need_dw=False)
+    # z = -10.0625 in the tanh form: u = -88.8, logistic 2.7e-39 (flushed), |z| u' = 224
+    assert_close(db, slope, rel * mag + 2.0 ** -125 * (1 + zd.abs() * du), "slope")
+    assert fw.wsattn_op_status() == 0
+
+
 def test_linear_capture_and_streams():
     fw = _fw()
     dt = torch.bfloat16
