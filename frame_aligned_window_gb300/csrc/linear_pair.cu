@@ -325,6 +325,68 @@ __device__ __forceinline__ void act16(float (&y)[16]) {
   for (int i = 0; i < 16; ++i) y[i] = act_value<ACT>(y[i]);
 }
 
+// The bias of 16 columns (0 past the last one).
+template <typename T>
+__device__ __forceinline__ void load_bias16(const GemmParams& p, int col, float (&b)[16]) {
+  const T* bp = static_cast<const T*>(p.bias) + col;
+  if (p.bias_vec && col + 16 <= p.C) {
+    const uint4 b0 = __ldg(reinterpret_cast<const uint4*>(bp));
+    const uint4 b1 = __ldg(reinterpret_cast<const uint4*>(bp) + 1);
+    const uint32_t w[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = unpack_pair(w[i], T());
+      b[2 * i] = f.x;
+      b[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = col + i < p.C ? to_f32(bp[i]) : 0.f;
+  }
+}
+
+// A chunk of the output that is the product, with a bias or without: its 128
+// bytes a row go to staging in one sweep.  An eighth of the instructions of
+// the general way below, which a short contraction would wait for.
+template <typename T, typename O>
+__device__ __forceinline__ void plain_chunk(const GemmParams& p, uint32_t taddr, uint32_t buf,
+                                            int col0, int lane) {
+  constexpr int kBlocks = 8 / sizeof(O);  // of 16 columns
+  uint32_t r[kBlocks][16];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) tmem_ld16(taddr + 16 * i, r[i]);
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) tmem_wait_ld16(r[i]);
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      float b[16];
+      load_bias16<T>(p, col0 + 16 * i, b);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) r[i][e] = __float_as_uint(__uint_as_float(r[i][e]) + b[e]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        st_shared_v4(unit_at(buf, lane, 4 * i + u), r[i][4 * u], r[i][4 * u + 1], r[i][4 * u + 2],
+                     r[i][4 * u + 3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_pair(__uint_as_float(r[i][8 * u + 2 * e]),
+                           __uint_as_float(r[i][8 * u + 2 * e + 1]), T());
+        st_shared_v4(unit_at(buf, lane, 2 * i + u), w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
 template <typename T, typename O, int BN, bool TWO>
 __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t staging, int pair,
                          int pairs, uint32_t rank, uint32_t tbase) {
@@ -343,6 +405,7 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
     const int tr = ref.tr, tc = ref.tc;
     // pre-activations of 16 bits beside outputs of 16 bits go through staging
     const bool stage_pre = p.pre != nullptr && sizeof(O) == 2;
+    const bool plain = !p.pre && !p.res && p.act == WSATTN_ACT_NONE;
     const uint32_t ab = it & 1u, use = it >> 1;
     const int64_t row0 = static_cast<int64_t>(tr) * kPairRows + 128 * rank + 32 * wq;
     const bool tile_ok =
@@ -399,35 +462,21 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
         waited = true;
       }
       __syncwarp();
+      if (on && plain) plain_chunk<T, O>(p, tlane + ab * BN + tcol, buf, col0, lane);
 #pragma unroll 1
-      for (int g = 0; on && g < kCols / 16; ++g) {
+      for (int g = 0; on && !plain && g < kCols / 16; ++g) {
         uint32_t r[16];
         tmem_ld16(tlane + ab * BN + tcol + 16 * g, r);
         const int col = col0 + 16 * g;
         float y[16], bv[16];
-        if (p.bias) {
-          const T* bp = static_cast<const T*>(p.bias) + col;
-          if (p.bias_vec && col + 16 <= p.C) {
-            const uint4 b0 = __ldg(reinterpret_cast<const uint4*>(bp));
-            const uint4 b1 = __ldg(reinterpret_cast<const uint4*>(bp) + 1);
-            const uint32_t w[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = unpack_pair(w[i], T());
-              bv[2 * i] = f.x;
-              bv[2 * i + 1] = f.y;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) bv[i] = col + i < p.C ? to_f32(bp[i]) : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) bv[i] = 0.f;
-        }
+        if (p.bias) load_bias16<T>(p, col, bv);
         tmem_wait_ld16(r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(r[i]) + bv[i];
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(r[i]);
+        if (p.bias) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] += bv[i];
+        }
         if (p.pre) {
           uint32_t w[8];
 #pragma unroll
