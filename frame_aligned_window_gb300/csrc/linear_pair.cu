@@ -431,7 +431,7 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_free[ab]);
+      if (lane == 0) mbar_arrive_relaxed(acc_free[ab]);
       continue;
     }
     bool waited = false;
@@ -537,7 +537,7 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
       if (j == BN / 2 / kCols - 1) {  // this warp has read its columns of the accumulator
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_free[ab]);
+        if (lane == 0) mbar_arrive_relaxed(acc_free[ab]);
       }
       if (!on) continue;
       fence_proxy_async_smem();
