@@ -355,9 +355,29 @@ __device__ __forceinline__ void plain_chunk(const GemmParams& p, uint32_t taddr,
   uint32_t r[kBlocks][16];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i) tmem_ld16(taddr + 16 * i, r[i]);
+  // a whole chunk's bias is on its way while the accumulator is
+  const bool whole = p.bias && p.bias_vec && col0 + 16 * kBlocks <= p.C;
+  uint4 raw[2 * kBlocks];
+  if (whole) {
+    const uint4* bp = reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + col0);
+#pragma unroll
+    for (int i = 0; i < 2 * kBlocks; ++i) raw[i] = __ldg(bp + i);
+  }
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i) tmem_wait_ld16(r[i]);
-  if (p.bias) {
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < 2 * kBlocks; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t* d = r[i / 2] + 8 * (i % 2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_pair(w[e], T());
+        d[2 * e] = __float_as_uint(__uint_as_float(d[2 * e]) + f.x);
+        d[2 * e + 1] = __float_as_uint(__uint_as_float(d[2 * e + 1]) + f.y);
+      }
+    }
+  } else if (p.bias) {
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
       float b[16];
