@@ -286,37 +286,38 @@ __device__ void store_rows(uint32_t buf, void* out, int64_t ld, int64_t row0, in
       }
 }
 
-// Residual rows -> staging buffer.
+// Residual rows -> staging buffer, by way of registers where the rows are on
+// 16 bytes, so that a chunk's loads can go out before its turn comes.
+template <typename O>
+__device__ __forceinline__ void fetch_rows(const GemmParams& p, int64_t row0, int col0, int lane,
+                                           uint4 (&v)[8]) {
+  using W = typename Raw<O>::type;
+  const int col = col0 + (lane & 7) * (16 / static_cast<int>(sizeof(O)));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = row0 + 4 * i + lane / 8;
+    v[i] = row < p.R && col < p.C ? *reinterpret_cast<const uint4*>(static_cast<const W*>(p.res) +
+                                                                    row * p.ldr + col)
+                                  : make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ void put_rows(uint32_t buf, int lane, const uint4 (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    st_shared_v4(unit_at(buf, 4 * i + lane / 8, lane & 7), v[i].x, v[i].y, v[i].z, v[i].w);
+}
 template <typename O>
 __device__ void load_rows(const GemmParams& p, uint32_t buf, int64_t row0, int col0, int lane) {
   using W = typename Raw<O>::type;
   constexpr int kCols = 128 / sizeof(O);
   const W* res = static_cast<const W*>(p.res);
-  if (p.res_vec) {
-    const int u = lane & 7;
-    const int col = col0 + u * (16 / static_cast<int>(sizeof(O)));
-    uint4 v[8];
+  for (int r = 0; r < 32; ++r)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + 4 * i + lane / 8;
-      v[i] = row < p.R && col < p.C
-                 ? *reinterpret_cast<const uint4*>(res + row * p.ldr + col)
-                 : make_uint4(0, 0, 0, 0);
+    for (int e = 0; e < kCols; e += 32) {
+      const bool on = row0 + r < p.R && col0 + e + lane < p.C;
+      st_elem(elem_at<O>(buf, r, e + lane),
+              on ? res[(row0 + r) * p.ldr + col0 + e + lane] : static_cast<W>(0));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t a = unit_at(buf, 4 * i + lane / 8, u);
-      st_shared_v4(a, v[i].x, v[i].y, v[i].z, v[i].w);
-    }
-  } else {
-    for (int r = 0; r < 32; ++r)
-#pragma unroll
-      for (int e = 0; e < kCols; e += 32) {
-        const bool on = row0 + r < p.R && col0 + e + lane < p.C;
-        st_elem(elem_at<O>(buf, r, e + lane),
-                on ? res[(row0 + r) * p.ldr + col0 + e + lane] : static_cast<W>(0));
-      }
-  }
 }
 
 template <typename T, int ACT>
@@ -325,33 +326,32 @@ __device__ __forceinline__ void act16(float (&y)[16]) {
   for (int i = 0; i < 16; ++i) y[i] = act_value<ACT>(y[i]);
 }
 
-// The bias of 16 columns (0 past the last one).
+// Adds eight 16-bit values.
+template <typename T>
+__device__ __forceinline__ void add8(float* y, const uint4& b) {
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_pair(w[i], T());
+    y[2 * i] += f.x;
+    y[2 * i + 1] += f.y;
+  }
+}
+// The bias of 16 columns of any alignment (0 past the last one).
 template <typename T>
 __device__ __forceinline__ void load_bias16(const GemmParams& p, int col, float (&b)[16]) {
   const T* bp = static_cast<const T*>(p.bias) + col;
-  if (p.bias_vec && col + 16 <= p.C) {
-    const uint4 b0 = __ldg(reinterpret_cast<const uint4*>(bp));
-    const uint4 b1 = __ldg(reinterpret_cast<const uint4*>(bp) + 1);
-    const uint32_t w[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = unpack_pair(w[i], T());
-      b[2 * i] = f.x;
-      b[2 * i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = col + i < p.C ? to_f32(bp[i]) : 0.f;
-  }
+  for (int i = 0; i < 16; ++i) b[i] = col + i < p.C ? to_f32(bp[i]) : 0.f;
 }
 
 // A chunk of the output that is the product, with a bias or without: its 128
 // bytes a row go to staging in one sweep.  An eighth of the instructions of
 // the general way below, which a short contraction would wait for.
 template <typename T, typename O>
-__device__ __forceinline__ void plain_chunk(const GemmParams& p, uint32_t taddr, uint32_t buf,
-                                            int col0, int lane) {
-  constexpr int kBlocks = 8 / sizeof(O);  // of 16 columns
+__device__ __forceinline__ void plain_half(const GemmParams& p, uint32_t taddr, uint32_t buf,
+                                           int col0, int first, int lane) {
+  constexpr int kBlocks = 4 / sizeof(O);  // of 16 columns
   uint32_t r[kBlocks][16];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i) tmem_ld16(taddr + 16 * i, r[i]);
@@ -391,7 +391,7 @@ __device__ __forceinline__ void plain_chunk(const GemmParams& p, uint32_t taddr,
     if constexpr (sizeof(O) == 4) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        st_shared_v4(unit_at(buf, lane, 4 * i + u), r[i][4 * u], r[i][4 * u + 1], r[i][4 * u + 2],
+        st_shared_v4(unit_at(buf, lane, first + 4 * i + u), r[i][4 * u], r[i][4 * u + 1], r[i][4 * u + 2],
                      r[i][4 * u + 3]);
     } else {
 #pragma unroll
@@ -401,10 +401,18 @@ __device__ __forceinline__ void plain_chunk(const GemmParams& p, uint32_t taddr,
         for (int e = 0; e < 4; ++e)
           w[e] = pack_pair(__uint_as_float(r[i][8 * u + 2 * e]),
                            __uint_as_float(r[i][8 * u + 2 * e + 1]), T());
-        st_shared_v4(unit_at(buf, lane, 2 * i + u), w[0], w[1], w[2], w[3]);
+        st_shared_v4(unit_at(buf, lane, first + 2 * i + u), w[0], w[1], w[2], w[3]);
       }
     }
   }
+}
+template <typename T, typename O>
+__device__ __forceinline__ void plain_chunk(const GemmParams& p, uint32_t taddr, uint32_t buf,
+                                            int col0, int lane) {
+  constexpr int kCols = 64 / sizeof(O);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i)
+    plain_half<T, O>(p, taddr + kCols * i, buf, col0 + kCols * i, 4 * i, lane);
 }
 
 template <typename T, typename O, int BN, bool TWO>
@@ -425,7 +433,6 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
     const int tr = ref.tr, tc = ref.tc;
     // pre-activations of 16 bits beside outputs of 16 bits go through staging
     const bool stage_pre = p.pre != nullptr && sizeof(O) == 2;
-    const bool plain = !p.pre && !p.res && p.act == WSATTN_ACT_NONE;
     const uint32_t ab = it & 1u, use = it >> 1;
     const int64_t row0 = static_cast<int64_t>(tr) * kPairRows + 128 * rank + 32 * wq;
     const bool tile_ok =
@@ -454,6 +461,40 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
       if (lane == 0) mbar_arrive_relaxed(acc_free[ab]);
       continue;
     }
+    if (!p.pre && !p.res && p.act == WSATTN_ACT_NONE) {
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; ok && j < BN / 2 / kCols; ++j) {
+        const int tcol = half * (BN / 2) + j * kCols;
+        const int col0 = tc * BN + tcol;
+        const bool on = tile_ok && row0 < p.R && col0 < p.C;
+        const uint32_t buf = buf0 + ob * kBuf;
+        if (on && lane == 0) bulk_wait_read_1();  // the buffer's previous store has read it
+        if (j == 0) {
+          ok = __all_sync(0xffffffffu,
+                          wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        __syncwarp();
+        if (on) plain_chunk<T, O>(p, tlane + ab * BN + tcol, buf, col0, lane);
+        if (j == BN / 2 / kCols - 1) {  // this warp has read its columns of the accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed(acc_free[ab]);
+        }
+        if (!on) continue;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (!p.out_vec) store_rows<O>(buf, p.out, p.ldo, row0, p.R, col0, p.C, lane);
+        else if (lane == 0) tma_store_2d(&p.tm_out, buf, col0, static_cast<int>(row0));
+        if (lane == 0) bulk_commit_group();
+        __syncwarp();
+        ob ^= 1u;
+      }
+      aborted = !ok;
+      continue;
+    }
     bool waited = false;
 #pragma unroll 1
     for (int j = 0; j < BN / 2 / kCols; ++j) {
@@ -470,7 +511,13 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
           else bulk_wait_read_1();
         }
         __syncwarp();
-        if (p.res) load_rows<O>(p, buf, row0, col0, lane);
+        if (p.res_vec) {
+          uint4 res[8];
+          fetch_rows<O>(p, row0, col0, lane, res);
+          put_rows(buf, lane, res);
+        } else if (p.res) {
+          load_rows<O>(p, buf, row0, col0, lane);
+        }
       }
       if (!waited) {
         const bool ok = wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax);
@@ -482,21 +529,38 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
         waited = true;
       }
       __syncwarp();
-      if (on && plain) plain_chunk<T, O>(p, tlane + ab * BN + tcol, buf, col0, lane);
-#pragma unroll 1
-      for (int g = 0; on && !plain && g < kCols / 16; ++g) {
-        uint32_t r[16];
+      // 16 columns at a time: the next ones' accumulators and bias are on
+      // their way while these are worked on
+      const bool bias_fast = p.bias_vec && col0 + kCols <= p.C;
+      uint32_t r[16];
+      uint4 b0, b1;
+      auto start = [&](int g) {
         tmem_ld16(tlane + ab * BN + tcol + 16 * g, r);
+        if (bias_fast) {
+          const uint4* bp =
+              reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + col0 + 16 * g);
+          b0 = __ldg(bp);
+          b1 = __ldg(bp + 1);
+        }
+      };
+      if (on) start(0);
+#pragma unroll 1
+      for (int g = 0; on && g < kCols / 16; ++g) {
         const int col = col0 + 16 * g;
-        float y[16], bv[16];
-        if (p.bias) load_bias16<T>(p, col, bv);
+        float y[16];
         tmem_wait_ld16(r);
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(r[i]);
-        if (p.bias) {
+        if (bias_fast) {
+          add8<T>(y, b0);
+          add8<T>(y + 8, b1);
+        } else if (p.bias) {
+          float bv[16];
+          load_bias16<T>(p, col, bv);
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i] += bv[i];
         }
+        if (g + 1 < kCols / 16) start(g + 1);
         if (p.pre) {
           uint32_t w[8];
 #pragma unroll
