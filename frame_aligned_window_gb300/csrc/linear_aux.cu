@@ -190,18 +190,19 @@ cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s) {
 }
 
 // Estimated time of each tiling in nanoseconds; the least one wins.  The
-// constants are fitted to the timings of every tiling at 60 shapes (1 to
-// 20000 rows, 128 to 5120 columns and values, all three orders of the
+// constants are fitted to the timings of every tiling at 60 to 90 shapes (1 to
+// 20000 rows, 64 to 5120 columns and values, all three orders of the
 // operands, back to back with operands from HBM): the tiling taken is then
-// within 5 % of the best one on average, 1.33 at worst.
+// within 2.5 % of the best one on average, 1.25 at worst.
 //   pair   a 64-wide step of a 256-column tile takes 290 ns (the MMAs alone
 //          270 at full clocks), of a 128-column tile 269 (bound by the 24 KB a
-//          CTA reads of L2 for it); 1.4 to 2.5 us a tile for its epilogue
+//          CTA reads of L2 for it); a tile 1.2 or 0.65 us beside its steps,
+//          and the first loads and the last epilogue are seen once
 //   tile   a step of a CTA takes the time of its bytes at 134 KB a
 //          microsecond and SM, shared by two CTAs, or 200 ns; a row of the
 //          tile 45 ns of epilogue, and the cluster's exchange 800 ns
-constexpr double kPairStart = 2670.0, kPairTile256 = 2520.0, kPairStep256 = 290.0,
-                 kPairTile128 = 1420.0, kPairStep128 = 269.0;
+constexpr double kPairStart256 = 4000.0, kPairTile256 = 1200.0, kPairStep256 = 290.0,
+                 kPairStart128 = 3500.0, kPairTile128 = 650.0, kPairStep128 = 269.0;
 
 GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, double* ns) {
   constexpr int sms = kTilingSms;
@@ -218,8 +219,8 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, double* ns) {
   const double steps = static_cast<double>(ksteps);
   for (int bn = 256; bn >= 128; bn -= 128) {
     const double waves = static_cast<double>(cdiv(cdiv(R, kPairRows) * cdiv(C, bn), sms / 2));
-    consider(kPairStart + waves * (bn == 256 ? steps * kPairStep256 + kPairTile256
-                                             : steps * kPairStep128 + kPairTile128),
+    consider(bn == 256 ? kPairStart256 + waves * (steps * kPairStep256 + kPairTile256)
+                       : kPairStart128 + waves * (steps * kPairStep128 + kPairTile128),
              GemmShape{bn, 0, 1, 0});
   }
   // pairs whose last round is split: parts of at least 8 steps, one a pair.
@@ -234,7 +235,7 @@ GemmShape choose_gemm(int64_t R, int C, int K, bool p_mn, double* ns) {
     if (parts > ksteps / 8) parts = ksteps / 8;
     if (parts > 16) parts = 16;
     if (parts >= 2 && tiles <= INT32_MAX)
-      consider(kPairStart + static_cast<double>(tiles / pairs) * (steps * kPairStep256 + kPairTile256) +
+      consider(kPairStart256 + static_cast<double>(tiles / pairs) * (steps * kPairStep256 + kPairTile256) +
                    static_cast<double>(cdiv(ksteps, parts)) * kPairStep256 + 4000.0 +
                    100.0 * static_cast<double>(rest * parts),
                GemmShape{256, 0, static_cast<int>(parts), static_cast<int>(tiles - rest)});
@@ -292,7 +293,7 @@ double pair_time_of_two(int64_t Ra, int Ca, int Ka, int64_t Rb, int Cb, int Kb) 
                       static_cast<double>(first + rounds + (extra > rest)) * lb;
     t = t1 > t2 ? t1 : t2;
   }
-  return kPairStart + t;
+  return kPairStart256 + t;
 }
 
 }  // namespace wsattn
