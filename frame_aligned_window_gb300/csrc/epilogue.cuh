@@ -59,6 +59,7 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
+// Slope for |z| <= 1000 (clamp_pair): beyond, it is 0 or 1 as at the ends.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == WSATTN_ACT_GELU) {
@@ -67,8 +68,7 @@ __device__ __forceinline__ float act_slope(float z) {
     return fmaf(z * 0.39894228040143f, e, c);
   }
   if (ACT == WSATTN_ACT_GELU_TANH) {
-    // past |z| = 1000, s (1 - s) is zero: the square is kept finite for it
-    const float zz = fminf(z * z, 1e6f);
+    const float zz = z * z;
     const float s = logistic_log2(gelu_log2(z, zz));
     return fmaf(s * (1.f - s) * z, fmaf(0.2140644488178f, zz, 1.5957691216057f), s);
   }
@@ -101,6 +101,23 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __nv_bfloat16)
 }
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __half) {
   const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Pre-activations held to +-1000 (exact in both types) before their slope is
+// taken: past 65504 rounding to fp16 made them infinite where the forward pass
+// was finite, and a slope's 0 * infinity would be a NaN.  A NaN stays one.  Two
+// at a time: the sums of 21952 x 5120 behind the tanh form take 79 us with it
+// and without, 86 when each fp32 value is held by itself.
+__device__ __forceinline__ uint32_t clamp_pair(uint32_t w, __nv_bfloat16) {
+  const __nv_bfloat162 v = __hmax2_nan(
+      __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(1000.f)),
+      __float2bfloat162_rn(-1000.f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t clamp_pair(uint32_t w, __half) {
+  const __half2 v =
+      __hmax2_nan(__hmin2_nan(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1000.f)),
+                  __float2half2_rn(-1000.f));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ float to_f32(float v) { return v; }

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(DactParams p) {
           float2 d = unpack_pair(g[i], T());
           if (ACT != WSATTN_ACT_NONE) {
             // rounded here, so that the sums are the same with and without dz
-            const float2 y = unpack_pair(z[i], T());
+            const float2 y = unpack_pair(clamp_pair(z[i], T()), T());
             d.x = __fmul_rn(d.x, act_slope<ACT>(y.x));
             d.y = __fmul_rn(d.y, act_slope<ACT>(y.y));
           }

@@ -383,7 +383,8 @@ int wsattn_linear_workspace(const wsattn_linear_args* args, size_t* bytes);
  *   dx = dz w     [m, k]      dw = dz^T x   [n, k]      db = sum of dz's rows
  * Any of dx, dw and db may be NULL to skip it.
  *   dtype    of dout, x, w, preact, dx and dw
- *   preact   as wsattn_linear left it; NULL only without an activation
+ *   preact   as wsattn_linear left it; NULL only without an activation.  Where
+ *            rounding made it infinite (fp16 past 65504) the slope is 0 or 1
  *   db       fp32 [n], of the unrounded dz, in a fixed order
  * Strides, alignment and workspace as for wsattn_linear; with m = 0, dw and
  * db are zeroed.  dx, dw and db must not overlap any input.
