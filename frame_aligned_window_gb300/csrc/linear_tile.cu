@@ -33,21 +33,23 @@ __device__ __forceinline__ uint32_t bar(const GemmShared& s, int i) {
   return s.bars + 8u * static_cast<uint32_t>(i);
 }
 
-__device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t parity, int code) {
+__device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t parity, int code,
+                                       long long limit) {
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(b, parity)) return true;
     if (*s.abort_flag) return false;
-    if (clock64() - t0 > kGemmWaitLimit) {
+    if (clock64() - t0 > limit) {
       atomicOr(s.status, code);
       *s.abort_flag = 1;
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t parity, int code) {
+__device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t parity, int code,
+                                     long long limit = kGemmWaitLimit) {
   if (mbar_try_wait(b, parity)) return true;
-  return wait_slow(s, b, parity, code);
+  return wait_slow(s, b, parity, code, limit);
 }
 
 __device__ void producer(const GemmParams& p, const GemmShared& s, int row0, int col0, int k0,
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
     side_sums(p, static_cast<int>(blockIdx.x) * 128 + static_cast<int>(threadIdx.x) - 64,
               static_cast<int>(gridDim.x) * 128);
     __syncwarp();
-    bool have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax);
+    bool have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax,
+                                accumulator_limit(k1 - k0));
     have = __all_sync(0xffffffffu, have);
     tc_fence_after();
     if (have) {
