@@ -558,10 +558,15 @@ def _positions(rot, t, batch, tokens, dev):
     return t.data_ptr(), stride
 
 
+_INT_MAX = (1 << 31) - 1  # batch elements and heads are ints of the C ABI
+
+
 def _heads_shape(t, name, rot):
     shape = t.shape
     if len(shape) != 4 or shape[3] != rot.head_dim:
         raise ValueError(f"{name} must be [B, H, N, {rot.head_dim}], got {list(shape)}")
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:  # ctypes would drop the upper bits
+        raise ValueError(f"{name} has more than {_INT_MAX} batch elements or heads: {list(shape)}")
     return shape
 
 

@@ -1,0 +1,41 @@
+"""The binding of the operators around the attention on the CPU: what it
+refuses or passes on before any tensor is read (shapes alone, on the meta
+device)."""
+import pytest
+import torch
+
+
+def _fw():
+    import frame_aligned_window_gb300 as fw
+    return fw
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 1, 1, 1, 16), (1 << 31, 1, 3, 16), (1, 1 << 31, 1, 16)])
+def test_sizes_past_an_int_are_refused(shape):
+    # 2^32 + 1 batch elements would be one of the C call's
+    fw = _fw()
+    rot = fw.wsattn_rotary_plan(16, (8,))
+    big = torch.empty((1, 1, 1, 16), device="meta").expand(shape)
+    one = torch.empty((1, 1, 1, 16), device="meta")
+    with pytest.raises(ValueError):
+        fw._heads_shape(big, "x", rot)
+    with pytest.raises(ValueError):
+        fw._qkv_shapes(rot, big, big, None)
+    most = torch.empty((1, 1, 1, 16), device="meta").expand((1 << 31) - 1, 1, 1, 16)
+    assert fw._heads_shape(most, "x", rot)[0] == (1 << 31) - 1
+    assert fw._qkv_shapes(rot, one, one, one)[2] == one.shape
+
+
+@pytest.mark.gpu
+def test_batches_past_an_int_are_refused_before_any_memory_is_taken():
+    fw = _fw()
+    rot = fw.wsattn_rotary_plan(16, (8,))
+    x = torch.zeros((1, 1, 1, 16), dtype=torch.bfloat16, device="cuda").expand((1 << 32) + 1, 1, 1, 16)
+    pos = torch.zeros((1, 1), device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for call in (lambda: fw.wsattn_rotary(rot, x, pos), lambda: fw.wsattn_qknorm(rot, x, x, pos),
+                 lambda: fw.wsattn_qknorm_backward(rot, x, x, x, x, pos)):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.cuda.max_memory_allocated() == before
