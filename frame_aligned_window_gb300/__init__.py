@@ -879,8 +879,15 @@ def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="n
 
 
 def wsattn_op_status(stream=None) -> int:
-    """Status of the operators above on the current device (synchronises)."""
-    return int(_lib.wsattn_op_status(_stream_ptr(stream)))
+    """Status of the operators above on the stream's device (default: the
+    current stream).  One word a device, shared by its streams: see wsattn.h.
+    Synchronises the stream."""
+    dev = _current_device() if stream is None else stream.device.index
+    raw = _raw_stream(dev, stream)
+    if _current_device() == dev:
+        return int(_lib.wsattn_op_status(raw))
+    with torch.cuda.device(dev):
+        return int(_lib.wsattn_op_status(raw))
 
 
 def raw_call(name: str):

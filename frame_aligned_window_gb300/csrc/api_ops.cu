@@ -785,12 +785,17 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* a, void* workspace,
 int wsattn_op_status(void* stream) {
   int* w = wsattn::op_status_ptr();
   if (!w) return WSATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   int st = 0;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-      cudaMemcpy(&st, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(&st, w, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
     return WSATTN_ERR_CUDA;
   if (st == 0) return WSATTN_OK;
-  if (cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return WSATTN_ERR_CUDA;
+  // the bits reported here and no others: one that another stream's kernel sets
+  // meanwhile is left for the next query
+  if (wsattn::launch_clear_status(w, st, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return WSATTN_ERR_CUDA;
   return (st & wsattn::kStatusBounds) ? WSATTN_ERR_BOUNDS : WSATTN_ERR_TIMEOUT;
 }
 

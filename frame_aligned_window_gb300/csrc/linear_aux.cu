@@ -153,6 +153,8 @@ cudaError_t dact_t(const DactParams& p, cudaStream_t s) {
 
 __device__ int g_op_status;
 
+__global__ void clear_status(int* word, int seen) { atomicAnd(word, ~seen); }
+
 }  // namespace
 
 int* op_status_ptr() {
@@ -165,6 +167,11 @@ int* op_status_ptr() {
     ptr[dev] = static_cast<int*>(a);
   }
   return ptr[dev];
+}
+
+cudaError_t launch_clear_status(int* word, int seen, cudaStream_t s) {
+  clear_status<<<1, 1, 0, s>>>(word, seen);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_pack(int dtype, const PackJob& a, const PackJob& b, cudaStream_t s) {

@@ -157,6 +157,8 @@ cudaError_t launch_gemm_tile(const GemmParams& p, int dtype, bool out_f32, cudaS
 // Device status word of the operators that have no plan (one per device, in
 // the library's image; its address is looked up once per device).
 int* op_status_ptr();
+// Clears the bits `seen` of a status word.
+cudaError_t launch_clear_status(int* word, int seen, cudaStream_t s);
 
 // Copies [rows, cols] matrices with any row stride and alignment to rows of
 // `ldd` elements (a multiple of 8), up to two in one launch; f32_heads > 0

@@ -414,9 +414,13 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* args, void* workspace,
 int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes);
 
 /* Synchronises `stream` and reports the status word of the operators above on
- * the current device: OK, TIMEOUT if a device-side wait expired (outputs are
- * invalid), BOUNDS (debug build); the word is then cleared.  CUDA if the
- * synchronisation failed. */
+ * the current device: OK, TIMEOUT if a device-side wait expired, BOUNDS (debug
+ * build); what was reported is then cleared.  CUDA if the synchronisation
+ * failed.  The word is one per device, shared by all streams and threads:
+ * anything but OK says that an operator on any of them, since the last query
+ * on any of them, left invalid outputs.  Only kernels that are complete have
+ * set it, so a query speaks for the work before it on `stream` and for
+ * whatever other streams have finished. */
 int wsattn_op_status(void* stream);
 
 /* ---------------------------------------------------------- introspection */

@@ -39,3 +39,27 @@ def test_batches_past_an_int_are_refused_before_any_memory_is_taken():
         with pytest.raises(ValueError):
             call()
     assert torch.cuda.max_memory_allocated() == before
+
+
+def test_status_is_asked_on_the_streams_device(monkeypatch):
+    from types import SimpleNamespace
+    fw = _fw()
+    now, asked = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(fw, "_current_device", lambda: now[0])
+    monkeypatch.setattr(fw._lib, "wsattn_op_status", lambda raw: asked.append((now[0], getattr(raw, "value", raw))) or 7)
+    stream = SimpleNamespace(device=SimpleNamespace(index=3), cuda_stream=77)
+    assert fw.wsattn_op_status(stream) == 7
+    stream.device.index = 0
+    assert fw.wsattn_op_status(stream) == 7
+    assert asked == [(3, 77), (0, 77)] and now == [0]
