@@ -738,8 +738,9 @@ def _scratch(query, what, args, workspace, dev, like, stream):
     return *_scratch_args(workspace, dev), workspace
 
 
-def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, stream):
-    """The packed wsattn_linear_args, the output and the device."""
+def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, stream, query=False):
+    """The packed wsattn_linear_args, the output and the device.  query: for
+    the workspace's size, which depends on x and weight alone (no output)."""
     dev = _device_of(weight, "weight")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
@@ -762,6 +763,9 @@ def _linear_args(x, weight, bias, residual, activation, preact, out, out_dtype, 
     ldw = _rows(weight, "weight", k, None, dt, dev)
     xp, wp = x.data_ptr(), weight.data_ptr()
     bp = rp = pp = ldr = ldp = 0
+    if query:
+        return _LINEAR(code, code, m, n, k, xp, ldx, heads, tokens, wp, ldw, bp, rp, ldr, 0, n, pp,
+                       ldp, act), None, dev, False
     if bias is not None:
         _check_tensor(bias, "bias", dev, dt)
         if bias.shape != (n,) or (n > 1 and bias.stride(0) != 1):
@@ -808,15 +812,17 @@ def wsattn_linear_workspace(x, weight) -> int:
     """Bytes of scratch wsattn_linear takes for these operands (0 for products
     below 2^33 multiply-adds whose rows start on 16-byte boundaries, unless x
     is the attention's output)."""
-    args, _, dev, _ = _linear_args(x, weight, None, None, "none", None, None, None, None)
+    args, _, dev, _ = _linear_args(x, weight, None, None, "none", None, None, None, None, query=True)
     n = _SZ()
     _run(dev, "wsattn_linear_workspace", _lib.wsattn_linear_workspace, args, ctypes.byref(n))
     return int(n.value)
 
 
 def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need_dx, need_dw, need_db,
-                      stream):
-    """The packed wsattn_linear_grad_args, the gradients and the device."""
+                      stream, query=False):
+    """The packed wsattn_linear_grad_args, the gradients and the device.  query:
+    for the workspace's size, which depends on which gradients are wanted, not
+    on where they go (any address stands for them, and nothing is allocated)."""
     dev = _device_of(weight, "weight")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n, k], got {list(weight.shape)}")
@@ -833,6 +839,10 @@ def _linear_grad_args(dout, x, weight, preact, activation, dx, dw, db, need_dx, 
     pp = ldp = dxp = lddx = dwp = lddw = dbp = 0
     if preact is not None:
         ldp, pp = _rows(preact, "preact", n, lead, dt, dev), preact.data_ptr()
+    if query:
+        dxp, dwp, dbp = (256 if need else 0 for need in (need_dx, need_dw, need_db))
+        return _LINEAR_GRAD(code, m, n, k, dout.data_ptr(), ldd, x.data_ptr(), ldx,
+                            weight.data_ptr(), ldw, pp, ldp, act, dxp, k, dwp, k, dbp), dx, dw, db, dev
     if need_dx or dx is not None:
         dx = _empty(x.shape, dt, weight, stream) if dx is None else dx
         lddx, dxp = _rows(dx, "dx", k, lead, dt, dev), dx.data_ptr()
@@ -871,7 +881,7 @@ def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="n
                                      need_dw=True, need_db=True) -> int:
     """Bytes of scratch wsattn_linear_backward takes for these operands."""
     args, *_, dev = _linear_grad_args(dout, x, weight, preact, activation, None, None, None,
-                                      need_dx, need_dw, need_db, None)
+                                      need_dx, need_dw, need_db, None, query=True)
     n = _SZ()
     _run(dev, "wsattn_linear_backward_workspace", _lib.wsattn_linear_backward_workspace, args,
          ctypes.byref(n))
