@@ -27,10 +27,22 @@ import struct
 
 import numpy as np
 
-try:
-    import torch
-except ImportError:  # the host-only calls (plans, block maps) need no torch
-    torch = None
+
+class _Deferred:
+    """Stands for torch until a call first uses it: plans, block maps and the
+    other host-only calls do without it, and without its start-up."""
+
+    def __getattr__(self, name):
+        global torch, _raw_current_stream, _current_device
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+        # the raw handle of a device's current stream without a Stream object
+        _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        return getattr(torch, name)
+
+
+torch = _Deferred()
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("WSATTN_LIBRARY") or os.path.join(_HERE, "libwsattn.so")
@@ -389,12 +401,13 @@ def wsattn_prepare_static_outputs(batch, heads, n_tokens, head_dim, device="cuda
 
 # ------------------------------------------------ operators around the attention
 
-_DTYPES = {} if torch is None else {torch.bfloat16: BF16, torch.float16: FP16,
-                                    torch.float32: FP32}
-# the raw handle of a device's current stream without a Stream object
-_raw_current_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
-_current_device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None) or (
-    lambda: torch.cuda.current_device())
+# filled and replaced by faster ones when torch is imported
+_DTYPES = {}
+_raw_current_stream = None
+
+
+def _current_device():
+    return torch.cuda.current_device()
 
 
 def _dtype_code(t, name, allowed=(BF16, FP16, FP32)):

@@ -44,6 +44,7 @@ def test_batches_past_an_int_are_refused_before_any_memory_is_taken():
 def test_status_is_asked_on_the_streams_device(monkeypatch):
     from types import SimpleNamespace
     fw = _fw()
+    assert fw.torch.cuda is torch.cuda
     now, asked = [0], []
 
     class Device:
@@ -63,3 +64,33 @@ def test_status_is_asked_on_the_streams_device(monkeypatch):
     stream.device.index = 0
     assert fw.wsattn_op_status(stream) == 7
     assert asked == [(3, 77), (0, 77)] and now == [0]
+
+
+@pytest.mark.parametrize("missing", [False, True])
+def test_host_only_calls_do_without_torch(missing):
+    # plans and their readers start without torch, where there is none too; a
+    # call on tensors imports it
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import sys
+if {missing}:
+    sys.modules["torch"] = None            # any import of it fails
+import frame_aligned_window_gb300 as fw
+plan = fw.wsattn_plan(4, 48, 1, 1, 2, 64)
+fw.wsattn_get_block_map(plan), fw.wsattn_get_csr(plan), fw.wsattn_get_tiles(plan), fw.wsattn_plan_info(plan)
+rot = fw.wsattn_rotary_plan(64, (16, 16))
+fw.wsattn_qknorm_backward_workspace(rot), fw.wsattn_build_flags(), fw.wsattn_status_string(0)
+assert sys.modules.get("torch") is None
+try:
+    fw.wsattn_rotary(rot, 1, 2)
+except TypeError:
+    assert not {missing} and "torch" in sys.modules and fw.torch is sys.modules["torch"]
+except ImportError:
+    assert {missing}
+print("done")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
