@@ -249,7 +249,7 @@ enum wsattn_dtype { WSATTN_BF16 = 0, WSATTN_FP16 = 1, WSATTN_FP32 = 2 };
  *   head_dim     D: a multiple of 16, 16 .. 256
  *   axes         columns of the positions, 1 .. 4 (time, height, width, ...)
  *   pair_axis    int32 [D / 2], each in [0, axes)
- *   pair_freq    double [D / 2], finite; 0 leaves a pair as it is
+ *   pair_freq    double [D / 2], at most 1e30 in size; 0 leaves a pair as it is
  *   interleaved  1: pairs are dims (2p, 2p + 1), as in wsattn_produce;
  *                0: pairs are dims (p, p + D / 2)
  * Errors: BAD_ARG, UNSUPPORTED (head_dim), NO_MEMORY.
@@ -272,8 +272,10 @@ typedef struct wsattn_heads {
 /*
  * y = x turned by its tokens' positions (inverse = 1: turned back, which is
  * also the gradient: dx = turned back dy).  y may be x itself.
- *   dtype      of x and y (wsattn_dtype); arithmetic is fp32, angles are
- *              reduced with their full precision at any position
+ *   dtype      of x and y (wsattn_dtype); arithmetic is fp32.  An angle of t
+ *              turns (t = pos * freq / 2 pi) is reduced to a fraction of a turn
+ *              that is off by at most 2^-25 + 2^-46 |t| turns; past 2^127 turns
+ *              it is not finite
  *   positions  fp32 [N, axes], or [batch, N, axes] with batch stride
  *              pos_stride_b (0: shared by the batch); contiguous otherwise
  * Rows need no alignment beyond the type's own (16-byte aligned rows are
@@ -286,7 +288,8 @@ int wsattn_rotary(wsattn_rotary_t rot, int dtype, int batch, int64_t n_tokens,
 
 /*
  * Queries and keys for the attention from a projection's output, in one
- * pass: per head row, y = turn(g * x / sqrt(mean_d x_d^2 + eps)), and v copied
+ * pass: per head row, y = turn(g * x / sqrt(mean_d x_d^2 + eps)) (the squares
+ * are summed in fp32: rows of values past 1e18 are not served), and v copied
  * (each [batch, heads, N, D]; q_out, k_out and v_out contiguous are what
  * wsattn_prepare and wsattn_forward read).  q, k and v may have different
  * head counts; v and v_out may be NULL.  An output may be its own input.
