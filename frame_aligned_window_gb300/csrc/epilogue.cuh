@@ -146,11 +146,11 @@ struct IsHalf<__half> {
 // Waits of these kernels are bounded (about one second); an expired one sets
 // a status bit and the CTA's abort flag, and every role then leaves.
 constexpr long long kGemmWaitLimit = 1LL << 31;
-// The wait for a tile's accumulator spans its whole contraction, of up to 2^22
-// steps a CTA (a weight gradient over 2^31 rows): 2048 cycles more for each,
-// which takes 600.
-__device__ __forceinline__ long long accumulator_limit(int steps) {
-  return kGemmWaitLimit + (static_cast<long long>(steps) << 11);
+// The wait for a tile's accumulator spans its contraction, of up to 2^31 values
+// (a weight gradient's rows): 32 cycles more for each, of which it takes 10.
+// Formed where a wait has become slow: the epilogue has no registers to spare.
+__device__ __forceinline__ long long accumulator_limit(int values) {
+  return kGemmWaitLimit + (static_cast<long long>(values) << 5);
 }
 
 struct GemmShared {

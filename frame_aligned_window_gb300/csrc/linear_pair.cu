@@ -64,12 +64,12 @@ __device__ __forceinline__ uint32_t bar(const GemmShared& s, int i) {
 }
 
 __device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t parity, int code,
-                                       long long limit) {
+                                       int values) {
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(b, parity)) return true;
     if (*s.abort_flag) return false;
-    if (clock64() - t0 > limit) {
+    if (clock64() - t0 > accumulator_limit(values)) {
       atomicOr(s.status, code);
       *s.abort_flag = 1;
       return false;
@@ -77,9 +77,9 @@ __device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t
   }
 }
 __device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t parity, int code,
-                                     long long limit = kGemmWaitLimit) {
+                                     int values = 0) {
   if (mbar_try_wait(b, parity)) return true;
-  return wait_slow(s, b, parity, code, limit);
+  return wait_slow(s, b, parity, code, values);
 }
 
 // A pair's it-th tile: which product, its row and column tile, the steps of
@@ -440,11 +440,10 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
     const bool stage_pre = p.pre != nullptr && sizeof(O) == 2;
     const uint32_t ab = it & 1u, use = it >> 1;
     const int64_t row0 = static_cast<int64_t>(tr) * kPairRows + 128 * rank + 32 * wq;
-    const long long limit = accumulator_limit(ref.k1 - ref.k0);
     const bool tile_ok =
         WSATTN_BOUNDS(p.status, tr >= 0 && tr < p.tiles_r && tc >= 0 && tc < p.tiles_c);
     if (!TWO && ref.part >= 0) {  // fp32 partial tile [256][256] to global memory
-      const bool ok = wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax, limit);
+      const bool ok = wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax, p.K);
       if (!__all_sync(0xffffffffu, ok)) {
         aborted = true;
         break;
@@ -478,7 +477,7 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
         if (on && lane == 0) bulk_wait_read_1();  // the buffer's previous store has read it
         if (j == 0) {
           ok = __all_sync(0xffffffffu,
-                          wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax, limit));
+                          wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax, p.K));
           if (!ok) break;
           tc_fence_after();
         }
@@ -526,7 +525,7 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
         }
       }
       if (!waited) {
-        const bool ok = wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax, limit);
+        const bool ok = wait(s, bar(s, ACCFULL0 + ab), use & 1u, kStatusTimeoutSoftmax, p.K);
         if (!__all_sync(0xffffffffu, ok)) {
           aborted = true;
           break;

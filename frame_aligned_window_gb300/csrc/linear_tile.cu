@@ -34,12 +34,12 @@ __device__ __forceinline__ uint32_t bar(const GemmShared& s, int i) {
 }
 
 __device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t parity, int code,
-                                       long long limit) {
+                                       int values) {
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(b, parity)) return true;
     if (*s.abort_flag) return false;
-    if (clock64() - t0 > limit) {
+    if (clock64() - t0 > accumulator_limit(values)) {
       atomicOr(s.status, code);
       *s.abort_flag = 1;
       return false;
@@ -47,9 +47,9 @@ __device__ __noinline__ bool wait_slow(const GemmShared& s, uint32_t b, uint32_t
   }
 }
 __device__ __forceinline__ bool wait(const GemmShared& s, uint32_t b, uint32_t parity, int code,
-                                     long long limit = kGemmWaitLimit) {
+                                     int values = 0) {
   if (mbar_try_wait(b, parity)) return true;
-  return wait_slow(s, b, parity, code, limit);
+  return wait_slow(s, b, parity, code, values);
 }
 
 __device__ void producer(const GemmParams& p, const GemmShared& s, int row0, int col0, int k0,
@@ -279,8 +279,7 @@ __global__ void __launch_bounds__(kThreads) gemm_tile_kernel(const __grid_consta
     side_sums(p, static_cast<int>(blockIdx.x) * 128 + static_cast<int>(threadIdx.x) - 64,
               static_cast<int>(gridDim.x) * 128);
     __syncwarp();
-    bool have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax,
-                                accumulator_limit(k1 - k0));
+    bool have = tile_ok && wait(s, bar(s, ACCFULL), 0, kStatusTimeoutSoftmax, p.K);
     have = __all_sync(0xffffffffu, have);
     tc_fence_after();
     if (have) {
