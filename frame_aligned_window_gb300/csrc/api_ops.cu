@@ -245,10 +245,16 @@ bool fill(const Product& g, const wsattn::GemmShape& shape, void* partial, GemmP
   if (shape.pair_cols) {
     tr = cdiv(g.R, wsattn::kPairRows);
     tc = cdiv(g.C, shape.pair_cols);
-    if (prm.out_vec && !encode(&prm.tm_out, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, esize,
+    auto tma_cols = [&](bool rows_ok, int size) {
+      return !rows_ok ? 0 : g.C % (16 / size) == 0 ? g.C : g.C / (128 / size) * (128 / size);
+    };
+    prm.out_tma = tma_cols(prm.out_vec, esize);
+    prm.pre_tma = tma_cols(prm.pre_vec && !g.out_f32, 2);
+    prm.edge_tile = prm.out_vec && g.C % (16 / esize) ? static_cast<int>(tc) - 1 : -1;
+    if (prm.out_tma && !encode(&prm.tm_out, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, esize,
                                g.out, g.C, g.R, g.ldo, 128 / esize, 32))
       return false;
-    if (prm.pre_vec && !g.out_f32 && !encode(&prm.tm_pre, type, 2, g.pre, g.C, g.R, g.ldp, 64, 32))
+    if (prm.pre_tma && !encode(&prm.tm_pre, type, 2, g.pre, g.C, g.R, g.ldp, 64, 32))
       return false;
   } else {
     tr = cdiv(g.R, shape.bn);

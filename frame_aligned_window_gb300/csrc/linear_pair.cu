@@ -33,12 +33,16 @@
 // that neither product ends in a wave of its own that is mostly empty.
 //
 // Epilogue: residual rows are read and outputs are written in whole lines
-// through a 128-byte-swizzled staging buffer (TMA store, or per-row stores
-// when out's rows are not 16-byte aligned); sums and activation in fp32, one
-// rounding at the end.  With a short contraction it bounds the kernel, so
-// tiles without residual, activation and pre-activation take a loop of their
-// own that moves 32 columns at a time and does nothing else: 43904 x 192 ->
-// 5120 takes 84 us (80 % of a copy's rate) instead of the general loop's 140.
+// through a 128-byte-swizzled staging buffer (TMA store; per-row stores when
+// out's rows are not 16-byte aligned, and for the chunk of the last columns when
+// they do not fill 16 bytes, which TMA would); sums and activation in fp32, one
+// rounding at the end.  With a short contraction it bounds the kernel, so tiles
+// without residual, activation and pre-activation take a loop of their own that
+// moves 32 columns at a time and does nothing else: 43904 x 192 -> 5120 takes
+// 84 us (80 % of a copy's rate) instead of the general loop's 140.  The column
+// tile that ends inside 16 bytes goes through the general loop (93 us for 5117
+// columns in rows of 5120; with the question in both loops every width takes
+// 88).
 #include "epilogue.cuh"
 #include "ptx.cuh"
 
@@ -466,7 +470,7 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
       if (lane == 0) mbar_arrive_relaxed(acc_free[ab]);
       continue;
     }
-    if (!p.pre && !p.res && p.act == WSATTN_ACT_NONE) {
+    if (!p.pre && !p.res && p.act == WSATTN_ACT_NONE && tc != p.edge_tile) {
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; ok && j < BN / 2 / kCols; ++j) {
@@ -637,13 +641,13 @@ __device__ void epilogue(const PairParams& pp, const GemmShared& s, uint32_t sta
       fence_proxy_async_smem();
       __syncwarp();
       if (stage_pre) {
-        if (p.pre_vec) {
+        if (col0 < p.pre_tma) {
           if (lane == 0) tma_store_2d(&p.tm_pre, buf0, col0, static_cast<int>(row0));
         } else {
           store_rows<T>(buf0, p.pre, p.ldp, row0, p.R, col0, p.C, lane);
         }
       }
-      if (p.out_vec) {
+      if (col0 < p.out_tma) {
         if (lane == 0) tma_store_2d(&p.tm_out, buf, col0, static_cast<int>(row0));
       } else {
         store_rows<O>(buf, p.out, p.ldo, row0, p.R, col0, p.C, lane);
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&p.g[0].tm_p);
     prefetch_tensormap(&p.g[0].tm_q);
-    if (p.g[0].out_vec) prefetch_tensormap(&p.g[0].tm_out);
+    if (p.g[0].out_tma) prefetch_tensormap(&p.g[0].tm_out);
   }
   if (warp == 2) {
     tmem_alloc_pair(smem_u32(tslot), 2 * BN);

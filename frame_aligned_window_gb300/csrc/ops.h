@@ -104,6 +104,10 @@ struct GemmParams {
   // CTA pairs
   int whole_tiles;     // tiles before those that are split
   float* partial;      // [(tiles - whole_tiles) * split][256][256]
+  // TMA writes units of 16 bytes, and the one that the last column ends in
+  // whole, zeros behind it: columns that it stores (up to the last whole staging
+  // chunk then), and the column tile that holds the rest (-1: none)
+  int out_tma, pre_tma, edge_tile;
   // single-CTA tiles
   int bn;              // rows of a tile (the MMA's N)
   int stages;
