@@ -11,10 +11,14 @@
 namespace wsattn {
 
 // Activations and their slopes in fp32, on the approximate exponential and
-// reciprocal of the special-function unit (each within 2^-22 relative, and
-// the exponential's argument within 2^-23 of itself): far below the rounding
-// of the stored 16-bit value, and a third of the instructions of the exact
-// ones, which the epilogue of a short contraction would wait for.
+// reciprocal of the special-function unit (each within 2^-22 relative, and the
+// exponential's argument u within 2^-21 of itself): 2^-18 + 2^-21 |u| relative
+// in all, |u| being |z| (silu), z^2 / 2 (gelu) or the tanh form's 2 u; what is
+// below 2^-126 counts as zero.  That is far below the rounding of a stored
+// 16-bit value, and not above what the product itself is off by in an fp32
+// output (two truncations of 2^-23 for each 16 values of the contraction), at a
+// third of the instructions of the exact functions, which the epilogue of a
+// short contraction would wait for.
 //
 // logistic(x) = 1 / (1 + exp(-x)), from t = -x log2(e)
 __device__ __forceinline__ float logistic_log2(float t) {

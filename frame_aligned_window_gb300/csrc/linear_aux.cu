@@ -3,6 +3,13 @@
 //   pack   rows of any stride and alignment, or the attention's fp32
 //          [B, H, N, D], to 16-bit rows that TMA can read
 //   dact   dz = dout * act'(preact) with its column sums (the bias gradient)
+//
+// Both round an operand of a product to 16 bits, because the tensor cores' full
+// rate is for 16-bit operands: a second 16-bit term for what the rounding drops
+// would double a product that is the operator's whole time.  The attention's
+// output was itself made from 16-bit probabilities and values; dz costs dx and
+// dw a second rounding (2.3e-3 relative in bf16 against 1.7e-3 of one, an eighth
+// of that in fp16).  The bias gradient sums the unrounded dz.
 #include "epilogue.cuh"
 #include "ptx.cuh"
 
@@ -202,9 +209,12 @@ cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s) {
 // operands, back to back with operands from HBM): the tiling taken is then
 // within 2.5 % of the best one on average, 1.25 at worst.
 //   pair   a 64-wide step of a 256-column tile takes 290 ns (the MMAs alone
-//          270 at full clocks), of a 128-column tile 269 (bound by the 24 KB a
-//          CTA reads of L2 for it); a tile 1.2 or 0.65 us beside its steps,
-//          and the first loads and the last epilogue are seen once
+//          270 at full clocks), of a 128-column tile 269, for half the MMAs: its
+//          24 KB a CTA come at 89 KB a microsecond, less than the 110 of the
+//          256-column tile's 32 KB, so L2's rate is not what it waits for (six
+//          slices in flight at their latency may be; not measured apart); a tile
+//          1.2 or 0.65 us beside its steps, and the first loads and the last
+//          epilogue are seen once
 //   tile   a step of a CTA takes the time of its bytes at 134 KB a
 //          microsecond and SM, shared by two CTAs, or 200 ns; a row of the
 //          tile 45 ns of epilogue, and the cluster's exchange 800 ns

@@ -335,7 +335,10 @@ enum wsattn_activation {
 /*
  * out = residual + act(x w^T + bias) in one kernel: the products run on the
  * tensor cores from 16-bit inputs into fp32 accumulators; bias, activation
- * and residual are applied in fp32 and the result is rounded once.
+ * and residual are applied in fp32 and the result is rounded once.  What an
+ * fp32 output shows: a product over k values is off by up to k / 16 truncations
+ * of a partial sum (2^-23 each), an activation by 2^-18 relative near zero and
+ * by 2^-21 of its exponential's argument far from it.
  *   dtype      of x, w, bias and preact: WSATTN_BF16 or WSATTN_FP16
  *   out_dtype  of residual and out: dtype or WSATTN_FP32
  *   m, n, k    rows, output and input features (m >= 0, n, k >= 1)
