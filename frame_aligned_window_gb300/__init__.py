@@ -17,10 +17,12 @@ The names mirror the C ABI:
     wsattn_rotary_plan, wsattn_rotary_destroy, wsattn_rotary, wsattn_qknorm,
     wsattn_qknorm_backward, wsattn_qknorm_backward_workspace, wsattn_linear,
     wsattn_linear_workspace, wsattn_linear_backward, wsattn_linear_backward_workspace,
+    wsattn_block_norm, wsattn_block_norm_backward, wsattn_block_norm_backward_workspace,
     wsattn_op_status
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import struct
@@ -59,6 +61,7 @@ EXPORTS = (
     "wsattn_rotary_plan", "wsattn_rotary_destroy", "wsattn_rotary", "wsattn_qknorm",
     "wsattn_qknorm_backward", "wsattn_qknorm_backward_workspace", "wsattn_linear",
     "wsattn_linear_workspace", "wsattn_linear_backward", "wsattn_linear_backward_workspace",
+    "wsattn_block_norm", "wsattn_block_norm_backward", "wsattn_block_norm_backward_workspace",
     "wsattn_op_status",
 )
 
@@ -76,6 +79,9 @@ BF16, FP16, FP32 = 0, 1, 2
 
 # wsattn_activation, by the name the linear products take
 ACTIVATIONS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
+
+# wsattn_norm_kind, by the name the norms take
+NORMS = {None: 0, "rms": 1, "layer": 2}
 
 STATUS = {0: "OK", 1: "BAD_ARG", 2: "BAD_BLOCK", 3: "UNSUPPORTED", 4: "NOT_PREPARED",
           5: "BATCH_MISMATCH", 6: "CUDA", 7: "TIMEOUT", 8: "NO_MEMORY", 9: "BOUNDS"}
@@ -128,6 +134,15 @@ _LINEAR = struct.Struct("@iiqiiPqiqPqPPqPqPqi0q").pack
 # ldp, activation, dx, lddx, dw, lddw, db
 _LINEAR_GRAD = struct.Struct("@iqiiPqPqPqPqiPqPqP0q").pack
 
+# wsattn_block_norm_args: dtype, stream_dtype, mod_dtype, weight_dtype, m, n, norm,
+# post_norm, eps, residual_scale, group, x, ldx, residual, ldr, gate, ldg, scale,
+# lds, shift, ldf, weight, bias, post_weight, hidden, ldh, out, ldo
+_BLOCK_NORM = struct.Struct("@iiiiqiiiffqPqPqPqPqPqPPPPqPq0q").pack
+# wsattn_block_norm_grad_args: the same up to group, then dout, ldo, dhidden, lddh,
+# hidden, ldh, x, ldx, gate, ldg, scale, lds, weight, bias, post_weight, dx, lddx,
+# dresidual, lddr, dgate, dscale, dshift, dweight, dbias, dpost_weight
+_BLOCK_NORM_GRAD = struct.Struct("@iiiiqiiiffqPqPqPqPqPqPqPPPPqPqPPPPPP0q").pack
+
 _I64, _SZP = ctypes.c_int64, ctypes.POINTER(_SZ)
 _lib.wsattn_rotary_plan.argtypes = [_I, _I, _P, _P, _I, ctypes.POINTER(_P)]
 _lib.wsattn_rotary_destroy.argtypes = [_P]
@@ -141,6 +156,9 @@ _lib.wsattn_linear.argtypes = [_P, _P, _SZ, _P]
 _lib.wsattn_linear_workspace.argtypes = [_P, _SZP]
 _lib.wsattn_linear_backward.argtypes = [_P, _P, _SZ, _P]
 _lib.wsattn_linear_backward_workspace.argtypes = [_P, _SZP]
+_lib.wsattn_block_norm.argtypes = [_P, _P]
+_lib.wsattn_block_norm_backward.argtypes = [_P, _P, _SZ, _P]
+_lib.wsattn_block_norm_backward_workspace.argtypes = [_P, _SZP]
 _lib.wsattn_op_status.argtypes = [_P]
 _lib.wsattn_status_string.restype = ctypes.c_char_p
 for _name in EXPORTS:
@@ -897,6 +915,226 @@ def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="n
                                       need_dx, need_dw, need_db, None, query=True)
     n = _SZ()
     _run(dev, "wsattn_linear_backward_workspace", _lib.wsattn_linear_backward_workspace, args,
+         ctypes.byref(n))
+    return int(n.value)
+
+
+def _norm_kind(name, what, none=False):
+    code = NORMS.get(name)
+    if code is None or not (code or none):
+        raise ValueError(f"{what} must be one of {[k for k in NORMS if k or none]}, got {name!r}")
+    return code
+
+
+def _groups_of(t, name, lead, n):
+    """Vectors that t [..., n] holds for rows of leading dimensions `lead`: one
+    for all rows, or one for each part of a leading dimension's rows."""
+    shape = t.shape
+    if not shape or shape[-1] != n:
+        raise ValueError(f"{name} must be [..., {n}], got {list(shape)}")
+    g = shape[:-1].numel()
+    if g == 1:
+        return 1
+    own = list(shape[:-1])
+    while own and own[-1] == 1:
+        own.pop()
+    k = len(own) - 1
+    if k >= len(lead) or tuple(own[:k]) != tuple(lead[:k]) or not own[k] or lead[k] % own[k]:
+        raise ValueError(f"{name} must be [{n}], or have the rows' leading dimensions {list(lead)}, or "
+                         f"their first ones with the last a divisor, got {list(shape)}")
+    return g
+
+
+def _modulation(vectors, lead, n, dt, dev):
+    """(rows a vector serves, groups, type, {name: (pointer, row stride)}) of gate, scale and shift."""
+    groups, kind, at, first = None, None, {}, None
+    for name, t in vectors:
+        if t is None:
+            at[name] = (0, 0)
+            continue
+        _check_tensor(t, name, dev)
+        if t.dtype != dt and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be {dt} or torch.float32, got {t.dtype}")
+        g = _groups_of(t, name, lead, n)
+        if groups is None:
+            groups, kind, first = g, t.dtype, name
+        elif groups != g or kind != t.dtype:
+            raise ValueError(f"{name} must have {first}'s shape and type")
+        at[name] = (t.data_ptr(), _rows(t, name, n, None, t.dtype, dev))
+    m = lead.numel()
+    groups = groups or 1
+    return (max(m // groups, 1) if groups > 1 else max(m, 1)), groups, kind, at
+
+
+def _weights(vectors, n, dt, dev):
+    """(type, {name: pointer}) of weight, bias and post_weight."""
+    kind, at, first = None, {}, None
+    for name, t in vectors:
+        if t is None:
+            at[name] = 0
+            continue
+        _check_tensor(t, name, dev)
+        if t.dtype != dt and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be {dt} or torch.float32, got {t.dtype}")
+        if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be contiguous [{n}], got {list(t.shape)}")
+        if kind is None:
+            kind, first = t.dtype, name
+        elif kind != t.dtype:
+            raise TypeError(f"{name} must have {first}'s type")
+        at[name] = t.data_ptr()
+    return kind, at
+
+
+def wsattn_block_norm(x, residual=None, gate=None, scale=None, shift=None, weight=None, bias=None,
+                      norm="layer", eps: float = 1e-6, post_norm=None, post_weight=None,
+                      residual_scale: float = 1.0, hidden=None, out=None, need_out=True,
+                      stream=None):
+    """The end of one part of a block and the start of the next, in one pass
+    over the rows of x [..., n] (bf16, fp16 or fp32):
+        hidden = residual_scale * residual + gate * u,  u = x or norm(x) * post_weight
+        out    = (norm(hidden) * weight + bias) * (1 + scale) + shift
+    norm, post_norm: "layer" or "rms" (post_norm None: u = x).  residual and
+    hidden: x's type or fp32.  gate, scale, shift: [n], or one vector for each
+    part of the rows (x [B, N, n]: [B, n], [B, F, n] with F a divisor of N, or
+    [B, N, n]); they and weight, bias, post_weight [n] have x's type or fp32.
+    Returns (out, hidden); hidden is None without a residual, gate or post_norm
+    (it is x then) unless given, out is None when not needed.  hidden may be
+    the residual or x, out may be x."""
+    dev = _device_of(x, "x")
+    if not x.dim():
+        raise ValueError("x must be [..., n], got []")
+    n, dt, code = x.shape[-1], x.dtype, _dtype_code(x, "x")
+    lead = x.shape[:-1]
+    m = lead.numel()
+    kind, post = _norm_kind(norm, "norm"), _norm_kind(post_norm, "post_norm", none=True)
+    if post_weight is not None and not post:
+        raise ValueError("post_weight without post_norm")
+    group, _, mod, at = _modulation((("gate", gate), ("scale", scale), ("shift", shift)), lead, n, dt, dev)
+    wt, wat = _weights((("weight", weight), ("bias", bias), ("post_weight", post_weight)), n, dt, dev)
+    raw = _raw_stream(dev, stream)
+    ldx = _rows(x, "x", n, None, dt, dev)
+    st = residual.dtype if residual is not None else dt if hidden is None else hidden.dtype
+    if st != dt and st != torch.float32:
+        raise TypeError(f"residual and hidden must be {dt} or torch.float32, got {st}")
+    rp = ldr = hp = ldh = op = ldo = 0
+    if residual is not None:
+        ldr, rp = _rows(residual, "residual", n, lead, st, dev), residual.data_ptr()
+    if hidden is None and (residual is not None or gate is not None or post):
+        hidden = _empty(x.shape, st, x, stream)
+    if hidden is not None:
+        ldh, hp = _rows(hidden, "hidden", n, lead, st, dev), hidden.data_ptr()
+    if out is None and need_out:
+        out = _empty(x.shape, dt, x, stream)
+    if out is not None:
+        ldo, op = _rows(out, "out", n, lead, dt, dev), out.data_ptr()
+    args = _BLOCK_NORM(code, code if st == dt else FP32, code if mod in (None, dt) else FP32,
+                       code if wt in (None, dt) else FP32, m, n, kind, post, eps, residual_scale,
+                       group, x.data_ptr(), ldx, rp, ldr, *at["gate"], *at["scale"], *at["shift"],
+                       wat["weight"], wat["bias"], wat["post_weight"], hp, ldh, op, ldo)
+    _run(dev, "wsattn_block_norm", _lib.wsattn_block_norm, args, raw)
+    return out, hidden
+
+
+BlockNormGrads = collections.namedtuple(
+    "BlockNormGrads", "dx dresidual dgate dscale dshift dweight dbias dpost_weight")
+
+
+def _block_norm_grad_args(dout, hidden, x, dhidden, gate, scale, shift, weight, bias, norm, eps,
+                          post_norm, post_weight, residual_scale, dx, dresidual, need_dx,
+                          need_dresidual, need_vectors, stream, query=False):
+    """The packed wsattn_block_norm_grad_args, the gradients and the device.
+    query: for the workspace's size (nothing is allocated)."""
+    like = dout if dout is not None else dhidden
+    if like is None:
+        raise ValueError("give dout, dhidden or both")
+    dev = _device_of(like, "dout" if dout is not None else "dhidden")
+    typed = dout if dout is not None else x if x is not None else like
+    dt, code = typed.dtype, _dtype_code(typed, "dout")
+    if not like.dim():
+        raise ValueError("dout must be [..., n], got []")
+    n, lead = like.shape[-1], like.shape[:-1]
+    m = lead.numel()
+    kind, post = _norm_kind(norm, "norm"), _norm_kind(post_norm, "post_norm", none=True)
+    if post_weight is not None and not post:
+        raise ValueError("post_weight without post_norm")
+    if dout is not None and hidden is None:
+        raise ValueError("dout needs hidden (what wsattn_block_norm left, or x where nothing joined it)")
+    if x is None and (gate is not None or post):
+        raise ValueError("the gradients of a gate or of post_norm need x")
+    group, _, mod, at = _modulation((("gate", gate), ("scale", scale), ("shift", shift)), lead, n, dt, dev)
+    wt, wat = _weights((("weight", weight), ("bias", bias), ("post_weight", post_weight)), n, dt, dev)
+    st = hidden.dtype if hidden is not None else dhidden.dtype
+    if st != dt and st != torch.float32:
+        raise TypeError(f"hidden and dhidden must be {dt} or torch.float32, got {st}")
+    rows = {}
+    for name, t, ty in (("dout", dout, dt), ("dhidden", dhidden, st), ("hidden", hidden, st), ("x", x, dt)):
+        rows[name] = (0, 0) if t is None else (t.data_ptr(), _rows(t, name, n, lead, ty, dev))
+    # without a gate, a first norm or a scale, both are hidden's gradient
+    same = gate is None and not post and residual_scale == 1.0 and st == dt
+    need_dx, need_dresidual = need_dx or dx is not None, need_dresidual or dresidual is not None
+    one = same and need_dx and need_dresidual and (dx is None or dresidual is None)
+    if need_dx and dx is None and not query:
+        dx = dresidual if one and dresidual is not None else _empty(like.shape, dt, like, stream)
+    if need_dresidual and dresidual is None and not query:
+        dresidual = dx if one else _empty(like.shape, st, like, stream)
+    for name, t, ty in (("dx", dx, dt), ("dresidual", dresidual, st)):
+        rows[name] = (0, 0) if t is None else (t.data_ptr(), _rows(t, name, n, lead, ty, dev))
+    if one:
+        rows["dresidual"] = (0, 0)
+    sums = []
+    for t, like_t in (("dgate", gate), ("dscale", scale), ("dshift", shift if shift is not None else scale),
+                      ("dweight", weight), ("dbias", bias), ("dpost_weight", post_weight)):
+        if like_t is None or not need_vectors:
+            sums.append(None)
+        elif query:
+            sums.append(256)
+        else:
+            # no rows: nothing is summed
+            make = _empty(like_t.shape, torch.float32, like, stream)
+            sums.append(make.zero_() if not m else make)
+    ptr = [0 if t is None else t if query else t.data_ptr() for t in sums]
+    args = _BLOCK_NORM_GRAD(
+        code, code if st == dt else FP32, code if mod in (None, dt) else FP32,
+        code if wt in (None, dt) else FP32, m, n, kind, post, eps, residual_scale, group,
+        *rows["dout"], *rows["dhidden"], *rows["hidden"], *rows["x"], *at["gate"], *at["scale"],
+        wat["weight"], wat["bias"], wat["post_weight"], *rows["dx"], *rows["dresidual"], *ptr)
+    return args, BlockNormGrads(dx, dresidual, *sums), dev, like
+
+
+def wsattn_block_norm_backward(dout, hidden, x=None, dhidden=None, gate=None, scale=None, shift=None,
+                               weight=None, bias=None, norm="layer", eps: float = 1e-6,
+                               post_norm=None, post_weight=None, residual_scale: float = 1.0,
+                               dx=None, dresidual=None, need_dx=True, need_dresidual=True,
+                               need_vectors=True, workspace=None, stream=None) -> BlockNormGrads:
+    """Gradients of wsattn_block_norm from dout (of out, or None) and dhidden
+    (what reaches hidden by other ways, or None): BlockNormGrads of dx,
+    dresidual and, in fp32 and in the vectors' shapes, dgate, dscale, dshift
+    (with scale or shift), dweight, dbias and dpost_weight; None for what is
+    not needed or was not there.  hidden: what the forward left (x itself where
+    there was no residual, gate or post_norm); x is needed with a gate or
+    post_norm.  Where dx and dresidual are equal by the formula (no gate,
+    post_norm or residual_scale, one type) they are one tensor unless given."""
+    args, grads, dev, like = _block_norm_grad_args(
+        dout, hidden, x, dhidden, gate, scale, shift, weight, bias, norm, eps, post_norm, post_weight,
+        residual_scale, dx, dresidual, need_dx, need_dresidual, need_vectors, stream)
+    raw = _raw_stream(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_block_norm_backward_workspace,
+                                 "wsattn_block_norm_backward_workspace", args, workspace, dev, like,
+                                 stream)
+    _run(dev, "wsattn_block_norm_backward", _lib.wsattn_block_norm_backward, args, ws, nbytes, raw)
+    return grads
+
+
+def wsattn_block_norm_backward_workspace(dout, hidden, x=None, dhidden=None, gate=None, scale=None,
+                                         shift=None, weight=None, bias=None, norm="layer",
+                                         post_norm=None, post_weight=None, need_vectors=True) -> int:
+    """Bytes of scratch wsattn_block_norm_backward takes for these operands."""
+    args, _, dev, _ = _block_norm_grad_args(
+        dout, hidden, x, dhidden, gate, scale, shift, weight, bias, norm, 1e-6, post_norm, post_weight,
+        1.0, None, None, False, False, need_vectors, None, query=True)
+    n = _SZ()
+    _run(dev, "wsattn_block_norm_backward_workspace", _lib.wsattn_block_norm_backward_workspace, args,
          ctypes.byref(n))
     return int(n.value)
 

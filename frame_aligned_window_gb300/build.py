@@ -31,8 +31,9 @@ LIB = os.path.join(HERE, "libwsattn.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libwsattn_debug.so")
 SOURCES = ["plan.cpp", "prepare.cu", "forward.cu", "api.cu", "prepare_static.cu", "produce.cu",
-           "qknorm.cu", "qknorm_back.cu", "linear_pair.cu", "linear_tile.cu", "linear_aux.cu", "api_ops.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "ops.h", "epilogue.cuh", "qknorm.cuh"]
+           "qknorm.cu", "qknorm_back.cu", "linear_pair.cu", "linear_tile.cu", "linear_aux.cu", "api_ops.cu",
+           "norm.cu", "norm_back.cu", "api_norm.cu"]
+HEADERS = ["internal.h", "ptx.cuh", "ops.h", "epilogue.cuh", "qknorm.cuh", "api_args.h", "norm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

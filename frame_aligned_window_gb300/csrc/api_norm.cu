@@ -1,0 +1,221 @@
+// C ABI of a block's norms (declared in include/wsattn.h): argument checks,
+// the backward pass's workspace, and launches.
+#include <cmath>
+#include <cstring>
+
+#include "api_args.h"
+#include "ops.h"
+
+using wsattn::NormParams;
+
+namespace {
+
+using namespace wsattn::args;
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
+
+// What forward and backward arguments share.
+template <typename A>
+bool common_ok(const A* a) {
+  if (!a || !dtype_ok(a->dtype) || a->m < 0 || a->m > kMaxRows || a->n < 1 || a->group < 1)
+    return false;
+  auto type = [&](int t) { return t == a->dtype || t == WSATTN_FP32; };
+  if (!type(a->stream_dtype) || !type(a->mod_dtype) || !type(a->weight_dtype)) return false;
+  if ((a->norm != WSATTN_NORM_RMS && a->norm != WSATTN_NORM_LAYER) ||
+      a->post_norm < WSATTN_NORM_NONE || a->post_norm > WSATTN_NORM_LAYER)
+    return false;
+  if (!(a->eps >= 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->residual_scale)) return false;
+  const int ms = dtype_size(a->mod_dtype), ws = dtype_size(a->weight_dtype);
+  return elem_aligned(a->gate, ms) && elem_aligned(a->scale, ms) && elem_aligned(a->weight, ws) &&
+         elem_aligned(a->bias, ws) && elem_aligned(a->post_weight, ws) &&
+         (!a->gate || a->ldg >= a->n) && (!a->scale || a->lds >= a->n) &&
+         (!a->post_weight || a->post_norm != WSATTN_NORM_NONE);
+}
+// A matrix that may be absent.
+bool rows_ok(const void* p, int64_t ld, int n, int esize) {
+  return !p || (ld >= n && elem_aligned(p, esize));
+}
+// Its rows are readable in 16-byte words (n is a multiple of 8).
+bool wide(const void* p, int64_t ld, int64_t rows, int esize) {
+  return !p || (aligned16(p) && (rows <= 1 || ld % (16 / esize) == 0));
+}
+
+template <typename A>
+void fill_common(const A* a, NormParams* p) {
+  std::memset(p, 0, sizeof(*p));
+  p->m = a->m;
+  p->group = a->group < a->m ? a->group : a->m;
+  p->groups = cdiv(a->m, p->group);
+  p->n = a->n;
+  p->norm = a->norm;
+  p->post = a->post_norm;
+  p->eps = a->eps;
+  p->res_scale = a->residual_scale;
+  p->mod_f32 = a->mod_dtype == WSATTN_FP32;
+  p->weight_f32 = a->weight_dtype == WSATTN_FP32;
+  p->x = a->x;
+  p->ldx = a->ldx;
+  p->gate = a->gate;
+  p->ldg = a->ldg;
+  p->scale = a->scale;
+  p->lds = a->lds;
+  p->weight = a->weight;
+  p->bias = a->bias;
+  p->post_weight = a->post_weight;
+  p->hidden = const_cast<void*>(static_cast<const void*>(a->hidden));
+  p->ldh = a->ldh;
+  p->out = nullptr;
+  p->ldo = a->ldo;
+}
+template <typename A>
+bool common_wide(const A* a, int64_t groups) {
+  const int es = dtype_size(a->dtype), ss = dtype_size(a->stream_dtype),
+            ms = dtype_size(a->mod_dtype);
+  return a->n % 8 == 0 && wide(a->x, a->ldx, a->m, es) && wide(a->hidden, a->ldh, a->m, ss) &&
+         wide(a->gate, a->ldg, groups, ms) && wide(a->scale, a->lds, groups, ms) &&
+         wide(a->weight, 0, 1, 4) && wide(a->bias, 0, 1, 4) && wide(a->post_weight, 0, 1, 4);
+}
+
+bool has_weights(const wsattn_block_norm_grad_args* a) {
+  return a->dweight || a->dbias || a->dpost_weight;
+}
+bool has_vectors(const wsattn_block_norm_grad_args* a) {
+  return a->dgate || a->dscale || a->dshift;
+}
+
+// Rows that share vectors; without any, all of them.
+int64_t grad_group(const wsattn_block_norm_grad_args* a) {
+  if (!a->gate && !a->scale && !has_vectors(a)) return a->m;
+  return a->group < a->m ? a->group : a->m;
+}
+// Shares of the rows, and whether each ends where a group does: with at least
+// four groups a share the shares come out nearly even, and no group's sums
+// have to be joined.
+struct Shares {
+  int units;
+  bool whole;
+  size_t part, wpart;  // bytes
+};
+Shares plan_shares(const wsattn_block_norm_grad_args* a) {
+  Shares s{0, true, 0, 0};
+  if (a->m == 0) return s;
+  s.units = wsattn::norm_backward_units(a->m, a->n);
+  const int64_t groups = cdiv(a->m, grad_group(a));
+  s.whole = groups >= 4 * static_cast<int64_t>(s.units) || s.units == 1;
+  const size_t row = sizeof(float) * 3 * static_cast<size_t>(a->n) * s.units;
+  if (has_vectors(a) && !s.whole) s.part = up256(2 * row);
+  if (has_weights(a)) s.wpart = up256(row);
+  return s;
+}
+
+bool grad_args_ok(const wsattn_block_norm_grad_args* a) { return common_ok(a); }
+
+}  // namespace
+
+extern "C" {
+
+int wsattn_block_norm(const wsattn_block_norm_args* a, void* stream) {
+  if (!common_ok(a)) return WSATTN_ERR_BAD_ARG;
+  if (a->n > wsattn::kNormMaxCols) return WSATTN_ERR_UNSUPPORTED;
+  const int es = dtype_size(a->dtype), ss = dtype_size(a->stream_dtype),
+            ms = dtype_size(a->mod_dtype);
+  if (!rows_ok(a->x, a->ldx, a->n, es) || !rows_ok(a->residual, a->ldr, a->n, ss) ||
+      !rows_ok(a->shift, a->ldf, a->n, ms) || !rows_ok(a->hidden, a->ldh, a->n, ss) ||
+      !rows_ok(a->out, a->ldo, a->n, es) || (a->hidden && a->hidden == a->out))
+    return WSATTN_ERR_BAD_ARG;
+  if (a->m == 0 || (!a->hidden && !a->out)) return WSATTN_OK;
+  if (!a->x) return WSATTN_ERR_BAD_ARG;
+  NormParams p;
+  fill_common(a, &p);
+  p.out = a->out;
+  p.res = a->residual;
+  p.ldr = a->ldr;
+  p.shift = a->shift;
+  p.ldf = a->ldf;
+  p.status = wsattn::op_status_ptr();
+  if (!p.status) return WSATTN_ERR_CUDA;
+  p.vec = common_wide(a, p.groups) && wide(a->residual, a->ldr, a->m, ss) &&
+                   wide(a->shift, a->ldf, p.groups, ms) && wide(a->out, a->ldo, a->m, es);
+  return wsattn::launch_norm_forward(p, a->dtype, a->stream_dtype == WSATTN_FP32,
+                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? WSATTN_OK
+             : WSATTN_ERR_CUDA;
+}
+
+int wsattn_block_norm_backward_workspace(const wsattn_block_norm_grad_args* a, size_t* bytes) {
+  if (!bytes || !grad_args_ok(a)) return WSATTN_ERR_BAD_ARG;
+  if (a->n > wsattn::kNormMaxCols) return WSATTN_ERR_UNSUPPORTED;
+  const Shares s = plan_shares(a);
+  *bytes = s.part + s.wpart;
+  return WSATTN_OK;
+}
+
+int wsattn_block_norm_backward(const wsattn_block_norm_grad_args* a, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (!grad_args_ok(a)) return WSATTN_ERR_BAD_ARG;
+  if (a->n > wsattn::kNormMaxCols) return WSATTN_ERR_UNSUPPORTED;
+  const int es = dtype_size(a->dtype), ss = dtype_size(a->stream_dtype);
+  float* const sums[6] = {a->dgate, a->dscale, a->dshift, a->dweight, a->dbias, a->dpost_weight};
+  bool sums_wide = true;
+  for (float* t : sums) {
+    if (!elem_aligned(t, 4)) return WSATTN_ERR_BAD_ARG;
+    sums_wide = sums_wide && aligned16(t);
+  }
+  if (!rows_ok(a->dout, a->ldo, a->n, es) || !rows_ok(a->dhidden, a->lddh, a->n, ss) ||
+      !rows_ok(a->hidden, a->ldh, a->n, ss) || !rows_ok(a->x, a->ldx, a->n, es) ||
+      !rows_ok(a->dx, a->lddx, a->n, es) || !rows_ok(a->dresidual, a->lddr, a->n, ss) ||
+      (a->dx && a->dx == a->dresidual))
+    return WSATTN_ERR_BAD_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->m == 0) {
+    for (int i = 3; i < 6; ++i)
+      if (sums[i] && cudaMemsetAsync(sums[i], 0, sizeof(float) * a->n, s) != cudaSuccess)
+        return WSATTN_ERR_CUDA;
+    return WSATTN_OK;
+  }
+  const bool post = a->post_norm != WSATTN_NORM_NONE;
+  const bool need_x = a->dgate || a->dpost_weight || (post && a->dx);
+  if ((!a->dout && !a->dhidden) || (a->dout && !a->hidden) || (need_x && !a->x))
+    return WSATTN_ERR_BAD_ARG;
+  const Shares sh = plan_shares(a);
+  const size_t need = sh.part + sh.wpart;
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return WSATTN_ERR_BAD_ARG;
+  NormParams p;
+  fill_common(a, &p);
+  p.group = grad_group(a);
+  p.groups = cdiv(a->m, p.group);
+  if (!need_x) {
+    p.x = nullptr;
+    p.post = WSATTN_NORM_NONE;
+  }
+  p.out = const_cast<void*>(a->dout);
+  p.dhidden = a->dhidden;
+  p.lddh = a->lddh;
+  p.dx = a->dx;
+  p.lddx = a->lddx;
+  p.dres = a->dresidual;
+  p.lddr = a->lddr;
+  p.dgate = a->dgate;
+  p.dscale = a->dscale;
+  p.dshift = a->dshift;
+  p.dweight = a->dweight;
+  p.dbias = a->dbias;
+  p.dpost = a->dpost_weight;
+  char* ws = static_cast<char*>(workspace);
+  p.part = sh.part ? reinterpret_cast<float*>(ws) : nullptr;
+  p.wpart = sh.wpart ? reinterpret_cast<float*>(ws + sh.part) : nullptr;
+  p.units = sh.units;
+  p.whole = sh.whole;
+  p.status = wsattn::op_status_ptr();
+  if (!p.status) return WSATTN_ERR_CUDA;
+  p.vec = common_wide(a, p.groups) && sums_wide && wide(a->dout, a->ldo, a->m, es) &&
+                   wide(a->dhidden, a->lddh, a->m, ss) && wide(a->dx, a->lddx, a->m, es) &&
+                   wide(a->dresidual, a->lddr, a->m, ss);
+  return wsattn::launch_norm_backward(p, a->dtype, a->stream_dtype == WSATTN_FP32, s) ==
+                 cudaSuccess
+             ? WSATTN_OK
+             : WSATTN_ERR_CUDA;
+}
+
+}  // extern "C"

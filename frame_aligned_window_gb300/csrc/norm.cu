@@ -1,0 +1,165 @@
+// Forward pass of a block's norms (norm.cuh has the formulas).
+//
+// Bound by HBM: x and the residual are read once, hidden and out written once.
+// The vectors come from the L1 cache (many rows share them).  Rows of up to 1024 columns
+// take a warp each, four to a CTA; wider ones a CTA of up to 12 warps.
+#include "norm.cuh"
+
+namespace wsattn {
+namespace {
+
+using namespace norm;
+
+constexpr int kRowsPerCta = 4;  // rows of one warp
+
+template <typename T, typename R, int V>
+__global__ void __launch_bounds__(384) norm_forward_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[kReducerFloats];
+  Reducer rd{red, p.warps, 0};
+  const int threads = 32 * p.warps;
+  const int team = threadIdx.x / threads, lane = threadIdx.x - team * threads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (p.warps == 1 ? kRowsPerCta : 1) + team;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (row >= p.m) return;  // a whole warp, or (wide rows) no thread
+  const int n = p.n;
+  const bool vec = p.vec != 0;
+  const float inv_n = 1.f / static_cast<float>(n);
+  const int64_t g = row / p.group;
+  const bool ok = WSATTN_BOUNDS(p.status, g < p.groups && threads * V * 8 >= n && p.warps <= 12);
+  if (!ok) return;
+
+  Raw8<T> xr[V];
+  Raw8<R> rr[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    xr[j] = load_raw(static_cast<const T*>(p.x) + row * p.ldx, n, column(lane, threads, j), vec);
+  if (p.res) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      rr[j] = load_raw(static_cast<const R*>(p.res) + row * p.ldr, n, column(lane, threads, j), vec);
+  }
+  float h[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j) unpack(xr[j], h[j]);
+
+  auto inside = [&](int j, int i) { return column(lane, threads, j) + i < n; };
+  // h becomes std(h); elements behind the row's end stay zero
+  auto standardise = [&](int kind) {
+    if (kind == WSATTN_NORM_LAYER) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] += h[j][i];
+      row_sums(rd, s);
+      const float mean = s[0] * inv_n;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (inside(j, i)) h[j][i] -= mean;
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[0] = fmaf(h[j][i], h[j][i], q[0]);
+    row_sums(rd, q);
+    const float r = rsqrtf(fmaf(q[0], inv_n, p.eps));
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] *= r;
+  };
+  auto times = [&](const void* v, int64_t at, int f32) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[8];
+      vector8<T>(v, at, f32, n, column(lane, threads, j), vec, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] *= f[i];
+    }
+  };
+
+  if (p.post != WSATTN_NORM_NONE) {
+    standardise(p.post);
+    if (p.post_weight) times(p.post_weight, 0, p.weight_f32);
+  }
+  if (p.gate) times(p.gate, g * p.ldg, p.mod_f32);
+  if (p.res) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[8];
+      unpack(rr[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = fmaf(p.res_scale, f[i], h[j][i]);
+    }
+  }
+  if (p.hidden) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      store8(static_cast<R*>(p.hidden) + row * p.ldh, n, column(lane, threads, j), vec, h[j]);
+  }
+  if (!p.out) return;
+  standardise(p.norm);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = column(lane, threads, j);
+    float f[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = h[j][i];
+    if (p.weight) {
+      vector8<T>(p.weight, 0, p.weight_f32, n, c, vec, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= f[i];
+    }
+    if (p.bias) {
+      vector8<T>(p.bias, 0, p.weight_f32, n, c, vec, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += f[i];
+    }
+    if (p.scale) {
+      vector8<T>(p.scale, g * p.lds, p.mod_f32, n, c, vec, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i], f[i], y[i]);
+    }
+    if (p.shift) {
+      vector8<T>(p.shift, g * p.ldf, p.mod_f32, n, c, vec, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += f[i];
+    }
+    store8(static_cast<T*>(p.out) + row * p.ldo, n, c, vec, y);
+  }
+}
+
+template <typename T, typename R>
+cudaError_t forward(const NormParams& p, int v, cudaStream_t s) {
+  const int64_t grid = p.warps == 1 ? (p.m + kRowsPerCta - 1) / kRowsPerCta : p.m;
+  const dim3 g(static_cast<unsigned>(grid)), b(32 * p.warps * (p.warps == 1 ? kRowsPerCta : 1));
+  switch (v) {
+    case 1: return launch_dependent(norm_forward_kernel<T, R, 1>, g, b, 0, s, p);
+    case 2: return launch_dependent(norm_forward_kernel<T, R, 2>, g, b, 0, s, p);
+    default: return launch_dependent(norm_forward_kernel<T, R, 4>, g, b, 0, s, p);
+  }
+}
+
+}  // namespace
+
+// A warp a row as long as four pieces a thread hold it.
+static int norm_forward_width(int n) { return n <= 256 ? 1 : n <= 512 ? 2 : 4; }
+
+cudaError_t launch_norm_forward(const NormParams& q, int dtype, bool f32, cudaStream_t s) {
+  NormParams p = q;
+  const int v = norm_forward_width(p.n);
+  p.warps = (p.n + 256 * v - 1) / (256 * v);
+  switch (dtype) {
+    case WSATTN_BF16:
+      return f32 ? forward<__nv_bfloat16, float>(p, v, s) : forward<__nv_bfloat16, __nv_bfloat16>(p, v, s);
+    case WSATTN_FP16:
+      return f32 ? forward<__half, float>(p, v, s) : forward<__half, __half>(p, v, s);
+    default: return forward<float, float>(p, v, s);
+  }
+}
+
+}  // namespace wsattn

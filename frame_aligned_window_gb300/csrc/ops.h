@@ -203,4 +203,53 @@ cudaError_t launch_dact(const DactParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_sum_parts(const DactParams& p, float* db, cudaStream_t s);
 constexpr int kDactCols = 256;
 
+// ------------------------------------------------------- norms of a block
+// Vectors of gate, scale and shift: one row for `group` consecutive rows.
+struct NormParams {
+  int64_t m, group, groups;  // rows, rows per vector, vectors
+  int n;                     // columns
+  int norm, post;            // wsattn_norm of out and of x
+  float eps, res_scale;
+  int mod_f32, weight_f32;   // type of gate, scale, shift / weight, bias, post_weight: fp32, else x's
+  const void* x;
+  const void* res;
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  const void* weight;
+  const void* bias;
+  const void* post_weight;
+  int64_t ldx, ldr, ldg, lds, ldf;
+  void* hidden;
+  void* out;
+  int64_t ldh, ldo;
+  // backward (hidden and out are read: the forward's hidden, and dout)
+  const void* dhidden;
+  int64_t lddh;
+  void* dx;
+  void* dres;
+  int64_t lddx, lddr;
+  float* dgate;   // [groups, n] each
+  float* dscale;
+  float* dshift;
+  float* dweight;  // [n] each
+  float* dbias;
+  float* dpost;
+  float* part;     // [units][2][3][n] sums of groups that several units share
+  float* wpart;    // [units][3][n] sums for the [n] gradients
+  int units;       // CTAs, each with a contiguous share of the rows
+  int whole;       // shares end where groups do
+  int stages;      // rows of the ring in shared memory
+  // work split
+  int warps;       // warps of a row
+  int vec;         // every row and vector is accessed in 16-byte words
+  int* status;
+};
+constexpr int kNormMaxCols = 12288;  // a row of the backward's four tensors fits shared memory
+// dtype of x and out; stream_f32: residual and hidden are fp32.
+cudaError_t launch_norm_forward(const NormParams& p, int dtype, bool stream_f32, cudaStream_t s);
+// CTAs of the backward pass (their number does not depend on the device).
+int norm_backward_units(int64_t m, int n);
+cudaError_t launch_norm_backward(const NormParams& p, int dtype, bool stream_f32, cudaStream_t s);
+
 }  // namespace wsattn

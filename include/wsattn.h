@@ -419,6 +419,118 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* args, void* workspace,
                            size_t workspace_bytes, void* stream);
 int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes);
 
+/*
+ * Norms of a block: the end of one part (its norm, gate and residual) and the
+ * start of the next (norm, weight, scale and shift), in one pass:
+ *   u      = x, or std(x) * post_weight
+ *   hidden = residual_scale * residual + gate * u
+ *   out    = (std(hidden) * weight + bias) (1 + scale) + shift
+ * where std(t) = (t - mean t) / sqrt(var t + eps) over a row's n columns
+ * (WSATTN_NORM_LAYER) or t / sqrt(mean t^2 + eps) (WSATTN_NORM_RMS).  All of
+ * it in fp32; out is formed from hidden before hidden is rounded.
+ *   dtype         of x and out (wsattn_dtype)
+ *   stream_dtype  of residual and hidden: dtype or WSATTN_FP32
+ *   mod_dtype     of gate, scale and shift: dtype or WSATTN_FP32
+ *   weight_dtype  of weight, bias and post_weight: dtype or WSATTN_FP32
+ *   m, n          rows (below 2^31 - 511) and columns (1 .. 12288)
+ *   group         >= 1: row r takes row r / group of gate, scale and shift
+ *                 (tokens of a clip, of a frame, or 1 for vectors a token)
+ *   norm          of out; post_norm: of x, WSATTN_NORM_NONE for none
+ *   eps           >= 0; residual_scale: finite
+ *   x             [m, n], row stride ldx >= n
+ *   residual      [m, n] or NULL (0)
+ *   gate, scale, shift         [ceil(m / group), n], each or NULL (1, 0, 0)
+ *   weight, bias, post_weight  [n], each or NULL (1, 0, 1)
+ *   hidden        [m, n] or NULL: not wanted; may be residual or x itself
+ *   out           [m, n] or NULL: not wanted; may be x itself, or residual when
+ *                 hidden is not
+ * Rows need no alignment beyond the type's own; rows and vectors on 16-byte
+ * boundaries with n a multiple of 8 are read in 16-byte words.
+ * Errors: BAD_ARG, UNSUPPORTED (n above 12288), CUDA.
+ */
+enum wsattn_norm_kind { WSATTN_NORM_NONE = 0, WSATTN_NORM_RMS = 1, WSATTN_NORM_LAYER = 2 };
+typedef struct wsattn_block_norm_args {
+  int dtype, stream_dtype, mod_dtype, weight_dtype;
+  int64_t m;
+  int n, norm, post_norm;
+  float eps, residual_scale;
+  int64_t group;
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* gate;
+  int64_t ldg;
+  const void* scale;
+  int64_t lds;
+  const void* shift;
+  int64_t ldf;
+  const void* weight;
+  const void* bias;
+  const void* post_weight;
+  void* hidden;
+  int64_t ldh;
+  void* out;
+  int64_t ldo;
+} wsattn_block_norm_args;
+int wsattn_block_norm(const wsattn_block_norm_args* args, void* stream);
+
+/*
+ * Gradients of wsattn_block_norm from dout and dhidden (what reaches hidden
+ * other than through out), either NULL for zero:
+ *   dx [m, n] of dtype, dresidual [m, n] of stream_dtype, and fp32 sums
+ *   dgate, dscale, dshift [ceil(m / group), n] over the rows of a group,
+ *   dweight, dbias, dpost_weight [n] over all rows, in a fixed order;
+ * each NULL to skip it.
+ *   dout     [m, n] of dtype
+ *   dhidden  [m, n] of stream_dtype
+ *   hidden   as the forward left it (x itself, in stream_dtype = dtype, when
+ *            there is no residual, gate or post_norm); needed with dout
+ *   x        needed for dgate, dpost_weight and with post_norm
+ *   gate, scale, weight, bias, post_weight, eps, residual_scale as in the
+ *            forward (shift is not needed)
+ * dx and dresidual may be dout, dhidden, hidden or x itself, where the types
+ * agree, not each other.  With m = 0 the sums are zeroed.
+ * workspace: wsattn_block_norm_backward_workspace bytes, 16-byte aligned
+ * (NULL when that is 0).
+ * Errors: BAD_ARG (also a workspace too small), UNSUPPORTED, CUDA.
+ */
+typedef struct wsattn_block_norm_grad_args {
+  int dtype, stream_dtype, mod_dtype, weight_dtype;
+  int64_t m;
+  int n, norm, post_norm;
+  float eps, residual_scale;
+  int64_t group;
+  const void* dout;
+  int64_t ldo;
+  const void* dhidden;
+  int64_t lddh;
+  const void* hidden;
+  int64_t ldh;
+  const void* x;
+  int64_t ldx;
+  const void* gate;
+  int64_t ldg;
+  const void* scale;
+  int64_t lds;
+  const void* weight;
+  const void* bias;
+  const void* post_weight;
+  void* dx;
+  int64_t lddx;
+  void* dresidual;
+  int64_t lddr;
+  float* dgate;
+  float* dscale;
+  float* dshift;
+  float* dweight;
+  float* dbias;
+  float* dpost_weight;
+} wsattn_block_norm_grad_args;
+int wsattn_block_norm_backward(const wsattn_block_norm_grad_args* args, void* workspace,
+                               size_t workspace_bytes, void* stream);
+int wsattn_block_norm_backward_workspace(const wsattn_block_norm_grad_args* args, size_t* bytes);
+
 /* Synchronises `stream` and reports the status word of the operators above on
  * the current device: OK, TIMEOUT if a device-side wait expired, BOUNDS (debug
  * build); what was reported is then cleared.  CUDA if the synchronisation
