@@ -17,6 +17,7 @@ The names mirror the C ABI:
     wsattn_rotary_plan, wsattn_rotary_destroy, wsattn_rotary, wsattn_qknorm,
     wsattn_qknorm_backward, wsattn_qknorm_backward_workspace, wsattn_linear,
     wsattn_linear_workspace, wsattn_linear_backward, wsattn_linear_backward_workspace,
+    wsattn_cross, wsattn_cross_workspace, wsattn_cross_backward, wsattn_cross_backward_workspace,
     wsattn_block_norm, wsattn_block_norm_backward, wsattn_block_norm_backward_workspace,
     wsattn_op_status
 """
@@ -61,6 +62,8 @@ EXPORTS = (
     "wsattn_rotary_plan", "wsattn_rotary_destroy", "wsattn_rotary", "wsattn_qknorm",
     "wsattn_qknorm_backward", "wsattn_qknorm_backward_workspace", "wsattn_linear",
     "wsattn_linear_workspace", "wsattn_linear_backward", "wsattn_linear_backward_workspace",
+    "wsattn_cross", "wsattn_cross_workspace", "wsattn_cross_backward",
+    "wsattn_cross_backward_workspace",
     "wsattn_block_norm", "wsattn_block_norm_backward", "wsattn_block_norm_backward_workspace",
     "wsattn_op_status",
 )
@@ -134,6 +137,12 @@ _LINEAR = struct.Struct("@iiqiiPqiqPqPPqPqPqi0q").pack
 # ldp, activation, dx, lddx, dw, lddw, db
 _LINEAR_GRAD = struct.Struct("@iqiiPqPqPqPqiPqPqP0q").pack
 
+# wsattn_cross_args: dtype, head_dim, batch, n_tokens, n_keys, q, k, v, out (each
+# data, heads, strides b, h, n), k_lengths, scale, lse
+_CROSS = struct.Struct("@iiiqq" + "Piqqq" * 4 + "PfP0q").pack
+# wsattn_cross_grad_args: dtype, head_dim, batch, n_tokens, n_keys, dout, q, k, v,
+# out, lse, k_lengths, scale, dq, dk, dv
+_CROSS_GRAD = struct.Struct("@iiiqq" + "Piqqq" * 5 + "PPf" + "Piqqq" * 3 + "0q").pack
 # wsattn_block_norm_args: dtype, stream_dtype, mod_dtype, weight_dtype, m, n, norm,
 # post_norm, eps, residual_scale, group, x, ldx, residual, ldr, gate, ldg, scale,
 # lds, shift, ldf, weight, bias, post_weight, hidden, ldh, out, ldo
@@ -156,6 +165,10 @@ _lib.wsattn_linear.argtypes = [_P, _P, _SZ, _P]
 _lib.wsattn_linear_workspace.argtypes = [_P, _SZP]
 _lib.wsattn_linear_backward.argtypes = [_P, _P, _SZ, _P]
 _lib.wsattn_linear_backward_workspace.argtypes = [_P, _SZP]
+_lib.wsattn_cross.argtypes = [_P, _P, _SZ, _P]
+_lib.wsattn_cross_workspace.argtypes = [_P, _SZP]
+_lib.wsattn_cross_backward.argtypes = [_P, _P, _SZ, _P]
+_lib.wsattn_cross_backward_workspace.argtypes = [_P, _SZP]
 _lib.wsattn_block_norm.argtypes = [_P, _P]
 _lib.wsattn_block_norm_backward.argtypes = [_P, _P, _SZ, _P]
 _lib.wsattn_block_norm_backward_workspace.argtypes = [_P, _SZP]
@@ -915,6 +928,145 @@ def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="n
                                       need_dx, need_dw, need_db, None, query=True)
     n = _SZ()
     _run(dev, "wsattn_linear_backward_workspace", _lib.wsattn_linear_backward_workspace, args,
+         ctypes.byref(n))
+    return int(n.value)
+
+
+def _token_major(b, h, n, d, dtype, like, stream):
+    """[B, H, N, D] whose memory is [B, N, H, D]: a token's heads side by side,
+    as wsattn_linear reads them (t.transpose(1, 2).flatten(2))."""
+    return _empty((b, n, h, d), dtype, like, stream).transpose(1, 2)
+
+
+def _view_fields(t, name, shape, dt, dev):
+    """A wsattn_heads' fields."""
+    if t.dtype is not dt or t.get_device() != dev or t.shape != shape:
+        _check_tensor(t, name, dev, dt)
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    sb, sh, sn, sd = t.stride()
+    if sd != 1 and t.numel():
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), shape[1], sb, sh, sn
+
+
+def _cross_operands(q, k, v, k_lengths, scale):
+    """Checked operands: (device, type code, D, shapes of q and k, lengths' pointer, scale)."""
+    dev = _device_of(q, "q")
+    code = _dtype_code(q, "q", (BF16, FP16))
+    sq, sk = q.shape, k.shape
+    if len(sq) != 4 or len(sk) != 4 or sq[3] != sk[3] or sq[0] != sk[0]:
+        raise ValueError(f"q and k must be [B, H, N, D] and [B, Hk, M, D], got {list(sq)} and {list(sk)}")
+    if sq[0] > _INT_MAX or sq[1] > _INT_MAX or sk[1] > _INT_MAX:
+        raise ValueError(f"more than {_INT_MAX} batch elements or heads: {list(sq)}, {list(sk)}")
+    if not sk[1] or sq[1] % sk[1] or not sq[1]:
+        raise ValueError(f"q's {sq[1]} heads must be a multiple of k's {sk[1]}")
+    lp = 0
+    if k_lengths is not None:
+        _check_tensor(k_lengths, "k_lengths", dev, torch.int32)
+        if k_lengths.shape != sq[:1] or not k_lengths.is_contiguous():
+            raise ValueError(f"k_lengths must be contiguous [{sq[0]}], got {list(k_lengths.shape)}")
+        lp = k_lengths.data_ptr()
+    if scale is None:
+        scale = sq[3] ** -0.5 if sq[3] else 1.0
+    return dev, code, sq[3], sq, sk, lp, scale
+
+
+def _lse_ptr(lse, shape, dev):
+    _check_tensor(lse, "lse", dev, torch.float32)
+    if lse.shape != shape[:3] or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous {list(shape[:3])}, got {list(lse.shape)}")
+    return lse.data_ptr()
+
+
+def _cross_args(q, k, v, k_lengths, scale, out, lse, stream, query=False):
+    dev, code, d, sq, sk, lp, scale = _cross_operands(q, k, v, k_lengths, scale)
+    dt = q.dtype
+    b, h, n = sq[:3]
+    if query:  # any aligned address stands for the output
+        of = (256, h, n * h * d, d, h * d)
+    else:
+        out = _token_major(b, h, n, d, dt, q, stream) if out is None else out
+        of = _view_fields(out, "out", sq, dt, dev)
+    return _CROSS(code, d, b, n, sk[2], *_view_fields(q, "q", sq, dt, dev),
+                  *_view_fields(k, "k", sk, dt, dev), *_view_fields(v, "v", sk, dt, dev), *of, lp,
+                  scale, 0 if lse is None else _lse_ptr(lse, sq, dev)), out, dev
+
+
+def wsattn_cross(q, k, v, k_lengths=None, scale=None, out=None, lse=None, workspace=None,
+                 stream=None):
+    """Attention of q [B, H, N, D] to an encoder's k, v [B, Hk, M, D] (bf16 or
+    fp16 views of any strides with 16-byte aligned rows; Hk divides H; D a
+    multiple of 16 up to 128): softmax(scale q k^T) v over the first
+    k_lengths[b] keys (int32 [B] on the device; default: all M).  scale:
+    default D ** -0.5.  lse: an fp32 tensor [B, H, N] that receives the rows'
+    log of the sum of exponentials, for wsattn_cross_backward.  Returns out
+    [B, H, N, D], by default with a token's heads side by side in memory (as
+    wsattn_linear reads them: out.transpose(1, 2).flatten(2)).  Rows that no key
+    is left for are 0, their lse -inf."""
+    args, out, dev = _cross_args(q, k, v, k_lengths, scale, out, lse, stream)
+    raw = _raw_stream(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_cross_workspace, "wsattn_cross_workspace", args,
+                                 workspace, dev, q, stream)
+    _run(dev, "wsattn_cross", _lib.wsattn_cross, args, ws, nbytes, raw)
+    return out
+
+
+def wsattn_cross_workspace(q, k, v) -> int:
+    """Bytes of scratch wsattn_cross takes for these operands."""
+    args, _, dev = _cross_args(q, k, v, None, None, None, None, None, query=True)
+    n = _SZ()
+    _run(dev, "wsattn_cross_workspace", _lib.wsattn_cross_workspace, args, ctypes.byref(n))
+    return int(n.value)
+
+
+_NO_VIEW = (0, 1, 0, 0, 0)
+
+
+def _cross_grad_args(dout, q, k, v, out, lse, k_lengths, scale, dq, dk, dv, need_dq, need_dk,
+                     need_dv, stream, query=False):
+    dev, code, d, sq, sk, lp, scale = _cross_operands(q, k, v, k_lengths, scale)
+    dt = q.dtype
+    grads, fields = [], []
+    for name, t, need, s in (("dq", dq, need_dq, sq), ("dk", dk, need_dk, sk), ("dv", dv, need_dv, sk)):
+        if t is None and not need:
+            fields += _NO_VIEW
+        elif query:
+            fields += (256, s[1], s[2] * s[1] * d, d, s[1] * d)
+        else:
+            t = _token_major(s[0], s[1], s[2], d, dt, q, stream) if t is None else t
+            fields += _view_fields(t, name, s, dt, dev)
+        grads.append(t)
+    args = _CROSS_GRAD(code, d, sq[0], sq[2], sk[2], *_view_fields(dout, "dout", sq, dt, dev),
+                       *_view_fields(q, "q", sq, dt, dev), *_view_fields(k, "k", sk, dt, dev),
+                       *_view_fields(v, "v", sk, dt, dev), *_view_fields(out, "out", sq, dt, dev),
+                       _lse_ptr(lse, sq, dev), lp, scale, *fields)
+    return args, grads, dev
+
+
+def wsattn_cross_backward(dout, q, k, v, out, lse, k_lengths=None, scale=None, dq=None, dk=None,
+                          dv=None, need_dq=True, need_dk=True, need_dv=True, workspace=None,
+                          stream=None):
+    """Gradients (dq, dk, dv) of wsattn_cross from dout, with out and lse as it
+    left them (same k_lengths and scale); None for what is not needed.  dq, dk
+    and dv: views of any strides (default: a token's heads side by side in
+    memory, as a projection's gradient is read); dk and dv are summed over the
+    query heads that share a key head."""
+    args, (dq, dk, dv), dev = _cross_grad_args(dout, q, k, v, out, lse, k_lengths, scale, dq, dk, dv,
+                                               need_dq, need_dk, need_dv, stream)
+    raw = _raw_stream(dev, stream)
+    ws, nbytes, _hold = _scratch(_lib.wsattn_cross_backward_workspace,
+                                 "wsattn_cross_backward_workspace", args, workspace, dev, q, stream)
+    _run(dev, "wsattn_cross_backward", _lib.wsattn_cross_backward, args, ws, nbytes, raw)
+    return dq, dk, dv
+
+
+def wsattn_cross_backward_workspace(dout, q, k, v, out, lse, need_dq=True, need_dk=True,
+                                    need_dv=True) -> int:
+    """Bytes of scratch wsattn_cross_backward takes for these operands."""
+    args, _, dev = _cross_grad_args(dout, q, k, v, out, lse, None, None, None, None, None, need_dq,
+                                    need_dk, need_dv, None, query=True)
+    n = _SZ()
+    _run(dev, "wsattn_cross_backward_workspace", _lib.wsattn_cross_backward_workspace, args,
          ctypes.byref(n))
     return int(n.value)
 

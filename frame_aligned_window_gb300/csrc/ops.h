@@ -252,4 +252,23 @@ cudaError_t launch_norm_forward(const NormParams& p, int dtype, bool stream_f32,
 int norm_backward_units(int64_t m, int n);
 cudaError_t launch_norm_backward(const NormParams& p, int dtype, bool stream_f32, cudaStream_t s);
 
+// -------------------------------------------------------- cross attention
+// A [batch, heads, rows, D] view in global memory (strides in elements).
+struct CrossView {
+  const void* data;
+  int64_t sb, sh, sn;
+};
+struct CrossParams {
+  CrossView q, k, v, o, dout;          // o: the forward's output (written, or read by the backward)
+  CrossView dq, dk, dv;
+  const int32_t* lengths;              // [batch] keys that count, or null: all
+  float* lse;                          // [batch, heads, n] or null
+  int batch, heads, kv_heads, dim;
+  int n, m;                            // queries, keys
+  float scale, scale_log2;
+  int* status;
+};
+cudaError_t launch_cross_forward(const CrossParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cross_backward(const CrossParams& p, int dtype, cudaStream_t s);
+
 }  // namespace wsattn

@@ -420,6 +420,70 @@ int wsattn_linear_backward(const wsattn_linear_grad_args* args, void* workspace,
 int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t* bytes);
 
 /*
+ * Attention of queries to an encoder's states, whose number is another one:
+ *   out = softmax(scale q k^T) v,   lse = log of the sum of exp(scale q k^T)
+ * per (b, head), over the first k_lengths[b] of n_keys keys (query heads share
+ * key heads in order: head h reads key head h / (q.heads / k.heads)).  A row
+ * that no key is left for is 0, its lse -infinity.  What lies in k and v behind
+ * a length is never used, whatever it is.  The products take 16-bit rows and
+ * keep fp32 sums; the probabilities are rounded to dtype for the second one
+ * (their sum is not).
+ *   dtype      of q, k, v and out: WSATTN_BF16 or WSATTN_FP16
+ *   head_dim   D: a multiple of 16, 16 .. 128
+ *   n_tokens, n_keys  below 2^31 - 511; either may be 0
+ *   q, out     [batch, heads, n_tokens, D] views
+ *   k, v       [batch, kv heads, n_keys, D] views of one head count that
+ *              divides q's; inputs may have strides of 0 (broadcast)
+ *   k_lengths  int32 [batch] in device memory, or NULL: n_keys for all.  Values
+ *              outside 0 .. n_keys count as the nearest of them
+ *   scale      > 0, finite; 1 / sqrt(D) is the usual one
+ *   lse        fp32 [batch, heads, n_tokens] contiguous, or NULL: not wanted
+ * Rows of every view start on 16-byte boundaries (the base, and the strides of
+ * dimensions longer than 1).
+ *   workspace  wsattn_cross_workspace bytes, 16-byte aligned (NULL when 0)
+ * Errors: BAD_ARG (also a workspace too small), UNSUPPORTED (dtype, head_dim),
+ *         CUDA.
+ */
+typedef struct wsattn_cross_args {
+  int dtype, head_dim, batch;
+  int64_t n_tokens, n_keys;
+  wsattn_heads q, k, v, out;
+  const int32_t* k_lengths;
+  float scale;
+  float* lse;
+} wsattn_cross_args;
+int wsattn_cross(const wsattn_cross_args* args, void* workspace, size_t workspace_bytes,
+                 void* stream);
+int wsattn_cross_workspace(const wsattn_cross_args* args, size_t* bytes);
+
+/*
+ * Gradients of wsattn_cross from dout, with p = exp(scale q k^T - lse):
+ *   dv = p^T dout,  ds = scale p (dout v^T - sum_d dout out),  dq = ds k,  dk = ds^T q
+ * p and ds are rounded to dtype for the products, whose sums are fp32; dk and
+ * dv are summed over the query heads that share a key head, in a fixed order.
+ * Keys behind a length get zeros, and so do rows that no key was left for.
+ *   out, lse   as wsattn_cross left them, for the same k_lengths and scale
+ *   dout       as out; dq like q, dk and dv like k: views, whose elements must
+ *              lie apart (of a broadcast input the caller sums the copies); dq,
+ *              dk or dv with NULL data is skipped.  They must not overlap inputs
+ * Alignment and workspace as for wsattn_cross.
+ * Errors: BAD_ARG (also a workspace too small), UNSUPPORTED (dtype, head_dim),
+ *         CUDA.
+ */
+typedef struct wsattn_cross_grad_args {
+  int dtype, head_dim, batch;
+  int64_t n_tokens, n_keys;
+  wsattn_heads dout, q, k, v, out;
+  const float* lse;
+  const int32_t* k_lengths;
+  float scale;
+  wsattn_heads dq, dk, dv;
+} wsattn_cross_grad_args;
+int wsattn_cross_backward(const wsattn_cross_grad_args* args, void* workspace,
+                          size_t workspace_bytes, void* stream);
+int wsattn_cross_backward_workspace(const wsattn_cross_grad_args* args, size_t* bytes);
+
+/*
  * Norms of a block: the end of one part (its norm, gate and residual) and the
  * start of the next (norm, weight, scale and shift), in one pass:
  *   u      = x, or std(x) * post_weight

@@ -150,3 +150,90 @@ def norm_backward(dout, hidden, x, dhidden, gate, scale, shift, weight, bias, no
 def rounded(tol, want, dtype):
     """A tolerance with the rounding to a type."""
     return tol + half_step(dtype) * (want.abs() + tol) + tiny(dtype) + 1e-37
+
+
+# ------------------------------------------------------------ cross attention
+
+def heads_of(t, h):
+    return t.double().repeat_interleave(h // t.shape[1], 1)
+
+
+def lengths_of(lengths, b, m, dev):
+    if lengths is None:
+        return torch.full((b,), m, device=dev)
+    return lengths.long().clamp(0, m)
+
+
+def cleaned(t, lens):
+    """fp64 keys or values with zeros behind each length."""
+    keep = torch.arange(t.shape[2], device=t.device) < lens[:, None]
+    return torch.where(keep[:, None, :, None], t.double(), 0.0)
+
+
+def logits(q, k, lens, scale):
+    """(scale q k^T with -inf behind the lengths, its error on the tensor cores)."""
+    h, d = q.shape[1], q.shape[3]
+    qd, kd = q.double(), heads_of(cleaned(k, lens), h)
+    s = scale * qd @ kd.transpose(2, 3)
+    size = scale * qd.abs() @ kd.abs().transpose(2, 3)
+    dead = torch.arange(k.shape[2], device=k.device) >= lens[:, None, None, None]
+    # truncations of the product's partial sums, the multiplication by scale log2(e) and the subtraction of the maximum
+    # or the sum (fp32, of values up to `size` and 40 more), the exponential's own 2^-22
+    err = (d / 16 + 8) * 2.0 ** -22 * size + 2.0 ** -22 * (size.amax(-1, keepdim=True) + 40) if k.shape[2] else size
+    return s.masked_fill(dead, float("-inf")), torch.where(dead, 0.0, err)
+
+
+def cross_forward(q, k, v, lengths, scale):
+    """(out, its tolerance, lse, its tolerance)."""
+    b, h, n, d = q.shape
+    m, dt = k.shape[2], q.dtype
+    lens = lengths_of(lengths, b, m, q.device)
+    if m == 0:
+        zero = torch.zeros((b, h, n, d), dtype=torch.float64, device=q.device)
+        return zero, zero, torch.full((b, h, n), float("-inf"), dtype=torch.float64, device=q.device), torch.zeros((b, h, n)).to(q.device)
+    s, es = logits(q, k, lens, scale)
+    lse = torch.logsumexp(s, -1)
+    empty = (lens == 0)[:, None, None]
+    p = torch.where(empty[..., None], 0.0, torch.exp(s - lse.masked_fill(empty, 0.0)[..., None]))
+    vd = heads_of(cleaned(v, lens), h)
+    out = p @ vd
+    # p: rounded, and off by its logit's error; below the type's smallest values relative to the largest p (1 / sum >= p)
+    step = half_step(dt) + 2 * es + 2.0 ** -20
+    small = torch.where(empty[..., None], 0.0, torch.exp(s.amax(-1, keepdim=True) - lse[..., None])) * tiny(dt)
+    tol = (p * step) @ vd.abs() + small * vd.abs().sum(2, keepdim=True)
+    # the sum of the probabilities is off by as much as they are, and the product by its truncations
+    rel = (p * (2 * es + 2.0 ** -20)).sum(-1, keepdim=True) + 2.0 ** -19
+    tol = tol + rel * out.abs() + (m / 16 + 8) * 2.0 ** -22 * (p @ vd.abs())
+    return out, tol, lse, torch.where(empty, 0.0, rel.squeeze(-1) + 2.0 ** -22 * (1 + lse.masked_fill(empty, 0.0).abs()))
+
+
+def cross_backward(dout, q, k, v, out, lse, lengths, scale):
+    """{name: (gradient, tolerance)} of the definition with out and lse as given."""
+    b, h, n, d = q.shape
+    hk, m, dt = k.shape[1], k.shape[2], q.dtype
+    r = h // hk
+    lens = lengths_of(lengths, b, m, q.device)
+    s, es = logits(q, k, lens, scale)
+    empty = (lens == 0)[:, None, None]
+    p = torch.exp(s - lse.double().masked_fill(empty, 0.0)[..., None])
+    do, qd = dout.double(), q.double()
+    kd, vd = heads_of(cleaned(k, lens), h), heads_of(cleaned(v, lens), h)
+    delta = (do * out.double()).sum(-1, keepdim=True)
+    dp = do @ vd.transpose(2, 3)
+    ds = p * (dp - delta)
+    rel = 2 * es + 2.0 ** -20
+    size = do.abs() @ vd.abs().transpose(2, 3)
+    e_ds = ds.abs() * (rel + half_step(dt) + 2.0 ** -21) + tiny(dt) * (p > 0) \
+        + p * ((d / 16 + 8) * 2.0 ** -22 * size + 2.0 ** -20 * (do * out.double()).abs().sum(-1, keepdim=True))
+
+    def shared(t):
+        return t.view(b, hk, r, m, d).sum(2)
+
+    w = {}
+    w["dq"] = scale * ds @ kd, scale * (e_ds @ kd.abs() + (m / 16 + 8) * 2.0 ** -22 * (ds.abs() @ kd.abs()))
+    many = (n * r / 16 + 8) * 2.0 ** -22
+    w["dk"] = scale * shared(ds.transpose(2, 3) @ qd), \
+        scale * shared(e_ds.transpose(2, 3) @ qd.abs() + many * (ds.abs().transpose(2, 3) @ qd.abs()))
+    e_p = p * (rel + half_step(dt)) + tiny(dt) * (p > 0)
+    w["dv"] = shared(p.transpose(2, 3) @ do), shared(e_p.transpose(2, 3) @ do.abs() + many * (p.transpose(2, 3) @ do.abs()))
+    return w
