@@ -33,8 +33,8 @@ LIB_DEBUG = os.path.join(HERE, "libwsattn_debug.so")
 SOURCES = ["plan.cpp", "prepare.cu", "forward.cu", "api.cu", "prepare_static.cu", "produce.cu",
            "qknorm.cu", "qknorm_back.cu", "linear_pair.cu", "linear_tile.cu", "linear_aux.cu", "api_ops.cu",
            "norm.cu", "norm_back.cu", "api_norm.cu",
-           "cross.cu", "api_cross.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "ops.h", "epilogue.cuh", "qknorm.cuh", "api_args.h", "norm.cuh"]
+           "cross.cu", "cross_back.cu", "api_cross.cu"]
+HEADERS = ["internal.h", "ptx.cuh", "ops.h", "epilogue.cuh", "qknorm.cuh", "api_args.h", "norm.cuh", "cross.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -43,6 +43,32 @@ CrossView view(const wsattn_heads* v) {
   return CrossView{v->data, v->stride_b, v->stride_h, v->stride_n};
 }
 
+// {D, rows, heads, batch} with 64-column boxes, 128-byte swizzle.  A dimension
+// of stride 0 (a broadcast) has one element, which the kernels read at 0.
+bool encode(CUtensorMap* m, int dtype, const wsattn_heads* v, int dim, int batch, int64_t n,
+            int box_n, int box_h, int* by_head = nullptr, int* by_batch = nullptr) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = wsattn::tensor_map_encoder();
+  if (!fn) return false;
+  const bool one_h = v->heads == 1 || v->stride_h == 0, one_b = batch == 1 || v->stride_b == 0;
+  if (by_head) *by_head = !one_h;
+  if (by_batch) *by_batch = !one_b;
+  const bool one_n = n <= 1;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(n),
+                              static_cast<cuuint64_t>(one_h ? 1 : v->heads),
+                              static_cast<cuuint64_t>(one_b ? 1 : batch)};
+  // strides of single elements are never used, but must be valid ones
+  const cuuint64_t row = static_cast<cuuint64_t>(dim) * 2;
+  const cuuint64_t strides[3] = {one_n ? row : static_cast<cuuint64_t>(v->stride_n) * 2,
+                                 one_h ? row : static_cast<cuuint64_t>(v->stride_h) * 2,
+                                 one_b ? row : static_cast<cuuint64_t>(v->stride_b) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_n), static_cast<cuuint32_t>(box_h), 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, dtype == WSATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            4, v->data, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename A>
 void fill_common(const A* a, CrossParams* p) {
   std::memset(p, 0, sizeof(*p));
@@ -70,10 +96,16 @@ int wsattn_cross_workspace(const wsattn_cross_args* a, size_t* bytes) {
   if (!bytes || !sizes_ok(a)) return WSATTN_ERR_BAD_ARG;
   if (!supported(a)) return WSATTN_ERR_UNSUPPORTED;
   *bytes = 0;
+  if (a->batch == 0 || a->n_tokens == 0) return WSATTN_OK;
+  CrossParams p;
+  fill_common(a, &p);
+  wsattn::split_cross(&p);
+  *bytes = wsattn::cross_partial_bytes(p);
   return WSATTN_OK;
 }
 
-int wsattn_cross(const wsattn_cross_args* a, void*, size_t, void* stream) {
+int wsattn_cross(const wsattn_cross_args* a, void* workspace, size_t workspace_bytes,
+                 void* stream) {
   if (!sizes_ok(a)) return WSATTN_ERR_BAD_ARG;
   if (!supported(a)) return WSATTN_ERR_UNSUPPORTED;
   const int64_t n = a->n_tokens, m = a->n_keys;
@@ -85,9 +117,26 @@ int wsattn_cross(const wsattn_cross_args* a, void*, size_t, void* stream) {
   if (!a->q.data || !a->out.data || (m && (!a->k.data || !a->v.data))) return WSATTN_ERR_BAD_ARG;
   CrossParams p;
   fill_common(a, &p);
+  wsattn::split_cross(&p);
+  if (p.items < 0) return WSATTN_ERR_BAD_ARG;
+  const size_t need = wsattn::cross_partial_bytes(p);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return WSATTN_ERR_BAD_ARG;
+  if (need) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_l = p.part_o + static_cast<size_t>(p.batch) * p.heads * p.n * p.splits * p.dim;
+  }
   p.status = wsattn::op_status_ptr();
-  if (!p.status) return WSATTN_ERR_CUDA;
-  return wsattn::launch_cross_forward(p, a->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  const int sms = sm_count();
+  if (!p.status || !sms) return WSATTN_ERR_CUDA;
+  const int d = a->head_dim, rows = wsattn::kCrossRows;
+  // without keys no step is loaded, and the maps of k and v are not used
+  if (!encode(&p.tm_q, a->dtype, &a->q, d, a->batch, n, p.box_n, p.box_h, &p.q_h, &p.q_b) ||
+      !encode(&p.tm_o, a->dtype, &a->out, d, a->batch, n, 32, 1) ||
+      (m && (!encode(&p.tm_k, a->dtype, &a->k, d, a->batch, m, rows, 1, &p.k_h, &p.k_b) ||
+             !encode(&p.tm_v, a->dtype, &a->v, d, a->batch, m, rows, 1, &p.v_h, &p.v_b))))
+    return WSATTN_ERR_CUDA;
+  return wsattn::launch_cross_forward(p, a->dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? WSATTN_OK
              : WSATTN_ERR_CUDA;
 }

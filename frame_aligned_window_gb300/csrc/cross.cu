@@ -1,149 +1,618 @@
-// Attention to an encoder's states: out = softmax(scale q k^T) v with the
-// running maximum and sum of the softmax.  A warp takes a query.
-#include "epilogue.cuh"
+// Attention to an encoder's states for sm_103a: out = softmax(scale q k^T) v
+// over the first len_b keys of another sequence.
+//
+//   s_ij = q_i . k_j,  m_i = running maximum of scale s_ij,
+//   p_ij = exp(scale s_ij - m_i),  l_i = sum p_ij,  o_i = sum p_ij v_j / l_i
+// in steps of 128 keys; where a row's maximum grows by more than 2^8, o_i and
+// l_i are rescaled (o / l does not depend on m).
+//
+// Queries are many and keys few (a text, an image's patches) or the other way
+// round (a token or some learned queries over a long memory).  A row tile is
+// 128 queries of a head, or, with fewer queries, those of several heads that
+// share a key head.  A work item is a pair of row tiles of one key head, which
+// share every key step that is loaded; a persistent CTA an SM walks the items.
+//   warp 0     TMA: row tiles of q (a ring of three), key and value steps (a
+//              ring of four)
+//   warp 1     MMA issue (one elected lane): S_u = Q_u K^T, O_u += P_u V for
+//              the two row tiles u in turn, tensor memory
+//   warps 4-11 softmax and epilogue, a warpgroup for each row tile; thread =
+//              row = tensor-memory lane
+// Tensor memory: O_0, O_1 (D columns each), S_0, S_1 (128 columns each).  P_u
+// takes S_u's place: the softmax holds S_u in registers when it stores P_u, and
+// the MMAs of one thread run in order, so that S_u of the next step cannot
+// overtake the P_u V that reads P_u.  While one row tile's softmax runs, the
+// tensor core works on the other's two products.
+//
+// The epilogue writes a row tile over its own queries in shared memory and
+// from there by TMA, which drops the rows behind the last query.  With few row
+// tiles and many keys, `splits` parts of the keys go to different CTAs, which
+// leave fp32 rows and their sums in the workspace, and a second kernel joins
+// them.
+#include "cross.cuh"
 
 namespace wsattn {
 namespace {
 
-using namespace ptx;
+using namespace cross;
 
-template <typename T>
-__device__ __forceinline__ const T* row_of(const CrossView& v, int64_t b, int64_t h, int64_t i) {
-  return static_cast<const T*>(v.data) + b * v.sb + h * v.sh + i * v.sn;
-}
-__device__ __forceinline__ int keys_of(const CrossParams& p, int b) {
-  return p.lengths ? max(0, min(p.lengths[b], p.m)) : p.m;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int dim, float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 32 * i + (threadIdx.x & 31);
-    f[i] = c < dim ? to_f32(p[c]) : 0.f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store4(const T* p, int dim, const float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 32 * i + (threadIdx.x & 31);
-    if (c < dim) const_cast<T*>(p)[c] = from_f32<T>(f[i]);
-  }
-}
-__device__ __forceinline__ float dot(const float (&a)[4], const float (&b)[4]) {
-  return warp_sum(a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]);
-}
+constexpr int kThreads = 384;
+constexpr int kQTiles = 3;    // ring of row tiles
+constexpr int kSteps = 4;     // ring of key and value steps
+constexpr float kLazyMax = 8.f;  // rescale when a maximum grows by more than 2^8
 
-template <typename T>
-__global__ void __launch_bounds__(128) cross_forward_kernel(const __grid_constant__ CrossParams p) {
-  griddep_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
-  if (row >= static_cast<int64_t>(p.batch) * p.heads * p.n) return;
-  const int i = static_cast<int>(row % p.n);
-  const int h = static_cast<int>(row / p.n % p.heads), b = static_cast<int>(row / p.n / p.heads);
-  const int e = h / (p.heads / p.kv_heads), len = keys_of(p, b);
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, top = -INFINITY, sum = 0.f;
-  load4(row_of<T>(p.q, b, h, i), p.dim, q);
-  for (int j = 0; j < len; ++j) {
-    float k[4], v[4];
-    load4(row_of<T>(p.k, b, e, j), p.dim, k);
-    load4(row_of<T>(p.v, b, e, j), p.dim, v);
-    const float s = dot(q, k) * p.scale, m = fmaxf(top, s);
-    const float a = top == m ? 1.f : expf(top - m), w = expf(s - m);
-    sum = sum * a + w;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = o[c] * a + w * v[c];
-    top = m;
-  }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) o[c] = len ? o[c] / sum : 0.f;
-  store4(row_of<T>(p.o, b, h, i), p.dim, o);
-  if (p.lse && (threadIdx.x & 31) == 0) p.lse[row] = len ? top + logf(sum) : -INFINITY;
+enum : int {
+  B_QFULL = 0,
+  B_QEMPTY = B_QFULL + kQTiles,
+  B_KVFULL = B_QEMPTY + kQTiles,
+  B_KVEMPTY = B_KVFULL + kSteps,
+  B_SFULL = B_KVEMPTY + kSteps,  // MMA -> softmax u: S_u written
+  B_PFULL = B_SFULL + 2,         // softmax u -> MMA: P_u written
+  B_OFULL = B_PFULL + 2,         // MMA -> softmax u: the item's last product done
+  B_COUNT = B_OFULL + 2
+};
+
+// A work item: two row tiles of key head e of batch element b, and its steps.
+struct Item {
+  int b, e, tile, part;
+  int len, step0, step1;
+  bool two;  // the second row tile exists
+};
+__device__ __forceinline__ Item item_of(const CrossParams& p, int i) {
+  Item t;
+  const int tiles = p.tiles_n * p.tiles_h, groups = (tiles + p.pair - 1) / p.pair;
+  t.part = i % p.splits;
+  i /= p.splits;
+  t.tile = i % groups * p.pair;
+  i /= groups;
+  t.e = i % p.kv_heads;
+  t.b = i / p.kv_heads;
+  t.two = p.pair == 2 && t.tile + 1 < tiles;
+  t.len = keys_of(p, t.b);
+  const int64_t steps = (t.len + kRows - 1) / kRows;
+  t.step0 = static_cast<int>(steps * t.part / p.splits);
+  t.step1 = static_cast<int>(steps * (t.part + 1) / p.splits);
+  return t;
+}
+// First query and first head of a row tile.
+__device__ __forceinline__ void tile_at(const CrossParams& p, const Item& t, int u, int& n0, int& h0) {
+  const int tile = t.tile + u;
+  n0 = tile % p.tiles_n * p.box_n;
+  h0 = t.e * p.shared + tile / p.tiles_n * p.box_h;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) cross_dq_kernel(const __grid_constant__ CrossParams p) {
-  griddep_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
-  if (row >= static_cast<int64_t>(p.batch) * p.heads * p.n) return;
-  const int i = static_cast<int>(row % p.n);
-  const int h = static_cast<int>(row / p.n % p.heads), b = static_cast<int>(row / p.n / p.heads);
-  const int e = h / (p.heads / p.kv_heads), len = keys_of(p, b);
-  float q[4], d[4], o[4], dq[4] = {0.f, 0.f, 0.f, 0.f};
-  load4(row_of<T>(p.q, b, h, i), p.dim, q);
-  load4(row_of<T>(p.dout, b, h, i), p.dim, d);
-  load4(row_of<T>(p.o, b, h, i), p.dim, o);
-  const float delta = dot(d, o), lse = p.lse[row];
-  for (int j = 0; j < len; ++j) {
-    float k[4], v[4];
-    load4(row_of<T>(p.k, b, e, j), p.dim, k);
-    load4(row_of<T>(p.v, b, e, j), p.dim, v);
-    const float ds = expf(dot(q, k) * p.scale - lse) * (dot(d, v) - delta) * p.scale;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) dq[c] += ds * k[c];
+// The steps of a CTA's items, one after another; items without keys are left out.
+struct Walk {
+  int i, step;
+  Item t;
+  __device__ __forceinline__ bool open(const CrossParams& p) {
+    while (i < p.items) {
+      t = item_of(p, i);
+      step = t.step0;
+      if (t.step0 < t.step1) return true;
+      i += gridDim.x;
+    }
+    return false;
   }
-  store4(row_of<T>(p.dq, b, h, i), p.dim, dq);
+  __device__ __forceinline__ bool next(const CrossParams& p) {
+    if (++step < t.step1) return true;
+    i += gridDim.x;
+    return open(p);
+  }
+  __device__ __forceinline__ bool first() const { return step == t.step0; }
+  __device__ __forceinline__ bool last() const { return step + 1 == t.step1; }
+  // Keys of the step, in whole chunks of 16.
+  __device__ __forceinline__ int keys16() const {
+    return min((t.len - step * kRows + 15) / 16 * 16, kRows);
+  }
+};
+
+template <int DB>
+struct Layout {
+  static constexpr uint32_t kTile = DB * kBoxBytes;  // a row tile, or a key step
+  uint32_t q, kv;
+  Sync s;
+};
+
+template <int DB>
+__device__ void producer(const CrossParams& p, const Layout<DB>& l) {
+  LoadRing<kQTiles> qr;
+  LoadRing<kSteps> kr;
+  const Sync& s = l.s;
+  auto leave = [&] {
+    qr.drain(bar(s, B_QFULL));
+    kr.drain(bar(s, B_KVFULL));
+  };
+  auto load_q = [&](const Item& t, int u) {
+    if (!wait(s, bar(s, B_QEMPTY + qr.slot), qr.phase ^ 1u, kStatusTimeoutProducer)) return false;
+    int n0, h0;
+    tile_at(p, t, u, n0, h0);
+    const uint32_t full = bar(s, B_QFULL + qr.slot);
+    const uint32_t dst = l.q + qr.slot * Layout<DB>::kTile;
+    if (WSATTN_BOUNDS(p.status, n0 >= 0 && n0 < p.n && h0 >= 0 && h0 < p.heads && t.b < p.batch &&
+                                    p.box_n * p.box_h <= kRows)) {
+      mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.box_n * p.box_h) * 128u * DB);
+#pragma unroll
+      for (int c = 0; c < DB; ++c)
+        tma_load_4d(dst + c * kBoxBytes, &p.tm_q, full, c * 64, n0, h0 * p.q_h, t.b * p.q_b);
+    } else {
+      mbar_arrive(full);
+    }
+    qr.loaded();
+    return true;
+  };
+  auto load_kv = [&](const Item& t, int step, bool values) {
+    if (!wait(s, bar(s, B_KVEMPTY + kr.slot), kr.phase ^ 1u, kStatusTimeoutProducer)) return false;
+    const uint32_t full = bar(s, B_KVFULL + kr.slot);
+    const uint32_t dst = l.kv + kr.slot * Layout<DB>::kTile;
+    if (WSATTN_BOUNDS(p.status, step >= 0 && step * kRows < p.m && t.e < p.kv_heads &&
+                                    t.b < p.batch)) {
+      mbar_arrive_expect_tx(full, Layout<DB>::kTile);
+#pragma unroll
+      for (int c = 0; c < DB; ++c)
+        tma_load_4d(dst + c * kBoxBytes, values ? &p.tm_v : &p.tm_k, full, c * 64, step * kRows,
+                    t.e * (values ? p.v_h : p.k_h), t.b * (values ? p.v_b : p.k_b));
+    } else {
+      mbar_arrive(full);
+    }
+    kr.loaded();
+    return true;
+  };
+  Walk w{static_cast<int>(blockIdx.x), 0, {}};
+  for (bool on = w.open(p); on; on = w.next(p)) {
+    if (w.first() && !load_q(w.t, 0)) return leave();
+    if (!load_kv(w.t, w.step, false)) return leave();
+    if (w.first() && w.t.two && !load_q(w.t, 1)) return leave();
+    if (!load_kv(w.t, w.step, true)) return leave();
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) cross_dkv_kernel(const __grid_constant__ CrossParams p) {
-  griddep_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
-  if (row >= static_cast<int64_t>(p.batch) * p.kv_heads * p.m) return;
-  const int j = static_cast<int>(row % p.m);
-  const int e = static_cast<int>(row / p.m % p.kv_heads), b = static_cast<int>(row / p.m / p.kv_heads);
-  const int r = p.heads / p.kv_heads;
-  float k[4], v[4], dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  if (j < keys_of(p, b)) {
-    load4(row_of<T>(p.k, b, e, j), p.dim, k);
-    load4(row_of<T>(p.v, b, e, j), p.dim, v);
-    for (int h = e * r; h < e * r + r; ++h)
-      for (int i = 0; i < p.n; ++i) {
-        float q[4], d[4], o[4];
-        load4(row_of<T>(p.q, b, h, i), p.dim, q);
-        load4(row_of<T>(p.dout, b, h, i), p.dim, d);
-        load4(row_of<T>(p.o, b, h, i), p.dim, o);
-        const float w = expf(dot(q, k) * p.scale - p.lse[(static_cast<int64_t>(b) * p.heads + h) * p.n + i]);
-        const float ds = w * (dot(d, v) - dot(d, o)) * p.scale;
+template <bool BF16, int DB>
+__device__ void mma_issuer(const CrossParams& p, const Layout<DB>& l, uint32_t tbase) {
+  const Sync& s = l.s;
+  const int ksteps = p.dim / 16;
+  const uint32_t t_o = tbase, t_s = tbase + 2u * 64u * DB;
+  const uint32_t id_qk = idesc_16_f32(kRows, 0, BF16, false, false);  // N filled per step
+  const uint32_t id_pv = idesc_16_f32(kRows, p.dim, BF16, false, true);
+  const uint64_t q0 = sdesc_sw128(l.q, 16, 1024), k0 = sdesc_sw128(l.kv, 16, 1024);
+  const uint64_t v0 = sdesc_sw128(l.kv, kBoxBytes, 1024);
+  constexpr uint64_t kTile16 = Layout<DB>::kTile >> 4, kBox16 = kBoxBytes >> 4;
+  Ring<kQTiles> qr;
+  Ring<kSteps> kr;       // the next step to take: K and V in turn
+  uint32_t pphase = 0;   // bit u: parity of P_u's next use
+  uint32_t q_slot[2] = {0, 0};
+  auto wait_mma = [&](uint32_t b, uint32_t parity) {
+    return wait_warp(s, b, parity, kStatusTimeoutMma);
+  };
+  auto qk = [&](const Walk& w, int u, uint32_t kslot) {
+    if (w.first()) {
+      q_slot[u] = qr.slot;
+      if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return false;
+      qr.next();
+      tc_fence_after();
+    }
+    const uint32_t id = id_qk | (static_cast<uint32_t>(w.keys16()) >> 3) << 17;
+    const uint64_t a = q0 + q_slot[u] * kTile16, b = k0 + kslot * kTile16;
+    for (int kk = 0; kk < ksteps; ++kk) {
+      const uint64_t off = static_cast<uint64_t>(kk >> 2) * kBox16 + (kk & 3) * 2;
+      mma_ss_warp(t_s + u * kRows, a + off, b + off, id, kk > 0 ? 1u : 0u);
+    }
+    tc_commit_warp(bar(s, B_SFULL + u));
+    return true;
+  };
+  Walk cur{static_cast<int>(blockIdx.x), 0, {}};
+  bool on = cur.open(p);
+  if (!on) return;
+  if (!wait_mma(bar(s, B_KVFULL + kr.slot), kr.phase)) return;
+  tc_fence_after();
+  for (int u = 0; u < (cur.t.two ? 2 : 1); ++u)
+    if (!qk(cur, u, kr.slot)) return;
+  tc_commit_warp(bar(s, B_KVEMPTY + kr.slot));
+  kr.next();
+  while (on) {
+    Walk nxt = cur;
+    const bool more = nxt.next(p);
+    const Ring<kSteps> vr = kr;
+    kr.next();
+    const int units = cur.t.two ? 2 : 1, next_units = !more ? 0 : nxt.t.two ? 2 : 1;
+    const int chunks = cur.keys16() / 16;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          dk[c] += ds * q[c];
-          dv[c] += w * d[c];
+    for (int u = 0; u < 2; ++u) {
+      if (u < units) {
+        if (u == 0 && !wait_mma(bar(s, B_KVFULL + vr.slot), vr.phase)) return;
+        if (!wait_mma(bar(s, B_PFULL + u), pphase >> u & 1u)) return;
+        pphase ^= 1u << u;
+        tc_fence_after();
+        const uint64_t b = v0 + vr.slot * kTile16;
+        for (int kk = 0; kk < chunks; ++kk)  // 16 rows of V (2 KB), 8 columns of P
+          mma_ts_warp(t_o + u * 64 * DB, t_s + u * kRows + kk * 8, b + kk * 128, id_pv,
+                      kk > 0 || !cur.first() ? 1u : 0u);
+        if (cur.last()) tc_commit_warp(bar(s, B_OFULL + u));
+        if (u == units - 1) tc_commit_warp(bar(s, B_KVEMPTY + vr.slot));
+      }
+      if (u < next_units) {
+        if (u == 0) {
+          if (!wait_mma(bar(s, B_KVFULL + kr.slot), kr.phase)) return;
+          tc_fence_after();
+        }
+        if (!qk(nxt, u, kr.slot)) return;
+        if (u == next_units - 1) tc_commit_warp(bar(s, B_KVEMPTY + kr.slot));
+      }
+    }
+    if (more) kr.next();
+    cur = nxt;
+    on = more;
+  }
+}
+
+// P of 16 logits: their exponentials 2^(s c + nb), added to the packed row sums,
+// rounded to pairs and stored as eight columns.
+template <bool BF16>
+__device__ __forceinline__ void exp_store(const uint32_t (&sv)[16], uint64_t c2, uint64_t nb2,
+                                          uint64_t& la, uint64_t& lb, uint32_t taddr) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 t = f2_unpack(
+        f2_fma(f2_pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, nb2));
+    const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
+    if (i & 1) lb = f2_add(lb, f2_pack(p0, p1));
+    else la = f2_add(la, f2_pack(p0, p1));
+    w[i] = pack_pair(p0, p1, typename Elem<BF16>::type());
+  }
+  tmem_st8(taddr, w);
+}
+
+template <bool BF16, int DB>
+__device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbase) {
+  const Sync& s = l.s;
+  const int warp = threadIdx.x / 32, u = (warp - 4) / 4, wq = warp & 3;
+  const int r = wq * 32 + (threadIdx.x & 31);
+  const uint32_t lane = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+  const uint32_t t_o = lane + u * 64 * DB, t_s = lane + 2 * 64 * DB + u * kRows;
+  const float c = p.scale_log2;
+  const uint64_t c2 = f2_pack(c, c);
+  const int dim16 = p.dim / 16;
+  auto wait_s = [&](uint32_t b, uint32_t parity) {
+    return wait_warp(s, b, parity, kStatusTimeoutSoftmax);
+  };
+  Ring<kQTiles> qr;            // row tiles of both warpgroups, in order
+  Ring<kSteps> kr;             // key and value steps, in order
+  uint32_t sphase = 0, ophase = 0;
+  for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+    const Item t = item_of(p, i);
+    const bool mine = u == 0 || t.two, any = t.step0 < t.step1;
+    uint32_t q_slot = qr.slot;
+    if (any) {
+      qr.next();
+      if (t.two) {
+        if (u == 1) q_slot = qr.slot;
+        qr.next();
+      }
+    }
+    if (!mine) {
+      for (int j = t.step0; j < t.step1; ++j) {
+        kr.next();
+        kr.next();
+      }
+      continue;
+    }
+    float m = -INFINITY, sum = 0.f;
+    for (int j = t.step0; j < t.step1; ++j) {
+      const int rem = t.len - j * kRows;  // keys from here on
+      kr.next();
+      const Ring<kSteps> vr = kr;
+      kr.next();
+      if (!wait_s(bar(s, B_SFULL + u), sphase)) return;
+      sphase ^= 1u;
+      tc_fence_after();
+      uint32_t sv[8][16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) tmem_ld16(t_s + 16 * k, sv[k]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) reg_fence16(sv[k]);
+      const int chunks = rem >= kRows ? 8 : (rem + 15) / 16;
+      if (rem < kRows) {
+        // behind the length: no probability, and (up to the chunk's end, where
+        // the product reads on) no value, whatever lies there
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            if (16 * k + x >= rem) sv[k][x] = 0xff800000u;
+        if (u == 0 && (rem & 15)) {
+          if (!wait_s(bar(s, B_KVFULL + vr.slot), vr.phase)) return;
+          const uint32_t v = l.kv + vr.slot * Layout<DB>::kTile;
+          for (int x = r; x < (16 * chunks - rem) * 8 * DB; x += kRows)
+            st_shared_v4(swizzled(v, rem + x / (8 * DB), x % (8 * DB)), 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
         }
       }
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(sv[k][x]));
+      const float m_top = fmaxf(m, top * c);
+      const float m_new = m_top > m + kLazyMax ? m_top : m;
+      const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+      const float nb = m_new == -INFINITY ? 0.f : -m_new;
+      const uint64_t nb2 = f2_pack(nb, nb);
+      uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < chunks) exp_store<BF16>(sv[k], c2, nb2, la, lb, t_s + 8 * k);
+      const float2 ab = f2_unpack(f2_add(la, lb));
+      sum = sum * alpha + (ab.x + ab.y);
+      m = m_new;
+      // S_u of this step comes behind the last step's product: O_u is complete
+      if (j > t.step0 && __any_sync(0xffffffffu, alpha < 1.f)) {
+        const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+        for (int k = 0; k < dim16; ++k) {
+          uint32_t o[16];
+          tmem_ld16(t_o + 16 * k, o);
+          tmem_wait_ld16(o);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float2 v = f2_unpack(
+                f2_mul(f2_pack(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1])), a2));
+            o[2 * x] = __float_as_uint(v.x);
+            o[2 * x + 1] = __float_as_uint(v.y);
+          }
+          tmem_st16(t_o + 16 * k, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar(s, B_PFULL + u));
+    }
+
+    // where this thread's row goes
+    int n0, h0;
+    tile_at(p, t, u, n0, h0);
+    const int n = n0 + r % p.box_n, h = h0 + r / p.box_n;
+    const bool valid = r < p.box_n * p.box_h && n < p.n && h < (t.e + 1) * p.shared &&
+                       WSATTN_BOUNDS(p.status, n >= 0 && h < p.heads && t.b < p.batch);
+    const int64_t row = (static_cast<int64_t>(t.b) * p.heads + h) * p.n + n;
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
+    const float log2_sum = any ? m + log2f(sum) : -INFINITY;
+    if (valid) {
+      if (p.splits > 1) p.part_l[t.part * rows + row] = log2_sum;
+      else if (p.lse) p.lse[row] = log2_sum * kLn2;
+    }
+    using E = typename Elem<BF16>::type;
+    E* out = static_cast<E*>(const_cast<void*>(p.o.data)) + t.b * p.o.sb + h * p.o.sh + n * p.o.sn;
+    if (!any) {
+      if (valid && p.splits == 1)
+        for (int k = 0; k < 2 * dim16; ++k)
+          reinterpret_cast<uint4*>(out)[k] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    if (!wait_s(bar(s, B_OFULL + u), ophase)) return;
+    ophase ^= 1u;
+    tc_fence_after();
+    const float inv = 1.f / sum;
+    const bool whole = p.splits == 1 && p.box_h == 1;  // rows of one head: by TMA
+    const uint32_t tile = l.q + q_slot * Layout<DB>::kTile;
+#pragma unroll 1
+    for (int k = 0; k < dim16; ++k) {
+      uint32_t o[16];
+      tmem_ld16(t_o + 16 * k, o);
+      tmem_wait_ld16(o);
+      if (p.splits > 1) {
+        if (valid) {
+          float4* to = reinterpret_cast<float4*>(p.part_o + (t.part * rows + row) * p.dim + 16 * k);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            to[x] = make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
+                                __uint_as_float(o[4 * x + 2]) * inv,
+                                __uint_as_float(o[4 * x + 3]) * inv);
+        }
+        continue;
+      }
+      uint32_t w[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        w[x] = pack_pair(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv, E());
+      if (whole) {
+        st_shared_v4(swizzled(tile, r, 2 * k), w[0], w[1], w[2], w[3]);
+        st_shared_v4(swizzled(tile, r, 2 * k + 1), w[4], w[5], w[6], w[7]);
+      } else if (valid) {
+        reinterpret_cast<uint4*>(out)[2 * k] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(out)[2 * k + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+    tc_fence_before();
+    if (whole) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0 && n0 + 32 * wq < p.n) {
+        for (int k = 0; 4 * k < dim16; ++k)
+          tma_store_4d(&p.tm_o, tile + k * kBoxBytes + wq * 4096u, 64 * k, n0 + 32 * wq, h0, t.b);
+        bulk_commit_group();
+        bulk_wait_read_all();
+      }
+    }
+    warp_arrive(bar(s, B_QEMPTY + q_slot));
   }
-  if (p.dk.data) store4(row_of<T>(p.dk, b, e, j), p.dim, dk);
-  if (p.dv.data) store4(row_of<T>(p.dv, b, e, j), p.dim, dv);
 }
 
-template <typename F>
-cudaError_t by_rows(F* kernel, const CrossParams& p, int64_t rows, cudaStream_t s) {
-  return launch_dependent(kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, p);
+template <bool BF16, int DB>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_forward_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  Layout<DB> l;
+  l.q = base;
+  l.kv = base + kQTiles * Layout<DB>::kTile;
+  l.s.bars = l.kv + kSteps * Layout<DB>::kTile;
+  uint8_t* gb = smem_raw + (l.s.bars - raw);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * B_COUNT);
+  l.s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  l.s.status = p.status;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kQTiles; ++i) {
+      mbar_init(bar(l.s, B_QFULL + i), 1);
+      mbar_init(bar(l.s, B_QEMPTY + i), 4);
+    }
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(bar(l.s, B_KVFULL + i), 1);
+      mbar_init(bar(l.s, B_KVEMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(l.s, B_SFULL + i), 1);
+      mbar_init(bar(l.s, B_PFULL + i), 4);
+      mbar_init(bar(l.s, B_OFULL + i), 1);
+    }
+    *l.s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&p.tm_q);
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+    prefetch_tensormap(&p.tm_o);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tslot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  griddep_wait();
+  if (warp == 0) {
+    if (lane == 0) producer<DB>(p, l);
+  } else if (warp == 1) {
+    mma_issuer<BF16, DB>(p, l, tbase);
+  } else if (warp >= 4) {
+    softmax<BF16, DB>(p, l, tbase);
+    if (lane == 0) bulk_wait_all();  // the stores must be complete before the CTA leaves
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+}
+
+// Joins the parts of the keys: a warp a row.  Each part's row is weighted by
+// its share of the sum, 2^(l_s - max) / sum of them.
+template <bool BF16>
+__global__ void __launch_bounds__(128) cross_join_kernel(const __grid_constant__ CrossParams p) {
+  using E = typename Elem<BF16>::type;
+  griddep_wait();
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  for (int i = lane; i < p.splits; i += 32) top = fmaxf(top, p.part_l[i * rows + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  const int c = 4 * lane;
+  for (int i = 0; i < p.splits; ++i) {
+    const float l = p.part_l[i * rows + row];
+    if (l == -INFINITY) continue;  // no keys: nothing was written
+    const float w = ex2_approx(l - base);
+    sum += w;
+    if (c < p.dim) {
+      const float4 o = *reinterpret_cast<const float4*>(p.part_o + (i * rows + row) * p.dim + c);
+      v[0] = fmaf(w, o.x, v[0]);
+      v[1] = fmaf(w, o.y, v[1]);
+      v[2] = fmaf(w, o.z, v[2]);
+      v[3] = fmaf(w, o.w, v[3]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int n = static_cast<int>(row % p.n);
+  const int64_t bh = row / p.n;
+  const int h = static_cast<int>(bh % p.heads), b = static_cast<int>(bh / p.heads);
+  E* out = static_cast<E*>(const_cast<void*>(p.o.data)) + b * p.o.sb + h * p.o.sh + n * p.o.sn;
+  if (c < p.dim)
+    *reinterpret_cast<uint2*>(out + c) =
+        make_uint2(pack_pair(v[0] * inv, v[1] * inv, E()), pack_pair(v[2] * inv, v[3] * inv, E()));
+  if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+}
+
+template <bool BF16, int DB>
+cudaError_t forward(const CrossParams& p, int sms, cudaStream_t s) {
+  static bool attr_set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  constexpr size_t kSmem = 1024 + (kQTiles + kSteps) * Layout<DB>::kTile + 8 * B_COUNT + 16;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+  if (!attr_set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(cross_forward_kernel<BF16, DB>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaError_t e = launch_dependent(cross_forward_kernel<BF16, DB>,
+                                   dim3(p.items < sms ? p.items : sms), dim3(kThreads), kSmem, s, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
+  return launch_dependent(cross_join_kernel<BF16>, dim3(static_cast<unsigned>((rows + 3) / 4)),
+                          dim3(128), 0, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_forward(const CrossParams& p, int dtype, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
-  return dtype == WSATTN_BF16 ? by_rows(cross_forward_kernel<__nv_bfloat16>, p, rows, s)
-                              : by_rows(cross_forward_kernel<__half>, p, rows, s);
+// Row tiles of 128 queries of a head; with fewer queries, of as many heads of
+// one key head as fit (heads of their own: a broadcast one has one row to load).  A CTA takes about kStep cycles for a key step with one
+// row tile or two, kItem for an item's beginning and end, and joining parts
+// costs about kJoin: the pair and the number of parts that make the least of it
+// (a machine of 152 SMs whatever the device has, so that the workspace's size
+// needs no device).
+void split_cross(CrossParams* p) {
+  constexpr double kStep[2] = {2300, 2500}, kItem = 4000, kJoin = 7000;
+  p->shared = p->heads / p->kv_heads;
+  p->box_n = kCrossRows;
+  p->box_h = 1;
+  if (p->n < kCrossRows && p->shared > 1 && p->q.sh > 0) {
+    p->box_n = p->n;
+    p->box_h = kCrossRows / p->n < p->shared ? kCrossRows / p->n : p->shared;
+  }
+  p->tiles_n = (p->n + p->box_n - 1) / p->box_n;
+  p->tiles_h = (p->shared + p->box_h - 1) / p->box_h;
+  const int64_t tiles = static_cast<int64_t>(p->tiles_n) * p->tiles_h;
+  const int64_t heads = static_cast<int64_t>(p->batch) * p->kv_heads;
+  const int64_t steps = (p->m + kCrossRows - 1) / kCrossRows;
+  double best = 0.0;
+  p->pair = 1;
+  p->splits = 1;
+  for (int pair = 1; pair <= (tiles > 1 ? 2 : 1); ++pair) {
+    const int64_t items = heads * ((tiles + pair - 1) / pair);
+    for (int64_t s = 1; s == 1 || (s <= steps && items * s <= kTilingSms); ++s) {
+      const int64_t rounds = (items * s + kTilingSms - 1) / kTilingSms;
+      const double t = static_cast<double>(rounds) *
+                           (kItem + kStep[pair - 1] * static_cast<double>((steps + s - 1) / s)) +
+                       (s > 1 ? kJoin : 0.0);
+      if (best == 0.0 || t < best) {
+        best = t;
+        p->pair = pair;
+        p->splits = static_cast<int>(s);
+      }
+    }
+  }
+  const int64_t items = heads * ((tiles + p->pair - 1) / p->pair) * p->splits;
+  p->items = items <= INT32_MAX ? static_cast<int>(items) : -1;
 }
 
-cudaError_t launch_cross_backward(const CrossParams& p, int dtype, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
-  const int64_t keys = static_cast<int64_t>(p.batch) * p.kv_heads * p.m;
-  cudaError_t e = cudaSuccess;
-  if (p.dq.data && rows)
-    e = dtype == WSATTN_BF16 ? by_rows(cross_dq_kernel<__nv_bfloat16>, p, rows, s)
-                             : by_rows(cross_dq_kernel<__half>, p, rows, s);
-  if (e != cudaSuccess || !keys || (!p.dk.data && !p.dv.data)) return e;
-  return dtype == WSATTN_BF16 ? by_rows(cross_dkv_kernel<__nv_bfloat16>, p, keys, s)
-                              : by_rows(cross_dkv_kernel<__half>, p, keys, s);
+// fp32 rows first, then their sums.
+size_t cross_partial_bytes(const CrossParams& p) {
+  if (p.splits < 2) return 0;
+  const size_t rows = static_cast<size_t>(p.batch) * p.heads * p.n;
+  return rows * p.splits * (static_cast<size_t>(p.dim) + 1) * sizeof(float);
+}
+
+cudaError_t launch_cross_forward(const CrossParams& p, int dtype, int sms, cudaStream_t s) {
+  if (dtype == WSATTN_BF16) return p.dim <= 64 ? forward<true, 1>(p, sms, s) : forward<true, 2>(p, sms, s);
+  return p.dim <= 64 ? forward<false, 1>(p, sms, s) : forward<false, 2>(p, sms, s);
 }
 
 }  // namespace wsattn

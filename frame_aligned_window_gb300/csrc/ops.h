@@ -259,16 +259,34 @@ struct CrossView {
   int64_t sb, sh, sn;
 };
 struct CrossParams {
+  CUtensorMap tm_q;                    // {D, n, heads, batch}, box {64, box_n, box_h, 1}
+  CUtensorMap tm_k, tm_v;              // {D, m, kv heads, batch}, box {64, 128, 1, 1}
+  CUtensorMap tm_o;                    // {D, n, heads, batch}, box {64, 32, 1, 1}
   CrossView q, k, v, o, dout;          // o: the forward's output (written, or read by the backward)
   CrossView dq, dk, dv;
   const int32_t* lengths;              // [batch] keys that count, or null: all
   float* lse;                          // [batch, heads, n] or null
   int batch, heads, kv_heads, dim;
   int n, m;                            // queries, keys
+  int shared;                          // query heads of a key head
+  // a tensor map's coordinate of a broadcast dimension (stride 0) is 0
+  int k_h, k_b, v_h, v_b, q_h, q_b;
   float scale, scale_log2;
+  // work split
+  int box_n, box_h;                    // a row tile: box_h heads of box_n queries
+  int tiles_n, tiles_h;                // row tiles of a key head
+  int pair;                            // row tiles of a work item (1 or 2)
+  int splits;                          // parts of the keys
+  int items;
+  float* part_o;                       // [splits][batch, heads, n][D] (splits > 1)
+  float* part_l;                       // [splits][batch, heads, n] log2 of the sums
   int* status;
 };
-cudaError_t launch_cross_forward(const CrossParams& p, int dtype, cudaStream_t s);
+constexpr int kCrossRows = 128;  // of a row tile and of a key step
+// Row tiles, pairs and splits of a shape.
+void split_cross(CrossParams* p);
+size_t cross_partial_bytes(const CrossParams& p);
+cudaError_t launch_cross_forward(const CrossParams& p, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_cross_backward(const CrossParams& p, int dtype, cudaStream_t s);
 
 }  // namespace wsattn
