@@ -88,6 +88,19 @@ void fill_common(const A* a, CrossParams* p) {
   p->scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634074);
 }
 
+// delta, where the dk, dv kernel needs it, and the sums of shared key tiles.
+struct GradScratch {
+  size_t delta, part;
+  size_t total() const { return delta + part; }
+};
+GradScratch grad_scratch(const wsattn_cross_grad_args* a, const CrossParams& p) {
+  GradScratch s{0, 0};
+  if ((!a->dk.data && !a->dv.data) || p.batch == 0 || p.n == 0 || p.m == 0) return s;
+  s.delta = up256(sizeof(float) * static_cast<size_t>(p.batch) * p.heads * p.n);
+  s.part = sizeof(float) * static_cast<size_t>(p.ctas) * 4 * wsattn::kCrossRows * p.dim;
+  return s;
+}
+
 }  // namespace
 
 extern "C" {
@@ -144,11 +157,16 @@ int wsattn_cross(const wsattn_cross_args* a, void* workspace, size_t workspace_b
 int wsattn_cross_backward_workspace(const wsattn_cross_grad_args* a, size_t* bytes) {
   if (!bytes || !sizes_ok(a)) return WSATTN_ERR_BAD_ARG;
   if (!supported(a)) return WSATTN_ERR_UNSUPPORTED;
-  *bytes = 0;
+  CrossParams p;
+  fill_common(a, &p);
+  p.dout = view(&a->dout);
+  wsattn::split_cross_backward(&p);
+  *bytes = grad_scratch(a, p).total();
   return WSATTN_OK;
 }
 
-int wsattn_cross_backward(const wsattn_cross_grad_args* a, void*, size_t, void* stream) {
+int wsattn_cross_backward(const wsattn_cross_grad_args* a, void* workspace, size_t workspace_bytes,
+                          void* stream) {
   if (!sizes_ok(a)) return WSATTN_ERR_BAD_ARG;
   if (!supported(a)) return WSATTN_ERR_UNSUPPORTED;
   const int64_t n = a->n_tokens, m = a->n_keys;
@@ -171,9 +189,27 @@ int wsattn_cross_backward(const wsattn_cross_grad_args* a, void*, size_t, void* 
   p.dq = view(&a->dq);
   p.dk = view(&a->dk);
   p.dv = view(&a->dv);
+  wsattn::split_cross_backward(&p);
+  const int64_t key_tiles = static_cast<int64_t>(b) * e * cdiv(m, wsattn::kCrossRows);
+  if (p.items < 0 || key_tiles > INT32_MAX) return WSATTN_ERR_BAD_ARG;
+  const GradScratch need = grad_scratch(a, p);
+  if (need.total() && (!workspace || !aligned16(workspace) || workspace_bytes < need.total()))
+    return WSATTN_ERR_BAD_ARG;
+  char* ws = static_cast<char*>(workspace);
+  p.delta = need.delta ? reinterpret_cast<float*>(ws) : nullptr;
+  p.part_kv = need.part ? reinterpret_cast<float*>(ws + need.delta) : nullptr;
   p.status = wsattn::op_status_ptr();
-  if (!p.status) return WSATTN_ERR_CUDA;
-  return wsattn::launch_cross_backward(p, a->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  const int sms = sm_count();
+  if (!p.status || !sms) return WSATTN_ERR_CUDA;
+  const int d = a->head_dim, rows = wsattn::kCrossRows;
+  if ((n && (!encode(&p.tm_q, a->dtype, &a->q, d, b, n, p.box_n, p.box_h, &p.q_h, &p.q_b) ||
+             !encode(&p.tm_do, a->dtype, &a->dout, d, b, n, p.box_n, p.box_h, &p.do_h, &p.do_b))) ||
+      (n && p.dq.data && !encode(&p.tm_dq, a->dtype, &a->dq, d, b, n, 32, 1)) ||
+      (n && m && (!encode(&p.tm_k, a->dtype, &a->k, d, b, m, rows, 1, &p.k_h, &p.k_b) ||
+                  !encode(&p.tm_v, a->dtype, &a->v, d, b, m, rows, 1, &p.v_h, &p.v_b))))
+    return WSATTN_ERR_CUDA;
+  return wsattn::launch_cross_backward(p, a->dtype, sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? WSATTN_OK
              : WSATTN_ERR_CUDA;
 }

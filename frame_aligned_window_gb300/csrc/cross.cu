@@ -372,7 +372,7 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
     int n0, h0;
     tile_at(p, t, u, n0, h0);
     const int n = n0 + r % p.box_n, h = h0 + r / p.box_n;
-    const bool valid = r < p.box_n * p.box_h && n < p.n && h < (t.e + 1) * p.shared &&
+    const bool valid = r < p.box_n * p.box_h && n < p.n &&
                        WSATTN_BOUNDS(p.status, n >= 0 && h < p.heads && t.b < p.batch);
     const int64_t row = (static_cast<int64_t>(t.b) * p.heads + h) * p.n + n;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
@@ -573,9 +573,11 @@ void split_cross(CrossParams* p) {
   p->shared = p->heads / p->kv_heads;
   p->box_n = kCrossRows;
   p->box_h = 1;
-  if (p->n < kCrossRows && p->shared > 1 && p->q.sh > 0) {
+  if (p->n > 0 && p->n < kCrossRows && p->shared > 1 && p->q.sh > 0 &&
+      (!p->dout.data || p->dout.sh > 0)) {
     p->box_n = p->n;
     p->box_h = kCrossRows / p->n < p->shared ? kCrossRows / p->n : p->shared;
+    while (p->shared % p->box_h) --p->box_h;  // no tile reaches into another key head's
   }
   p->tiles_n = (p->n + p->box_n - 1) / p->box_n;
   p->tiles_h = (p->shared + p->box_h - 1) / p->box_h;

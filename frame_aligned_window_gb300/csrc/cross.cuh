@@ -23,7 +23,7 @@ struct Sync {
 __device__ __forceinline__ uint32_t bar(const Sync& s, int i) {
   return s.bars + 8u * static_cast<uint32_t>(i);
 }
-__device__ __noinline__ bool wait_slow(const Sync& s, uint32_t b, uint32_t parity, int code) {
+static __device__ __noinline__ bool wait_slow(const Sync& s, uint32_t b, uint32_t parity, int code) {
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(b, parity)) return true;

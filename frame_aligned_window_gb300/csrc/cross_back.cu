@@ -1,116 +1,1090 @@
-// Gradients of the attention to an encoder's states.  A warp takes a query, or
-// a key.
-#include "epilogue.cuh"
+// Gradients of the attention to an encoder's states for sm_103a, with
+//   p_ij = exp(scale q_i . k_j - lse_i),  delta_i = dout_i . out_i,
+//   ds_ij = p_ij (dout_i . v_j - delta_i):
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
+//
+// Two kernels, each with the sums of its own gradient in tensor memory: one
+// holds a row tile of 128 queries and walks the keys (dq, and delta on the
+// way), one holds a tile of 128 keys and walks the queries of all heads that
+// share it (dk, dv).  p and ds are formed in both: seven matrix products
+// instead of five, but no sum leaves the chip before it is complete (dq summed
+// over key tiles elsewhere would be fp32 traffic of 4 D bytes per query and key
+// tile), and none depends on the order in which CTAs finish.
+#include "cross.cuh"
 
 namespace wsattn {
 namespace {
 
-using namespace ptx;
+using namespace cross;
 
-template <typename T>
-__device__ __forceinline__ const T* row_of(const CrossView& v, int64_t b, int64_t h, int64_t i) {
-  return static_cast<const T*>(v.data) + b * v.sb + h * v.sh + i * v.sn;
+constexpr int kThreads = 384;
+constexpr int kEltWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Chunks of 16 columns that warpgroup w of two takes of n: the first takes the
+// larger half.
+__device__ __forceinline__ void share_of(int n, int w, int& first, int& count) {
+  first = w ? (n + 1) / 2 : 0;
+  count = w ? n / 2 : (n + 1) / 2;
 }
-__device__ __forceinline__ int keys_of(const CrossParams& p, int b) {
-  return p.lengths ? max(0, min(p.lengths[b], p.m)) : p.m;
+
+// Where chunk k of n lies once it is rounded to pairs (8 columns): each
+// warpgroup writes over its own part of what it read, so neither waits for the
+// other.
+__device__ __forceinline__ uint32_t chunk_at(int k, int n) {
+  const int c = (n + 1) / 2;
+  return static_cast<uint32_t>(k < c ? 8 * k : 16 * c + 8 * (k - c));
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int dim, float (&f)[4]) {
+
+// Adds the products of eight pairs of elements, in order.
+template <typename E>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = 32 * i + (threadIdx.x & 31);
-    f[i] = c < dim ? to_f32(p[c]) : 0.f;
+    const float2 u = unpack_pair(x[i], E()), v = unpack_pair(y[i], E());
+    sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
   }
-}
-template <typename T>
-__device__ __forceinline__ void store4(const T* p, int dim, const float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 32 * i + (threadIdx.x & 31);
-    if (c < dim) const_cast<T*>(p)[c] = from_f32<T>(f[i]);
-  }
-}
-__device__ __forceinline__ float dot(const float (&a)[4], const float (&b)[4]) {
-  return warp_sum(a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]);
+  return sum;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) cross_dq_kernel(const __grid_constant__ CrossParams p) {
-  griddep_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
-  if (row >= static_cast<int64_t>(p.batch) * p.heads * p.n) return;
-  const int i = static_cast<int>(row % p.n);
-  const int h = static_cast<int>(row / p.n % p.heads), b = static_cast<int>(row / p.n / p.heads);
-  const int e = h / (p.heads / p.kv_heads), len = keys_of(p, b);
-  float q[4], d[4], o[4], dq[4] = {0.f, 0.f, 0.f, 0.f};
-  load4(row_of<T>(p.q, b, h, i), p.dim, q);
-  load4(row_of<T>(p.dout, b, h, i), p.dim, d);
-  load4(row_of<T>(p.o, b, h, i), p.dim, o);
-  const float delta = dot(d, o), lse = p.lse[row];
-  for (int j = 0; j < len; ++j) {
-    float k[4], v[4];
-    load4(row_of<T>(p.k, b, e, j), p.dim, k);
-    load4(row_of<T>(p.v, b, e, j), p.dim, v);
-    const float ds = expf(dot(q, k) * p.scale - lse) * (dot(d, v) - delta) * p.scale;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) dq[c] += ds * k[c];
-  }
-  store4(row_of<T>(p.dq, b, h, i), p.dim, dq);
+// Row r of a row tile: its query and head, and its index in [batch, heads, n].
+struct RowAt {
+  int n, h;
+  int64_t index;
+  bool valid;
+};
+__device__ __forceinline__ RowAt row_at(const CrossParams& p, int b, int n0, int h0, int r) {
+  RowAt x;
+  x.n = n0 + r % p.box_n;
+  x.h = h0 + r / p.box_n;
+  x.valid = r < p.box_n * p.box_h && x.n < p.n;
+  x.index = (static_cast<int64_t>(b) * p.heads + x.h) * p.n + x.n;
+  return x;
+}
+// First query and first head of row tile i of key head e.
+__device__ __forceinline__ void tile_at(const CrossParams& p, int e, int i, int& n0, int& h0) {
+  n0 = i % p.tiles_n * p.box_n;
+  h0 = e * p.shared + i / p.tiles_n * p.box_h;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) cross_dkv_kernel(const __grid_constant__ CrossParams p) {
-  griddep_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
-  if (row >= static_cast<int64_t>(p.batch) * p.kv_heads * p.m) return;
-  const int j = static_cast<int>(row % p.m);
-  const int e = static_cast<int>(row / p.m % p.kv_heads), b = static_cast<int>(row / p.m / p.kv_heads);
-  const int r = p.heads / p.kv_heads;
-  float k[4], v[4], dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  if (j < keys_of(p, b)) {
-    load4(row_of<T>(p.k, b, e, j), p.dim, k);
-    load4(row_of<T>(p.v, b, e, j), p.dim, v);
-    for (int h = e * r; h < e * r + r; ++h)
-      for (int i = 0; i < p.n; ++i) {
-        float q[4], d[4], o[4];
-        load4(row_of<T>(p.q, b, h, i), p.dim, q);
-        load4(row_of<T>(p.dout, b, h, i), p.dim, d);
-        load4(row_of<T>(p.o, b, h, i), p.dim, o);
-        const float w = expf(dot(q, k) * p.scale - p.lse[(static_cast<int64_t>(b) * p.heads + h) * p.n + i]);
-        const float ds = w * (dot(d, v) - dot(d, o)) * p.scale;
+// ------------------------------------------------------------- dq
+// Tensor memory: dQ [0, 128), S [128, 256), dP [256, 384), Q [384, 448),
+// dO [448, 512) (pairs).  dS takes dP's place.
+//   warp 0     TMA: q and dout of a row tile, key and value steps (a ring)
+//   warp 1     MMA: S = Q K^T, dP = dO V^T, dQ += dS K
+//   warps 4-11 two warpgroups: thread = row, each half of a step's columns.
+//              The first copies Q to tensor memory, the second dO (and forms
+//              delta from it)
+// S of the next step is written as soon as both warpgroups hold this one's in
+// registers, and p is formed while dP is on its way.
+enum : int {
+  A_QFULL = 0,   // TMA -> elements: q and dout staged
+  A_QEMPTY,      // elements -> TMA
+  A_TFULL,       // elements -> MMA: Q and dO in tensor memory
+  A_SFULL,       // MMA -> elements
+  A_SEMPTY,      // elements -> MMA: S is in registers
+  A_PFULL,       // MMA -> elements: dP written
+  A_DSFULL,      // elements -> MMA: dS written
+  A_OFULL,       // MMA -> elements: the tile's dQ is complete
+  A_XCH,         // the two warpgroups: delta exchanged
+  A_KVFULL,
+  A_KVEMPTY = A_KVFULL + 4,
+  A_COUNT = A_KVEMPTY + 4
+};
+constexpr int kSteps = 4;
+constexpr uint32_t kTdq = 0, kTs = 128, kTdp = 256, kTq = 384, kTdo = 448;
+
+template <int DB>
+struct LayoutA {
+  static constexpr uint32_t kTile = DB * kBoxBytes;
+  uint32_t q, dout, out, kv;
+  float* delta;  // [128]
+  Sync s;
+};
+
+// Row tiles of a CTA, and their key steps.
+struct TileA {
+  int b, e, tile, len, steps;
+};
+__device__ __forceinline__ TileA tile_a(const CrossParams& p, int i) {
+  TileA t;
+  const int tiles = p.tiles_n * p.tiles_h;
+  t.tile = i % tiles;
+  i /= tiles;
+  t.e = i % p.kv_heads;
+  t.b = i / p.kv_heads;
+  t.len = keys_of(p, t.b);
+  t.steps = (t.len + kRows - 1) / kRows;
+  return t;
+}
+
+template <int DB>
+__device__ void dq_producer(const CrossParams& p, const LayoutA<DB>& l) {
+  LoadRing<1> qr;
+  LoadRing<kSteps> kr;
+  const Sync& s = l.s;
+  auto leave = [&] {
+    qr.drain(bar(s, A_QFULL));
+    kr.drain(bar(s, A_KVFULL));
+  };
+  for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+    const TileA t = tile_a(p, i);
+    if (!t.steps) continue;
+    int n0, h0;
+    tile_at(p, t.e, t.tile, n0, h0);
+    if (!wait(s, bar(s, A_QEMPTY), qr.phase ^ 1u, kStatusTimeoutProducer)) return leave();
+    if (WSATTN_BOUNDS(p.status, n0 < p.n && h0 < p.heads && t.b < p.batch)) {
+      mbar_arrive_expect_tx(bar(s, A_QFULL), 2u * static_cast<uint32_t>(p.box_n * p.box_h) * 128u * DB);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          dk[c] += ds * q[c];
-          dv[c] += w * d[c];
+      for (int c = 0; c < DB; ++c) {
+        tma_load_4d(l.q + c * kBoxBytes, &p.tm_q, bar(s, A_QFULL), c * 64, n0, h0 * p.q_h, t.b * p.q_b);
+        tma_load_4d(l.dout + c * kBoxBytes, &p.tm_do, bar(s, A_QFULL), c * 64, n0, h0 * p.do_h,
+                    t.b * p.do_b);
+      }
+    } else {
+      mbar_arrive(bar(s, A_QFULL));
+    }
+    qr.loaded();
+    for (int j = 0; j < 2 * t.steps; ++j) {
+      const bool values = j & 1;
+      if (!wait(s, bar(s, A_KVEMPTY + kr.slot), kr.phase ^ 1u, kStatusTimeoutProducer)) return leave();
+      const uint32_t full = bar(s, A_KVFULL + kr.slot), dst = l.kv + kr.slot * LayoutA<DB>::kTile;
+      if (WSATTN_BOUNDS(p.status, (j >> 1) * kRows < p.m && t.e < p.kv_heads)) {
+        mbar_arrive_expect_tx(full, LayoutA<DB>::kTile);
+#pragma unroll
+        for (int c = 0; c < DB; ++c)
+          tma_load_4d(dst + c * kBoxBytes, values ? &p.tm_v : &p.tm_k, full, c * 64, (j >> 1) * kRows,
+                      t.e * (values ? p.v_h : p.k_h), t.b * (values ? p.v_b : p.k_b));
+      } else {
+        mbar_arrive(full);
+      }
+      kr.loaded();
+    }
+  }
+}
+
+template <bool BF16, int DB>
+__device__ void dq_issuer(const CrossParams& p, const LayoutA<DB>& l, uint32_t tbase) {
+  const Sync& s = l.s;
+  const int ksteps = p.dim / 16;
+  const uint32_t id_s = idesc_16_f32(kRows, 0, BF16, false, false);
+  const uint32_t id_dq = idesc_16_f32(kRows, p.dim, BF16, false, true);
+  const uint64_t k0 = sdesc_sw128(l.kv, 16, 1024), kt0 = sdesc_sw128(l.kv, kBoxBytes, 1024);
+  constexpr uint64_t kTile16 = LayoutA<DB>::kTile >> 4, kBox16 = kBoxBytes >> 4;
+  auto wait_mma = [&](uint32_t b, uint32_t parity) {
+    const bool ok = wait_warp(s, b, parity, kStatusTimeoutMma);
+    tc_fence_after();
+    return ok;
+  };
+  Ring<1> tr, sr, dr;   // Q and dO, S, dS
+  Ring<kSteps> kr;      // next step of S
+  // S or dP of a step: A in tensor memory, N keys
+  auto rows_by_keys = [&](uint32_t d, uint32_t a, uint32_t slot, int keys16) {
+    const uint32_t id = id_s | (static_cast<uint32_t>(keys16) >> 3) << 17;
+    const uint64_t b = k0 + slot * kTile16;
+    for (int kk = 0; kk < ksteps; ++kk)
+      mma_ts_warp(tbase + d, tbase + a + kk * 8, b + static_cast<uint64_t>(kk >> 2) * kBox16 + (kk & 3) * 2,
+                  id, kk > 0 ? 1u : 0u);
+  };
+  for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+    const TileA t = tile_a(p, i);
+    if (!t.steps) continue;
+    if (!wait_mma(bar(s, A_TFULL), tr.phase)) return;
+    tr.next();
+    auto keys16 = [&](int j) { return min((t.len - j * kRows + 15) / 16 * 16, kRows); };
+    auto issue_s = [&](int j) {
+      if (!wait_mma(bar(s, A_KVFULL + kr.slot), kr.phase)) return false;
+      if (!wait_mma(bar(s, A_SEMPTY), sr.phase ^ 1u)) return false;
+      sr.next();
+      rows_by_keys(kTs, kTq, kr.slot, keys16(j));
+      tc_commit_warp(bar(s, A_SFULL));
+      return true;
+    };
+    if (!issue_s(0)) return;
+    for (int j = 0; j < t.steps; ++j) {
+      const uint32_t kslot = kr.slot;
+      kr.next();
+      // dP: behind the last step's dQ, which read dS in its place
+      if (!wait_mma(bar(s, A_KVFULL + kr.slot), kr.phase)) return;
+      rows_by_keys(kTdp, kTdo, kr.slot, keys16(j));
+      tc_commit_warp(bar(s, A_PFULL));
+      tc_commit_warp(bar(s, A_KVEMPTY + kr.slot));
+      kr.next();
+      if (j + 1 < t.steps && !issue_s(j + 1)) return;
+      if (!wait_mma(bar(s, A_DSFULL), dr.phase)) return;
+      dr.next();
+      const uint64_t b = kt0 + kslot * kTile16;
+      const int chunks = keys16(j) / 16;
+      for (int kk = 0; kk < chunks; ++kk)
+        mma_ts_warp(tbase + kTdq, tbase + kTdp + chunk_at(kk, chunks), b + kk * 128, id_dq,
+                    kk > 0 || j > 0 ? 1u : 0u);
+      tc_commit_warp(bar(s, A_KVEMPTY + kslot));
+    }
+    tc_commit_warp(bar(s, A_OFULL));
+  }
+}
+
+template <bool BF16, int DB>
+__device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t tbase) {
+  using E = typename Elem<BF16>::type;
+  const Sync& s = l.s;
+  const int warp = threadIdx.x / 32, wg = (warp - 4) / 4, wq = warp & 3;
+  const int r = wq * 32 + (threadIdx.x & 31);
+  const uint32_t lane = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+  const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+  const int dim16 = p.dim / 16;
+  auto wait_e = [&](uint32_t b, uint32_t parity) {
+    const bool ok = wait_warp(s, b, parity, kStatusTimeoutSoftmax);
+    tc_fence_after();
+    return ok;
+  };
+  Ring<1> qr, sr, pr, orr, xr;
+  Ring<kSteps> kr;
+  // Q (first warpgroup) or dO (second) of a tile to tensor memory; delta with it.
+  auto stage = [&](const TileA& t, const RowAt& at, float& lse2, float& delta) -> bool {
+    float part = 0.f;
+    const E* o = static_cast<const E*>(p.o.data) + t.b * p.o.sb + at.h * p.o.sh + at.n * p.o.sn;
+    const bool with_o = wg == 1 && at.valid;
+    lse2 = at.valid ? p.lse[at.index] * kLog2e : INFINITY;  // rows behind the last query: p = 0
+    if (!wait_e(bar(s, A_QFULL), qr.phase)) return false;
+    qr.next();
+    const uint32_t src = wg ? l.dout : l.q, dst = lane + (wg ? kTdo : kTq);
+    const bool inside = r < p.box_n * p.box_h;
+#pragma unroll 2
+    for (int k = 0; k < dim16; ++k) {
+      uint32_t w[8];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint4 v = ld_shared_v4(swizzled(src, r, 2 * k + x));
+        w[4 * x] = inside ? v.x : 0u;
+        w[4 * x + 1] = inside ? v.y : 0u;
+        w[4 * x + 2] = inside ? v.z : 0u;
+        w[4 * x + 3] = inside ? v.w : 0u;
+      }
+      tmem_st8(dst + 8 * k, w);
+      if (with_o) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          part = dot8<E>(make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]),
+                         reinterpret_cast<const uint4*>(o)[2 * k + x], part);
+      }
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(bar(s, A_TFULL));
+    warp_arrive(bar(s, A_QEMPTY));
+    if (wg == 1) {
+      l.delta[r] = part;
+      if (at.valid && p.delta) p.delta[at.index] = part;
+    }
+    warp_arrive(bar(s, A_XCH));
+    if (!wait_e(bar(s, A_XCH), xr.phase)) return false;
+    xr.next();
+    delta = l.delta[r];
+    return true;
+  };
+  // this tile's rows: statistics of the next one are taken before its epilogue
+  int i = blockIdx.x;
+  TileA t{};
+  RowAt at{};
+  float lse2 = 0.f, delta = 0.f;
+  auto open = [&]() -> bool {  // to the next tile with keys; others' rows are zero
+    for (; i < p.items; i += gridDim.x) {
+      t = tile_a(p, i);
+      int n0, h0;
+      tile_at(p, t.e, t.tile, n0, h0);
+      at = row_at(p, t.b, n0, h0, r);
+      if (t.steps) break;
+      if (at.valid && p.dq.data && wg == 0) {
+        E* to = static_cast<E*>(const_cast<void*>(p.dq.data)) + t.b * p.dq.sb + at.h * p.dq.sh +
+                at.n * p.dq.sn;
+        for (int k = 0; k < 2 * dim16; ++k) reinterpret_cast<uint4*>(to)[k] = make_uint4(0, 0, 0, 0);
+      }
+      if (at.valid && p.delta && wg == 1) p.delta[at.index] = 0.f;
+    }
+    return i >= p.items || stage(t, at, lse2, delta);
+  };
+  if (!open()) return;
+  while (i < p.items) {
+    const TileA cur = t;
+    const RowAt cur_at = at;
+    const float nl = -lse2, nd = -delta;
+    const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    for (int j = 0; j < cur.steps; ++j) {
+      const int rem = cur.len - j * kRows;
+      const int chunks = rem >= kRows ? 8 : (rem + 15) / 16;
+      int c0, nc;
+      share_of(chunks, wg, c0, nc);
+      const uint32_t kslot = kr.slot;
+      kr.next();
+      kr.next();
+      if (!wait_e(bar(s, A_SFULL), sr.phase)) return;
+      sr.next();
+      uint32_t pv[4][16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld16(lane + kTs + 16 * (c0 + k), pv[k]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) reg_fence16(pv[k]);
+      tc_fence_before();
+      warp_arrive(bar(s, A_SEMPTY));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float2 e = f2_unpack(f2_fma(
+              f2_pack(__uint_as_float(pv[k][2 * x]), __uint_as_float(pv[k][2 * x + 1])), c2, nl2));
+          pv[k][2 * x] = __float_as_uint(ex2_approx(e.x));
+          pv[k][2 * x + 1] = __float_as_uint(ex2_approx(e.y));
+        }
+      // keys behind the length: the product with K reads up to the chunk's end,
+      // where nothing may be left but zeros
+      if (rem < kRows && (rem & 15) && wg == 0) {
+        const uint32_t k = l.kv + kslot * LayoutA<DB>::kTile;
+        for (int x = r; x < (16 * chunks - rem) * 8 * DB; x += kRows)
+          st_shared_v4(swizzled(k, rem + x / (8 * DB), x % (8 * DB)), 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
+      if (!wait_e(bar(s, A_PFULL), pr.phase)) return;
+      pr.next();
+      uint32_t w[4][8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t d[16];
+        tmem_ld16(lane + kTdp + 16 * (c0 + k), d);
+        tmem_wait_ld16(d);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          float2 v = f2_unpack(f2_mul(
+              f2_add(f2_pack(__uint_as_float(d[2 * x]), __uint_as_float(d[2 * x + 1])), nd2),
+              f2_pack(__uint_as_float(pv[k][2 * x]), __uint_as_float(pv[k][2 * x + 1]))));
+          const int col = 16 * (c0 + k) + 2 * x;
+          if (rem < kRows) {
+            if (col >= rem) v.x = 0.f;
+            if (col + 1 >= rem) v.y = 0.f;
+          }
+          w[k][x] = pack_pair(v.x, v.y, E());
         }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < nc) tmem_st8(lane + kTdp + chunk_at(c0 + k, chunks), w[k]);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar(s, A_DSFULL));
+    }
+    // the next tile's q and dout while the last product runs (its S and dP are
+    // complete: nothing reads the old ones any more)
+    i += gridDim.x;
+    if (!open()) return;
+    if (!wait_e(bar(s, A_OFULL), orr.phase)) return;
+    orr.next();
+    const bool whole = p.box_h == 1;
+    int c0, nc;
+    share_of(dim16, wg, c0, nc);
+    E* to = static_cast<E*>(const_cast<void*>(p.dq.data)) + cur.b * p.dq.sb + cur_at.h * p.dq.sh +
+            cur_at.n * p.dq.sn;
+    int n0, h0;
+    tile_at(p, cur.e, cur.tile, n0, h0);
+#pragma unroll 1
+    for (int k = c0; k < c0 + nc; ++k) {
+      uint32_t d[16];
+      tmem_ld16(lane + kTdq + 16 * k, d);
+      tmem_wait_ld16(d);
+      uint32_t w[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        w[x] = pack_pair(__uint_as_float(d[2 * x]) * p.scale, __uint_as_float(d[2 * x + 1]) * p.scale, E());
+      if (!p.dq.data) continue;
+      if (whole) {
+        st_shared_v4(swizzled(l.out, r, 2 * k), w[0], w[1], w[2], w[3]);
+        st_shared_v4(swizzled(l.out, r, 2 * k + 1), w[4], w[5], w[6], w[7]);
+      } else if (cur_at.valid) {
+        reinterpret_cast<uint4*>(to)[2 * k] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(to)[2 * k + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+    tc_fence_before();
+    if (whole && p.dq.data) {
+      // both warpgroups' columns are in shared memory before the first one's
+      // warps send them, and read from there before the next tile's
+      fence_proxy_async_smem();
+      warp_arrive(bar(s, A_XCH));
+      if (!wait_e(bar(s, A_XCH), xr.phase)) return;
+      xr.next();
+      if (wg == 0 && (threadIdx.x & 31) == 0 && n0 + 32 * wq < p.n) {
+        for (int k = 0; 4 * k < dim16; ++k)
+          tma_store_4d(&p.tm_dq, l.out + k * kBoxBytes + wq * 4096u, 64 * k, n0 + 32 * wq, h0, cur.b);
+        bulk_commit_group();
+        bulk_wait_read_all();
+      }
+    }
+    // dQ and the output tile are free: the next dS says so to the MMAs, this
+    // to the other warpgroup
+    warp_arrive(bar(s, A_XCH));
+    if (!wait_e(bar(s, A_XCH), xr.phase)) return;
+    xr.next();
   }
-  if (p.dk.data) store4(row_of<T>(p.dk, b, e, j), p.dim, dk);
-  if (p.dv.data) store4(row_of<T>(p.dv, b, e, j), p.dim, dv);
+}
+
+template <bool BF16, int DB>
+__global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  LayoutA<DB> l;
+  constexpr uint32_t kTile = LayoutA<DB>::kTile;
+  l.q = base;
+  l.dout = base + kTile;
+  l.out = base + 2 * kTile;
+  l.kv = base + 3 * kTile;
+  l.s.bars = l.kv + kSteps * kTile;
+  uint8_t* gb = smem_raw + (l.s.bars - raw);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * A_COUNT);
+  l.s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  l.s.status = p.status;
+  l.delta = reinterpret_cast<float*>(tslot + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(bar(l.s, A_QFULL), 1);
+    mbar_init(bar(l.s, A_QEMPTY), kEltWarps);
+    mbar_init(bar(l.s, A_TFULL), kEltWarps);
+    mbar_init(bar(l.s, A_SFULL), 1);
+    mbar_init(bar(l.s, A_SEMPTY), kEltWarps);
+    mbar_init(bar(l.s, A_PFULL), 1);
+    mbar_init(bar(l.s, A_DSFULL), kEltWarps);
+    mbar_init(bar(l.s, A_OFULL), 1);
+    mbar_init(bar(l.s, A_XCH), kEltWarps);
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(bar(l.s, A_KVFULL + i), 1);
+      mbar_init(bar(l.s, A_KVEMPTY + i), 1);
+    }
+    *l.s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&p.tm_q);
+    prefetch_tensormap(&p.tm_do);
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tslot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  griddep_wait();
+  if (warp == 0) {
+    if (lane == 0) dq_producer<DB>(p, l);
+  } else if (warp == 1) {
+    dq_issuer<BF16, DB>(p, l, tbase);
+  } else if (warp >= 4) {
+    dq_elements<BF16, DB>(p, l, tbase);
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+}
+
+// ------------------------------------------------------------- dk, dv
+// Tensor memory: dV [0, 128), dK [128, 256), S^T [256, 384), dP^T [384, 512):
+// all of it.  P^T takes S^T's place and dS^T dP^T's; both are the A operands
+// of the sums, so nothing goes through shared memory.
+//   warp 0     TMA: the key tile (k and v), row tiles of q and dout (a ring)
+//   warp 1     MMA, in the order  S(j+1), dK(j), dP(j+1), dV(j+1):  p(j+1) is
+//              formed beside dK(j) and dP(j+1), ds(j+1) beside dV(j+1) and S(j+2)
+//   warp 2     the row tiles' lse and delta
+//   warps 4-11 two warpgroups: thread = key, each half of a tile's queries
+//
+// The units of work are (key tile, row tile) in order; a CTA takes a
+// contiguous share of them, of equal size.  A key tile inside one share is
+// finished there; of one that several shares hold parts of, each leaves its sums
+// in the workspace, and a second kernel adds them in the shares' order.
+enum : int {
+  B_KFULL = 0,   // TMA: k and v of the key tile
+  B_KEMPTY,      // MMA: all products with them done
+  B_QFULL,                 // [2] q and dout
+  B_QEMPTY = B_QFULL + 2,  // [2]
+  B_STFULL = B_QEMPTY + 2, // [2] lse and delta
+  B_SFULL = B_STFULL + 2,  // MMA -> elements: S^T
+  B_PFULL,                 // elements -> MMA: P^T
+  B_DPFULL,                // MMA -> elements: dP^T
+  B_DSFULL,                // elements -> MMA: dS^T
+  B_ACCFULL,               // MMA -> elements: dK, dV of the share complete
+  B_ACCEMPTY,              // elements -> MMA
+  B_COUNT
+};
+constexpr int kStages = 2;
+constexpr uint32_t kTdv = 0, kTdk = 128, kTst = 256, kTdpt = 384;
+
+template <int DB>
+struct LayoutB {
+  static constexpr uint32_t kTile = DB * kBoxBytes;
+  uint32_t k, v, q;  // q: stages of q and dout
+  float* stats;      // [kStages][2][128]: -lse log2(e), -delta
+  Sync s;
+};
+
+// Key tiles with keys, in order, and the units of a CTA.
+struct WalkB {
+  int b, e, kt;          // batch element, key head, key tile
+  int tiles;             // key tiles of this batch element
+  int row;               // row tile
+  int64_t left;          // units from here on, this one included
+  int len;
+};
+__device__ __forceinline__ int key_tiles(const CrossParams& p, int b) {
+  return (keys_of(p, b) + kRows - 1) / kRows;
+}
+// Units of all key tiles with keys (every lane of the warp gets it).
+__device__ __forceinline__ int64_t live_units(const CrossParams& p) {
+  int64_t n = 0;
+  for (int b = threadIdx.x & 31; b < p.batch; b += 32) n += key_tiles(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * p.kv_heads * p.tiles_n * p.tiles_h;
+}
+__device__ __forceinline__ int64_t first_unit(const CrossParams& p, int64_t units, int cta) {
+  return units * cta / p.ctas;
+}
+__device__ __forceinline__ WalkB walk_b(const CrossParams& p, int64_t unit, int64_t end) {
+  WalkB w{};
+  w.left = end - unit;
+  if (w.left <= 0) return w;
+  const int rows = p.tiles_n * p.tiles_h;
+  for (w.b = 0;; ++w.b) {
+    w.tiles = key_tiles(p, w.b);
+    const int64_t n = static_cast<int64_t>(w.tiles) * p.kv_heads * rows;
+    if (unit < n) break;
+    unit -= n;
+  }
+  w.row = static_cast<int>(unit % rows);
+  unit /= rows;
+  w.kt = static_cast<int>(unit % w.tiles);
+  w.e = static_cast<int>(unit / w.tiles);
+  w.len = keys_of(p, w.b);
+  return w;
+}
+// To the next unit; true where it belongs to another key tile.
+__device__ __forceinline__ bool step_b(const CrossParams& p, WalkB& w) {
+  if (--w.left <= 0) return true;
+  if (++w.row < p.tiles_n * p.tiles_h) return false;
+  w.row = 0;
+  if (++w.kt == w.tiles) {
+    w.kt = 0;
+    if (++w.e == p.kv_heads) {
+      w.e = 0;
+      do w.tiles = key_tiles(p, ++w.b);
+      while (!w.tiles);
+      w.len = keys_of(p, w.b);
+    }
+  }
+  return true;
+}
+// Whether the unit is its key tile's first or last one in this share.
+__device__ __forceinline__ bool last_b(const CrossParams& p, const WalkB& w) {
+  return w.left == 1 || w.row + 1 == p.tiles_n * p.tiles_h;
+}
+
+template <int DB>
+__device__ void dkv_producer(const CrossParams& p, const LayoutB<DB>& l, WalkB w) {
+  LoadRing<1> kr;
+  LoadRing<kStages> qr;
+  const Sync& s = l.s;
+  auto leave = [&] {
+    kr.drain(bar(s, B_KFULL));
+    qr.drain(bar(s, B_QFULL));
+  };
+  bool fresh = true;
+  while (w.left > 0) {
+    if (fresh) {
+      if (!wait(s, bar(s, B_KEMPTY), kr.phase ^ 1u, kStatusTimeoutProducer)) return leave();
+      if (WSATTN_BOUNDS(p.status, w.kt * kRows < p.m && w.e < p.kv_heads && w.b < p.batch)) {
+        mbar_arrive_expect_tx(bar(s, B_KFULL), 2 * LayoutB<DB>::kTile);
+#pragma unroll
+        for (int c = 0; c < DB; ++c) {
+          tma_load_4d(l.k + c * kBoxBytes, &p.tm_k, bar(s, B_KFULL), c * 64, w.kt * kRows, w.e * p.k_h,
+                      w.b * p.k_b);
+          tma_load_4d(l.v + c * kBoxBytes, &p.tm_v, bar(s, B_KFULL), c * 64, w.kt * kRows, w.e * p.v_h,
+                      w.b * p.v_b);
+        }
+      } else {
+        mbar_arrive(bar(s, B_KFULL));
+      }
+      kr.loaded();
+    }
+    int n0, h0;
+    tile_at(p, w.e, w.row, n0, h0);
+    if (!wait(s, bar(s, B_QEMPTY + qr.slot), qr.phase ^ 1u, kStatusTimeoutProducer)) return leave();
+    const uint32_t full = bar(s, B_QFULL + qr.slot), dst = l.q + qr.slot * 2 * LayoutB<DB>::kTile;
+    if (WSATTN_BOUNDS(p.status, n0 < p.n && h0 < p.heads)) {
+      mbar_arrive_expect_tx(full, 2u * static_cast<uint32_t>(p.box_n * p.box_h) * 128u * DB);
+#pragma unroll
+      for (int c = 0; c < DB; ++c) {
+        tma_load_4d(dst + c * kBoxBytes, &p.tm_q, full, c * 64, n0, h0 * p.q_h, w.b * p.q_b);
+        tma_load_4d(dst + LayoutB<DB>::kTile + c * kBoxBytes, &p.tm_do, full, c * 64, n0, h0 * p.do_h,
+                    w.b * p.do_b);
+      }
+    } else {
+      mbar_arrive(full);
+    }
+    qr.loaded();
+    fresh = step_b(p, w);
+  }
+}
+
+// lse and delta of the row tiles: 4 rows a lane.
+template <bool BF16, int DB>
+__device__ void dkv_stats(const CrossParams& p, const LayoutB<DB>& l, WalkB w) {
+  const Sync& s = l.s;
+  Ring<kStages> qr;
+  const int lane = threadIdx.x & 31;
+  // p is held 2^10 times its value in fp16 (dv divides by it), where long rows'
+  // probabilities would fall below the type's normal values; ds is not
+  constexpr float kShift = BF16 ? 0.f : 10.f, kUnshift = BF16 ? 1.f : 0.0009765625f;
+  while (w.left > 0) {
+    int n0, h0;
+    tile_at(p, w.e, w.row, n0, h0);
+    float a[4], d[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const RowAt at = row_at(p, w.b, n0, h0, lane + 32 * x);
+      a[x] = at.valid ? kShift - p.lse[at.index] * kLog2e : -INFINITY;
+      d[x] = at.valid ? -p.delta[at.index] * kUnshift : 0.f;
+    }
+    if (!wait_warp(s, bar(s, B_QEMPTY + qr.slot), qr.phase ^ 1u, kStatusTimeoutProducer)) return;
+    float* to = l.stats + qr.slot * 2 * kRows;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      to[lane + 32 * x] = a[x];
+      to[kRows + lane + 32 * x] = d[x];
+    }
+    warp_arrive(bar(s, B_STFULL + qr.slot));
+    qr.next();
+    step_b(p, w);
+  }
+}
+
+template <bool BF16, int DB>
+__device__ void dkv_issuer(const CrossParams& p, const LayoutB<DB>& l, uint32_t tbase, WalkB w) {
+  const Sync& s = l.s;
+  const int ksteps = p.dim / 16;
+  const uint32_t id_s = idesc_16_f32(kRows, kRows, BF16, false, false);
+  const uint32_t id_d = idesc_16_f32(kRows, p.dim, BF16, false, true);
+  constexpr uint64_t kTile16 = LayoutB<DB>::kTile >> 4, kBox16 = kBoxBytes >> 4;
+  const uint64_t k0 = sdesc_sw128(l.k, 16, 1024), v0 = sdesc_sw128(l.v, 16, 1024);
+  const uint64_t q0 = sdesc_sw128(l.q, 16, 1024), qt0 = sdesc_sw128(l.q, kBoxBytes, 1024);
+  // queries of a row tile, in whole chunks of 16
+  const int chunks = (p.box_n * p.box_h + 15) / 16;
+  auto wait_mma = [&](uint32_t b, uint32_t parity) {
+    const bool ok = wait_warp(s, b, parity, kStatusTimeoutMma);
+    tc_fence_after();
+    return ok;
+  };
+  auto keys_by_rows = [&](uint32_t d, uint64_t a, uint64_t b) {
+    for (int kk = 0; kk < ksteps; ++kk) {
+      const uint64_t off = static_cast<uint64_t>(kk >> 2) * kBox16 + (kk & 3) * 2;
+      mma_ss_warp(tbase + d, a + off, b + off, id_s, kk > 0 ? 1u : 0u);
+    }
+  };
+  auto sum_rows = [&](uint32_t d, uint32_t a, uint64_t b, bool add) {
+    for (int kk = 0; kk < chunks; ++kk)
+      mma_ts_warp(tbase + d, tbase + a + chunk_at(kk, chunks), b + kk * 128, id_d,
+                  kk > 0 || add ? 1u : 0u);
+  };
+  Ring<1> kr, pr, dsr, ar;
+  Ring<kStages> qr;
+  if (w.left <= 0) return;
+  // S of the first unit
+  bool first = true;  // of its key tile in this share
+  if (!wait_mma(bar(s, B_KFULL), kr.phase)) return;
+  kr.next();
+  if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return;
+  keys_by_rows(kTst, k0, q0 + qr.slot * 2 * kTile16);
+  tc_commit_warp(bar(s, B_SFULL));
+  keys_by_rows(kTdpt, v0, q0 + (qr.slot * 2 + 1) * kTile16);
+  tc_commit_warp(bar(s, B_DPFULL));
+  while (w.left > 0) {
+    const uint32_t slot = qr.slot;
+    qr.next();
+    const bool last = last_b(p, w);
+    WalkB nxt = w;
+    step_b(p, nxt);
+    const bool more = nxt.left > 0;
+    // dV += P^T dO
+    if (!wait_mma(bar(s, B_PFULL), pr.phase)) return;
+    pr.next();
+    if (first && !wait_mma(bar(s, B_ACCEMPTY), ar.phase ^ 1u)) return;
+    sum_rows(kTdv, kTst, qt0 + (slot * 2 + 1) * kTile16, !first);
+    // S of the next unit, in P^T's place (behind dV)
+    if (more && !last) {
+      if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return;
+      keys_by_rows(kTst, k0, q0 + qr.slot * 2 * kTile16);
+      tc_commit_warp(bar(s, B_SFULL));
+    }
+    // dK += dS^T Q
+    if (!wait_mma(bar(s, B_DSFULL), dsr.phase)) return;
+    dsr.next();
+    sum_rows(kTdk, kTdpt, qt0 + slot * 2 * kTile16, !first);
+    tc_commit_warp(bar(s, B_QEMPTY + slot));
+    first = false;
+    if (last) {
+      ar.next();
+      tc_commit_warp(bar(s, B_ACCFULL));
+      tc_commit_warp(bar(s, B_KEMPTY));
+      first = true;
+      if (more) {
+        if (!wait_mma(bar(s, B_KFULL), kr.phase)) return;
+        kr.next();
+        if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return;
+        keys_by_rows(kTst, k0, q0 + qr.slot * 2 * kTile16);
+        tc_commit_warp(bar(s, B_SFULL));
+      }
+    }
+    if (more) {
+      keys_by_rows(kTdpt, v0, q0 + (qr.slot * 2 + 1) * kTile16);
+      tc_commit_warp(bar(s, B_DPFULL));
+    }
+    w = nxt;
+  }
+}
+
+template <bool BF16, int DB>
+__device__ void dkv_elements(const CrossParams& p, const LayoutB<DB>& l, uint32_t tbase, WalkB w) {
+  using E = typename Elem<BF16>::type;
+  const Sync& s = l.s;
+  const int warp = threadIdx.x / 32, wg = (warp - 4) / 4, wq = warp & 3;
+  const int r = wq * 32 + (threadIdx.x & 31);
+  const uint32_t lane = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+  constexpr float kUnshift = BF16 ? 1.f : 0.0009765625f;
+  const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), u2 = f2_pack(kUnshift, kUnshift);
+  const int dim16 = p.dim / 16;
+  const int chunks = (p.box_n * p.box_h + 15) / 16;
+  int c0, nc;
+  share_of(chunks, wg, c0, nc);
+  auto wait_e = [&](uint32_t b, uint32_t parity) {
+    const bool ok = wait_warp(s, b, parity, kStatusTimeoutSoftmax);
+    tc_fence_after();
+    return ok;
+  };
+  Ring<1> sr, dr, ar;
+  Ring<kStages> qr;
+  bool begun = w.row == 0;  // this share has the key tile's first unit
+  while (w.left > 0) {
+    const bool last = last_b(p, w);
+    const bool dead = w.kt * kRows + r >= w.len;  // this thread's key counts not
+    if (!wait_e(bar(s, B_STFULL + qr.slot), qr.phase)) return;
+    const uint32_t st = smem_u32(l.stats + qr.slot * 2 * kRows) + 64u * c0;
+    if (!wait_e(bar(s, B_SFULL), sr.phase)) return;
+    sr.next();
+    uint32_t pv[4][16];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tmem_ld16(lane + kTst + 16 * (c0 + k), pv[k]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reg_fence16(pv[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k < nc) {
+        uint32_t o[8];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint4 nl = ld_shared_v4(st + 64u * k + 16u * x);
+          const float2 e0 = f2_unpack(f2_fma(
+              f2_pack(__uint_as_float(pv[k][4 * x]), __uint_as_float(pv[k][4 * x + 1])), c2,
+              f2_pack(__uint_as_float(nl.x), __uint_as_float(nl.y))));
+          const float2 e1 = f2_unpack(f2_fma(
+              f2_pack(__uint_as_float(pv[k][4 * x + 2]), __uint_as_float(pv[k][4 * x + 3])), c2,
+              f2_pack(__uint_as_float(nl.z), __uint_as_float(nl.w))));
+          const float f0 = dead ? 0.f : ex2_approx(e0.x), f1 = dead ? 0.f : ex2_approx(e0.y);
+          const float f2 = dead ? 0.f : ex2_approx(e1.x), f3 = dead ? 0.f : ex2_approx(e1.y);
+          o[2 * x] = pack_pair(f0, f1, E());
+          o[2 * x + 1] = pack_pair(f2, f3, E());
+          pv[k][4 * x] = __float_as_uint(f0);
+          pv[k][4 * x + 1] = __float_as_uint(f1);
+          pv[k][4 * x + 2] = __float_as_uint(f2);
+          pv[k][4 * x + 3] = __float_as_uint(f3);
+        }
+        tmem_st8(lane + kTst + chunk_at(c0 + k, chunks), o);
+      }
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(bar(s, B_PFULL));
+    if (!wait_e(bar(s, B_DPFULL), dr.phase)) return;
+    dr.next();
+    uint32_t o[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t d[16];
+      tmem_ld16(lane + kTdpt + 16 * (c0 + k), d);
+      tmem_wait_ld16(d);
+      if (k < nc) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint4 nd = ld_shared_v4(st + 4u * kRows + 64u * k + 16u * x);
+          const float2 a = f2_unpack(f2_mul(
+              f2_fma(f2_pack(__uint_as_float(d[4 * x]), __uint_as_float(d[4 * x + 1])), u2,
+                     f2_pack(__uint_as_float(nd.x), __uint_as_float(nd.y))),
+              f2_pack(__uint_as_float(pv[k][4 * x]), __uint_as_float(pv[k][4 * x + 1]))));
+          const float2 b = f2_unpack(f2_mul(
+              f2_fma(f2_pack(__uint_as_float(d[4 * x + 2]), __uint_as_float(d[4 * x + 3])), u2,
+                     f2_pack(__uint_as_float(nd.z), __uint_as_float(nd.w))),
+              f2_pack(__uint_as_float(pv[k][4 * x + 2]), __uint_as_float(pv[k][4 * x + 3]))));
+          o[k][2 * x] = dead ? 0u : pack_pair(a.x, a.y, E());
+          o[k][2 * x + 1] = dead ? 0u : pack_pair(b.x, b.y, E());
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < nc) tmem_st8(lane + kTdpt + chunk_at(c0 + k, chunks), o[k]);
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(bar(s, B_DSFULL));
+    warp_arrive(bar(s, B_QEMPTY + qr.slot));
+    qr.next();
+    if (last) {
+      if (!wait_e(bar(s, B_ACCFULL), ar.phase)) return;
+      ar.next();
+      const bool whole = begun && w.row + 1 == p.tiles_n * p.tiles_h;
+      const int key = w.kt * kRows + r;
+      // dV by the first warpgroup, dK by the second
+      const CrossView& g = wg ? p.dk : p.dv;
+      const float scale = wg ? p.scale : kUnshift;
+      E* to = static_cast<E*>(const_cast<void*>(g.data)) + w.b * g.sb + w.e * g.sh + key * g.sn;
+      // a share's first key tile may have begun in others, its last one go on in others
+      float* part = p.part_kv +
+                    (((static_cast<int64_t>(blockIdx.x) * 2 + (begun ? 1 : 0)) * 2 + (wg ? 0 : 1)) * kRows + r) *
+                        p.dim;
+#pragma unroll 1
+      for (int k = 0; k < dim16; ++k) {
+        uint32_t d[16];
+        tmem_ld16(lane + (wg ? kTdk : kTdv) + 16 * k, d);
+        tmem_wait_ld16(d);
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            reinterpret_cast<float4*>(part + 16 * k)[x] =
+                make_float4(__uint_as_float(d[4 * x]), __uint_as_float(d[4 * x + 1]),
+                            __uint_as_float(d[4 * x + 2]), __uint_as_float(d[4 * x + 3]));
+        } else if (g.data && key < p.m) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              v[y] = dead ? 0u
+                          : pack_pair(__uint_as_float(d[8 * x + 2 * y]) * scale,
+                                      __uint_as_float(d[8 * x + 2 * y + 1]) * scale, E());
+            reinterpret_cast<uint4*>(to + 16 * k)[x] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      warp_arrive(bar(s, B_ACCEMPTY));
+      begun = true;
+    }
+    step_b(p, w);
+  }
+}
+
+template <bool BF16, int DB>
+__global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  LayoutB<DB> l;
+  constexpr uint32_t kTile = LayoutB<DB>::kTile;
+  l.k = base;
+  l.v = base + kTile;
+  l.q = base + 2 * kTile;
+  l.s.bars = l.q + kStages * 2 * kTile;
+  uint8_t* gb = smem_raw + (l.s.bars - raw);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * B_COUNT);
+  l.s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  l.s.status = p.status;
+  l.stats = reinterpret_cast<float*>(gb + 256);  // on a 16-byte boundary
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(bar(l.s, B_KFULL), 1);
+    mbar_init(bar(l.s, B_KEMPTY), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(l.s, B_QFULL + i), 1);
+      mbar_init(bar(l.s, B_QEMPTY + i), 1 + kEltWarps);
+      mbar_init(bar(l.s, B_STFULL + i), 1);
+    }
+    mbar_init(bar(l.s, B_SFULL), 1);
+    mbar_init(bar(l.s, B_PFULL), kEltWarps);
+    mbar_init(bar(l.s, B_DPFULL), 1);
+    mbar_init(bar(l.s, B_DSFULL), kEltWarps);
+    mbar_init(bar(l.s, B_ACCFULL), 1);
+    mbar_init(bar(l.s, B_ACCEMPTY), kEltWarps);
+    *l.s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&p.tm_q);
+    prefetch_tensormap(&p.tm_do);
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tslot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (p.box_n * p.box_h % 16) {
+    // row tiles that end inside a chunk of the products: zeros behind them,
+    // which no load writes over
+    for (uint32_t i = threadIdx.x; i < kStages * 2 * kTile / 16; i += kThreads)
+      st_shared_v4(l.q + 16 * i, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  griddep_wait();
+  const int64_t units = live_units(p);
+  const WalkB w = walk_b(p, first_unit(p, units, blockIdx.x), first_unit(p, units, blockIdx.x + 1));
+  if (warp == 0) {
+    if (lane == 0) dkv_producer<DB>(p, l, w);
+  } else if (warp == 1) {
+    dkv_issuer<BF16, DB>(p, l, tbase, w);
+  } else if (warp == 2) {
+    dkv_stats<BF16, DB>(p, l, w);
+  } else if (warp >= 4) {
+    dkv_elements<BF16, DB>(p, l, tbase, w);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+}
+
+// Key tiles that several shares hold parts of: their sums, in the shares'
+// order; keys behind the lengths: zeros.  A CTA a key tile (of all, with keys
+// or without), a thread four columns of a row.
+template <bool BF16>
+__global__ void __launch_bounds__(256) cross_finish_kernel(const __grid_constant__ CrossParams p) {
+  using E = typename Elem<BF16>::type;
+  griddep_wait();
+  const int all = (p.m + kRows - 1) / kRows;
+  const int kt = blockIdx.x % all, e = blockIdx.x / all % p.kv_heads, b = blockIdx.x / all / p.kv_heads;
+  const int rows = p.n ? p.tiles_n * p.tiles_h : 0;
+  const int tiles = key_tiles(p, b), len = keys_of(p, b);
+  int64_t c0 = 0, c1 = -1;
+  int64_t begin = 0, units = 0;
+  const bool live = kt < tiles && rows > 0;
+  if (live) {
+    units = live_units(p);
+    for (int i = 0; i < b; ++i) begin += key_tiles(p, i);
+    begin = (begin * p.kv_heads + static_cast<int64_t>(e) * tiles + kt) * rows;
+    // share of a unit: the largest c with first_unit(c) <= unit
+    c0 = ((begin + 1) * p.ctas - 1) / units;
+    c1 = ((begin + rows) * p.ctas - 1) / units;
+    if (c0 == c1) return;  // finished in its share
+  }
+  const int cols = p.dim / 4;
+  for (int x = threadIdx.x; x < 2 * kRows * cols; x += 256) {
+    const int c = x % cols * 4, r = x / cols % kRows, which = x / cols / kRows;  // 0: dk, 1: dv
+    const int key = kt * kRows + r;
+    const CrossView& g = which ? p.dv : p.dk;
+    if (key >= p.m || !g.data) continue;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t i = c0; key < len && i <= c1; ++i) {
+      const int64_t first = first_unit(p, units, static_cast<int>(i));
+      if (first == first_unit(p, units, static_cast<int>(i) + 1)) continue;  // an empty share
+      const int slot = first > begin ? 0 : 1;
+      const float4 t = *reinterpret_cast<const float4*>(
+          p.part_kv + (((i * 2 + slot) * 2 + which) * kRows + r) * p.dim + c);
+      v[0] += t.x;
+      v[1] += t.y;
+      v[2] += t.z;
+      v[3] += t.w;
+    }
+    const float scale = which ? (BF16 ? 1.f : 0.0009765625f) : p.scale;
+    E* to = static_cast<E*>(const_cast<void*>(g.data)) + b * g.sb + e * g.sh + key * g.sn + c;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair(v[0] * scale, v[1] * scale, E()),
+                                               pack_pair(v[2] * scale, v[3] * scale, E()));
+  }
+}
+
+// delta alone, where dq is not wanted: a thread a row, its sum in the order of
+// the dq kernel (so that dk and dv do not depend on what else is asked for).
+template <bool BF16>
+__global__ void __launch_bounds__(128) cross_delta_kernel(const __grid_constant__ CrossParams p) {
+  using E = typename Elem<BF16>::type;
+  griddep_wait();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  if (row >= static_cast<int64_t>(p.batch) * p.heads * p.n) return;
+  const int n = static_cast<int>(row % p.n);
+  const int64_t bh = row / p.n;
+  const int h = static_cast<int>(bh % p.heads), b = static_cast<int>(bh / p.heads);
+  const uint4* o = reinterpret_cast<const uint4*>(static_cast<const E*>(p.o.data) + b * p.o.sb +
+                                                  h * p.o.sh + n * p.o.sn);
+  const uint4* d = reinterpret_cast<const uint4*>(static_cast<const E*>(p.dout.data) +
+                                                  b * p.dout.sb + h * p.dout.sh + n * p.dout.sn);
+  float part = 0.f;
+  for (int k = 0; k < p.dim / 8; ++k) part = dot8<E>(d[k], o[k], part);
+  p.delta[row] = part;
 }
 
 template <typename F>
-cudaError_t by_rows(F* kernel, const CrossParams& p, int64_t rows, cudaStream_t s) {
-  return launch_dependent(kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, p);
+cudaError_t run(F* kernel, bool* attr_set, const CrossParams& p, int grid, size_t smem, cudaStream_t s) {
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p);
+}
+
+template <bool BF16, int DB>
+cudaError_t backward(const CrossParams& p, int sms, cudaStream_t s) {
+  constexpr size_t kSmemA = 1024 + (3 + kSteps) * LayoutA<DB>::kTile + 8 * A_COUNT + 16 + 4 * kRows;
+  constexpr size_t kSmemB = 1024 + (2 + 2 * kStages) * LayoutB<DB>::kTile + 256 + kStages * 2 * kRows * 4;
+  static_assert(kSmemA <= 232448 && kSmemB <= 232448, "shared memory of a CTA");
+  static_assert(8 * B_COUNT + 16 <= 256, "barriers of the dk, dv kernel");
+  static bool set_a[kMaxDevices] = {}, set_b[kMaxDevices] = {};
+  const bool keys = (p.dk.data || p.dv.data) && p.m > 0;
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
+  cudaError_t e = cudaSuccess;
+  if (p.n > 0) {
+    if (p.dq.data)
+      e = run(cross_dq_kernel<BF16, DB>, set_a, p, p.items < sms ? p.items : sms, kSmemA, s);
+    else if (keys)
+      e = launch_dependent(cross_delta_kernel<BF16>, dim3(static_cast<unsigned>((rows + 127) / 128)),
+                           dim3(128), 0, s, p);
+    if (e == cudaSuccess && keys) e = run(cross_dkv_kernel<BF16, DB>, set_b, p, p.ctas, kSmemB, s);
+  }
+  if (e != cudaSuccess || !keys) return e;
+  const int64_t tiles = static_cast<int64_t>(p.batch) * p.kv_heads * ((p.m + kRows - 1) / kRows);
+  return launch_dependent(cross_finish_kernel<BF16>, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s,
+                          p);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_backward(const CrossParams& p, int dtype, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
-  const int64_t keys = static_cast<int64_t>(p.batch) * p.kv_heads * p.m;
-  cudaError_t e = cudaSuccess;
-  if (p.dq.data && rows)
-    e = dtype == WSATTN_BF16 ? by_rows(cross_dq_kernel<__nv_bfloat16>, p, rows, s)
-                             : by_rows(cross_dq_kernel<__half>, p, rows, s);
-  if (e != cudaSuccess || !keys || (!p.dk.data && !p.dv.data)) return e;
-  return dtype == WSATTN_BF16 ? by_rows(cross_dkv_kernel<__nv_bfloat16>, p, keys, s)
-                              : by_rows(cross_dkv_kernel<__half>, p, keys, s);
+void split_cross_backward(CrossParams* p) {
+  split_cross(p);
+  p->pair = p->splits = 1;
+  const int64_t heads = static_cast<int64_t>(p->batch) * p->kv_heads;
+  const int64_t rows = static_cast<int64_t>(p->tiles_n) * p->tiles_h;
+  p->items = heads * rows <= INT32_MAX ? static_cast<int>(heads * rows) : -1;
+  // a share of two units at least
+  const int64_t units = heads * ((p->m + kCrossRows - 1) / kCrossRows) * rows;
+  p->ctas = units < 2 * kTilingSms ? static_cast<int>((units + 1) / 2) : kTilingSms;
+}
+
+cudaError_t launch_cross_backward(const CrossParams& p, int dtype, int sms, cudaStream_t s) {
+  if (dtype == WSATTN_BF16) return p.dim <= 64 ? backward<true, 1>(p, sms, s) : backward<true, 2>(p, sms, s);
+  return p.dim <= 64 ? backward<false, 1>(p, sms, s) : backward<false, 2>(p, sms, s);
 }
 
 }  // namespace wsattn

@@ -280,6 +280,13 @@ struct CrossParams {
   int items;
   float* part_o;                       // [splits][batch, heads, n][D] (splits > 1)
   float* part_l;                       // [splits][batch, heads, n] log2 of the sums
+  // backward: dq by row tiles, dk and dv by key tiles
+  CUtensorMap tm_do;                   // like tm_q
+  CUtensorMap tm_dq;                   // like tm_o
+  int do_h, do_b;
+  float* delta;                        // [batch, heads, n] sum_d dout out
+  float* part_kv;                      // [ctas][2][dk, dv][128][D] sums of shares of a key tile
+  int ctas;                            // of the dk, dv kernel
   int* status;
 };
 constexpr int kCrossRows = 128;  // of a row tile and of a key step
@@ -287,6 +294,8 @@ constexpr int kCrossRows = 128;  // of a row tile and of a key step
 void split_cross(CrossParams* p);
 size_t cross_partial_bytes(const CrossParams& p);
 cudaError_t launch_cross_forward(const CrossParams& p, int dtype, int sms, cudaStream_t s);
-cudaError_t launch_cross_backward(const CrossParams& p, int dtype, cudaStream_t s);
+// Row tiles of the backward pass and the CTAs of its dk, dv kernel.
+void split_cross_backward(CrossParams* p);
+cudaError_t launch_cross_backward(const CrossParams& p, int dtype, int sms, cudaStream_t s);
 
 }  // namespace wsattn

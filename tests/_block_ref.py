@@ -154,6 +154,10 @@ def rounded(tol, want, dtype):
 
 # ------------------------------------------------------------ cross attention
 
+# The exponential of the special-function unit counts what is below fp32's normal
+# values as zero: a probability is off by less than 2^-126 for that.
+LEAST = 2.0 ** -126
+
 def heads_of(t, h):
     return t.double().repeat_interleave(h // t.shape[1], 1)
 
@@ -199,7 +203,7 @@ def cross_forward(q, k, v, lengths, scale):
     out = p @ vd
     # p: rounded, and off by its logit's error; below the type's smallest values relative to the largest p (1 / sum >= p)
     step = half_step(dt) + 2 * es + 2.0 ** -20
-    small = torch.where(empty[..., None], 0.0, torch.exp(s.amax(-1, keepdim=True) - lse[..., None])) * tiny(dt)
+    small = torch.where(empty[..., None], 0.0, torch.exp(s.amax(-1, keepdim=True) - lse[..., None])) * max(tiny(dt), LEAST)
     tol = (p * step) @ vd.abs() + small * vd.abs().sum(2, keepdim=True)
     # the sum of the probabilities is off by as much as they are, and the product by its truncations
     rel = (p * (2 * es + 2.0 ** -20)).sum(-1, keepdim=True) + 2.0 ** -19
@@ -224,7 +228,8 @@ def cross_backward(dout, q, k, v, out, lse, lengths, scale):
     rel = 2 * es + 2.0 ** -20
     size = do.abs() @ vd.abs().transpose(2, 3)
     e_ds = ds.abs() * (rel + half_step(dt) + 2.0 ** -21) + tiny(dt) * (p > 0) \
-        + p * ((d / 16 + 8) * 2.0 ** -22 * size + 2.0 ** -20 * (do * out.double()).abs().sum(-1, keepdim=True))
+        + p * ((d / 16 + 8) * 2.0 ** -22 * size + 2.0 ** -20 * (do * out.double()).abs().sum(-1, keepdim=True)) \
+        + LEAST * (dp - delta).abs() * (p > 0)
 
     def shared(t):
         return t.view(b, hk, r, m, d).sum(2)
@@ -234,6 +239,6 @@ def cross_backward(dout, q, k, v, out, lse, lengths, scale):
     many = (n * r / 16 + 8) * 2.0 ** -22
     w["dk"] = scale * shared(ds.transpose(2, 3) @ qd), \
         scale * shared(e_ds.transpose(2, 3) @ qd.abs() + many * (ds.abs().transpose(2, 3) @ qd.abs()))
-    e_p = p * (rel + half_step(dt)) + tiny(dt) * (p > 0)
+    e_p = p * (rel + half_step(dt)) + (tiny(dt) + LEAST) * (p > 0)
     w["dv"] = shared(p.transpose(2, 3) @ do), shared(e_p.transpose(2, 3) @ do.abs() + many * (p.transpose(2, 3) @ do.abs()))
     return w
