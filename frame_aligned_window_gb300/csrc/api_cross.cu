@@ -203,7 +203,8 @@ int wsattn_cross_backward(const wsattn_cross_grad_args* a, void* workspace, size
   if (!p.status || !sms) return WSATTN_ERR_CUDA;
   const int d = a->head_dim, rows = wsattn::kCrossRows;
   if ((n && (!encode(&p.tm_q, a->dtype, &a->q, d, b, n, p.box_n, p.box_h, &p.q_h, &p.q_b) ||
-             !encode(&p.tm_do, a->dtype, &a->dout, d, b, n, p.box_n, p.box_h, &p.do_h, &p.do_b))) ||
+             !encode(&p.tm_do, a->dtype, &a->dout, d, b, n, p.box_n, p.box_h, &p.do_h, &p.do_b) ||
+             !encode(&p.tm_o, a->dtype, &a->out, d, b, n, p.box_n, p.box_h, &p.o_h, &p.o_b))) ||
       (n && p.dq.data && !encode(&p.tm_dq, a->dtype, &a->dq, d, b, n, 32, 1)) ||
       (n && m && (!encode(&p.tm_k, a->dtype, &a->k, d, b, m, rows, 1, &p.k_h, &p.k_b) ||
                   !encode(&p.tm_v, a->dtype, &a->v, d, b, m, rows, 1, &p.v_h, &p.v_b))))

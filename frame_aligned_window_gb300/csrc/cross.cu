@@ -13,13 +13,13 @@
 // share every key step that is loaded; a persistent CTA an SM walks the items.
 //   warp 0     TMA: row tiles of q (a ring of three), key and value steps (a
 //              ring of four)
-//   warp 1     MMA issue (one elected lane): S_u = Q_u K^T, O_u += P_u V for
-//              the two row tiles u in turn, tensor memory
+//   warps 1, 2 MMA issue (one elected lane), each for its row tile u:
+//              S_u = Q_u K^T, O_u += P_u V; tensor memory
 //   warps 4-11 softmax and epilogue, a warpgroup for each row tile; thread =
 //              row = tensor-memory lane
 // Tensor memory: O_0, O_1 (D columns each), S_0, S_1 (128 columns each).  P_u
 // takes S_u's place: the softmax holds S_u in registers when it stores P_u, and
-// the MMAs of one thread run in order, so that S_u of the next step cannot
+// the MMAs of one issuer run in order, so that S_u of the next step cannot
 // overtake the P_u V that reads P_u.  While one row tile's softmax runs, the
 // tensor core works on the other's two products.
 //
@@ -38,7 +38,7 @@ using namespace cross;
 constexpr int kThreads = 384;
 constexpr int kQTiles = 3;    // ring of row tiles
 constexpr int kSteps = 4;     // ring of key and value steps
-constexpr float kLazyMax = 8.f;  // rescale when a maximum grows by more than 2^8
+constexpr float kSlack = 8.f;  // rows are rescaled when a maximum grows by more than 2^8
 
 enum : int {
   B_QFULL = 0,
@@ -175,7 +175,7 @@ __device__ void mma_issuer(const CrossParams& p, const Layout<DB>& l, uint32_t t
   const uint32_t id_pv = idesc_16_f32(kRows, p.dim, BF16, false, true);
   const uint64_t q0 = sdesc_sw128(l.q, 16, 1024), k0 = sdesc_sw128(l.kv, 16, 1024);
   const uint64_t v0 = sdesc_sw128(l.kv, kBoxBytes, 1024);
-  constexpr uint64_t kTile16 = Layout<DB>::kTile >> 4, kBox16 = kBoxBytes >> 4;
+  constexpr uint64_t kTile16 = Layout<DB>::kTile >> 4;
   Ring<kQTiles> qr;
   Ring<kSteps> kr;       // the next step to take: K and V in turn
   uint32_t pphase = 0;   // bit u: parity of P_u's next use
@@ -192,10 +192,7 @@ __device__ void mma_issuer(const CrossParams& p, const Layout<DB>& l, uint32_t t
     }
     const uint32_t id = id_qk | (static_cast<uint32_t>(w.keys16()) >> 3) << 17;
     const uint64_t a = q0 + q_slot[u] * kTile16, b = k0 + kslot * kTile16;
-    for (int kk = 0; kk < ksteps; ++kk) {
-      const uint64_t off = static_cast<uint64_t>(kk >> 2) * kBox16 + (kk & 3) * 2;
-      mma_ss_warp(t_s + u * kRows, a + off, b + off, id, kk > 0 ? 1u : 0u);
-    }
+    issue_ss(t_s + u * kRows, a, b, id, ksteps);
     tc_commit_warp(bar(s, B_SFULL + u));
     return true;
   };
@@ -223,9 +220,7 @@ __device__ void mma_issuer(const CrossParams& p, const Layout<DB>& l, uint32_t t
         pphase ^= 1u << u;
         tc_fence_after();
         const uint64_t b = v0 + vr.slot * kTile16;
-        for (int kk = 0; kk < chunks; ++kk)  // 16 rows of V (2 KB), 8 columns of P
-          mma_ts_warp(t_o + u * 64 * DB, t_s + u * kRows + kk * 8, b + kk * 128, id_pv,
-                      kk > 0 || !cur.first() ? 1u : 0u);
+        issue_sum(t_o + u * 64 * DB, t_s + u * kRows, 0, b, id_pv, chunks, !cur.first());
         if (cur.last()) tc_commit_warp(bar(s, B_OFULL + u));
         if (u == units - 1) tc_commit_warp(bar(s, B_KVEMPTY + vr.slot));
       }
@@ -244,6 +239,7 @@ __device__ void mma_issuer(const CrossParams& p, const Layout<DB>& l, uint32_t t
   }
 }
 
+
 // P of 16 logits: their exponentials 2^(s c + nb), added to the packed row sums,
 // rounded to pairs and stored as eight columns.
 template <bool BF16>
@@ -260,6 +256,75 @@ __device__ __forceinline__ void exp_store(const uint32_t (&sv)[16], uint64_t c2,
     w[i] = pack_pair(p0, p1, typename Elem<BF16>::type());
   }
   tmem_st8(taddr, w);
+}
+
+// Keys from column `rem` on are masked (FULL: none of the 128 are).
+template <bool FULL>
+__device__ __forceinline__ void mask16(uint32_t (&sv)[16], int col, int rem) {
+  if constexpr (!FULL) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (col + x >= rem) sv[x] = 0xff800000u;
+  }
+}
+// Largest logit of a row's step: 64 columns are loaded while the other 64 are
+// compared.
+template <bool FULL>
+__device__ __forceinline__ float step_max(uint32_t t_s, int rem) {
+  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t sv[2][4][16];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) tmem_ld16(t_s + 16 * k, sv[0][k]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reg_fence16(sv[h][k]);
+    if (h == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld16(t_s + 64 + 16 * k, sv[1][k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      mask16<FULL>(sv[h][k], 64 * h + 16 * k, rem);
+#pragma unroll
+      for (int x = 0; x < 16; x += 8)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          t[y] = max3(t[y], __uint_as_float(sv[h][k][x + y]), __uint_as_float(sv[h][k][x + 4 + y]));
+    }
+  }
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+// A step's probabilities 2^(s c + nb), stored in pairs over its logits, and
+// their sum.  The logits are read again (a read costs less than 128 registers
+// that hold them), 32 columns ahead.
+template <bool BF16, bool FULL>
+__device__ __forceinline__ float step_exp(uint32_t t_s, int rem, uint64_t c2, float nb) {
+  const uint64_t nb2 = f2_pack(nb, nb);
+  const int chunks = FULL ? 8 : (rem + 15) / 16;
+  uint64_t la = f2_pack(0.f, 0.f), lb = la;
+  uint32_t sv[2][2][16];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) tmem_ld16(t_s + 16 * k, sv[0][k]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) reg_fence16(sv[q & 1][k]);
+    if (q < 3) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) tmem_ld16(t_s + 32 * (q + 1) + 16 * k, sv[(q + 1) & 1][k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mask16<FULL>(sv[q & 1][k], 32 * q + 16 * k, rem);
+      if (FULL || 2 * q + k < chunks)
+        exp_store<BF16>(sv[q & 1][k], c2, nb2, la, lb, t_s + 8 * (2 * q + k));
+    }
+  }
+  const float2 ab = f2_unpack(f2_add(la, lb));
+  return ab.x + ab.y;
 }
 
 template <bool BF16, int DB>
@@ -305,46 +370,24 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
       if (!wait_s(bar(s, B_SFULL + u), sphase)) return;
       sphase ^= 1u;
       tc_fence_after();
-      uint32_t sv[8][16];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) tmem_ld16(t_s + 16 * k, sv[k]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) reg_fence16(sv[k]);
-      const int chunks = rem >= kRows ? 8 : (rem + 15) / 16;
-      if (rem < kRows) {
-        // behind the length: no probability, and (up to the chunk's end, where
-        // the product reads on) no value, whatever lies there
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            if (16 * k + x >= rem) sv[k][x] = 0xff800000u;
-        if (u == 0 && (rem & 15)) {
-          if (!wait_s(bar(s, B_KVFULL + vr.slot), vr.phase)) return;
-          const uint32_t v = l.kv + vr.slot * Layout<DB>::kTile;
-          for (int x = r; x < (16 * chunks - rem) * 8 * DB; x += kRows)
-            st_shared_v4(swizzled(v, rem + x / (8 * DB), x % (8 * DB)), 0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-        }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(sv[k][x]));
-      const float m_top = fmaxf(m, top * c);
-      const float m_new = m_top > m + kLazyMax ? m_top : m;
+      const bool full = rem >= kRows;
+      const float top = c * (full ? step_max<true>(t_s, rem) : step_max<false>(t_s, rem));
+      // the reference moves only where the maximum has grown past it by far
+      const float m_new = top > m + kSlack ? top : m;
       const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
-      const float nb = m_new == -INFINITY ? 0.f : -m_new;
-      const uint64_t nb2 = f2_pack(nb, nb);
-      uint64_t la = f2_pack(0.f, 0.f), lb = la;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < chunks) exp_store<BF16>(sv[k], c2, nb2, la, lb, t_s + 8 * k);
-      const float2 ab = f2_unpack(f2_add(la, lb));
-      sum = sum * alpha + (ab.x + ab.y);
       m = m_new;
+      const float nb = m == -INFINITY ? 0.f : -m;
+      sum = sum * alpha + (full ? step_exp<BF16, true>(t_s, rem, c2, nb)
+                                : step_exp<BF16, false>(t_s, rem, c2, nb));
+      if (rem < kRows && (rem & 15)) {
+        // the product reads on to the chunk's end: no value there, whatever lies
+        // behind the length (each warpgroup before its own product)
+        if (!wait_s(bar(s, B_KVFULL + vr.slot), vr.phase)) return;
+        const uint32_t v = l.kv + vr.slot * Layout<DB>::kTile;
+        for (int x = r; x < ((rem + 15) / 16 * 16 - rem) * 8 * DB; x += kRows)
+          st_shared_v4(swizzled(v, rem + x / (8 * DB), x % (8 * DB)), 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
       // S_u of this step comes behind the last step's product: O_u is complete
       if (j > t.step0 && __any_sync(0xffffffffu, alpha < 1.f)) {
         const uint64_t a2 = f2_pack(alpha, alpha);
@@ -396,31 +439,39 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
     const bool whole = p.splits == 1 && p.box_h == 1;  // rows of one head: by TMA
     const uint32_t tile = l.q + q_slot * Layout<DB>::kTile;
 #pragma unroll 1
-    for (int k = 0; k < dim16; ++k) {
-      uint32_t o[16];
-      tmem_ld16(t_o + 16 * k, o);
-      tmem_wait_ld16(o);
-      if (p.splits > 1) {
-        if (valid) {
-          float4* to = reinterpret_cast<float4*>(p.part_o + (t.part * rows + row) * p.dim + 16 * k);
+    for (int k0 = 0; k0 < dim16; k0 += 4) {
+      uint32_t o4[4][16];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            to[x] = make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
-                                __uint_as_float(o[4 * x + 2]) * inv,
-                                __uint_as_float(o[4 * x + 3]) * inv);
+      for (int k = 0; k < 4; ++k) tmem_ld16(t_o + 16 * (k0 + k), o4[k]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) reg_fence16(o4[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= dim16) break;
+        uint32_t(&o)[16] = o4[k];
+        if (p.splits > 1) {
+          if (valid) {
+            float4* to = reinterpret_cast<float4*>(p.part_o + (t.part * rows + row) * p.dim + 16 * (k0 + k));
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              to[x] = make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
+                                  __uint_as_float(o[4 * x + 2]) * inv,
+                                  __uint_as_float(o[4 * x + 3]) * inv);
+          }
+          continue;
         }
-        continue;
-      }
-      uint32_t w[8];
+        uint32_t w[8];
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        w[x] = pack_pair(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv, E());
-      if (whole) {
-        st_shared_v4(swizzled(tile, r, 2 * k), w[0], w[1], w[2], w[3]);
-        st_shared_v4(swizzled(tile, r, 2 * k + 1), w[4], w[5], w[6], w[7]);
-      } else if (valid) {
-        reinterpret_cast<uint4*>(out)[2 * k] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(out)[2 * k + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int x = 0; x < 8; ++x)
+          w[x] = pack_pair(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv, E());
+        if (whole) {
+          st_shared_v4(swizzled(tile, r, 2 * (k0 + k)), w[0], w[1], w[2], w[3]);
+          st_shared_v4(swizzled(tile, r, 2 * (k0 + k) + 1), w[4], w[5], w[6], w[7]);
+        } else if (valid) {
+          reinterpret_cast<uint4*>(out)[2 * (k0 + k)] = make_uint4(w[0], w[1], w[2], w[3]);
+          reinterpret_cast<uint4*>(out)[2 * (k0 + k) + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
     }
     tc_fence_before();
@@ -574,7 +625,7 @@ void split_cross(CrossParams* p) {
   p->box_n = kCrossRows;
   p->box_h = 1;
   if (p->n > 0 && p->n < kCrossRows && p->shared > 1 && p->q.sh > 0 &&
-      (!p->dout.data || p->dout.sh > 0)) {
+      (!p->dout.data || (p->dout.sh > 0 && p->o.sh > 0))) {
     p->box_n = p->n;
     p->box_h = kCrossRows / p->n < p->shared ? kCrossRows / p->n : p->shared;
     while (p->shared % p->box_h) --p->box_h;  // no tile reaches into another key head's

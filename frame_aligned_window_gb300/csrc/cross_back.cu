@@ -31,9 +31,11 @@ __device__ __forceinline__ void share_of(int n, int w, int& first, int& count) {
 // Where chunk k of n lies once it is rounded to pairs (8 columns): each
 // warpgroup writes over its own part of what it read, so neither waits for the
 // other.
+__device__ __forceinline__ uint32_t second_at(int n) {  // of the second half's chunk k, less 8 k
+  return 8u * static_cast<uint32_t>((n + 1) / 2);
+}
 __device__ __forceinline__ uint32_t chunk_at(int k, int n) {
-  const int c = (n + 1) / 2;
-  return static_cast<uint32_t>(k < c ? 8 * k : 16 * c + 8 * (k - c));
+  return 8u * static_cast<uint32_t>(k) + (k < (n + 1) / 2 ? 0u : second_at(n));
 }
 
 // Adds the products of eight pairs of elements, in order.
@@ -71,15 +73,18 @@ __device__ __forceinline__ void tile_at(const CrossParams& p, int e, int i, int&
 // ------------------------------------------------------------- dq
 // Tensor memory: dQ [0, 128), S [128, 256), dP [256, 384), Q [384, 448),
 // dO [448, 512) (pairs).  dS takes dP's place.
-//   warp 0     TMA: q and dout of a row tile, key and value steps (a ring)
-//   warp 1     MMA: S = Q K^T, dP = dO V^T, dQ += dS K
+//   warp 0     TMA: q, dout and out of a row tile, key and value steps (a ring)
+//   warp 1     MMA: S = Q K^T
+//   warp 2     MMA: dP = dO V^T, dQ += dS K
 //   warps 4-11 two warpgroups: thread = row, each half of a step's columns.
-//              The first copies Q to tensor memory, the second dO (and forms
-//              delta from it)
+//              The first copies Q to tensor memory, the second dO, and each
+//              forms half of delta
+// The tile that out is loaded to is where dq leaves from: out is used up (in
+// delta) before the tile before it writes its dq.
 // S of the next step is written as soon as both warpgroups hold this one's in
 // registers, and p is formed while dP is on its way.
 enum : int {
-  A_QFULL = 0,   // TMA -> elements: q and dout staged
+  A_QFULL = 0,   // TMA -> elements: q, dout and out staged
   A_QEMPTY,      // elements -> TMA
   A_TFULL,       // elements -> MMA: Q and dO in tensor memory
   A_SFULL,       // MMA -> elements
@@ -87,7 +92,8 @@ enum : int {
   A_PFULL,       // MMA -> elements: dP written
   A_DSFULL,      // elements -> MMA: dS written
   A_OFULL,       // MMA -> elements: the tile's dQ is complete
-  A_XCH,         // the two warpgroups: delta exchanged
+  A_XCH,         // the two warpgroups: output columns exchanged
+  A_OUTEMPTY,    // elements -> TMA: the output tile is sent, out's next one may come
   A_KVFULL,
   A_KVEMPTY = A_KVFULL + 4,
   A_COUNT = A_KVEMPTY + 4
@@ -99,7 +105,7 @@ template <int DB>
 struct LayoutA {
   static constexpr uint32_t kTile = DB * kBoxBytes;
   uint32_t q, dout, out, kv;
-  float* delta;  // [128]
+  float* part;  // [2][128]: halves of delta
   Sync s;
 };
 
@@ -123,6 +129,7 @@ template <int DB>
 __device__ void dq_producer(const CrossParams& p, const LayoutA<DB>& l) {
   LoadRing<1> qr;
   LoadRing<kSteps> kr;
+  uint32_t tiles = 0;  // the tile before the last one has sent its dq: the output tile is free
   const Sync& s = l.s;
   auto leave = [&] {
     qr.drain(bar(s, A_QFULL));
@@ -133,14 +140,18 @@ __device__ void dq_producer(const CrossParams& p, const LayoutA<DB>& l) {
     if (!t.steps) continue;
     int n0, h0;
     tile_at(p, t.e, t.tile, n0, h0);
-    if (!wait(s, bar(s, A_QEMPTY), qr.phase ^ 1u, kStatusTimeoutProducer)) return leave();
+    if (!wait(s, bar(s, A_QEMPTY), qr.phase ^ 1u, kStatusTimeoutProducer) ||
+        !wait(s, bar(s, A_OUTEMPTY), tiles > 1 ? tiles & 1u : 1u, kStatusTimeoutProducer))
+      return leave();
+    ++tiles;
     if (WSATTN_BOUNDS(p.status, n0 < p.n && h0 < p.heads && t.b < p.batch)) {
-      mbar_arrive_expect_tx(bar(s, A_QFULL), 2u * static_cast<uint32_t>(p.box_n * p.box_h) * 128u * DB);
+      mbar_arrive_expect_tx(bar(s, A_QFULL), 3u * static_cast<uint32_t>(p.box_n * p.box_h) * 128u * DB);
 #pragma unroll
       for (int c = 0; c < DB; ++c) {
         tma_load_4d(l.q + c * kBoxBytes, &p.tm_q, bar(s, A_QFULL), c * 64, n0, h0 * p.q_h, t.b * p.q_b);
         tma_load_4d(l.dout + c * kBoxBytes, &p.tm_do, bar(s, A_QFULL), c * 64, n0, h0 * p.do_h,
                     t.b * p.do_b);
+        tma_load_4d(l.out + c * kBoxBytes, &p.tm_o, bar(s, A_QFULL), c * 64, n0, h0 * p.o_h, t.b * p.o_b);
       }
     } else {
       mbar_arrive(bar(s, A_QFULL));
@@ -164,64 +175,56 @@ __device__ void dq_producer(const CrossParams& p, const LayoutA<DB>& l) {
   }
 }
 
+// Two issuers, so that one's waits run beside the other's MMAs: S, and dP with dQ.
 template <bool BF16, int DB>
-__device__ void dq_issuer(const CrossParams& p, const LayoutA<DB>& l, uint32_t tbase) {
+__device__ void dq_issuer(const CrossParams& p, const LayoutA<DB>& l, uint32_t tbase, bool sums) {
   const Sync& s = l.s;
-  const int ksteps = p.dim / 16;
+  const int chunks_d = p.dim / 16;
   const uint32_t id_s = idesc_16_f32(kRows, 0, BF16, false, false);
   const uint32_t id_dq = idesc_16_f32(kRows, p.dim, BF16, false, true);
   const uint64_t k0 = sdesc_sw128(l.kv, 16, 1024), kt0 = sdesc_sw128(l.kv, kBoxBytes, 1024);
-  constexpr uint64_t kTile16 = LayoutA<DB>::kTile >> 4, kBox16 = kBoxBytes >> 4;
+  constexpr uint64_t kTile16 = LayoutA<DB>::kTile >> 4;
   auto wait_mma = [&](uint32_t b, uint32_t parity) {
     const bool ok = wait_warp(s, b, parity, kStatusTimeoutMma);
     tc_fence_after();
     return ok;
   };
   Ring<1> tr, sr, dr;   // Q and dO, S, dS
-  Ring<kSteps> kr;      // next step of S
-  // S or dP of a step: A in tensor memory, N keys
-  auto rows_by_keys = [&](uint32_t d, uint32_t a, uint32_t slot, int keys16) {
-    const uint32_t id = id_s | (static_cast<uint32_t>(keys16) >> 3) << 17;
-    const uint64_t b = k0 + slot * kTile16;
-    for (int kk = 0; kk < ksteps; ++kk)
-      mma_ts_warp(tbase + d, tbase + a + kk * 8, b + static_cast<uint64_t>(kk >> 2) * kBox16 + (kk & 3) * 2,
-                  id, kk > 0 ? 1u : 0u);
-  };
+  Ring<kSteps> kr;      // K and V in turn
   for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
     const TileA t = tile_a(p, i);
     if (!t.steps) continue;
     if (!wait_mma(bar(s, A_TFULL), tr.phase)) return;
     tr.next();
-    auto keys16 = [&](int j) { return min((t.len - j * kRows + 15) / 16 * 16, kRows); };
-    auto issue_s = [&](int j) {
-      if (!wait_mma(bar(s, A_KVFULL + kr.slot), kr.phase)) return false;
-      if (!wait_mma(bar(s, A_SEMPTY), sr.phase ^ 1u)) return false;
-      sr.next();
-      rows_by_keys(kTs, kTq, kr.slot, keys16(j));
-      tc_commit_warp(bar(s, A_SFULL));
-      return true;
-    };
-    if (!issue_s(0)) return;
     for (int j = 0; j < t.steps; ++j) {
-      const uint32_t kslot = kr.slot;
+      const uint32_t keys16 = static_cast<uint32_t>(min((t.len - j * kRows + 15) / 16 * 16, kRows));
+      const uint32_t id = id_s | keys16 >> 3 << 17;
+      const Ring<kSteps> k = kr;
       kr.next();
+      const Ring<kSteps> v = kr;
+      kr.next();
+      if (!sums) {
+        if (!wait_mma(bar(s, A_KVFULL + k.slot), k.phase)) return;
+        if (!wait_mma(bar(s, A_SEMPTY), sr.phase ^ 1u)) return;
+        sr.next();
+        issue_ts(tbase + kTs, tbase + kTq, k0 + k.slot * kTile16, id, chunks_d);
+        tc_commit_warp(bar(s, A_SFULL));
+        tc_commit_warp(bar(s, A_KVEMPTY + k.slot));
+        continue;
+      }
       // dP: behind the last step's dQ, which read dS in its place
-      if (!wait_mma(bar(s, A_KVFULL + kr.slot), kr.phase)) return;
-      rows_by_keys(kTdp, kTdo, kr.slot, keys16(j));
+      if (!wait_mma(bar(s, A_KVFULL + v.slot), v.phase)) return;
+      issue_ts(tbase + kTdp, tbase + kTdo, k0 + v.slot * kTile16, id, chunks_d);
       tc_commit_warp(bar(s, A_PFULL));
-      tc_commit_warp(bar(s, A_KVEMPTY + kr.slot));
-      kr.next();
-      if (j + 1 < t.steps && !issue_s(j + 1)) return;
+      tc_commit_warp(bar(s, A_KVEMPTY + v.slot));
+      if (!wait_mma(bar(s, A_KVFULL + k.slot), k.phase)) return;
       if (!wait_mma(bar(s, A_DSFULL), dr.phase)) return;
       dr.next();
-      const uint64_t b = kt0 + kslot * kTile16;
-      const int chunks = keys16(j) / 16;
-      for (int kk = 0; kk < chunks; ++kk)
-        mma_ts_warp(tbase + kTdq, tbase + kTdp + chunk_at(kk, chunks), b + kk * 128, id_dq,
-                    kk > 0 || j > 0 ? 1u : 0u);
-      tc_commit_warp(bar(s, A_KVEMPTY + kslot));
+      const int chunks = static_cast<int>(keys16) / 16;
+      issue_sum(tbase + kTdq, tbase + kTdp, second_at(chunks), kt0 + k.slot * kTile16, id_dq, chunks, j > 0);
+      tc_commit_warp(bar(s, A_KVEMPTY + k.slot));
     }
-    tc_commit_warp(bar(s, A_OFULL));
+    if (sums) tc_commit_warp(bar(s, A_OFULL));
   }
 }
 
@@ -241,17 +244,14 @@ __device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t
   };
   Ring<1> qr, sr, pr, orr, xr;
   Ring<kSteps> kr;
-  // Q (first warpgroup) or dO (second) of a tile to tensor memory; delta with it.
-  auto stage = [&](const TileA& t, const RowAt& at, float& lse2, float& delta) -> bool {
-    float part = 0.f;
-    const E* o = static_cast<const E*>(p.o.data) + t.b * p.o.sb + at.h * p.o.sh + at.n * p.o.sn;
-    const bool with_o = wg == 1 && at.valid;
-    lse2 = at.valid ? p.lse[at.index] * kLog2e : INFINITY;  // rows behind the last query: p = 0
+  // Q (first warpgroup) or dO (second) of a tile to tensor memory; its rows' statistics.
+  auto stage = [&](const RowAt& at, float& nl, float& nd) -> bool {
+    const float lse = at.valid ? p.lse[at.index] : INFINITY;  // behind the last query: p = 0
     if (!wait_e(bar(s, A_QFULL), qr.phase)) return false;
     qr.next();
     const uint32_t src = wg ? l.dout : l.q, dst = lane + (wg ? kTdo : kTq);
     const bool inside = r < p.box_n * p.box_h;
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < dim16; ++k) {
       uint32_t w[8];
 #pragma unroll
@@ -263,32 +263,33 @@ __device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t
         w[4 * x + 3] = inside ? v.w : 0u;
       }
       tmem_st8(dst + 8 * k, w);
-      if (with_o) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          part = dot8<E>(make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]),
-                         reinterpret_cast<const uint4*>(o)[2 * k + x], part);
-      }
     }
     tmem_wait_st();
     tc_fence_before();
     warp_arrive(bar(s, A_TFULL));
-    warp_arrive(bar(s, A_QEMPTY));
-    if (wg == 1) {
-      l.delta[r] = part;
-      if (at.valid && p.delta) p.delta[at.index] = part;
-    }
+    // its half of delta
+    int d0, nd16;
+    share_of(dim16, wg, d0, nd16);
+    float half = 0.f;
+#pragma unroll 4
+    for (int k = 2 * d0; k < 2 * (d0 + nd16); ++k)
+      half = dot8<E>(ld_shared_v4(swizzled(l.dout, r, k)), ld_shared_v4(swizzled(l.out, r, k)), half);
+    l.part[wg * kRows + r] = half;
     warp_arrive(bar(s, A_XCH));
     if (!wait_e(bar(s, A_XCH), xr.phase)) return false;
     xr.next();
-    delta = l.delta[r];
+    const float delta = l.part[r] + l.part[kRows + r];
+    warp_arrive(bar(s, A_QEMPTY));  // (the halves are read, too, before the next tile's are written)
+    nl = -lse * kLog2e;
+    nd = inside ? -delta : 0.f;
+    if (wg && at.valid && p.delta) p.delta[at.index] = delta;
     return true;
   };
   // this tile's rows: statistics of the next one are taken before its epilogue
   int i = blockIdx.x;
   TileA t{};
   RowAt at{};
-  float lse2 = 0.f, delta = 0.f;
+  float next_nl = 0.f, next_nd = 0.f;
   auto open = [&]() -> bool {  // to the next tile with keys; others' rows are zero
     for (; i < p.items; i += gridDim.x) {
       t = tile_a(p, i);
@@ -296,21 +297,19 @@ __device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t
       tile_at(p, t.e, t.tile, n0, h0);
       at = row_at(p, t.b, n0, h0, r);
       if (t.steps) break;
-      if (at.valid && p.dq.data && wg == 0) {
+      if (at.valid && wg == 0) {
         E* to = static_cast<E*>(const_cast<void*>(p.dq.data)) + t.b * p.dq.sb + at.h * p.dq.sh +
                 at.n * p.dq.sn;
         for (int k = 0; k < 2 * dim16; ++k) reinterpret_cast<uint4*>(to)[k] = make_uint4(0, 0, 0, 0);
       }
-      if (at.valid && p.delta && wg == 1) p.delta[at.index] = 0.f;
     }
-    return i >= p.items || stage(t, at, lse2, delta);
+    return i >= p.items || stage(at, next_nl, next_nd);
   };
   if (!open()) return;
   while (i < p.items) {
     const TileA cur = t;
     const RowAt cur_at = at;
-    const float nl = -lse2, nd = -delta;
-    const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    const uint64_t nl2 = f2_pack(next_nl, next_nl), nd2 = f2_pack(next_nd, next_nd);
     for (int j = 0; j < cur.steps; ++j) {
       const int rem = cur.len - j * kRows;
       const int chunks = rem >= kRows ? 8 : (rem + 15) / 16;
@@ -348,24 +347,32 @@ __device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t
       }
       if (!wait_e(bar(s, A_PFULL), pr.phase)) return;
       pr.next();
-      uint32_t w[4][8];
+      uint32_t w[4][8], dp[4][16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld16(lane + kTdp + 16 * (c0 + k), dp[k]);
+      tmem_wait_ld();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t d[16];
-        tmem_ld16(lane + kTdp + 16 * (c0 + k), d);
-        tmem_wait_ld16(d);
+        reg_fence16(dp[k]);
+        uint32_t(&d)[16] = dp[k];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           float2 v = f2_unpack(f2_mul(
               f2_add(f2_pack(__uint_as_float(d[2 * x]), __uint_as_float(d[2 * x + 1])), nd2),
               f2_pack(__uint_as_float(pv[k][2 * x]), __uint_as_float(pv[k][2 * x + 1]))));
-          const int col = 16 * (c0 + k) + 2 * x;
-          if (rem < kRows) {
-            if (col >= rem) v.x = 0.f;
-            if (col + 1 >= rem) v.y = 0.f;
-          }
           w[k][x] = pack_pair(v.x, v.y, E());
         }
+      }
+      if (rem < kRows) {
+        asm volatile("" ::: "memory");  // a branch, not selections in every step
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int col = 16 * (c0 + k) + 2 * x;
+            if (col >= rem) w[k][x] = 0u;
+            else if (col + 1 >= rem) w[k][x] &= 0xffffu;
+          }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -387,26 +394,29 @@ __device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t
             cur_at.n * p.dq.sn;
     int n0, h0;
     tile_at(p, cur.e, cur.tile, n0, h0);
-#pragma unroll 1
-    for (int k = c0; k < c0 + nc; ++k) {
-      uint32_t d[16];
-      tmem_ld16(lane + kTdq + 16 * k, d);
-      tmem_wait_ld16(d);
+    uint32_t acc[4][16];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tmem_ld16(lane + kTdq + 16 * (c0 + k), acc[k]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      reg_fence16(acc[k]);
+      if (k >= nc) continue;
       uint32_t w[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x)
-        w[x] = pack_pair(__uint_as_float(d[2 * x]) * p.scale, __uint_as_float(d[2 * x + 1]) * p.scale, E());
-      if (!p.dq.data) continue;
+        w[x] = pack_pair(__uint_as_float(acc[k][2 * x]) * p.scale,
+                         __uint_as_float(acc[k][2 * x + 1]) * p.scale, E());
       if (whole) {
-        st_shared_v4(swizzled(l.out, r, 2 * k), w[0], w[1], w[2], w[3]);
-        st_shared_v4(swizzled(l.out, r, 2 * k + 1), w[4], w[5], w[6], w[7]);
+        st_shared_v4(swizzled(l.out, r, 2 * (c0 + k)), w[0], w[1], w[2], w[3]);
+        st_shared_v4(swizzled(l.out, r, 2 * (c0 + k) + 1), w[4], w[5], w[6], w[7]);
       } else if (cur_at.valid) {
-        reinterpret_cast<uint4*>(to)[2 * k] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(to)[2 * k + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        reinterpret_cast<uint4*>(to)[2 * (c0 + k)] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(to)[2 * (c0 + k) + 1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
     tc_fence_before();
-    if (whole && p.dq.data) {
+    if (whole) {
       // both warpgroups' columns are in shared memory before the first one's
       // warps send them, and read from there before the next tile's
       fence_proxy_async_smem();
@@ -420,11 +430,8 @@ __device__ void dq_elements(const CrossParams& p, const LayoutA<DB>& l, uint32_t
         bulk_wait_read_all();
       }
     }
-    // dQ and the output tile are free: the next dS says so to the MMAs, this
-    // to the other warpgroup
-    warp_arrive(bar(s, A_XCH));
-    if (!wait_e(bar(s, A_XCH), xr.phase)) return;
-    xr.next();
+    // dQ is free (the next dS says so to the MMAs), and so is the output tile
+    warp_arrive(bar(s, A_OUTEMPTY));
   }
 }
 
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * A_COUNT);
   l.s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   l.s.status = p.status;
-  l.delta = reinterpret_cast<float*>(tslot + 4);
+  l.part = reinterpret_cast<float*>(gb + 256);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar(l.s, A_QFULL), 1);
@@ -456,9 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     mbar_init(bar(l.s, A_DSFULL), kEltWarps);
     mbar_init(bar(l.s, A_OFULL), 1);
     mbar_init(bar(l.s, A_XCH), kEltWarps);
+    mbar_init(bar(l.s, A_OUTEMPTY), kEltWarps);
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(bar(l.s, A_KVFULL + i), 1);
-      mbar_init(bar(l.s, A_KVEMPTY + i), 1);
+      mbar_init(bar(l.s, A_KVEMPTY + i), i % 2 ? 1 : 2);  // steps of v, of k
     }
     *l.s.abort_flag = 0;
     fence_barrier_init();
@@ -478,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   griddep_wait();
   if (warp == 0) {
     if (lane == 0) dq_producer<DB>(p, l);
-  } else if (warp == 1) {
-    dq_issuer<BF16, DB>(p, l, tbase);
+  } else if (warp < 3) {
+    dq_issuer<BF16, DB>(p, l, tbase, warp == 2);
   } else if (warp >= 4) {
     dq_elements<BF16, DB>(p, l, tbase);
     if (lane == 0) bulk_wait_all();
@@ -495,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
 // all of it.  P^T takes S^T's place and dS^T dP^T's; both are the A operands
 // of the sums, so nothing goes through shared memory.
 //   warp 0     TMA: the key tile (k and v), row tiles of q and dout (a ring)
-//   warp 1     MMA, in the order  S(j+1), dK(j), dP(j+1), dV(j+1):  p(j+1) is
-//              formed beside dK(j) and dP(j+1), ds(j+1) beside dV(j+1) and S(j+2)
-//   warp 2     the row tiles' lse and delta
+//   warps 1, 2 MMA: S(j), dV(j), S(j+1), ... and dP(j), dK(j), dP(j+1), ...:
+//              p is formed beside the second's products, ds beside the first's
+//   warp 3     the row tiles' lse and delta
 //   warps 4-11 two warpgroups: thread = key, each half of a tile's queries
 //
 // The units of work are (key tile, row tile) in order; a CTA takes a
@@ -669,15 +677,20 @@ __device__ void dkv_stats(const CrossParams& p, const LayoutB<DB>& l, WalkB w) {
   }
 }
 
+// Two issuers: S with dV (P's side), and dP with dK (dS's).
 template <bool BF16, int DB>
-__device__ void dkv_issuer(const CrossParams& p, const LayoutB<DB>& l, uint32_t tbase, WalkB w) {
+__device__ void dkv_issuer(const CrossParams& p, const LayoutB<DB>& l, uint32_t tbase, WalkB w, bool ds) {
   const Sync& s = l.s;
-  const int ksteps = p.dim / 16;
+  const int chunks_d = p.dim / 16;
   const uint32_t id_s = idesc_16_f32(kRows, kRows, BF16, false, false);
   const uint32_t id_d = idesc_16_f32(kRows, p.dim, BF16, false, true);
-  constexpr uint64_t kTile16 = LayoutB<DB>::kTile >> 4, kBox16 = kBoxBytes >> 4;
-  const uint64_t k0 = sdesc_sw128(l.k, 16, 1024), v0 = sdesc_sw128(l.v, 16, 1024);
-  const uint64_t q0 = sdesc_sw128(l.q, 16, 1024), qt0 = sdesc_sw128(l.q, kBoxBytes, 1024);
+  constexpr uint64_t kTile16 = LayoutB<DB>::kTile >> 4;
+  // P^T's side: K, q, dO;  dS^T's side: V, dO, q
+  const uint64_t a0 = sdesc_sw128(ds ? l.v : l.k, 16, 1024);
+  const uint64_t b0 = sdesc_sw128(l.q, 16, 1024) + (ds ? kTile16 : 0);
+  const uint64_t c0 = sdesc_sw128(l.q, kBoxBytes, 1024) + (ds ? 0 : kTile16);
+  const uint32_t t_x = tbase + (ds ? kTdpt : kTst), t_sum = tbase + (ds ? kTdk : kTdv);
+  const uint32_t made = bar(s, ds ? B_DPFULL : B_SFULL), taken = bar(s, ds ? B_DSFULL : B_PFULL);
   // queries of a row tile, in whole chunks of 16
   const int chunks = (p.box_n * p.box_h + 15) / 16;
   auto wait_mma = [&](uint32_t b, uint32_t parity) {
@@ -685,71 +698,40 @@ __device__ void dkv_issuer(const CrossParams& p, const LayoutB<DB>& l, uint32_t 
     tc_fence_after();
     return ok;
   };
-  auto keys_by_rows = [&](uint32_t d, uint64_t a, uint64_t b) {
-    for (int kk = 0; kk < ksteps; ++kk) {
-      const uint64_t off = static_cast<uint64_t>(kk >> 2) * kBox16 + (kk & 3) * 2;
-      mma_ss_warp(tbase + d, a + off, b + off, id_s, kk > 0 ? 1u : 0u);
-    }
-  };
-  auto sum_rows = [&](uint32_t d, uint32_t a, uint64_t b, bool add) {
-    for (int kk = 0; kk < chunks; ++kk)
-      mma_ts_warp(tbase + d, tbase + a + chunk_at(kk, chunks), b + kk * 128, id_d,
-                  kk > 0 || add ? 1u : 0u);
-  };
-  Ring<1> kr, pr, dsr, ar;
+  Ring<1> kr, tr, ar;
   Ring<kStages> qr;
-  if (w.left <= 0) return;
-  // S of the first unit
   bool first = true;  // of its key tile in this share
-  if (!wait_mma(bar(s, B_KFULL), kr.phase)) return;
-  kr.next();
-  if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return;
-  keys_by_rows(kTst, k0, q0 + qr.slot * 2 * kTile16);
-  tc_commit_warp(bar(s, B_SFULL));
-  keys_by_rows(kTdpt, v0, q0 + (qr.slot * 2 + 1) * kTile16);
-  tc_commit_warp(bar(s, B_DPFULL));
+  // S^T or dP^T of a unit (behind the last one's sum, which read what takes its place)
+  auto make = [&](bool fresh) {
+    if (fresh) {
+      if (!wait_mma(bar(s, B_KFULL), kr.phase)) return false;
+      kr.next();
+    }
+    if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return false;
+    issue_ss(t_x, a0, b0 + qr.slot * 2 * kTile16, id_s, chunks_d);
+    tc_commit_warp(made);
+    return true;
+  };
+  if (w.left <= 0 || !make(true)) return;
   while (w.left > 0) {
     const uint32_t slot = qr.slot;
     qr.next();
     const bool last = last_b(p, w);
-    WalkB nxt = w;
-    step_b(p, nxt);
-    const bool more = nxt.left > 0;
-    // dV += P^T dO
-    if (!wait_mma(bar(s, B_PFULL), pr.phase)) return;
-    pr.next();
-    if (first && !wait_mma(bar(s, B_ACCEMPTY), ar.phase ^ 1u)) return;
-    sum_rows(kTdv, kTst, qt0 + (slot * 2 + 1) * kTile16, !first);
-    // S of the next unit, in P^T's place (behind dV)
-    if (more && !last) {
-      if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return;
-      keys_by_rows(kTst, k0, q0 + qr.slot * 2 * kTile16);
-      tc_commit_warp(bar(s, B_SFULL));
-    }
-    // dK += dS^T Q
-    if (!wait_mma(bar(s, B_DSFULL), dsr.phase)) return;
-    dsr.next();
-    sum_rows(kTdk, kTdpt, qt0 + slot * 2 * kTile16, !first);
-    tc_commit_warp(bar(s, B_QEMPTY + slot));
-    first = false;
-    if (last) {
+    step_b(p, w);
+    if (!wait_mma(taken, tr.phase)) return;
+    tr.next();
+    if (first) {
+      if (!wait_mma(bar(s, B_ACCEMPTY), ar.phase ^ 1u)) return;
       ar.next();
+    }
+    issue_sum(t_sum, t_x, second_at(chunks), c0 + slot * 2 * kTile16, id_d, chunks, !first);
+    tc_commit_warp(bar(s, B_QEMPTY + slot));
+    first = last;
+    if (last) {
       tc_commit_warp(bar(s, B_ACCFULL));
       tc_commit_warp(bar(s, B_KEMPTY));
-      first = true;
-      if (more) {
-        if (!wait_mma(bar(s, B_KFULL), kr.phase)) return;
-        kr.next();
-        if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return;
-        keys_by_rows(kTst, k0, q0 + qr.slot * 2 * kTile16);
-        tc_commit_warp(bar(s, B_SFULL));
-      }
     }
-    if (more) {
-      keys_by_rows(kTdpt, v0, q0 + (qr.slot * 2 + 1) * kTile16);
-      tc_commit_warp(bar(s, B_DPFULL));
-    }
-    w = nxt;
+    if (w.left > 0 && !make(last)) return;
   }
 }
 
@@ -912,17 +894,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar(l.s, B_KFULL), 1);
-    mbar_init(bar(l.s, B_KEMPTY), 1);
+    mbar_init(bar(l.s, B_KEMPTY), 2);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(l.s, B_QFULL + i), 1);
-      mbar_init(bar(l.s, B_QEMPTY + i), 1 + kEltWarps);
+      mbar_init(bar(l.s, B_QEMPTY + i), 2 + kEltWarps);
       mbar_init(bar(l.s, B_STFULL + i), 1);
     }
     mbar_init(bar(l.s, B_SFULL), 1);
     mbar_init(bar(l.s, B_PFULL), kEltWarps);
     mbar_init(bar(l.s, B_DPFULL), 1);
     mbar_init(bar(l.s, B_DSFULL), kEltWarps);
-    mbar_init(bar(l.s, B_ACCFULL), 1);
+    mbar_init(bar(l.s, B_ACCFULL), 2);
     mbar_init(bar(l.s, B_ACCEMPTY), kEltWarps);
     *l.s.abort_flag = 0;
     fence_barrier_init();
@@ -951,9 +933,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   const WalkB w = walk_b(p, first_unit(p, units, blockIdx.x), first_unit(p, units, blockIdx.x + 1));
   if (warp == 0) {
     if (lane == 0) dkv_producer<DB>(p, l, w);
-  } else if (warp == 1) {
-    dkv_issuer<BF16, DB>(p, l, tbase, w);
-  } else if (warp == 2) {
+  } else if (warp < 3) {
+    dkv_issuer<BF16, DB>(p, l, tbase, w, warp == 2);
+  } else if (warp == 3) {
     dkv_stats<BF16, DB>(p, l, w);
   } else if (warp >= 4) {
     dkv_elements<BF16, DB>(p, l, tbase, w);
@@ -965,8 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
 }
 
 // Key tiles that several shares hold parts of: their sums, in the shares'
-// order; keys behind the lengths: zeros.  A CTA a key tile (of all, with keys
-// or without), a thread four columns of a row.
+// order; keys behind the lengths: zeros.  A CTA eight rows of a key tile (of
+// all, with keys or without), a thread four columns of a row.
 template <bool BF16>
 __global__ void __launch_bounds__(256) cross_finish_kernel(const __grid_constant__ CrossParams p) {
   using E = typename Elem<BF16>::type;
@@ -987,29 +969,27 @@ __global__ void __launch_bounds__(256) cross_finish_kernel(const __grid_constant
     c1 = ((begin + rows) * p.ctas - 1) / units;
     if (c0 == c1) return;  // finished in its share
   }
-  const int cols = p.dim / 4;
-  for (int x = threadIdx.x; x < 2 * kRows * cols; x += 256) {
-    const int c = x % cols * 4, r = x / cols % kRows, which = x / cols / kRows;  // 0: dk, 1: dv
-    const int key = kt * kRows + r;
-    const CrossView& g = which ? p.dv : p.dk;
-    if (key >= p.m || !g.data) continue;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t i = c0; key < len && i <= c1; ++i) {
-      const int64_t first = first_unit(p, units, static_cast<int>(i));
-      if (first == first_unit(p, units, static_cast<int>(i) + 1)) continue;  // an empty share
-      const int slot = first > begin ? 0 : 1;
-      const float4 t = *reinterpret_cast<const float4*>(
-          p.part_kv + (((i * 2 + slot) * 2 + which) * kRows + r) * p.dim + c);
-      v[0] += t.x;
-      v[1] += t.y;
-      v[2] += t.z;
-      v[3] += t.w;
-    }
-    const float scale = which ? (BF16 ? 1.f : 0.0009765625f) : p.scale;
-    E* to = static_cast<E*>(const_cast<void*>(g.data)) + b * g.sb + e * g.sh + key * g.sn + c;
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair(v[0] * scale, v[1] * scale, E()),
-                                               pack_pair(v[2] * scale, v[3] * scale, E()));
+  // grid row y: rows y * 8 .. of dk (y < 16) or dv
+  const int which = blockIdx.y / 16, c = 4 * (threadIdx.x & 31), r = blockIdx.y % 16 * 8 + threadIdx.x / 32;
+  const int key = kt * kRows + r;
+  const CrossView& g = which ? p.dv : p.dk;
+  if (key >= p.m || c >= p.dim || !g.data) return;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t i = c0; key < len && i <= c1; ++i) {
+    const int64_t first = first_unit(p, units, static_cast<int>(i));
+    if (first == first_unit(p, units, static_cast<int>(i) + 1)) continue;  // an empty share
+    const int slot = first > begin ? 0 : 1;
+    const float4 t = *reinterpret_cast<const float4*>(
+        p.part_kv + (((i * 2 + slot) * 2 + which) * kRows + r) * p.dim + c);
+    v[0] += t.x;
+    v[1] += t.y;
+    v[2] += t.z;
+    v[3] += t.w;
   }
+  const float scale = which ? (BF16 ? 1.f : 0.0009765625f) : p.scale;
+  E* to = static_cast<E*>(const_cast<void*>(g.data)) + b * g.sb + e * g.sh + key * g.sn + c;
+  *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair(v[0] * scale, v[1] * scale, E()),
+                                             pack_pair(v[2] * scale, v[3] * scale, E()));
 }
 
 // delta alone, where dq is not wanted: a thread a row, its sum in the order of
@@ -1027,9 +1007,14 @@ __global__ void __launch_bounds__(128) cross_delta_kernel(const __grid_constant_
                                                   h * p.o.sh + n * p.o.sn);
   const uint4* d = reinterpret_cast<const uint4*>(static_cast<const E*>(p.dout.data) +
                                                   b * p.dout.sb + h * p.dout.sh + n * p.dout.sn);
-  float part = 0.f;
-  for (int k = 0; k < p.dim / 8; ++k) part = dot8<E>(d[k], o[k], part);
-  p.delta[row] = part;
+  int d0, nd;
+  float half[2];
+  for (int w = 0; w < 2; ++w) {
+    share_of(p.dim / 16, w, d0, nd);
+    half[w] = 0.f;
+    for (int k = 2 * d0; k < 2 * (d0 + nd); ++k) half[w] = dot8<E>(d[k], o[k], half[w]);
+  }
+  p.delta[row] = half[0] + half[1];
 }
 
 template <typename F>
@@ -1047,10 +1032,10 @@ cudaError_t run(F* kernel, bool* attr_set, const CrossParams& p, int grid, size_
 
 template <bool BF16, int DB>
 cudaError_t backward(const CrossParams& p, int sms, cudaStream_t s) {
-  constexpr size_t kSmemA = 1024 + (3 + kSteps) * LayoutA<DB>::kTile + 8 * A_COUNT + 16 + 4 * kRows;
+  constexpr size_t kSmemA = 1024 + (3 + kSteps) * LayoutA<DB>::kTile + 256 + kRows * 8;
   constexpr size_t kSmemB = 1024 + (2 + 2 * kStages) * LayoutB<DB>::kTile + 256 + kStages * 2 * kRows * 4;
   static_assert(kSmemA <= 232448 && kSmemB <= 232448, "shared memory of a CTA");
-  static_assert(8 * B_COUNT + 16 <= 256, "barriers of the dk, dv kernel");
+  static_assert(8 * A_COUNT + 16 <= 256 && 8 * B_COUNT + 16 <= 256, "barriers");
   static bool set_a[kMaxDevices] = {}, set_b[kMaxDevices] = {};
   const bool keys = (p.dk.data || p.dv.data) && p.m > 0;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.heads * p.n;
@@ -1065,8 +1050,8 @@ cudaError_t backward(const CrossParams& p, int sms, cudaStream_t s) {
   }
   if (e != cudaSuccess || !keys) return e;
   const int64_t tiles = static_cast<int64_t>(p.batch) * p.kv_heads * ((p.m + kRows - 1) / kRows);
-  return launch_dependent(cross_finish_kernel<BF16>, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s,
-                          p);
+  return launch_dependent(cross_finish_kernel<BF16>, dim3(static_cast<unsigned>(tiles), 32), dim3(256), 0,
+                          s, p);
 }
 
 }  // namespace

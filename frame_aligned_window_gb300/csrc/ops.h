@@ -261,7 +261,7 @@ struct CrossView {
 struct CrossParams {
   CUtensorMap tm_q;                    // {D, n, heads, batch}, box {64, box_n, box_h, 1}
   CUtensorMap tm_k, tm_v;              // {D, m, kv heads, batch}, box {64, 128, 1, 1}
-  CUtensorMap tm_o;                    // {D, n, heads, batch}, box {64, 32, 1, 1}
+  CUtensorMap tm_o;                    // {D, n, heads, batch}, box {64, 32, 1, 1}; the backward reads it: as tm_q
   CrossView q, k, v, o, dout;          // o: the forward's output (written, or read by the backward)
   CrossView dq, dk, dv;
   const int32_t* lengths;              // [batch] keys that count, or null: all
@@ -282,8 +282,8 @@ struct CrossParams {
   float* part_l;                       // [splits][batch, heads, n] log2 of the sums
   // backward: dq by row tiles, dk and dv by key tiles
   CUtensorMap tm_do;                   // like tm_q
-  CUtensorMap tm_dq;                   // like tm_o
-  int do_h, do_b;
+  CUtensorMap tm_dq;                   // like the forward's tm_o
+  int do_h, do_b, o_h, o_b;
   float* delta;                        // [batch, heads, n] sum_d dout out
   float* part_kv;                      // [ctas][2][dk, dv][128][D] sums of shares of a key tile
   int ctas;                            // of the dk, dv kernel
