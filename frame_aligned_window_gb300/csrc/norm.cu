@@ -39,46 +39,53 @@ __global__ void __launch_bounds__(384) norm_forward_kernel(const __grid_constant
     for (int j = 0; j < V; ++j)
       rr[j] = load_raw(static_cast<const R*>(p.res) + row * p.ldr, n, column(lane, threads, j), vec);
   }
-  float h[V][8];
+  Pairs h[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) unpack(xr[j], h[j]);
 
-  auto inside = [&](int j, int i) { return column(lane, threads, j) + i < n; };
   // h becomes std(h); elements behind the row's end stay zero
   auto standardise = [&](int kind) {
+    uint64_t t;
     if (kind == WSATTN_NORM_LAYER) {
-      float s[1] = {0.f};
+      t = f2_pack(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += h[j][i];
+        for (int i = 0; i < 4; ++i) t = f2_add(t, h[j][i]);
+      float2 v = f2_unpack(t);
+      float s[1] = {v.x + v.y};
       row_sums(rd, s);
       const float mean = s[0] * inv_n;
+      const uint64_t m2 = f2_pack(-mean, -mean);
 #pragma unroll
-      for (int j = 0; j < V; ++j)
+      for (int j = 0; j < V; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (inside(j, i)) h[j][i] -= mean;
+        for (int i = 0; i < 4; ++i) h[j][i] = f2_add(h[j][i], m2);
+        trim(h[j], column(lane, threads, j), n);
+      }
     }
-    float q[1] = {0.f};
+    t = f2_pack(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[0] = fmaf(h[j][i], h[j][i], q[0]);
+      for (int i = 0; i < 4; ++i) t = f2_fma(h[j][i], h[j][i], t);
+    const float2 v = f2_unpack(t);
+    float q[1] = {v.x + v.y};
     row_sums(rd, q);
     const float r = rsqrtf(fmaf(q[0], inv_n, p.eps));
+    const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] *= r;
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_mul(h[j][i], r2);
   };
   auto times = [&](const void* v, int64_t at, int f32) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float f[8];
+      Pairs f;
       vector8<T>(v, at, f32, n, column(lane, threads, j), vec, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] *= f[i];
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_mul(h[j][i], f[i]);
     }
   };
 
@@ -88,12 +95,13 @@ __global__ void __launch_bounds__(384) norm_forward_kernel(const __grid_constant
   }
   if (p.gate) times(p.gate, g * p.ldg, p.mod_f32);
   if (p.res) {
+    const uint64_t s2 = f2_pack(p.res_scale, p.res_scale);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float f[8];
+      Pairs f;
       unpack(rr[j], f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = fmaf(p.res_scale, f[i], h[j][i]);
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_fma(s2, f[i], h[j][i]);
     }
   }
   if (p.hidden) {
@@ -106,30 +114,28 @@ __global__ void __launch_bounds__(384) norm_forward_kernel(const __grid_constant
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = column(lane, threads, j);
-    float f[8], y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = h[j][i];
+    Pairs f;
     if (p.weight) {
       vector8<T>(p.weight, 0, p.weight_f32, n, c, vec, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= f[i];
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_mul(h[j][i], f[i]);
     }
     if (p.bias) {
       vector8<T>(p.bias, 0, p.weight_f32, n, c, vec, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += f[i];
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_add(h[j][i], f[i]);
     }
     if (p.scale) {
       vector8<T>(p.scale, g * p.lds, p.mod_f32, n, c, vec, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i], f[i], y[i]);
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_fma(h[j][i], f[i], h[j][i]);
     }
     if (p.shift) {
       vector8<T>(p.shift, g * p.ldf, p.mod_f32, n, c, vec, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += f[i];
+      for (int i = 0; i < 4; ++i) h[j][i] = f2_add(h[j][i], f[i]);
     }
-    store8(static_cast<T*>(p.out) + row * p.ldo, n, c, vec, y);
+    store8(static_cast<T*>(p.out) + row * p.ldo, n, c, vec, h[j]);
   }
 }
 

@@ -73,51 +73,71 @@ __device__ __forceinline__ Raw8<T> load_raw(const T* row, int n, int c, bool vec
   }
   return r;
 }
-__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&f)[8]) {
-  f[0] = __uint_as_float(r.a.x), f[1] = __uint_as_float(r.a.y);
-  f[2] = __uint_as_float(r.a.z), f[3] = __uint_as_float(r.a.w);
-  f[4] = __uint_as_float(r.b.x), f[5] = __uint_as_float(r.b.y);
-  f[6] = __uint_as_float(r.b.z), f[7] = __uint_as_float(r.b.w);
+// Eight columns as four fp32 pairs (the arithmetic is on pairs: half the
+// instructions of single values).
+typedef uint64_t Pairs[4];
+__device__ __forceinline__ void unpack(const Raw8<float>& r, Pairs& f) {
+  f[0] = f2_pack(__uint_as_float(r.a.x), __uint_as_float(r.a.y));
+  f[1] = f2_pack(__uint_as_float(r.a.z), __uint_as_float(r.a.w));
+  f[2] = f2_pack(__uint_as_float(r.b.x), __uint_as_float(r.b.y));
+  f[3] = f2_pack(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
 }
 template <typename T>
-__device__ __forceinline__ void unpack(const Raw8<T>& r, float (&f)[8]) {
+__device__ __forceinline__ void unpack(const Raw8<T>& r, Pairs& f) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = unpack_pair(w[i], T());
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
+    f[i] = f2_pack(v.x, v.y);
+  }
+}
+__device__ __forceinline__ void fill(Pairs& f, float v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_pack(v, v);
+}
+// Columns behind the row's end (n) become zero.
+__device__ __forceinline__ void trim(Pairs& f, int c, int n) {
+  if (c + 8 <= n) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = f2_unpack(f[i]);
+    f[i] = f2_pack(c + 2 * i < n ? v.x : 0.f, c + 2 * i + 1 < n ? v.y : 0.f);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* row, int n, int c, bool vec, const float (&f)[8]) {
+__device__ __forceinline__ void store8(T* row, int n, int c, bool vec, const Pairs& f) {
+  const float2 a = f2_unpack(f[0]), b = f2_unpack(f[1]), d = f2_unpack(f[2]), e = f2_unpack(f[3]);
   if (vec) {
     if (c >= n) return;
     if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(row + c) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(row + c + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      *reinterpret_cast<float4*>(row + c) = make_float4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<float4*>(row + c + 4) = make_float4(d.x, d.y, e.x, e.y);
     } else {
       *reinterpret_cast<uint4*>(row + c) =
-          make_uint4(pack_pair(f[0], f[1], T()), pack_pair(f[2], f[3], T()),
-                     pack_pair(f[4], f[5], T()), pack_pair(f[6], f[7], T()));
+          make_uint4(pack_pair(a.x, a.y, T()), pack_pair(b.x, b.y, T()), pack_pair(d.x, d.y, T()),
+                     pack_pair(e.x, e.y, T()));
     }
   } else {
+    const float v[8] = {a.x, a.y, b.x, b.y, d.x, d.y, e.x, e.y};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < n) row[c + i] = from_f32<T>(f[i]);
+      if (c + i < n) row[c + i] = from_f32<T>(v[i]);
   }
 }
 
 // Columns c .. c + 7 of a vector (gate, weight, ...) of fp32 values or of T.
 template <typename T>
 __device__ __forceinline__ void vector8(const void* v, int64_t at, bool f32, int n, int c, bool vec,
-                                        float (&f)[8]) {
+                                        Pairs& f) {
   const float* pf = static_cast<const float*>(v) + at + c;
   const T* pt = static_cast<const T*>(v) + at + c;
   if (!vec) {
+    float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i >= n ? 0.f : f32 ? pf[i] : to_f32(pt[i]);
+    for (int i = 0; i < 8; ++i) t[i] = c + i >= n ? 0.f : f32 ? pf[i] : to_f32(pt[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2_pack(t[2 * i], t[2 * i + 1]);
     return;
   }
   Raw8<float> r;

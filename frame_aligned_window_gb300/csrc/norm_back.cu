@@ -76,7 +76,7 @@ __device__ __forceinline__ void copy_row(uint32_t at, const T* row, int n, int l
   }
 }
 template <typename T>
-__device__ __forceinline__ void piece(uint32_t at, int n, int c, float (&f)[8]) {
+__device__ __forceinline__ void piece(uint32_t at, int n, int c, Pairs& f) {
   Raw8<T> r;
   r.a = make_uint4(0, 0, 0, 0);
   if constexpr (sizeof(T) == 4) r.b = r.a;
@@ -85,6 +85,10 @@ __device__ __forceinline__ void piece(uint32_t at, int n, int c, float (&f)[8]) 
     if constexpr (sizeof(T) == 4) r.b = ld_shared_v4(at + c * 4 + 16);
   }
   unpack(r, f);
+}
+__device__ __forceinline__ float both(uint64_t v) {
+  const float2 t = f2_unpack(v);
+  return t.x + t.y;
 }
 
 template <typename T, typename R, int V, int MAXT, int MINB>
@@ -114,19 +118,26 @@ __global__ void __launch_bounds__(MAXT, MINB)
                                    threads == static_cast<int>(blockDim.x) && p.stages >= 1))
     return;
 
-  float a_sum[V][8], b_sum[V][8], e_sum[V][8];
+  Pairs a_sum[V], b_sum[V], e_sum[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a_sum[j][i] = b_sum[j][i] = e_sum[j][i] = 0.f;
+  for (int j = 0; j < V; ++j) {
+    fill(a_sum[j], 0.f);
+    fill(b_sum[j], 0.f);
+    fill(e_sum[j], 0.f);
+  }
   bool first_flush = true;
 
-  // times (or plus) a vector's columns
-  auto scaled = [&](const void* v, int64_t at, int f32, int c, float add, float (&t)[8]) {
-    float f[8];
+  // times (a vector's columns + add)
+  auto scaled = [&](const void* v, int64_t at, int f32, int c, float add, Pairs& t) {
+    Pairs f;
     vector8<T>(v, at, f32 != 0, n, c, vec, f);
+    const uint64_t a2 = f2_pack(add, add);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] *= f[i] + add;
+    for (int i = 0; i < 4; ++i) t[i] = add == 0.f ? f2_mul(t[i], f[i]) : f2_mul(t[i], f2_add(f[i], a2));
+  };
+  auto copy = [](Pairs& to, const Pairs& from) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = from[i];
   };
   // The sums of group g over this share's rows are complete: out with them.
   auto flush = [&](int64_t g) {
@@ -137,26 +148,23 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = column(lane, threads, j);
-      float t[8], u[8];
+      Pairs t, u;
       if (p.wpart) {
         auto add = [&](float* to) {  // t, to what earlier groups left
           if (!first_flush) {
             vector8<float>(to, 0, true, n, c, vec, u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] += u[i];
+            for (int i = 0; i < 4; ++i) t[i] = f2_add(t[i], u[i]);
           }
           store8(to, n, c, vec, t);
         };
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = a_sum[j][i];
+        copy(t, a_sum[j]);
         if (p.scale) scaled(p.scale, g * p.lds, p.mod_f32, c, 1.f, t);
         add(wpart);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = b_sum[j][i];
+        copy(t, b_sum[j]);
         if (p.scale) scaled(p.scale, g * p.lds, p.mod_f32, c, 1.f, t);
         add(wpart + n);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = e_sum[j][i];
+        copy(t, e_sum[j]);
         if (p.gate) scaled(p.gate, g * p.ldg, p.mod_f32, c, 0.f, t);
         add(wpart + 2 * n);
       }
@@ -168,26 +176,25 @@ __global__ void __launch_bounds__(MAXT, MINB)
         }
       } else {
         if (p.dscale) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = a_sum[j][i];
+          copy(t, a_sum[j]);
           if (p.weight) scaled(p.weight, 0, p.weight_f32, c, 0.f, t);
           if (p.bias) {
             vector8<T>(p.bias, 0, p.weight_f32 != 0, n, c, vec, u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = fmaf(b_sum[j][i], u[i], t[i]);
+            for (int i = 0; i < 4; ++i) t[i] = f2_fma(b_sum[j][i], u[i], t[i]);
           }
           store8(p.dscale + g * n, n, c, vec, t);
         }
         if (p.dshift) store8(p.dshift + g * n, n, c, vec, b_sum[j]);
         if (p.dgate) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = e_sum[j][i];
+          copy(t, e_sum[j]);
           if (p.post_weight) scaled(p.post_weight, 0, p.weight_f32, c, 0.f, t);
           store8(p.dgate + g * n, n, c, vec, t);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a_sum[j][i] = b_sum[j][i] = e_sum[j][i] = 0.f;
+      fill(a_sum[j], 0.f);
+      fill(b_sum[j], 0.f);
+      fill(e_sum[j], 0.f);
     }
     first_flush = false;
   };
@@ -228,11 +235,11 @@ __global__ void __launch_bounds__(MAXT, MINB)
     }
     if (++slot == static_cast<uint32_t>(p.stages)) slot = 0;
 
-    float h[V][8], d[V][8];  // h, then its deviations; g, then dh
+    Pairs h[V], d[V];  // h, then its deviations; g, then dh
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = d[j][i] = 0.f;
+      fill(h[j], 0.f);
+      fill(d[j], 0.f);
       if (dyp) {
         const int c = column(lane, threads, j);
         piece<R>(at + at_h, n, c, h[j]);
@@ -243,81 +250,107 @@ __global__ void __launch_bounds__(MAXT, MINB)
     }
     float mean = 0.f, x_mean = 0.f;
     if ((layer && dyp) || post_layer) {
-      float s[2] = {0.f, 0.f};
+      uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += h[j][i];
+        for (int i = 0; i < 4; ++i) s0 = f2_add(s0, h[j][i]);
         if (post_layer) {
-          float x[8];
+          Pairs x;
           piece<T>(at + at_x, n, column(lane, threads, j), x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[1] += x[i];
+          for (int i = 0; i < 4; ++i) s1 = f2_add(s1, x[i]);
         }
       }
-      row_sums(rd, s);
-      if (layer) mean = s[0] * inv_n;
-      x_mean = s[1] * inv_n;
+      if (post_layer) {
+        float s[2] = {both(s0), both(s1)};
+        row_sums(rd, s);
+        if (layer) mean = s[0] * inv_n;
+        x_mean = s[1] * inv_n;
+      } else {
+        float s[1] = {both(s0)};
+        row_sums(rd, s);
+        mean = s[0] * inv_n;
+      }
     }
     // squares of deviations, sums of g and of its product with them
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
+    const uint64_t mean2 = f2_pack(-mean, -mean), xmean2 = f2_pack(-x_mean, -x_mean);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = column(lane, threads, j);
+      if (layer) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[j][i] = c + i < n ? h[j][i] - mean : 0.f;
-        s[0] = fmaf(h[j][i], h[j][i], s[0]);
-        s[1] += d[j][i];
-        s[2] = fmaf(d[j][i], h[j][i], s[2]);
+        for (int i = 0; i < 4; ++i) h[j][i] = f2_add(h[j][i], mean2);
+        trim(h[j], c, n);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s0 = f2_fma(h[j][i], h[j][i], s0);
+        s1 = f2_add(s1, d[j][i]);
+        s2 = f2_fma(d[j][i], h[j][i], s2);
       }
       if (post) {
-        float x[8];
+        Pairs x;
         piece<T>(at + at_x, n, c, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float t = c + i < n ? x[i] - x_mean : 0.f;
-          s[3] = fmaf(t, t, s[3]);
-        }
+        for (int i = 0; i < 4; ++i) x[i] = f2_add(x[i], xmean2);
+        trim(x, c, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s3 = f2_fma(x[i], x[i], s3);
       }
     }
-    if (dyp || post) row_sums(rd, s);
+    float s[4] = {both(s0), both(s1), both(s2), 0.f};
+    if (post) {
+      s[3] = both(s3);
+      row_sums(rd, s);
+    } else if (dyp) {
+      float t[3] = {s[0], s[1], s[2]};
+      row_sums(rd, t);
+      s[0] = t[0], s[1] = t[1], s[2] = t[2];
+    }
     const float r = rsqrtf(fmaf(s[0], inv_n, p.eps));
     const float x_r = post ? rsqrtf(fmaf(s[3], inv_n, p.eps)) : 1.f;
     const float g_mean = layer ? s[1] * inv_n : 0.f;
     const float gs_mean = s[2] * r * inv_n;  // mean of g s
-    float ps[2] = {0.f, 0.f};
+    // dh = r g - r [mean g] - r s mean(g s), s = h r
+    const uint64_t r2 = f2_pack(r, r), rg2 = f2_pack(-r * g_mean, -r * g_mean);
+    const uint64_t rs2 = f2_pack(-r * gs_mean, -r * gs_mean), xr2 = f2_pack(x_r, x_r);
+    uint64_t p0 = f2_pack(0.f, 0.f), p1 = p0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = column(lane, threads, j);
-      float t[8];
+      Pairs t;
       if (dyp) {
         piece<T>(at, n, c, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float si = h[j][i] * r;
-          a_sum[j][i] = fmaf(t[i], si, a_sum[j][i]);
-          b_sum[j][i] += t[i];
-          d[j][i] = r * (d[j][i] - g_mean - si * gs_mean);
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t si = f2_mul(h[j][i], r2);
+          a_sum[j][i] = f2_fma(t[i], si, a_sum[j][i]);
+          b_sum[j][i] = f2_add(b_sum[j][i], t[i]);
+          d[j][i] = f2_fma(si, rs2, f2_fma(d[j][i], r2, rg2));
         }
       }
       if (dhp) {
         piece<R>(at + at_dh, n, c, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[j][i] += t[i];
+        for (int i = 0; i < 4; ++i) d[j][i] = f2_add(d[j][i], t[i]);
       }
       if (p.dres) {
+        const uint64_t k2 = f2_pack(p.res_scale, p.res_scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = p.res_scale * d[j][i];
+        for (int i = 0; i < 4; ++i) t[i] = f2_mul(k2, d[j][i]);
         store8(static_cast<R*>(p.dres) + row * p.lddr, n, c, vec, t);
       }
       if (xp) {
         piece<T>(at + at_x, n, c, t);
+        if (post) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          t[i] = c + i < n ? (t[i] - x_mean) * x_r : 0.f;
-          e_sum[j][i] = fmaf(d[j][i], t[i], e_sum[j][i]);
+          for (int i = 0; i < 4; ++i) t[i] = f2_mul(f2_add(t[i], xmean2), xr2);
+          trim(t, c, n);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e_sum[j][i] = f2_fma(d[j][i], t[i], e_sum[j][i]);
       }
       if (p.dx) {
         if (p.gate) scaled(p.gate, g * p.ldg, p.mod_f32, c, 0.f, d[j]);
@@ -325,24 +358,29 @@ __global__ void __launch_bounds__(MAXT, MINB)
           store8(static_cast<T*>(p.dx) + row * p.lddx, n, c, vec, d[j]);
         } else {
           if (p.post_weight) scaled(p.post_weight, 0, p.weight_f32, c, 0.f, d[j]);
+          trim(d[j], c, n);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (c + i < n) ps[0] += d[j][i];
-            ps[1] = fmaf(d[j][i], t[i], ps[1]);
+          for (int i = 0; i < 4; ++i) {
+            p0 = f2_add(p0, d[j][i]);
+            p1 = f2_fma(d[j][i], t[i], p1);
           }
         }
       }
     }
     if (post && p.dx) {
+      float ps[2] = {both(p0), both(p1)};
       row_sums(rd, ps);
       const float m1 = post_layer ? ps[0] * inv_n : 0.f, m2 = ps[1] * inv_n;
+      // dx = x_r (du - [mean du] - xh mean(du xh))
+      const uint64_t k1 = f2_pack(-m1, -m1), k2 = f2_pack(-x_r * m2, -x_r * m2);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = column(lane, threads, j);
-        float x[8];
+        Pairs x;
         piece<T>(at + at_x, n, c, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[j][i] = x_r * (d[j][i] - m1 - (x[i] - x_mean) * x_r * m2);
+        for (int i = 0; i < 4; ++i)
+          d[j][i] = f2_mul(xr2, f2_fma(f2_add(x[i], xmean2), k2, f2_add(d[j][i], k1)));
         store8(static_cast<T*>(p.dx) + row * p.lddx, n, c, vec, d[j]);
       }
     }
@@ -412,8 +450,8 @@ struct BackShape {
   int v, warps, per_sm;
 };
 BackShape back_shape(int n) {
-  const int v = n <= 2048 ? 1 : n <= 4096 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
-  int per_sm = v == 1 ? 24 / warps : v == 2 ? 2 : warps <= 5 ? 2 : 1;
+  const int v = n <= 2048 ? 1 : n <= 8192 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
+  int per_sm = v == 1 ? 24 / warps : 1;
   if (per_sm > 16) per_sm = 16;
   return {v, warps, per_sm};
 }
@@ -446,7 +484,7 @@ cudaError_t backward(const NormParams& q, cudaStream_t s) {
   p.stages = fit < 1 ? 1 : fit > kMaxStagesBack ? kMaxStagesBack : static_cast<int>(fit);
   switch (sh.v) {
     case 1: return backward_one<T, R, 1, 256, 3>(p, s);
-    case 2: return backward_one<T, R, 2, 256, 2>(p, s);
+    case 2: return backward_one<T, R, 2, 512, 1>(p, s);
     default: return backward_one<T, R, 4, 384, 1>(p, s);
   }
 }
