@@ -934,8 +934,14 @@ def wsattn_linear_backward_workspace(dout, x, weight, preact=None, activation="n
 
 def _token_major(b, h, n, d, dtype, like, stream):
     """[B, H, N, D] whose memory is [B, N, H, D]: a token's heads side by side,
-    as wsattn_linear reads them (t.transpose(1, 2).flatten(2))."""
-    return _empty((b, n, h, d), dtype, like, stream).transpose(1, 2)
+    as wsattn_linear reads them (t.transpose(1, 2).flatten(2)); and its fields."""
+    stride = (n * h * d, d, h * d, 1)
+    if stream is None:
+        t = torch.empty_strided((b, h, n, d), stride, dtype=dtype, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty_strided((b, h, n, d), stride, dtype=dtype, device=like.device)
+    return t, (t.data_ptr(), h, stride[0], d, stride[2])
 
 
 def _view_fields(t, name, shape, dt, dev):
@@ -984,8 +990,9 @@ def _cross_args(q, k, v, k_lengths, scale, out, lse, stream, query=False):
     b, h, n = sq[:3]
     if query:  # any aligned address stands for the output
         of = (256, h, n * h * d, d, h * d)
+    elif out is None:
+        out, of = _token_major(b, h, n, d, dt, q, stream)
     else:
-        out = _token_major(b, h, n, d, dt, q, stream) if out is None else out
         of = _view_fields(out, "out", sq, dt, dev)
     return _CROSS(code, d, b, n, sk[2], *_view_fields(q, "q", sq, dt, dev),
                   *_view_fields(k, "k", sk, dt, dev), *_view_fields(v, "v", sk, dt, dev), *of, lp,
@@ -1005,9 +1012,13 @@ def wsattn_cross(q, k, v, k_lengths=None, scale=None, out=None, lse=None, worksp
     is left for are 0, their lse -inf."""
     args, out, dev = _cross_args(q, k, v, k_lengths, scale, out, lse, stream)
     raw = _raw_stream(dev, stream)
-    ws, nbytes, _hold = _scratch(_lib.wsattn_cross_workspace, "wsattn_cross_workspace", args,
-                                 workspace, dev, q, stream)
-    _run(dev, "wsattn_cross", _lib.wsattn_cross, args, ws, nbytes, raw)
+    ws = nbytes = _hold = None
+    # one key step, or row tiles enough for every SM: the keys are not split
+    plain = k.shape[2] <= 128 or q.shape[0] * k.shape[1] * ((q.shape[2] + 255) // 256) > 76
+    if workspace is not None or not plain:
+        ws, nbytes, _hold = _scratch(_lib.wsattn_cross_workspace, "wsattn_cross_workspace", args,
+                                     workspace, dev, q, stream)
+    _run(dev, "wsattn_cross", _lib.wsattn_cross, args, ws, nbytes or 0, raw)
     return out
 
 
@@ -1032,8 +1043,10 @@ def _cross_grad_args(dout, q, k, v, out, lse, k_lengths, scale, dq, dk, dv, need
             fields += _NO_VIEW
         elif query:
             fields += (256, s[1], s[2] * s[1] * d, d, s[1] * d)
+        elif t is None:
+            t, of = _token_major(s[0], s[1], s[2], d, dt, q, stream)
+            fields += of
         else:
-            t = _token_major(s[0], s[1], s[2], d, dt, q, stream) if t is None else t
             fields += _view_fields(t, name, s, dt, dev)
         grads.append(t)
     args = _CROSS_GRAD(code, d, sq[0], sq[2], sk[2], *_view_fields(dout, "dout", sq, dt, dev),
@@ -1097,45 +1110,52 @@ def _groups_of(t, name, lead, n):
     return g
 
 
-def _modulation(vectors, lead, n, dt, dev):
-    """(rows a vector serves, groups, type, {name: (pointer, row stride)}) of gate, scale and shift."""
-    groups, kind, at, first = None, None, {}, None
-    for name, t in vectors:
+def _modulation(gate, scale, shift, lead, n, m, dt, dev):
+    """(rows a vector serves, type or None, gate's, scale's and shift's pointers
+    and row strides)."""
+    first, group, out = None, m if m else 1, []
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
-            at[name] = (0, 0)
+            out += (0, 0)
             continue
-        _check_tensor(t, name, dev)
-        if t.dtype != dt and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be {dt} or torch.float32, got {t.dtype}")
-        g = _groups_of(t, name, lead, n)
-        if groups is None:
-            groups, kind, first = g, t.dtype, name
-        elif groups != g or kind != t.dtype:
+        if first is None:
+            _check_tensor(t, name, dev)
+            kind = t.dtype
+            if kind is not dt and kind is not torch.float32:
+                raise TypeError(f"{name} must be {dt} or torch.float32, got {kind}")
+            groups = _groups_of(t, name, lead, n)
+            if groups > 1:
+                group = max(m // groups, 1)
+            ld = _rows(t, name, n, None, kind, dev)
+            first, shape, stride = name, t.shape, t.stride()
+        elif t.dtype is not kind or t.get_device() != dev or t.shape != shape:
+            _check_tensor(t, name, dev)
             raise ValueError(f"{name} must have {first}'s shape and type")
-        at[name] = (t.data_ptr(), _rows(t, name, n, None, t.dtype, dev))
-    m = lead.numel()
-    groups = groups or 1
-    return (max(m // groups, 1) if groups > 1 else max(m, 1)), groups, kind, at
+        elif t.stride() != stride:
+            ld = _rows(t, name, n, None, kind, dev)
+        out += (t.data_ptr(), ld)
+    return group, None if first is None else kind, out
 
 
-def _weights(vectors, n, dt, dev):
-    """(type, {name: pointer}) of weight, bias and post_weight."""
-    kind, at, first = None, {}, None
-    for name, t in vectors:
+def _weights(weight, bias, post_weight, n, dt, dev):
+    """(type or None, weight's, bias's and post_weight's pointers)."""
+    kind, first, out = None, None, []
+    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
         if t is None:
-            at[name] = 0
+            out.append(0)
             continue
-        _check_tensor(t, name, dev)
-        if t.dtype != dt and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be {dt} or torch.float32, got {t.dtype}")
+        if kind is None:
+            _check_tensor(t, name, dev)
+            kind, first = t.dtype, name
+            if kind is not dt and kind is not torch.float32:
+                raise TypeError(f"{name} must be {dt} or torch.float32, got {kind}")
+        elif t.dtype is not kind or t.get_device() != dev:
+            _check_tensor(t, name, dev)
+            raise TypeError(f"{name} must have {first}'s type")
         if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
             raise ValueError(f"{name} must be contiguous [{n}], got {list(t.shape)}")
-        if kind is None:
-            kind, first = t.dtype, name
-        elif kind != t.dtype:
-            raise TypeError(f"{name} must have {first}'s type")
-        at[name] = t.data_ptr()
-    return kind, at
+        out.append(t.data_ptr())
+    return kind, out
 
 
 def wsattn_block_norm(x, residual=None, gate=None, scale=None, shift=None, weight=None, bias=None,
@@ -1154,36 +1174,39 @@ def wsattn_block_norm(x, residual=None, gate=None, scale=None, shift=None, weigh
     (it is x then) unless given, out is None when not needed.  hidden may be
     the residual or x, out may be x."""
     dev = _device_of(x, "x")
-    if not x.dim():
+    shape, dt, code = x.shape, x.dtype, _dtype_code(x, "x")
+    if not shape:
         raise ValueError("x must be [..., n], got []")
-    n, dt, code = x.shape[-1], x.dtype, _dtype_code(x, "x")
-    lead = x.shape[:-1]
+    n, lead = shape[-1], shape[:-1]
     m = lead.numel()
-    kind, post = _norm_kind(norm, "norm"), _norm_kind(post_norm, "post_norm", none=True)
+    kind = NORMS.get(norm) or _norm_kind(norm, "norm")
+    post = 0 if post_norm is None else _norm_kind(post_norm, "post_norm", none=True)
     if post_weight is not None and not post:
         raise ValueError("post_weight without post_norm")
-    group, _, mod, at = _modulation((("gate", gate), ("scale", scale), ("shift", shift)), lead, n, dt, dev)
-    wt, wat = _weights((("weight", weight), ("bias", bias), ("post_weight", post_weight)), n, dt, dev)
+    group, mod, vectors = _modulation(gate, scale, shift, lead, n, m, dt, dev)
+    wt, weights = _weights(weight, bias, post_weight, n, dt, dev)
     raw = _raw_stream(dev, stream)
     ldx = _rows(x, "x", n, None, dt, dev)
     st = residual.dtype if residual is not None else dt if hidden is None else hidden.dtype
-    if st != dt and st != torch.float32:
+    if st is not dt and st is not torch.float32:
         raise TypeError(f"residual and hidden must be {dt} or torch.float32, got {st}")
-    rp = ldr = hp = ldh = op = ldo = 0
+    rp = hp = op = 0
+    ldr = ldh = ldo = n
     if residual is not None:
         ldr, rp = _rows(residual, "residual", n, lead, st, dev), residual.data_ptr()
-    if hidden is None and (residual is not None or gate is not None or post):
-        hidden = _empty(x.shape, st, x, stream)
     if hidden is not None:
         ldh, hp = _rows(hidden, "hidden", n, lead, st, dev), hidden.data_ptr()
-    if out is None and need_out:
-        out = _empty(x.shape, dt, x, stream)
+    elif residual is not None or gate is not None or post:
+        hidden = _empty(shape, st, x, stream)
+        hp = hidden.data_ptr()
     if out is not None:
         ldo, op = _rows(out, "out", n, lead, dt, dev), out.data_ptr()
-    args = _BLOCK_NORM(code, code if st == dt else FP32, code if mod in (None, dt) else FP32,
-                       code if wt in (None, dt) else FP32, m, n, kind, post, eps, residual_scale,
-                       group, x.data_ptr(), ldx, rp, ldr, *at["gate"], *at["scale"], *at["shift"],
-                       wat["weight"], wat["bias"], wat["post_weight"], hp, ldh, op, ldo)
+    elif need_out:
+        out = _empty(shape, dt, x, stream)
+        op = out.data_ptr()
+    args = _BLOCK_NORM(code, code if st is dt else FP32, code if mod is None or mod is dt else FP32,
+                       code if wt is None or wt is dt else FP32, m, n, kind, post, eps, residual_scale,
+                       group, x.data_ptr(), ldx, rp, ldr, *vectors, *weights, hp, ldh, op, ldo)
     _run(dev, "wsattn_block_norm", _lib.wsattn_block_norm, args, raw)
     return out, hidden
 
@@ -1214,8 +1237,8 @@ def _block_norm_grad_args(dout, hidden, x, dhidden, gate, scale, shift, weight, 
         raise ValueError("dout needs hidden (what wsattn_block_norm left, or x where nothing joined it)")
     if x is None and (gate is not None or post):
         raise ValueError("the gradients of a gate or of post_norm need x")
-    group, _, mod, at = _modulation((("gate", gate), ("scale", scale), ("shift", shift)), lead, n, dt, dev)
-    wt, wat = _weights((("weight", weight), ("bias", bias), ("post_weight", post_weight)), n, dt, dev)
+    group, mod, vectors = _modulation(gate, scale, shift, lead, n, m, dt, dev)
+    wt, weights = _weights(weight, bias, post_weight, n, dt, dev)
     st = hidden.dtype if hidden is not None else dhidden.dtype
     if st != dt and st != torch.float32:
         raise TypeError(f"hidden and dhidden must be {dt} or torch.float32, got {st}")
@@ -1226,12 +1249,14 @@ def _block_norm_grad_args(dout, hidden, x, dhidden, gate, scale, shift, weight, 
     same = gate is None and not post and residual_scale == 1.0 and st == dt
     need_dx, need_dresidual = need_dx or dx is not None, need_dresidual or dresidual is not None
     one = same and need_dx and need_dresidual and (dx is None or dresidual is None)
-    if need_dx and dx is None and not query:
-        dx = dresidual if one and dresidual is not None else _empty(like.shape, dt, like, stream)
-    if need_dresidual and dresidual is None and not query:
-        dresidual = dx if one else _empty(like.shape, st, like, stream)
     for name, t, ty in (("dx", dx, dt), ("dresidual", dresidual, st)):
         rows[name] = (0, 0) if t is None else (t.data_ptr(), _rows(t, name, n, lead, ty, dev))
+    if need_dx and dx is None and not query:
+        dx = dresidual if one and dresidual is not None else _empty(like.shape, dt, like, stream)
+        rows["dx"] = rows["dresidual"] if dx is dresidual else (dx.data_ptr(), n)
+    if need_dresidual and dresidual is None and not query:
+        dresidual = dx if one else _empty(like.shape, st, like, stream)
+        rows["dresidual"] = rows["dx"] if one else (dresidual.data_ptr(), n)
     if one:
         rows["dresidual"] = (0, 0)
     sums = []
@@ -1247,10 +1272,10 @@ def _block_norm_grad_args(dout, hidden, x, dhidden, gate, scale, shift, weight, 
             sums.append(make.zero_() if not m else make)
     ptr = [0 if t is None else t if query else t.data_ptr() for t in sums]
     args = _BLOCK_NORM_GRAD(
-        code, code if st == dt else FP32, code if mod in (None, dt) else FP32,
-        code if wt in (None, dt) else FP32, m, n, kind, post, eps, residual_scale, group,
-        *rows["dout"], *rows["dhidden"], *rows["hidden"], *rows["x"], *at["gate"], *at["scale"],
-        wat["weight"], wat["bias"], wat["post_weight"], *rows["dx"], *rows["dresidual"], *ptr)
+        code, code if st is dt else FP32, code if mod is None or mod is dt else FP32,
+        code if wt is None or wt is dt else FP32, m, n, kind, post, eps, residual_scale, group,
+        *rows["dout"], *rows["dhidden"], *rows["hidden"], *rows["x"], *vectors[:4],
+        *weights, *rows["dx"], *rows["dresidual"], *ptr)
     return args, BlockNormGrads(dx, dresidual, *sums), dev, like
 
 

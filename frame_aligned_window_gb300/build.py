@@ -32,9 +32,9 @@ BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libwsattn_debug.so")
 SOURCES = ["plan.cpp", "prepare.cu", "forward.cu", "api.cu", "prepare_static.cu", "produce.cu",
            "qknorm.cu", "qknorm_back.cu", "linear_pair.cu", "linear_tile.cu", "linear_aux.cu", "api_ops.cu",
-           "norm.cu", "norm_back.cu", "api_norm.cu",
+           "norm.cu", "norm_back.cu", "norm_back_bf16.cu", "norm_back_fp16.cu", "api_norm.cu",
            "cross.cu", "cross_back.cu", "api_cross.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "ops.h", "epilogue.cuh", "qknorm.cuh", "api_args.h", "norm.cuh", "cross.cuh"]
+HEADERS = ["internal.h", "ptx.cuh", "ops.h", "epilogue.cuh", "qknorm.cuh", "api_args.h", "norm.cuh", "norm_back.cuh", "cross.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -124,7 +124,7 @@ int wsattn_cross(const wsattn_cross_args* a, void* workspace, size_t workspace_b
   const int64_t n = a->n_tokens, m = a->n_keys;
   if (!tma_view(&a->q, a->q.heads, a->batch, n) || !tma_view(&a->k, a->k.heads, a->batch, m) ||
       !tma_view(&a->v, a->k.heads, a->batch, m) || !tma_view(&a->out, a->q.heads, a->batch, n) ||
-      !apart(&a->out, a->batch, n, a->head_dim))
+      (n && !apart(&a->out, a->batch, n, a->head_dim)))
     return WSATTN_ERR_BAD_ARG;
   if (a->batch == 0 || n == 0) return WSATTN_OK;
   if (!a->q.data || !a->out.data || (m && (!a->k.data || !a->v.data))) return WSATTN_ERR_BAD_ARG;
@@ -177,7 +177,8 @@ int wsattn_cross_backward(const wsattn_cross_grad_args* a, void* workspace, size
   const wsattn_heads* grads[3] = {&a->dq, &a->dk, &a->dv};
   for (int i = 0; i < 3; ++i)
     if (grads[i]->data &&
-        (!tma_view(grads[i], i ? e : h, b, i ? m : n) || !apart(grads[i], b, i ? m : n, a->head_dim)))
+        (!tma_view(grads[i], i ? e : h, b, i ? m : n) ||
+         ((i ? m : n) && !apart(grads[i], b, i ? m : n, a->head_dim))))
       return WSATTN_ERR_BAD_ARG;
   if (b == 0 || (!a->dq.data && !a->dk.data && !a->dv.data)) return WSATTN_OK;
   if ((n && (!a->q.data || !a->out.data || !a->dout.data || !a->lse)) ||

@@ -34,16 +34,6 @@ __device__ __forceinline__ int column(int lane, int threads, int j) {
   return 8 * (lane + threads * j);
 }
 
-// Rows that are read once leave the L1 cache to the vectors that many rows share.
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 __device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
@@ -57,8 +47,8 @@ __device__ __forceinline__ Raw8<T> load_raw(const T* row, int n, int c, bool vec
   if constexpr (sizeof(T) == 4) r.b = r.a;
   if (vec) {
     if (c < n) {
-      r.a = ld_once(row + c);
-      if constexpr (sizeof(T) == 4) r.b = ld_once(row + c + 4);
+      r.a = *reinterpret_cast<const uint4*>(row + c);
+      if constexpr (sizeof(T) == 4) r.b = *reinterpret_cast<const uint4*>(row + c + 4);
     }
   } else {
     uint32_t w[8];

@@ -1,0 +1,438 @@
+// Gradients of a block's norms (norm.cuh has the forward's formulas and what
+// the passes share).  From dy, the gradient dh' that reaches h by other ways,
+// h and x, with s = std(h), xh = std(x) (or x without a first norm):
+//
+//   g  = dy (1 + scale) weight
+//   dh = dh' + r (g - [mean g] - s mean(g s))          ([.]: layer norm only)
+//   d residual = res_scale dh
+//   du = gate dh;   dx = du, or the same form through the first norm
+// and over the rows of a group
+//   A = sum dy s,   B = sum dy,   E = sum dh xh
+//   dscale = weight A + bias B,   dshift = B,   dgate = post_weight E
+//   dweight = sum over groups of (1 + scale) A,   dbias of (1 + scale) B,
+//   dpost_weight of gate E
+// so that three sums a column, in registers, serve all six.
+//
+// Bound by HBM (dy, h, x, dh' in, dres and dx out).  A CTA takes a contiguous
+// share of the rows and one row at a time; the next rows are on their way
+// through a ring of cp.async stages in shared memory meanwhile (a thread reads
+// what it loaded itself: no barrier).  A group inside one share is finished
+// there; of a group that several shares hold parts of, each leaves its sums in
+// the workspace, and a second kernel adds them in the order of the shares.
+#pragma once
+
+#include "norm.cuh"
+
+namespace wsattn {
+namespace norm {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kMaxStagesBack = 4;
+
+// First row of share u, and the share of a row.
+__device__ __forceinline__ int64_t share_begin(const NormParams& p, int64_t u) {
+  if (!p.whole) return p.m * u / p.units;
+  const int64_t row = p.groups * u / p.units * p.group;
+  return row < p.m ? row : p.m;
+}
+__device__ __forceinline__ int64_t share_of(const NormParams& p, int64_t row) {
+  return ((row + 1) * p.units - 1) / p.m;
+}
+
+// A thread's pieces of one row, on their way into shared memory: asynchronous
+// copies, or (rows of any alignment) element by element.
+template <typename T, int V>
+__device__ __forceinline__ void copy_row(uint32_t at, const T* row, int n, int lane, int threads,
+                                         bool vec) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = column(lane, threads, j);
+    if (c >= n) break;
+    if (vec) {
+      cp_async16(at + c * sizeof(T), row + c);
+      if constexpr (sizeof(T) == 4) cp_async16(at + c * 4 + 16, row + c + 4);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {  // zeros behind the row's end
+        const uint32_t w = c + i < n ? bits_of(row[c + i]) : 0u;
+        if constexpr (sizeof(T) == 4)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4u * (c + i)), "r"(w) : "memory");
+        else
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2u * (c + i)),
+                       "h"(static_cast<uint16_t>(w))
+                       : "memory");
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void piece(uint32_t at, int n, int c, Pairs& f) {
+  Raw8<T> r;
+  r.a = make_uint4(0, 0, 0, 0);
+  if constexpr (sizeof(T) == 4) r.b = r.a;
+  if (c < n) {
+    r.a = ld_shared_v4(at + c * sizeof(T));
+    if constexpr (sizeof(T) == 4) r.b = ld_shared_v4(at + c * 4 + 16);
+  }
+  unpack(r, f);
+}
+__device__ __forceinline__ float both(uint64_t v) {
+  const float2 t = f2_unpack(v);
+  return t.x + t.y;
+}
+
+template <typename T, typename R, int V, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
+    norm_backward_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  __shared__ float red[kReducerFloats];
+  Reducer rd{red, p.warps, 0};
+  const int threads = 32 * p.warps, lane = threadIdx.x, n = p.n;
+  const bool vec = p.vec != 0;
+  const float inv_n = 1.f / static_cast<float>(n);
+  const int64_t r0 = share_begin(p, blockIdx.x), r1 = share_begin(p, blockIdx.x + 1);
+  const uint32_t ring = smem_u32(ring_raw);
+  // a slot: dy, x, h, dh'
+  const uint32_t cols = static_cast<uint32_t>(n + 7) / 8 * 8;
+  const uint32_t at_x = cols * sizeof(T), at_h = 2 * at_x, at_dh = at_h + cols * sizeof(R);
+  const uint32_t stage = at_dh + cols * sizeof(R);
+  const bool layer = p.norm == WSATTN_NORM_LAYER, post = p.post != WSATTN_NORM_NONE;
+  const bool post_layer = p.post == WSATTN_NORM_LAYER;
+  const T* const dyp = static_cast<const T*>(p.out);
+  const T* const xp = static_cast<const T*>(p.x);
+  const R* const hp = static_cast<const R*>(p.hidden);
+  const R* const dhp = static_cast<const R*>(p.dhidden);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!WSATTN_BOUNDS(p.status, r0 >= 0 && r1 <= p.m && threads * V * 8 >= n &&
+                                   threads == static_cast<int>(blockDim.x) && p.stages >= 1))
+    return;
+
+  Pairs a_sum[V], b_sum[V], e_sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    fill(a_sum[j], 0.f);
+    fill(b_sum[j], 0.f);
+    fill(e_sum[j], 0.f);
+  }
+  bool first_flush = true;
+
+  // times (a vector's columns + add)
+  auto scaled = [&](const void* v, int64_t at, int f32, int c, float add, Pairs& t) {
+    Pairs f;
+    vector8<T>(v, at, f32 != 0, n, c, vec, f);
+    const uint64_t a2 = f2_pack(add, add);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = add == 0.f ? f2_mul(t[i], f[i]) : f2_mul(t[i], f2_add(f[i], a2));
+  };
+  auto copy = [](Pairs& to, const Pairs& from) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = from[i];
+  };
+  // The sums of group g over this share's rows are complete: out with them.
+  auto flush = [&](int64_t g) {
+    const int64_t gs = g * p.group, ge = gs + p.group < p.m ? gs + p.group : p.m;
+    const bool whole = gs >= r0 && ge <= r1;
+    float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (gs < r0 ? 0 : 1)) * 3 * n;
+    float* wpart = p.wpart + static_cast<int64_t>(blockIdx.x) * 3 * n;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = column(lane, threads, j);
+      Pairs t, u;
+      if (p.wpart) {
+        auto add = [&](float* to) {  // t, to what earlier groups left
+          if (!first_flush) {
+            vector8<float>(to, 0, true, n, c, vec, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = f2_add(t[i], u[i]);
+          }
+          store8(to, n, c, vec, t);
+        };
+        copy(t, a_sum[j]);
+        if (p.scale) scaled(p.scale, g * p.lds, p.mod_f32, c, 1.f, t);
+        add(wpart);
+        copy(t, b_sum[j]);
+        if (p.scale) scaled(p.scale, g * p.lds, p.mod_f32, c, 1.f, t);
+        add(wpart + n);
+        copy(t, e_sum[j]);
+        if (p.gate) scaled(p.gate, g * p.ldg, p.mod_f32, c, 0.f, t);
+        add(wpart + 2 * n);
+      }
+      if (!whole) {
+        if (p.part) {
+          store8(part, n, c, vec, a_sum[j]);
+          store8(part + n, n, c, vec, b_sum[j]);
+          store8(part + 2 * n, n, c, vec, e_sum[j]);
+        }
+      } else {
+        if (p.dscale) {
+          copy(t, a_sum[j]);
+          if (p.weight) scaled(p.weight, 0, p.weight_f32, c, 0.f, t);
+          if (p.bias) {
+            vector8<T>(p.bias, 0, p.weight_f32 != 0, n, c, vec, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = f2_fma(b_sum[j][i], u[i], t[i]);
+          }
+          store8(p.dscale + g * n, n, c, vec, t);
+        }
+        if (p.dshift) store8(p.dshift + g * n, n, c, vec, b_sum[j]);
+        if (p.dgate) {
+          copy(t, e_sum[j]);
+          if (p.post_weight) scaled(p.post_weight, 0, p.weight_f32, c, 0.f, t);
+          store8(p.dgate + g * n, n, c, vec, t);
+        }
+      }
+      fill(a_sum[j], 0.f);
+      fill(b_sum[j], 0.f);
+      fill(e_sum[j], 0.f);
+    }
+    first_flush = false;
+  };
+
+  uint32_t load_slot = 0, slot = 0;
+  int64_t ahead = r0;
+  auto issue = [&] {
+    if (ahead < r1) {
+      const uint32_t at = ring + load_slot * stage;
+      if (dyp) {
+        copy_row<T, V>(at, dyp + ahead * p.ldo, n, lane, threads, vec);
+        copy_row<R, V>(at + at_h, hp + ahead * p.ldh, n, lane, threads, vec);
+      }
+      if (xp) copy_row<T, V>(at + at_x, xp + ahead * p.ldx, n, lane, threads, vec);
+      if (dhp) copy_row<R, V>(at + at_dh, dhp + ahead * p.lddh, n, lane, threads, vec);
+      ++ahead;
+    }
+    cp_async_commit();
+    if (++load_slot == static_cast<uint32_t>(p.stages)) load_slot = 0;
+  };
+  for (int k = 0; k + 1 < p.stages; ++k) issue();
+
+  int64_t g = r0 < r1 ? r0 / p.group : 0;
+  int64_t group_end = (g + 1) * p.group;
+  for (int64_t row = r0; row < r1; ++row) {
+    if (row == group_end) {
+      flush(g);
+      ++g;
+      group_end += p.group;
+    }
+    const uint32_t at = ring + slot * stage;
+    issue();
+    switch (p.stages) {
+      case 1: cp_async_wait<0>(); break;
+      case 2: cp_async_wait<1>(); break;
+      case 3: cp_async_wait<2>(); break;
+      default: cp_async_wait<3>(); break;
+    }
+    if (++slot == static_cast<uint32_t>(p.stages)) slot = 0;
+
+    Pairs h[V], d[V];  // h, then its deviations; g, then dh
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      fill(h[j], 0.f);
+      fill(d[j], 0.f);
+      if (dyp) {
+        const int c = column(lane, threads, j);
+        piece<R>(at + at_h, n, c, h[j]);
+        piece<T>(at, n, c, d[j]);
+        if (p.scale) scaled(p.scale, g * p.lds, p.mod_f32, c, 1.f, d[j]);
+        if (p.weight) scaled(p.weight, 0, p.weight_f32, c, 0.f, d[j]);
+      }
+    }
+    float mean = 0.f, x_mean = 0.f;
+    if ((layer && dyp) || post_layer) {
+      uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s0 = f2_add(s0, h[j][i]);
+        if (post_layer) {
+          Pairs x;
+          piece<T>(at + at_x, n, column(lane, threads, j), x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s1 = f2_add(s1, x[i]);
+        }
+      }
+      if (post_layer) {
+        float s[2] = {both(s0), both(s1)};
+        row_sums(rd, s);
+        if (layer) mean = s[0] * inv_n;
+        x_mean = s[1] * inv_n;
+      } else {
+        float s[1] = {both(s0)};
+        row_sums(rd, s);
+        mean = s[0] * inv_n;
+      }
+    }
+    // squares of deviations, sums of g and of its product with them
+    uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
+    const uint64_t mean2 = f2_pack(-mean, -mean), xmean2 = f2_pack(-x_mean, -x_mean);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = column(lane, threads, j);
+      if (layer) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[j][i] = f2_add(h[j][i], mean2);
+        trim(h[j], c, n);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s0 = f2_fma(h[j][i], h[j][i], s0);
+        s1 = f2_add(s1, d[j][i]);
+        s2 = f2_fma(d[j][i], h[j][i], s2);
+      }
+      if (post) {
+        Pairs x;
+        piece<T>(at + at_x, n, c, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f2_add(x[i], xmean2);
+        trim(x, c, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s3 = f2_fma(x[i], x[i], s3);
+      }
+    }
+    float s[4] = {both(s0), both(s1), both(s2), 0.f};
+    if (post) {
+      s[3] = both(s3);
+      row_sums(rd, s);
+    } else if (dyp) {
+      float t[3] = {s[0], s[1], s[2]};
+      row_sums(rd, t);
+      s[0] = t[0], s[1] = t[1], s[2] = t[2];
+    }
+    const float r = rsqrtf(fmaf(s[0], inv_n, p.eps));
+    const float x_r = post ? rsqrtf(fmaf(s[3], inv_n, p.eps)) : 1.f;
+    const float g_mean = layer ? s[1] * inv_n : 0.f;
+    const float gs_mean = s[2] * r * inv_n;  // mean of g s
+    // dh = r g - r [mean g] - r s mean(g s), s = h r
+    const uint64_t r2 = f2_pack(r, r), rg2 = f2_pack(-r * g_mean, -r * g_mean);
+    const uint64_t rs2 = f2_pack(-r * gs_mean, -r * gs_mean), xr2 = f2_pack(x_r, x_r);
+    uint64_t p0 = f2_pack(0.f, 0.f), p1 = p0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = column(lane, threads, j);
+      Pairs t;
+      if (dyp) {
+        piece<T>(at, n, c, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t si = f2_mul(h[j][i], r2);
+          a_sum[j][i] = f2_fma(t[i], si, a_sum[j][i]);
+          b_sum[j][i] = f2_add(b_sum[j][i], t[i]);
+          d[j][i] = f2_fma(si, rs2, f2_fma(d[j][i], r2, rg2));
+        }
+      }
+      if (dhp) {
+        piece<R>(at + at_dh, n, c, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[j][i] = f2_add(d[j][i], t[i]);
+      }
+      if (p.dres) {
+        const uint64_t k2 = f2_pack(p.res_scale, p.res_scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = f2_mul(k2, d[j][i]);
+        store8(static_cast<R*>(p.dres) + row * p.lddr, n, c, vec, t);
+      }
+      if (xp) {
+        piece<T>(at + at_x, n, c, t);
+        if (post) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = f2_mul(f2_add(t[i], xmean2), xr2);
+          trim(t, c, n);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e_sum[j][i] = f2_fma(d[j][i], t[i], e_sum[j][i]);
+      }
+      if (p.dx) {
+        if (p.gate) scaled(p.gate, g * p.ldg, p.mod_f32, c, 0.f, d[j]);
+        if (!post) {
+          store8(static_cast<T*>(p.dx) + row * p.lddx, n, c, vec, d[j]);
+        } else {
+          if (p.post_weight) scaled(p.post_weight, 0, p.weight_f32, c, 0.f, d[j]);
+          trim(d[j], c, n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p0 = f2_add(p0, d[j][i]);
+            p1 = f2_fma(d[j][i], t[i], p1);
+          }
+        }
+      }
+    }
+    if (post && p.dx) {
+      float ps[2] = {both(p0), both(p1)};
+      row_sums(rd, ps);
+      const float m1 = post_layer ? ps[0] * inv_n : 0.f, m2 = ps[1] * inv_n;
+      // dx = x_r (du - [mean du] - xh mean(du xh))
+      const uint64_t k1 = f2_pack(-m1, -m1), k2 = f2_pack(-x_r * m2, -x_r * m2);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = column(lane, threads, j);
+        Pairs x;
+        piece<T>(at + at_x, n, c, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          d[j][i] = f2_mul(xr2, f2_fma(f2_add(x[i], xmean2), k2, f2_add(d[j][i], k1)));
+        store8(static_cast<T*>(p.dx) + row * p.lddx, n, c, vec, d[j]);
+      }
+    }
+  }
+  if (r0 < r1) flush(g);
+}
+
+// How a row is held: `warps` warps with v pieces a thread, per_sm CTAs an SM.
+struct BackShape {
+  int v, warps, per_sm;
+};
+inline BackShape back_shape(int n) {
+  const int v = n <= 2048 ? 1 : n <= 8192 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
+  int per_sm = v == 1 ? 24 / warps : warps <= 10 ? 2 : 1;
+  if (per_sm > 16) per_sm = 16;
+  return {v, warps, per_sm};
+}
+
+constexpr size_t kRingBytes = 200 * 1024;  // of an SM, all its CTAs together
+
+template <typename T, typename R, int V, int MAXT, int MINB>
+cudaError_t backward_one(const NormParams& p, cudaStream_t s) {
+  static bool attr_set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<T, R, V, MAXT, MINB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kRingBytes));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const size_t smem = static_cast<size_t>(p.stages) * ((p.n + 7) / 8 * 8) * 2 * (sizeof(T) + sizeof(R));
+  return launch_dependent(norm_backward_kernel<T, R, V, MAXT, MINB>, dim3(p.units),
+                          dim3(32 * p.warps), smem, s, p);
+}
+template <typename T, typename R>
+cudaError_t backward(const NormParams& q, cudaStream_t s) {
+  NormParams p = q;
+  const BackShape sh = back_shape(p.n);
+  p.warps = sh.warps;
+  const size_t row = static_cast<size_t>((p.n + 7) / 8 * 8) * 2 * (sizeof(T) + sizeof(R));
+  const size_t fit = kRingBytes / sh.per_sm / row;
+  p.stages = fit < 1 ? 1 : fit > kMaxStagesBack ? kMaxStagesBack : static_cast<int>(fit);
+  switch (sh.v) {
+    case 1: return backward_one<T, R, 1, 256, 3>(p, s);
+    case 2:
+      if (sh.warps <= 10) return backward_one<T, R, 2, 320, 2>(p, s);
+      return backward_one<T, R, 2, 512, 1>(p, s);
+    default: return backward_one<T, R, 4, 384, 1>(p, s);
+  }
+}
+
+}  // namespace norm
+}  // namespace wsattn

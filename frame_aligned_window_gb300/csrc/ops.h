@@ -251,6 +251,10 @@ cudaError_t launch_norm_forward(const NormParams& p, int dtype, bool stream_f32,
 // CTAs of the backward pass (their number does not depend on the device).
 int norm_backward_units(int64_t m, int n);
 cudaError_t launch_norm_backward(const NormParams& p, int dtype, bool stream_f32, cudaStream_t s);
+// The pass over the rows, by the types of x and of the residual stream.
+cudaError_t norm_backward_bf16(const NormParams& p, bool stream_f32, cudaStream_t s);
+cudaError_t norm_backward_fp16(const NormParams& p, bool stream_f32, cudaStream_t s);
+cudaError_t norm_backward_f32(const NormParams& p, cudaStream_t s);
 
 // -------------------------------------------------------- cross attention
 // A [batch, heads, rows, D] view in global memory (strides in elements).
