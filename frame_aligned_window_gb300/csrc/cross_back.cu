@@ -9,7 +9,9 @@
 // share it (dk, dv).  p and ds are formed in both: seven matrix products
 // instead of five, but no sum leaves the chip before it is complete (dq summed
 // over key tiles elsewhere would be fp32 traffic of 4 D bytes per query and key
-// tile), and none depends on the order in which CTAs finish.
+// tile), and none depends on the order in which CTAs finish.  At 2 x 40 heads,
+// 21952 queries and 512 keys of 128: dq 740 us (933 TFLOP/s of its three
+// products, 2.5 TB/s), dk and dv 690 us (1330 TFLOP/s of their four).
 #include "cross.cuh"
 
 namespace wsattn {

@@ -472,18 +472,6 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
                : "memory");
 }
 
-// ------------------------------------------------------ register budgets
-// Every warp of a warpgroup: registers of a thread from here on.  The launch's
-// registers are what the warpgroups share: what some give up, others may take.
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ------------------------------------------------------------- packed f32
 // Two fp32 lanes in one 64-bit register: lo = first element.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
