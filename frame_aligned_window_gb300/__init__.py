@@ -999,6 +999,12 @@ def _cross_args(q, k, v, k_lengths, scale, out, lse, stream, query=False):
                   scale, 0 if lse is None else _lse_ptr(lse, sq, dev)), out, dev
 
 
+def _keys_stay_whole(sq, sk):
+    """True for shapes of q and k whose keys are not split, so that no workspace
+    is asked for: one key step, or row tiles for more than half of the SMs."""
+    return sk[2] <= 128 or sq[0] * sk[1] * ((sq[2] + 255) // 256) > 76
+
+
 def wsattn_cross(q, k, v, k_lengths=None, scale=None, out=None, lse=None, workspace=None,
                  stream=None):
     """Attention of q [B, H, N, D] to an encoder's k, v [B, Hk, M, D] (bf16 or
@@ -1013,9 +1019,7 @@ def wsattn_cross(q, k, v, k_lengths=None, scale=None, out=None, lse=None, worksp
     args, out, dev = _cross_args(q, k, v, k_lengths, scale, out, lse, stream)
     raw = _raw_stream(dev, stream)
     ws = nbytes = _hold = None
-    # one key step, or row tiles enough for every SM: the keys are not split
-    plain = k.shape[2] <= 128 or q.shape[0] * k.shape[1] * ((q.shape[2] + 255) // 256) > 76
-    if workspace is not None or not plain:
+    if workspace is not None or not _keys_stay_whole(q.shape, k.shape):
         ws, nbytes, _hold = _scratch(_lib.wsattn_cross_workspace, "wsattn_cross_workspace", args,
                                      workspace, dev, q, stream)
     _run(dev, "wsattn_cross", _lib.wsattn_cross, args, ws, nbytes or 0, raw)
@@ -1098,8 +1102,8 @@ def _groups_of(t, name, lead, n):
     if not shape or shape[-1] != n:
         raise ValueError(f"{name} must be [..., {n}], got {list(shape)}")
     g = shape[:-1].numel()
-    if g == 1:
-        return 1
+    if g == 1 or (not g and shape[:-1] == lead[:len(shape) - 1]):  # one, or none for no rows
+        return g
     own = list(shape[:-1])
     while own and own[-1] == 1:
         own.pop()
@@ -1267,9 +1271,10 @@ def _block_norm_grad_args(dout, hidden, x, dhidden, gate, scale, shift, weight, 
         elif query:
             sums.append(256)
         else:
-            # no rows: nothing is summed
-            make = _empty(like_t.shape, torch.float32, like, stream)
-            sums.append(make.zero_() if not m else make)
+            sums.append(_empty(like_t.shape, torch.float32, like, stream))
+            if not m:  # nothing is summed
+                with torch.cuda.stream(stream or torch.cuda.current_stream(like.device)):
+                    sums[-1].zero_()
     ptr = [0 if t is None else t if query else t.data_ptr() for t in sums]
     args = _BLOCK_NORM_GRAD(
         code, code if st is dt else FP32, code if mod is None or mod is dt else FP32,

@@ -36,7 +36,7 @@ bool supported(const A* a) {
 bool tma_view(const wsattn_heads* v, int heads, int batch, int64_t n) {
   auto stride = [](int64_t s, int64_t size) { return size <= 1 || (s % 8 == 0 && s <= kMaxStride); };
   return view_ok(v, 2) && v->heads == heads && aligned16(v->data) && stride(v->stride_b, batch) &&
-         stride(v->stride_h, heads) && stride(v->stride_n, n);
+         stride(v->stride_h, heads) && stride(v->stride_n, n) && (n <= 1 || v->stride_n > 0);
 }
 
 CrossView view(const wsattn_heads* v) {
@@ -88,15 +88,17 @@ void fill_common(const A* a, CrossParams* p) {
   p->scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634074);
 }
 
-// delta, where the dk, dv kernel needs it, and the sums of shared key tiles.
+// delta, where the dk, dv kernel needs it, the lengths' sums (there is room for
+// them without lengths too) and the sums of shared key tiles.
 struct GradScratch {
-  size_t delta, part;
-  size_t total() const { return delta + part; }
+  size_t delta, starts, part;
+  size_t total() const { return delta + starts + part; }
 };
 GradScratch grad_scratch(const wsattn_cross_grad_args* a, const CrossParams& p) {
-  GradScratch s{0, 0};
+  GradScratch s{0, 0, 0};
   if ((!a->dk.data && !a->dv.data) || p.batch == 0 || p.n == 0 || p.m == 0) return s;
   s.delta = up256(sizeof(float) * static_cast<size_t>(p.batch) * p.heads * p.n);
+  s.starts = up256(sizeof(int32_t) * (static_cast<size_t>(p.batch) + 1));
   s.part = sizeof(float) * static_cast<size_t>(p.ctas) * 4 * wsattn::kCrossRows * p.dim;
   return s;
 }
@@ -198,7 +200,8 @@ int wsattn_cross_backward(const wsattn_cross_grad_args* a, void* workspace, size
     return WSATTN_ERR_BAD_ARG;
   char* ws = static_cast<char*>(workspace);
   p.delta = need.delta ? reinterpret_cast<float*>(ws) : nullptr;
-  p.part_kv = need.part ? reinterpret_cast<float*>(ws + need.delta) : nullptr;
+  p.starts = need.starts ? reinterpret_cast<int32_t*>(ws + need.delta) : nullptr;
+  p.part_kv = need.part ? reinterpret_cast<float*>(ws + need.delta + need.starts) : nullptr;
   p.status = wsattn::op_status_ptr();
   const int sms = sm_count();
   if (!p.status || !sms) return WSATTN_ERR_CUDA;

@@ -52,6 +52,71 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum)
   return sum;
 }
 
+// Key tiles with keys, in order, and the units of a CTA.
+struct WalkB {
+  int b, e, kt;          // batch element, key head, key tile
+  int tiles;             // key tiles of this batch element
+  int row;               // row tile
+  int64_t left;          // units from here on, this one included
+  int len;
+};
+__device__ __forceinline__ int key_tiles(const CrossParams& p, int b) {
+  return (keys_of(p, b) + kRows - 1) / kRows;
+}
+// Key tiles with keys of one head, of the batch elements before b.
+__device__ __forceinline__ int tiles_before(const CrossParams& p, int b) {
+  return p.lengths ? p.starts[b] : b * ((p.m + kRows - 1) / kRows);
+}
+// Writes starts [batch + 1]; a warp of the kernel in front of the one that reads them.
+__device__ __forceinline__ void sum_lengths(const CrossParams& p) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int own = b0 + lane < p.batch ? key_tiles(p, b0 + lane) : 0;
+    int to = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += t;
+    }
+    if (b0 + lane < p.batch) p.starts[b0 + lane] = before + to - own;
+    before += __shfl_sync(0xffffffffu, to, 31);
+  }
+  if (lane == 0) p.starts[p.batch] = before;
+}
+// Units of all key tiles with keys.
+__device__ __forceinline__ int64_t live_units(const CrossParams& p) {
+  return static_cast<int64_t>(tiles_before(p, p.batch)) * p.kv_heads * p.tiles_n * p.tiles_h;
+}
+__device__ __forceinline__ int64_t first_unit(const CrossParams& p, int64_t units, int cta) {
+  return units * cta / p.ctas;
+}
+// The key tile of this rank among those with keys.
+__device__ __forceinline__ void key_tile_at(const CrossParams& p, int rank, WalkB& w) {
+  int lo = 0, hi = p.batch;  // the last element whose tiles begin at or before it
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (static_cast<int64_t>(tiles_before(p, mid)) * p.kv_heads <= rank)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  w.b = lo;
+  w.tiles = key_tiles(p, lo);
+  w.len = keys_of(p, lo);
+  rank -= tiles_before(p, lo) * p.kv_heads;
+  w.kt = rank % w.tiles;
+  w.e = rank / w.tiles;
+}
+__device__ __forceinline__ WalkB walk_b(const CrossParams& p, int64_t unit, int64_t end) {
+  WalkB w{};
+  w.left = end - unit;
+  if (w.left <= 0) return w;
+  const int rows = p.tiles_n * p.tiles_h;
+  w.row = static_cast<int>(unit % rows);
+  key_tile_at(p, static_cast<int>(unit / rows), w);
+  return w;
+}
 // Row r of a row tile: its query and head, and its index in [batch, heads, n].
 struct RowAt {
   int n, h;
@@ -490,7 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     if (lane == 0) dq_producer<DB>(p, l);
   } else if (warp < 3) {
     dq_issuer<BF16, DB>(p, l, tbase, warp == 2);
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    if (blockIdx.x == 0 && p.lengths && p.starts) sum_lengths(p);
+  } else {
     dq_elements<BF16, DB>(p, l, tbase);
     if (lane == 0) bulk_wait_all();
   }
@@ -539,46 +606,6 @@ struct LayoutB {
   Sync s;
 };
 
-// Key tiles with keys, in order, and the units of a CTA.
-struct WalkB {
-  int b, e, kt;          // batch element, key head, key tile
-  int tiles;             // key tiles of this batch element
-  int row;               // row tile
-  int64_t left;          // units from here on, this one included
-  int len;
-};
-__device__ __forceinline__ int key_tiles(const CrossParams& p, int b) {
-  return (keys_of(p, b) + kRows - 1) / kRows;
-}
-// Units of all key tiles with keys (every lane of the warp gets it).
-__device__ __forceinline__ int64_t live_units(const CrossParams& p) {
-  int64_t n = 0;
-  for (int b = threadIdx.x & 31; b < p.batch; b += 32) n += key_tiles(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n * p.kv_heads * p.tiles_n * p.tiles_h;
-}
-__device__ __forceinline__ int64_t first_unit(const CrossParams& p, int64_t units, int cta) {
-  return units * cta / p.ctas;
-}
-__device__ __forceinline__ WalkB walk_b(const CrossParams& p, int64_t unit, int64_t end) {
-  WalkB w{};
-  w.left = end - unit;
-  if (w.left <= 0) return w;
-  const int rows = p.tiles_n * p.tiles_h;
-  for (w.b = 0;; ++w.b) {
-    w.tiles = key_tiles(p, w.b);
-    const int64_t n = static_cast<int64_t>(w.tiles) * p.kv_heads * rows;
-    if (unit < n) break;
-    unit -= n;
-  }
-  w.row = static_cast<int>(unit % rows);
-  unit /= rows;
-  w.kt = static_cast<int>(unit % w.tiles);
-  w.e = static_cast<int>(unit / w.tiles);
-  w.len = keys_of(p, w.b);
-  return w;
-}
 // To the next unit; true where it belongs to another key tile.
 __device__ __forceinline__ bool step_b(const CrossParams& p, WalkB& w) {
   if (--w.left <= 0) return true;
@@ -948,48 +975,64 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   if (warp == 1) tmem_dealloc(tbase, kTmemCols);
 }
 
-// Key tiles that several shares hold parts of: their sums, in the shares'
-// order; keys behind the lengths: zeros.  A CTA eight rows of a key tile (of
-// all, with keys or without), a thread four columns of a row.
+// Key tiles that several shares hold parts of: their sums, in the shares' order,
+// 32 CTAs for each border between shares (eight rows of dk or dv, a thread four
+// columns of a row; the tile's first border does it).  The CTAs behind them write
+// zeros to the key tiles without keys.
+constexpr int kFinishParts = 32, kFinishThreads = 256;
 template <bool BF16>
-__global__ void __launch_bounds__(256) cross_finish_kernel(const __grid_constant__ CrossParams p) {
+__global__ void __launch_bounds__(kFinishThreads) cross_finish_kernel(const __grid_constant__ CrossParams p) {
   using E = typename Elem<BF16>::type;
   griddep_wait();
-  const int all = (p.m + kRows - 1) / kRows;
-  const int kt = blockIdx.x % all, e = blockIdx.x / all % p.kv_heads, b = blockIdx.x / all / p.kv_heads;
   const int rows = p.n ? p.tiles_n * p.tiles_h : 0;
-  const int tiles = key_tiles(p, b), len = keys_of(p, b);
-  int64_t c0 = 0, c1 = -1;
-  int64_t begin = 0, units = 0;
-  const bool live = kt < tiles && rows > 0;
-  if (live) {
-    units = live_units(p);
-    for (int i = 0; i < b; ++i) begin += key_tiles(p, i);
-    begin = (begin * p.kv_heads + static_cast<int64_t>(e) * tiles + kt) * rows;
-    // share of a unit: the largest c with first_unit(c) <= unit
-    c0 = ((begin + 1) * p.ctas - 1) / units;
-    c1 = ((begin + rows) * p.ctas - 1) / units;
-    if (c0 == c1) return;  // finished in its share
+  const int borders = rows && p.ctas ? p.ctas - 1 : 0;
+  if (blockIdx.x >= borders * kFinishParts) {
+    const int all = (p.m + kRows - 1) / kRows;
+    const int tiles = p.batch * p.kv_heads * all;
+    const int row16 = p.dim / 8;  // words of a row
+    for (int64_t i = blockIdx.x - borders * kFinishParts; i < tiles; i += gridDim.x - borders * kFinishParts) {
+      const int kt = static_cast<int>(i % all), e = static_cast<int>(i / all % p.kv_heads);
+      const int b = static_cast<int>(i / all / p.kv_heads);
+      if (rows && kt < key_tiles(p, b)) continue;
+      const int keys = min(kRows, p.m - kt * kRows);
+      for (int which = 0; which < 2; ++which) {
+        const CrossView& g = which ? p.dv : p.dk;
+        if (!g.data) continue;
+        E* to = static_cast<E*>(const_cast<void*>(g.data)) + b * g.sb + e * g.sh;
+        for (int x = threadIdx.x; x < keys * row16; x += kFinishThreads)
+          reinterpret_cast<uint4*>(to + static_cast<int64_t>(kt * kRows + x / row16) * g.sn)[x % row16] =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    return;
   }
-  // grid row y: rows y * 8 .. of dk (y < 16) or dv
-  const int which = blockIdx.y / 16, c = 4 * (threadIdx.x & 31), r = blockIdx.y % 16 * 8 + threadIdx.x / 32;
-  const int key = kt * kRows + r;
+  const int border = blockIdx.x / kFinishParts + 1, part = blockIdx.x % kFinishParts;
+  const int64_t units = live_units(p), at = first_unit(p, units, border);
+  const int64_t begin = at / rows * rows;
+  if (at == begin || first_unit(p, units, border - 1) > begin) return;  // between tiles, or not the first
+  WalkB w{};
+  key_tile_at(p, static_cast<int>(begin / rows), w);
+  const int which = part / 16, c = 4 * (threadIdx.x & 31), r = part % 16 * 8 + threadIdx.x / 32;
+  const int key = w.kt * kRows + r;
   const CrossView& g = which ? p.dv : p.dk;
   if (key >= p.m || c >= p.dim || !g.data) return;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t i = c0; key < len && i <= c1; ++i) {
-    const int64_t first = first_unit(p, units, static_cast<int>(i));
-    if (first == first_unit(p, units, static_cast<int>(i) + 1)) continue;  // an empty share
-    const int slot = first > begin ? 0 : 1;
-    const float4 t = *reinterpret_cast<const float4*>(
-        p.part_kv + (((i * 2 + slot) * 2 + which) * kRows + r) * p.dim + c);
-    v[0] += t.x;
-    v[1] += t.y;
-    v[2] += t.z;
-    v[3] += t.w;
+  int64_t first = first_unit(p, units, border - 1);
+  for (int i = border - 1; i < p.ctas && first < begin + rows; ++i) {
+    const int64_t next = first_unit(p, units, i + 1);
+    if (first < next && key < w.len) {  // a share that is not empty
+      const int slot = first > begin ? 0 : 1;
+      const float4 t = *reinterpret_cast<const float4*>(
+          p.part_kv + (((static_cast<int64_t>(i) * 2 + slot) * 2 + which) * kRows + r) * p.dim + c);
+      v[0] += t.x;
+      v[1] += t.y;
+      v[2] += t.z;
+      v[3] += t.w;
+    }
+    first = next;
   }
   const float scale = which ? (BF16 ? 1.f : 0.0009765625f) : p.scale;
-  E* to = static_cast<E*>(const_cast<void*>(g.data)) + b * g.sb + e * g.sh + key * g.sn + c;
+  E* to = static_cast<E*>(const_cast<void*>(g.data)) + w.b * g.sb + w.e * g.sh + key * g.sn + c;
   *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair(v[0] * scale, v[1] * scale, E()),
                                              pack_pair(v[2] * scale, v[3] * scale, E()));
 }
@@ -1000,6 +1043,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(128) cross_delta_kernel(const __grid_constant__ CrossParams p) {
   using E = typename Elem<BF16>::type;
   griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 32 && p.lengths) sum_lengths(p);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
   if (row >= static_cast<int64_t>(p.batch) * p.heads * p.n) return;
   const int n = static_cast<int>(row % p.n);
@@ -1052,8 +1096,10 @@ cudaError_t backward(const CrossParams& p, int sms, cudaStream_t s) {
   }
   if (e != cudaSuccess || !keys) return e;
   const int64_t tiles = static_cast<int64_t>(p.batch) * p.kv_heads * ((p.m + kRows - 1) / kRows);
-  return launch_dependent(cross_finish_kernel<BF16>, dim3(static_cast<unsigned>(tiles), 32), dim3(256), 0,
-                          s, p);
+  const int borders = p.n && p.ctas ? (p.ctas - 1) * kFinishParts : 0;
+  const int zeros = p.lengths || !p.n ? static_cast<int>(tiles < 8 * sms ? tiles : 8 * sms) : 0;
+  if (!(borders + zeros)) return e;
+  return launch_dependent(cross_finish_kernel<BF16>, dim3(borders + zeros), dim3(kFinishThreads), 0, s, p);
 }
 
 }  // namespace

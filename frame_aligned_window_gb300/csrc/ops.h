@@ -290,6 +290,7 @@ struct CrossParams {
   int do_h, do_b, o_h, o_b;
   float* delta;                        // [batch, heads, n] sum_d dout out
   float* part_kv;                      // [ctas][2][dk, dv][128][D] sums of shares of a key tile
+  int32_t* starts;                     // [batch + 1] sums of the lengths' key tiles
   int ctas;                            // of the dk, dv kernel
   int* status;
 };

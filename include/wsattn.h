@@ -433,7 +433,8 @@ int wsattn_linear_backward_workspace(const wsattn_linear_grad_args* args, size_t
  *   n_tokens, n_keys  below 2^31 - 511; either may be 0
  *   q, out     [batch, heads, n_tokens, D] views
  *   k, v       [batch, kv heads, n_keys, D] views of one head count that
- *              divides q's; inputs may have strides of 0 (broadcast)
+ *              divides q's; inputs may be broadcast over batch elements and
+ *              heads (strides of 0)
  *   k_lengths  int32 [batch] in device memory, or NULL: n_keys for all.  Values
  *              outside 0 .. n_keys count as the nearest of them
  *   scale      > 0, finite; 1 / sqrt(D) is the usual one
@@ -461,6 +462,8 @@ int wsattn_cross_workspace(const wsattn_cross_args* args, size_t* bytes);
  *   dv = p^T dout,  ds = scale p (dout v^T - sum_d dout out),  dq = ds k,  dk = ds^T q
  * p and ds are rounded to dtype for the products, whose sums are fp32; dk and
  * dv are summed over the query heads that share a key head, in a fixed order.
+ * (In fp16 ds keeps the type's range, as dq, dk and dv do: dout scaled so that
+ * they fit has to leave room for dout v^T too.)
  * Keys behind a length get zeros, and so do rows that no key was left for.
  *   out, lse   as wsattn_cross left them, for the same k_lengths and scale
  *   dout       as out; dq like q, dk and dv like k: views, whose elements must
