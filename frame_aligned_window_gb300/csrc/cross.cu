@@ -11,8 +11,8 @@
 // 128 queries of a head, or, with fewer queries, those of several heads that
 // share a key head.  A work item is a pair of row tiles of one key head, which
 // share every key step that is loaded; a persistent CTA an SM walks the items.
-//   warp 0     TMA: row tiles of q (a ring of three), key and value steps (a
-//              ring of four)
+//   warp 0     TMA: row tiles of q (two, each free when the item's last Q K^T is
+//              done), key and value steps (a ring of four)
 //   warp 1     MMA issue (one elected lane): S_u = Q_u K^T, O_u += P_u V for
 //              the two row tiles u in turn; tensor memory
 //   warps 4-11 softmax and epilogue, a warpgroup for each row tile; thread =
@@ -23,22 +23,27 @@
 // cannot overtake the P_u V that reads P_u.  While one row tile's softmax runs,
 // the tensor core works on the other's two products.
 //
-// What bounds it, measured at 24 heads x 8192 queries x 4096 keys of 128 (331 us,
-// 1244 TFLOP/s): a step of both row tiles takes 3900 cycles where its MMAs take
-// 2048 by themselves.  Q K^T with both operands in shared memory, the values and
-// what TMA writes add up to 256 KB a step, 2048 cycles of shared memory as well,
+// What bounds it, measured at 24 heads x 8192 queries x 4096 keys of 128 (318 us,
+// 1297 TFLOP/s): a step of both row tiles takes about 3000 cycles where its MMAs
+// take 2048 by themselves.  Q K^T with both operands in shared memory, the values
+// and what TMA writes add up to 256 KB a step, 2048 cycles of shared memory as well,
 // and a row's softmax (max 480 cycles, exponentials 1100, storing 290) stands
-// between two products of its tile.  Tried beside it, in the same call: an issuer
-// for each row tile 407 us (the two then run in step), logits held in registers
-// instead of read twice 363, one row tile with Q in tensor memory and both
-// warpgroups on it 488 to 620, with an O for each half of the keys 436; four
-// warpgroups a row tile 1150 (96 registers a thread).
+// between two products of its tile.  Few keys are bound by an item's beginning and
+// end, about 5000 cycles beside its steps: 22880 queries of 24 heads take 66 us with
+// 128 keys, 91 with 226 (3.1 TB/s); 21952 of 2 x 40 heads with 512 keys 408 (2.3
+// TB/s).  Tried beside it: row tiles of q in a ring of three that the outputs were
+// written over (452 us at 512 keys, 116 at 226), an issuer for each row tile (407 at
+// 4096 keys where one took 331: the two run in step), logits held in registers
+// instead of read twice (363), one row tile with Q in tensor memory and both
+// warpgroups on it (488 to 620, with an O for each half of the keys 436), four
+// warpgroups a row tile (1150: 96 registers a thread), the issue of the two row
+// tiles as a loop (faster with one step, 173 to 197 us at 2 x 40 heads and 128 keys,
+// slower with four, 439 to 412).
 //
-// The epilogue writes a row tile over its own queries in shared memory and
-// from there by TMA, which drops the rows behind the last query.  With few row
-// tiles and many keys, `splits` parts of the keys go to different CTAs, which
-// leave fp32 rows and their sums in the workspace, and a second kernel joins
-// them.
+// The epilogue writes 64 columns of a warp's rows to shared memory and from there
+// by TMA, which drops the rows behind the last query.  With few row tiles and many
+// keys, `splits` parts of the keys go to different CTAs, which leave fp32 rows and
+// their sums in the workspace, and a second kernel joins them.
 #include "cross.cuh"
 
 namespace wsattn {
@@ -47,8 +52,9 @@ namespace {
 using namespace cross;
 
 constexpr int kThreads = 384;
-constexpr int kQTiles = 3;    // ring of row tiles
+constexpr int kQTiles = 2;    // ring of row tiles
 constexpr int kSteps = 4;     // ring of key and value steps
+constexpr uint32_t kOutBytes = 32 * 128;  // of a softmax warp
 constexpr float kSlack = 8.f;  // rows are rescaled when a maximum grows by more than 2^8
 
 enum : int {
@@ -120,7 +126,7 @@ struct Walk {
 template <int DB>
 struct Layout {
   static constexpr uint32_t kTile = DB * kBoxBytes;  // a row tile, or a key step
-  uint32_t q, kv;
+  uint32_t q, kv, out;  // out: 64 columns of each softmax warp's rows
   Sync s;
 };
 
@@ -190,21 +196,23 @@ __device__ void mma_issuer(const CrossParams& p, const Layout<DB>& l, uint32_t t
   Ring<kQTiles> qr;
   Ring<kSteps> kr;       // the next step to take: K and V in turn
   uint32_t pphase = 0;   // bit u: parity of P_u's next use
-  uint32_t q_slot[2] = {0, 0};
+  uint32_t q_slots = 0;  // byte u: row tile u's slot
   auto wait_mma = [&](uint32_t b, uint32_t parity) {
     return wait_warp(s, b, parity, kStatusTimeoutMma);
   };
   auto qk = [&](const Walk& w, int u, uint32_t kslot) {
     if (w.first()) {
-      q_slot[u] = qr.slot;
+      q_slots = (q_slots & ~(255u << 8 * u)) | qr.slot << 8 * u;
       if (!wait_mma(bar(s, B_QFULL + qr.slot), qr.phase)) return false;
       qr.next();
       tc_fence_after();
     }
     const uint32_t id = id_qk | (static_cast<uint32_t>(w.keys16()) >> 3) << 17;
-    const uint64_t a = q0 + q_slot[u] * kTile16, b = k0 + kslot * kTile16;
+    const uint32_t q_slot = q_slots >> 8 * u & 255u;
+    const uint64_t a = q0 + q_slot * kTile16, b = k0 + kslot * kTile16;
     issue_ss(t_s + u * kRows, a, b, id, ksteps);
     tc_commit_warp(bar(s, B_SFULL + u));
+    if (w.last()) tc_commit_warp(bar(s, B_QEMPTY + q_slot));
     return true;
   };
   Walk cur{static_cast<int>(blockIdx.x), 0, {}};
@@ -269,19 +277,30 @@ __device__ __forceinline__ void exp_store(const uint32_t (&sv)[16], uint64_t c2,
   tmem_st8(taddr, w);
 }
 
-// Keys from column `rem` on are masked (FULL: none of the 128 are).
-template <bool FULL>
-__device__ __forceinline__ void mask16(uint32_t (&sv)[16], int col, int rem) {
-  if constexpr (!FULL) {
+// Logits of the keys from column `rem` on become -infinity.  (With that, a step of
+// fewer keys costs what a whole one does: one kind of maximum and exponentials, where
+// a second kind for the end of the keys took 10 us of 70 at 22880 queries, 77 keys.)
+__device__ __forceinline__ void mask_tail(uint32_t t_s, int rem) {
+  uint32_t sv[16];
+  int col = rem & ~15;
+  if (rem & 15) {
+    tmem_ld16(t_s + col, sv);
+    tmem_wait_ld16(sv);
 #pragma unroll
     for (int x = 0; x < 16; ++x)
-      if (col + x >= rem) sv[x] = 0xff800000u;
+      if (x >= (rem & 15)) sv[x] = 0xff800000u;
+    tmem_st16(t_s + col, sv);
+    col += 16;
   }
+#pragma unroll
+  for (int x = 0; x < 16; ++x) sv[x] = 0xff800000u;
+#pragma unroll 1
+  for (; col < kRows; col += 16) tmem_st16(t_s + col, sv);
+  tmem_wait_st();
 }
 // Largest logit of a row's step: 64 columns are loaded while the other 64 are
 // compared.
-template <bool FULL>
-__device__ __forceinline__ float step_max(uint32_t t_s, int rem) {
+__device__ __forceinline__ float step_max(uint32_t t_s) {
   float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   uint32_t sv[2][4][16];
 #pragma unroll
@@ -297,7 +316,6 @@ __device__ __forceinline__ float step_max(uint32_t t_s, int rem) {
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      mask16<FULL>(sv[h][k], 64 * h + 16 * k, rem);
 #pragma unroll
       for (int x = 0; x < 16; x += 8)
 #pragma unroll
@@ -310,10 +328,9 @@ __device__ __forceinline__ float step_max(uint32_t t_s, int rem) {
 // A step's probabilities 2^(s c + nb), stored in pairs over its logits, and
 // their sum.  The logits are read again (a read costs less than 128 registers
 // that hold them), 32 columns ahead.
-template <bool BF16, bool FULL>
-__device__ __forceinline__ float step_exp(uint32_t t_s, int rem, uint64_t c2, float nb) {
+template <bool BF16>
+__device__ __forceinline__ float step_exp(uint32_t t_s, uint64_t c2, float nb) {
   const uint64_t nb2 = f2_pack(nb, nb);
-  const int chunks = FULL ? 8 : (rem + 15) / 16;
   uint64_t la = f2_pack(0.f, 0.f), lb = la;
   uint32_t sv[2][2][16];
 #pragma unroll
@@ -328,11 +345,7 @@ __device__ __forceinline__ float step_exp(uint32_t t_s, int rem, uint64_t c2, fl
       for (int k = 0; k < 2; ++k) tmem_ld16(t_s + 32 * (q + 1) + 16 * k, sv[(q + 1) & 1][k]);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      mask16<FULL>(sv[q & 1][k], 32 * q + 16 * k, rem);
-      if (FULL || 2 * q + k < chunks)
-        exp_store<BF16>(sv[q & 1][k], c2, nb2, la, lb, t_s + 8 * (2 * q + k));
-    }
+    for (int k = 0; k < 2; ++k) exp_store<BF16>(sv[q & 1][k], c2, nb2, la, lb, t_s + 8 * (2 * q + k));
   }
   const float2 ab = f2_unpack(f2_add(la, lb));
   return ab.x + ab.y;
@@ -351,20 +364,11 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
   auto wait_s = [&](uint32_t b, uint32_t parity) {
     return wait_warp(s, b, parity, kStatusTimeoutSoftmax);
   };
-  Ring<kQTiles> qr;            // row tiles of both warpgroups, in order
-  Ring<kSteps> kr;             // key and value steps, in order
+  Ring<kSteps> kr;  // key and value steps, in order
   uint32_t sphase = 0, ophase = 0;
   for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
     const Item t = item_of(p, i);
     const bool mine = u == 0 || t.two, any = t.step0 < t.step1;
-    uint32_t q_slot = qr.slot;
-    if (any) {
-      qr.next();
-      if (t.two) {
-        if (u == 1) q_slot = qr.slot;
-        qr.next();
-      }
-    }
     if (!mine) {
       for (int j = t.step0; j < t.step1; ++j) {
         kr.next();
@@ -382,20 +386,22 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
       sphase ^= 1u;
       tc_fence_after();
       const bool full = rem >= kRows;
-      const float top = c * (full ? step_max<true>(t_s, rem) : step_max<false>(t_s, rem));
+      if (!full) mask_tail(t_s, rem);
+      const float top = c * step_max(t_s);
       // the reference moves only where the maximum has grown past it by far
       const float m_new = top > m + kSlack ? top : m;
       const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
       m = m_new;
       const float nb = m == -INFINITY ? 0.f : -m;
-      sum = sum * alpha + (full ? step_exp<BF16, true>(t_s, rem, c2, nb)
-                                : step_exp<BF16, false>(t_s, rem, c2, nb));
-      if (rem < kRows && (rem & 15)) {
+      sum = sum * alpha + step_exp<BF16>(t_s, c2, nb);
+      const int end = min((rem + 15) / 16 * 16, p.m - j * kRows);
+      if (!full && rem < end) {
         // the product reads on to the chunk's end: no value there, whatever lies
-        // behind the length (each warpgroup before its own product)
+        // behind the length (each warpgroup before its own product; behind the
+        // last key of all the load left zeros)
         if (!wait_s(bar(s, B_KVFULL + vr.slot), vr.phase)) return;
         const uint32_t v = l.kv + vr.slot * Layout<DB>::kTile;
-        for (int x = r; x < ((rem + 15) / 16 * 16 - rem) * 8 * DB; x += kRows)
+        for (int x = r; x < (end - rem) * 8 * DB; x += kRows)
           st_shared_v4(swizzled(v, rem + x / (8 * DB), x % (8 * DB)), 0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
       }
@@ -448,7 +454,7 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
     tc_fence_after();
     const float inv = 1.f / sum;
     const bool whole = p.splits == 1 && p.box_h == 1;  // rows of one head: by TMA
-    const uint32_t tile = l.q + q_slot * Layout<DB>::kTile;
+    const uint32_t stage = l.out + (warp - 4) * kOutBytes;
 #pragma unroll 1
     for (int k0 = 0; k0 < dim16; k0 += 4) {
       uint32_t o4[4][16];
@@ -457,6 +463,10 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
       tmem_wait_ld();
 #pragma unroll
       for (int k = 0; k < 4; ++k) reg_fence16(o4[k]);
+      if (whole) {  // what was stored from here before is on its way
+        if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
+        __syncwarp();
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (k0 + k >= dim16) break;
@@ -477,26 +487,23 @@ __device__ void softmax(const CrossParams& p, const Layout<DB>& l, uint32_t tbas
         for (int x = 0; x < 8; ++x)
           w[x] = pack_pair(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv, E());
         if (whole) {
-          st_shared_v4(swizzled(tile, r, 2 * (k0 + k)), w[0], w[1], w[2], w[3]);
-          st_shared_v4(swizzled(tile, r, 2 * (k0 + k) + 1), w[4], w[5], w[6], w[7]);
+          st_shared_v4(swizzled(stage, r & 31, 2 * k), w[0], w[1], w[2], w[3]);
+          st_shared_v4(swizzled(stage, r & 31, 2 * k + 1), w[4], w[5], w[6], w[7]);
         } else if (valid) {
           reinterpret_cast<uint4*>(out)[2 * (k0 + k)] = make_uint4(w[0], w[1], w[2], w[3]);
           reinterpret_cast<uint4*>(out)[2 * (k0 + k) + 1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-    }
-    tc_fence_before();
-    if (whole) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0 && n0 + 32 * wq < p.n) {
-        for (int k = 0; 4 * k < dim16; ++k)
-          tma_store_4d(&p.tm_o, tile + k * kBoxBytes + wq * 4096u, 64 * k, n0 + 32 * wq, h0, t.b);
-        bulk_commit_group();
-        bulk_wait_read_all();
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0 && n0 + 32 * wq < p.n) {
+          tma_store_4d(&p.tm_o, stage, 16 * k0, n0 + 32 * wq, h0, t.b);
+          bulk_commit_group();
+        }
       }
     }
-    warp_arrive(bar(s, B_QEMPTY + q_slot));
+    tc_fence_before();
   }
 }
 
@@ -509,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Layout<DB> l;
   l.q = base;
   l.kv = base + kQTiles * Layout<DB>::kTile;
-  l.s.bars = l.kv + kSteps * Layout<DB>::kTile;
+  l.out = l.kv + kSteps * Layout<DB>::kTile;
+  l.s.bars = l.out + 8 * kOutBytes;
   uint8_t* gb = smem_raw + (l.s.bars - raw);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(gb + 8 * B_COUNT);
   l.s.abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kQTiles; ++i) {
       mbar_init(bar(l.s, B_QFULL + i), 1);
-      mbar_init(bar(l.s, B_QEMPTY + i), 4);
+      mbar_init(bar(l.s, B_QEMPTY + i), 1);
     }
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(bar(l.s, B_KVFULL + i), 1);
@@ -605,7 +613,7 @@ cudaError_t forward(const CrossParams& p, int sms, cudaStream_t s) {
   static bool attr_set[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
-  constexpr size_t kSmem = 1024 + (kQTiles + kSteps) * Layout<DB>::kTile + 8 * B_COUNT + 16;
+  constexpr size_t kSmem = 1024 + (kQTiles + kSteps) * Layout<DB>::kTile + 8 * kOutBytes + 8 * B_COUNT + 16;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   if (!attr_set[dev]) {
     const cudaError_t e =
@@ -625,8 +633,8 @@ cudaError_t forward(const CrossParams& p, int sms, cudaStream_t s) {
 }  // namespace
 
 // Row tiles of 128 queries of a head; with fewer queries, of as many heads of
-// one key head as fit (heads of their own: a broadcast one has one row to load).  A CTA takes about kStep cycles for a key step with one
-// row tile or two, kItem for an item's beginning and end, and joining parts
+// one key head as fit (heads of their own: a broadcast one has one row to load).
+// A CTA takes about kStep cycles for a key step with one row tile or two, kItem for an item's beginning and end, and joining parts
 // costs about kJoin: the pair and the number of parts that make the least of it
 // (a machine of 152 SMs whatever the device has, so that the workspace's size
 // needs no device).
@@ -664,7 +672,7 @@ void split_cross(CrossParams* p) {
     }
   }
   const int64_t items = heads * ((tiles + p->pair - 1) / p->pair) * p->splits;
-  p->items = items <= INT32_MAX ? static_cast<int>(items) : -1;
+  p->items = items <= INT32_MAX / 2 ? static_cast<int>(items) : -1;
 }
 
 // fp32 rows first, then their sums.

@@ -100,59 +100,38 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t tile, int r, int u) {
          (static_cast<uint32_t>((u ^ r) & 7) << 4);
 }
 
-// The products of a step, issued by a converged warp.  Eight chunks (and four)
-// are straight code: a branch before each MMA makes its issue take 130 cycles,
-// twice the MMA's own 64.
+// The products of a step, issued by a converged warp: straight code, because a
+// branch before each MMA makes its issue take 130 cycles, twice the MMA's own 64.
+// Fewer than eight chunks are eight of which some are not issued.  (One kind of
+// code for both: beside another for whole steps, and a loop for the rest, the
+// forward pass took 435 us where it takes 412, at 2 x 40 heads, 21952 queries and
+// 512 keys; what the issuing warp executes has to stay in its instruction cache.)
 // D[128, N] = A B^T over up to eight chunks of the head's width, 16 columns each:
 // A and B row by row in shared memory (64-column boxes) ...
 constexpr uint64_t kBox16 = kBoxBytes >> 4;
-template <int N>
-__device__ __forceinline__ void ss_chunks(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
-#pragma unroll
-  for (int kk = 0; kk < N; ++kk)
-    mma_ss_warp(d, a + (kk >> 2) * kBox16 + (kk & 3) * 2, b + (kk >> 2) * kBox16 + (kk & 3) * 2, id,
-                kk > 0 ? 1u : 0u);
-}
 __device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int chunks) {
-  if (chunks == 8) return ss_chunks<8>(d, a, b, id);
-  if (chunks == 4) return ss_chunks<4>(d, a, b, id);
-#pragma unroll 1
-  for (int kk = 0; kk < chunks; ++kk)
-    mma_ss_warp(d, a + (kk >> 2) * kBox16 + (kk & 3) * 2, b + (kk >> 2) * kBox16 + (kk & 3) * 2, id,
-                kk > 0 ? 1u : 0u);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ss_warp_if(kk < chunks, d, a + (kk >> 2) * kBox16 + (kk & 3) * 2,
+                   b + (kk >> 2) * kBox16 + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
 }
 // ... or A in tensor memory (8 columns a chunk).
-template <int N>
-__device__ __forceinline__ void ts_chunks(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
-#pragma unroll
-  for (int kk = 0; kk < N; ++kk)
-    mma_ts_warp(d, a + kk * 8, b + (kk >> 2) * kBox16 + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
-}
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, int chunks) {
-  if (chunks == 8) return ts_chunks<8>(d, a, b, id);
-  if (chunks == 4) return ts_chunks<4>(d, a, b, id);
-#pragma unroll 1
-  for (int kk = 0; kk < chunks; ++kk)
-    mma_ts_warp(d, a + kk * 8, b + (kk >> 2) * kBox16 + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts_warp_if(kk < chunks, d, a + kk * 8, b + (kk >> 2) * kBox16 + (kk & 3) * 2, id,
+                   kk > 0 ? 1u : 0u);
 }
 // D[128, head width] (+)= A B over up to eight chunks of 16 rows of B: A in
 // tensor memory, 8 columns a chunk, the second half of the chunks `gap` columns
 // behind where the first ends.
 __device__ __forceinline__ void issue_sum(uint32_t d, uint32_t a, uint32_t gap, uint64_t b, uint32_t id,
                                           int chunks, bool add) {
-  if (chunks == 8) {
-    mma_ts_warp(d, a, b, id, add ? 1u : 0u);
-#pragma unroll
-    for (int kk = 1; kk < 4; ++kk) mma_ts_warp(d, a + kk * 8, b + kk * 128, id, 1u);
-    a += gap;
-#pragma unroll
-    for (int kk = 4; kk < 8; ++kk) mma_ts_warp(d, a + kk * 8, b + kk * 128, id, 1u);
-    return;
-  }
   const int low = (chunks + 1) / 2;
-#pragma unroll 1
-  for (int kk = 0; kk < chunks; ++kk)
-    mma_ts_warp(d, a + kk * 8 + (kk < low ? 0u : gap), b + kk * 128, id, kk > 0 || add ? 1u : 0u);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts_warp_if(kk < chunks, d, a + kk * 8 + (kk < low ? 0u : gap), b + kk * 128, id,
+                   kk > 0 || add ? 1u : 0u);
 }
 
 }  // namespace cross

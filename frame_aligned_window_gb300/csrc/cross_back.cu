@@ -10,7 +10,7 @@
 // instead of five, but no sum leaves the chip before it is complete (dq summed
 // over key tiles elsewhere would be fp32 traffic of 4 D bytes per query and key
 // tile), and none depends on the order in which CTAs finish.  At 2 x 40 heads,
-// 21952 queries and 512 keys of 128: dq 740 us (933 TFLOP/s of its three
+// 21952 queries and 512 keys of 128: dq 727 us (950 TFLOP/s of its three
 // products, 2.5 TB/s), dk and dv 690 us (1330 TFLOP/s of their four).
 #include "cross.cuh"
 
@@ -1109,7 +1109,7 @@ void split_cross_backward(CrossParams* p) {
   p->pair = p->splits = 1;
   const int64_t heads = static_cast<int64_t>(p->batch) * p->kv_heads;
   const int64_t rows = static_cast<int64_t>(p->tiles_n) * p->tiles_h;
-  p->items = heads * rows <= INT32_MAX ? static_cast<int>(heads * rows) : -1;
+  p->items = heads * rows <= INT32_MAX / 2 ? static_cast<int>(heads * rows) : -1;
   // a share of two units at least
   const int64_t units = heads * ((p->m + kCrossRows - 1) / kCrossRows) * rows;
   p->ctas = units < 2 * kTilingSms ? static_cast<int>((units + 1) / 2) : kTilingSms;

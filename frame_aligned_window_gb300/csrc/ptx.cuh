@@ -265,14 +265,24 @@ __device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accum)
       : "memory");
 }
-// mma_ss issued from a converged warp, likewise.
-__device__ __forceinline__ void mma_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accum) {
+// Issued only where `go` is not 0: a predicate where a branch would hold up the
+// MMAs behind it.
+__device__ __forceinline__ void mma_ts_warp_if(uint32_t go, uint32_t d_tmem, uint32_t a_tmem,
+                                               uint64_t b_desc, uint32_t idesc, uint32_t accum) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.b32 e, %5, 0, e;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accum), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss_warp_if(uint32_t go, uint32_t d_tmem, uint64_t a_desc,
+                                               uint64_t b_desc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.b32 e, %5, 0, e;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum), "r"(go)
       : "memory");
 }
 // tc_commit from a converged warp (one elected lane commits).
