@@ -976,10 +976,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
 }
 
 // Key tiles that several shares hold parts of: their sums, in the shares' order,
-// 32 CTAs for each border between shares (eight rows of dk or dv, a thread four
-// columns of a row; the tile's first border does it).  The CTAs behind them write
-// zeros to the key tiles without keys.
-constexpr int kFinishParts = 32, kFinishThreads = 256;
+// eight CTAs for each border between shares (32 rows of dk or dv, a thread four
+// columns of four rows; the tile's first border does it).  The CTAs behind them
+// write zeros to the key tiles without keys.
+constexpr int kFinishParts = 8, kFinishThreads = 256;
 template <bool BF16>
 __global__ void __launch_bounds__(kFinishThreads) cross_finish_kernel(const __grid_constant__ CrossParams p) {
   using E = typename Elem<BF16>::type;
@@ -1012,29 +1012,43 @@ __global__ void __launch_bounds__(kFinishThreads) cross_finish_kernel(const __gr
   if (at == begin || first_unit(p, units, border - 1) > begin) return;  // between tiles, or not the first
   WalkB w{};
   key_tile_at(p, static_cast<int>(begin / rows), w);
-  const int which = part / 16, c = 4 * (threadIdx.x & 31), r = part % 16 * 8 + threadIdx.x / 32;
-  const int key = w.kt * kRows + r;
+  const int which = part / 4, c = 4 * (threadIdx.x & 31), r0 = part % 4 * 32 + threadIdx.x / 32;
   const CrossView& g = which ? p.dv : p.dk;
-  if (key >= p.m || c >= p.dim || !g.data) return;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c >= p.dim || !g.data) return;
+  float4 v[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   int64_t first = first_unit(p, units, border - 1);
   for (int i = border - 1; i < p.ctas && first < begin + rows; ++i) {
     const int64_t next = first_unit(p, units, i + 1);
-    if (first < next && key < w.len) {  // a share that is not empty
+    if (first < next) {  // a share that is not empty
       const int slot = first > begin ? 0 : 1;
-      const float4 t = *reinterpret_cast<const float4*>(
-          p.part_kv + (((static_cast<int64_t>(i) * 2 + slot) * 2 + which) * kRows + r) * p.dim + c);
-      v[0] += t.x;
-      v[1] += t.y;
-      v[2] += t.z;
-      v[3] += t.w;
+      const float* from = p.part_kv +
+                          (((static_cast<int64_t>(i) * 2 + slot) * 2 + which) * kRows + r0) * p.dim + c;
+      float4 t[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) t[x] = *reinterpret_cast<const float4*>(from + 8 * x * p.dim);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        v[x].x += t[x].x;
+        v[x].y += t[x].y;
+        v[x].z += t[x].z;
+        v[x].w += t[x].w;
+      }
     }
     first = next;
   }
   const float scale = which ? (BF16 ? 1.f : 0.0009765625f) : p.scale;
-  E* to = static_cast<E*>(const_cast<void*>(g.data)) + w.b * g.sb + w.e * g.sh + key * g.sn + c;
-  *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair(v[0] * scale, v[1] * scale, E()),
-                                             pack_pair(v[2] * scale, v[3] * scale, E()));
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int key = w.kt * kRows + r0 + 8 * x;
+    if (key >= p.m) break;
+    E* to = static_cast<E*>(const_cast<void*>(g.data)) + w.b * g.sb + w.e * g.sh + key * g.sn + c;
+    *reinterpret_cast<uint2*>(to) =
+        key < w.len ? make_uint2(pack_pair(v[x].x * scale, v[x].y * scale, E()),
+                                 pack_pair(v[x].z * scale, v[x].w * scale, E()))
+                    : make_uint2(0u, 0u);
+  }
 }
 
 // delta alone, where dq is not wanted: a thread a row, its sum in the order of
