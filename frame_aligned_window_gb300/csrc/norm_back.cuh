@@ -13,7 +13,9 @@
 //   dpost_weight of gate E
 // so that three sums a column, in registers, serve all six.
 //
-// Bound by HBM (dy, h, x, dh' in, dres and dx out).  A CTA takes a contiguous
+// What it moves is dy, h, x, dh' in, dres and dx out: 43904 x 5120 bf16 take 836 us
+// (3.2 TB/s), bound by the latency of a row's reductions at the 20 to 30 warps an SM
+// that the sums leave registers for.  A CTA takes a contiguous
 // share of the rows and one row at a time; the next rows are on their way
 // through a ring of cp.async stages in shared memory meanwhile (a thread reads
 // what it loaded itself: no barrier).  A group inside one share is finished
@@ -388,13 +390,16 @@ __global__ void __launch_bounds__(MAXT, MINB)
   if (r0 < r1) flush(g);
 }
 
-// How a row is held: `warps` warps with v pieces a thread, per_sm CTAs an SM.
+// How a row is held: `warps` warps with v pieces a thread, per_sm CTAs an SM.  At
+// 22880 x 2560 one piece a thread and three CTAs take 214 us, two pieces and two CTAs
+// 367, one piece and four CTAs of 48 registers 286; at 43904 x 5120 two pieces and two
+// CTAs 836, three CTAs (64 registers) 984, one piece and two CTAs 1083.
 struct BackShape {
   int v, warps, per_sm;
 };
 inline BackShape back_shape(int n) {
-  const int v = n <= 2048 ? 1 : n <= 8192 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
-  int per_sm = v == 1 ? 24 / warps : warps <= 10 ? 2 : 1;
+  const int v = n <= 2560 ? 1 : n <= 8192 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
+  int per_sm = v == 1 ? (warps > 8 ? 3 : 24 / warps) : warps <= 10 ? 2 : 1;
   if (per_sm > 16) per_sm = 16;
   return {v, warps, per_sm};
 }
@@ -426,7 +431,9 @@ cudaError_t backward(const NormParams& q, cudaStream_t s) {
   const size_t fit = kRingBytes / sh.per_sm / row;
   p.stages = fit < 1 ? 1 : fit > kMaxStagesBack ? kMaxStagesBack : static_cast<int>(fit);
   switch (sh.v) {
-    case 1: return backward_one<T, R, 1, 256, 3>(p, s);
+    case 1:
+      if (sh.warps > 8) return backward_one<T, R, 1, 320, 3>(p, s);
+      return backward_one<T, R, 1, 256, 3>(p, s);
     case 2:
       if (sh.warps <= 10) return backward_one<T, R, 2, 320, 2>(p, s);
       return backward_one<T, R, 2, 512, 1>(p, s);
