@@ -392,14 +392,15 @@ __global__ void __launch_bounds__(MAXT, MINB)
 
 // How a row is held: `warps` warps with v pieces a thread, per_sm CTAs an SM.  At
 // 22880 x 2560 one piece a thread and three CTAs take 214 us, two pieces and two CTAs
-// 367, one piece and four CTAs of 48 registers 286; at 43904 x 5120 two pieces and two
+// 367, one piece and four CTAs of 48 registers 286; at 22880 x 4096 one piece and two
+// CTAs of 16 warps 323, two pieces 425; at 43904 x 5120 two pieces and two
 // CTAs 836, three CTAs (64 registers) 984, one piece and two CTAs 1083.
 struct BackShape {
   int v, warps, per_sm;
 };
 inline BackShape back_shape(int n) {
-  const int v = n <= 2560 ? 1 : n <= 8192 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
-  int per_sm = v == 1 ? (warps > 8 ? 3 : 24 / warps) : warps <= 10 ? 2 : 1;
+  const int v = n <= 4096 ? 1 : n <= 8192 ? 2 : 4, warps = (n + 256 * v - 1) / (256 * v);
+  int per_sm = v == 1 ? (warps > 10 ? 2 : warps > 8 ? 3 : 24 / warps) : warps <= 10 ? 2 : 1;
   if (per_sm > 16) per_sm = 16;
   return {v, warps, per_sm};
 }
@@ -432,6 +433,7 @@ cudaError_t backward(const NormParams& q, cudaStream_t s) {
   p.stages = fit < 1 ? 1 : fit > kMaxStagesBack ? kMaxStagesBack : static_cast<int>(fit);
   switch (sh.v) {
     case 1:
+      if (sh.warps > 10) return backward_one<T, R, 1, 512, 2>(p, s);
       if (sh.warps > 8) return backward_one<T, R, 1, 320, 3>(p, s);
       return backward_one<T, R, 1, 256, 3>(p, s);
     case 2:
